@@ -16,7 +16,10 @@ import ctypes
 import os
 import threading
 
+from . import attention as _attention
 from ._build import LIB_PATH, build, up_to_date
+from .attention import (TKS_DRAFTS_MAX, TKS_E_INDEX, TKS_I8, Cache, Queries, cache_read, cache_write,
+                        selected_attention, tree_attention, tree_mask)
 
 TKS_F32 = 0
 TKS_BF16 = 1
@@ -41,7 +44,7 @@ TKS_OPT_TEST_SKIP_ARRIVE = 4
 TKS_OPT_FORCE_THREADS = 5
 TKS_OPT_CLUSTER = 6
 
-# Every entry point include/tks.h declares, with its ctypes signature.
+# Every entry point include/tks.h and include/tks_attention.h declare, with its ctypes signature.
 _I32, _I64, _VP = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 SIGNATURES = {
     "tks_topk_indices": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
@@ -54,6 +57,7 @@ SIGNATURES = {
     "tks_topk_indices_noalloc": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
     "tks_topk_indices_sorted": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
     "tks_topk_indices_host": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
+    **_attention.SIGNATURES,
 }
 
 _lock = threading.Lock()
@@ -268,4 +272,6 @@ __all__ = [
     "TKS_E_TIMEOUT", "TKS_E_INTERNAL", "TKS_E_ROW_LEN", "TKS_E_TOO_LARGE", "TKS_NOALLOC_MAX_ROWS",
     "TKS_K_MAX", "TKS_SORTED_K_MAX", "TKS_OPT_FORCE_GROUP",
     "TKS_OPT_SPIN_LIMIT_NS", "TKS_OPT_MIN_PER_BLOCK", "TKS_OPT_TEST_SKIP_ARRIVE", "TKS_OPT_FORCE_THREADS", "TKS_OPT_CLUSTER",
+    "cache_write", "cache_read", "tree_attention", "selected_attention", "tree_mask", "Cache", "Queries",
+    "TKS_I8", "TKS_E_INDEX", "TKS_DRAFTS_MAX",
 ]

@@ -1,0 +1,464 @@
+// Host side of the cache and attention calls (include/tks_attention.h), and
+// the kernel that joins partial results.
+
+#include <cmath>
+#include <cstring>
+#include <map>
+#include <mutex>
+#include <utility>
+
+#include "tks_attention.h"
+#include "tks_attn.cuh"
+
+namespace tks {
+namespace attn {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Joining the partial results of units that were split over blocks:
+//     out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,  m = max_s m_s.
+// A unit's partials are few (most units are whole, and return at once) or, for
+// a lone long sequence, many; in the first case a warp takes a row (PER_BLOCK =
+// 8), in the second the block's warps share one row's partials.
+// ---------------------------------------------------------------------------
+template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Params p, int blocks) {
+  constexpr int kVec = D / 32, kStep = PER_BLOCK == 8 ? 1 : 8;
+  __shared__ long long total_s, cum_s;
+  __shared__ float acc_s[8][D], l_s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = p.kv_heads * p.row_tiles;
+  const int seq = blockIdx.x / per, in = blockIdx.x % per;
+  const int head = in / p.row_tiles, row_tile = in % p.row_tiles;
+  const int first = row_tile * ROWS + blockIdx.y * PER_BLOCK;
+  grid_wait();
+  grid_launch_dependents();
+  if (first >= p.rows) return;
+  const Seq len = seq_of<SEL>(p, seq);
+  const int tiles = tiles_of<TK>(len.len);
+  if (warp == 0) {
+    if (SEL) {
+      if (lane == 0) {
+        total_s = (long long)per * tiles * p.seqs;
+        cum_s = (long long)per * tiles * seq;
+      }
+    } else {
+      long long all = 0, before = 0;
+      for (int s = lane; s < p.seqs; s += 32) {
+        const int t = tiles_of<TK>(seq_of<SEL>(p, s).len);
+        all += t;
+        before += s < seq ? t : 0;
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+      }
+      if (lane == 0) {
+        total_s = all * per;
+        cum_s = before * per;
+      }
+    }
+  }
+  __syncthreads();
+  const long long W = total_s, w0 = cum_s + (long long)in * tiles;
+  const int c0 = block_of(W, w0, blocks), c1 = block_of(W, w0 + tiles - 1, blocks);
+  if (c0 == c1) return;  // whole: its block has written the output
+
+  const int r = first - row_tile * ROWS + (PER_BLOCK == 8 ? warp : 0);  // row in its tile
+  const int R = row_tile * ROWS + r;
+  const bool live = r < ROWS && R < p.rows;
+  auto part_of = [&](int c) -> const float* {
+    const int slot = c == c0 && block_start(W, c, blocks) != w0 ? 1 : 0;
+    return p.parts + (2LL * c + slot) * kPartFloats<ROWS, D>;
+  };
+  auto used = [&](int c) { return block_start(W, c, blocks) < block_start(W, c + 1, blocks); };
+
+  float m = -INFINITY;
+  if (live)
+    for (int c = c0 + lane; c <= c1; c += 32)
+      if (used(c)) {
+        const float2 q = *reinterpret_cast<const float2*>(part_of(c) + ROWS * D + 2 * r);
+        if (q.y != 0.f) m = fmaxf(m, q.x);
+      }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float l = 0.f, acc[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+  if (live) {
+#pragma unroll 4
+    for (int c = c0 + (kStep == 1 ? 0 : warp); c <= c1; c += kStep) {
+      if (!used(c)) continue;
+      const float* part = part_of(c);
+      const float2 q = *reinterpret_cast<const float2*>(part + ROWS * D + 2 * r);
+      float o[kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) o[i] = part[r * D + lane * kVec + i];
+      if (q.y == 0.f) continue;  // saw nothing
+      const float f = q.x == m ? 1.f : ex2(q.x - m);
+      l += f * q.y;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += f * o[i];
+    }
+  }
+  if (PER_BLOCK != 8) {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc_s[warp][lane * kVec + i] = acc[i];
+    if (lane == 0) l_s[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      l += l_s[k];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += acc_s[k][lane * kVec + i];
+    }
+  }
+  if (!live) return;
+  const float g = l == 0.f ? 0.f : 1.f / l;
+  const long long row = out_row<SEL>(p, seq, head, R);
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kVec);
+#pragma unroll
+  for (int i = 0; i < kVec / 2; ++i) out[i] = pack_bf16(acc[2 * i] * g, acc[2 * i + 1] * g);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
+}
+
+template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
+cudaError_t combine(const Params& p, int blocks, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  const int rows = p.rows < ROWS ? p.rows : ROWS;
+  cfg.gridDim = dim3((unsigned)(p.seqs * p.kv_heads * p.row_tiles), (unsigned)((rows + PER_BLOCK - 1) / PER_BLOCK));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1] = {};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<ROWS, D, TK, SEL, PER_BLOCK>, p, blocks);
+}
+
+template <int ROWS, int TK>
+cudaError_t launch_combine(const Params& p, int head_dim, bool selected, int blocks, cudaStream_t s) {
+  // many partials for a unit, or few
+  const bool many = (long long)p.seqs * p.kv_heads * p.row_tiles * 8 < blocks;
+  if (head_dim == 64) {
+    if (selected) return many ? combine<ROWS, 64, TK, true, 1>(p, blocks, s) : combine<ROWS, 64, TK, true, 8>(p, blocks, s);
+    return many ? combine<ROWS, 64, TK, false, 1>(p, blocks, s) : combine<ROWS, 64, TK, false, 8>(p, blocks, s);
+  }
+  if (selected) return many ? combine<ROWS, 128, TK, true, 1>(p, blocks, s) : combine<ROWS, 128, TK, true, 8>(p, blocks, s);
+  return many ? combine<ROWS, 128, TK, false, 1>(p, blocks, s) : combine<ROWS, 128, TK, false, 8>(p, blocks, s);
+}
+
+// ---------------------------------------------------------------------------
+// Devices and workspaces
+// ---------------------------------------------------------------------------
+struct Device {
+  int sms = 0;
+  bool ok = false;
+};
+struct Workspace {
+  unsigned char* ptr = nullptr;  // status word (256 bytes), then partial slots
+};
+
+constexpr size_t kHeaderBytes = 256;
+
+std::mutex g_mu;
+std::map<int, Device> g_dev;
+std::map<std::pair<int, void*>, Workspace> g_ws;
+
+size_t part_bytes(const Device& d) {
+  return (size_t)d.sms * kRowsBlocksPerSm * 2 * kPartFloats<kRowsTile, 128> * sizeof(float);
+}
+
+// The current device and its workspace for `stream`, allocated on first use.
+int prepare(void* stream, Device* dev, Workspace* ws) {
+  int id = 0;
+  if (cudaGetDevice(&id) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_UNSUPPORTED;
+  }
+  std::lock_guard<std::mutex> lock(g_mu);
+  auto di = g_dev.find(id);
+  if (di == g_dev.end()) {
+    Device d;
+    int major = 0, minor = 0;
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, id) == cudaSuccess &&
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, id) == cudaSuccess &&
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id) == cudaSuccess)
+      d.ok = major == 10 && minor == 3 && setup_rows() == cudaSuccess;
+    cudaGetLastError();
+    di = g_dev.emplace(id, d).first;
+  }
+  if (!di->second.ok) return TKS_E_UNSUPPORTED;
+  *dev = di->second;
+  const auto key = std::make_pair(id, stream);
+  auto wi = g_ws.find(key);
+  if (wi == g_ws.end()) {
+    Workspace w;
+    if (cudaMalloc(&w.ptr, kHeaderBytes + part_bytes(*dev)) != cudaSuccess) {
+      cudaGetLastError();
+      return TKS_E_CUDA;
+    }
+    if (cudaMemsetAsync(w.ptr, 0, kHeaderBytes, (cudaStream_t)stream) != cudaSuccess) {
+      cudaGetLastError();
+      cudaFree(w.ptr);
+      return TKS_E_CUDA;
+    }
+    wi = g_ws.emplace(key, w).first;
+  }
+  *ws = wi->second;
+  return TKS_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Argument checks (nothing is touched on the device)
+// ---------------------------------------------------------------------------
+bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+// Strides in elements of `size` bytes (with the extents they step over): none is
+// negative, all are whole 16-byte pieces, and every offset in bytes fits 60 bits.
+bool strides_ok(int64_t size, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2 = 0, int64_t s2 = 0) {
+  const int64_t unit = 16 / size;
+  if (s0 < 0 || s1 < 0 || s2 < 0 || s0 % unit || s1 % unit || s2 % unit) return false;
+  const __int128 span = (__int128)n0 * s0 + (__int128)n1 * s1 + (__int128)n2 * s2;
+  return span * size < ((__int128)1 << 60);
+}
+
+int check_cache(const tks_cache* c) {
+  if (c == nullptr) return TKS_E_INVAL;
+  if (c->held != TKS_BF16 && c->held != TKS_I8) return TKS_E_INVAL;
+  if (c->head_dim != 64 && c->head_dim != 128) return TKS_E_INVAL;
+  if (c->kv_heads < 1 || c->pages < 1 || c->page_size < 1 || (c->page_size & (c->page_size - 1)))
+    return TKS_E_INVAL;
+  if ((int64_t)c->pages * c->page_size > INT32_MAX) return TKS_E_INVAL;
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return TKS_E_INVAL;
+  const int64_t size = c->held == TKS_I8 ? 1 : 2;
+  if (!strides_ok(size, c->pages, c->page_stride, c->page_size, c->token_stride, c->kv_heads, c->head_stride))
+    return TKS_E_INVAL;
+  if (c->held == TKS_I8 && (!c->scales || !aligned(c->scales, 8))) return TKS_E_INVAL;
+  return TKS_OK;
+}
+
+int log2_of(int32_t n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
+}
+
+int check_queries(const tks_cache* c, const tks_queries* q) {
+  if (q == nullptr) return TKS_E_INVAL;
+  if (q->batch < 0 || q->tokens < 0 || q->q_heads < 1 || q->q_heads % c->kv_heads) return TKS_E_INVAL;
+  if (!std::isfinite(q->softmax_scale)) return TKS_E_INVAL;
+  if (q->table_pages < 0 || q->table_stride < 0) return TKS_E_INVAL;
+  if (q->batch == 0 || q->tokens == 0) return TKS_OK;
+  if ((int64_t)q->batch * q->tokens > INT32_MAX / q->q_heads) return TKS_E_INVAL;
+  if (!q->q || !q->out || !aligned(q->q, 16) || !aligned(q->out, 16) || !aligned(q->lse, 4)) return TKS_E_INVAL;
+  if (!strides_ok(2, q->batch, q->q_batch_stride, q->tokens, q->q_token_stride, q->q_heads, q->q_head_stride))
+    return TKS_E_INVAL;
+  if (q->table_stride > ((int64_t)1 << 56) / (q->batch > 0 ? q->batch : 1)) return TKS_E_INVAL;
+  if (q->table_pages > 0 && (!q->page_table || !aligned(q->page_table, 4))) return TKS_E_INVAL;
+  return TKS_OK;
+}
+
+Params params_of(const tks_cache* c, const tks_queries* q) {
+  Params p{};
+  const long long size = c->held == TKS_I8 ? 1 : 2;
+  p.k = static_cast<const unsigned char*>(c->k);
+  p.v = static_cast<const unsigned char*>(c->v);
+  p.scales = reinterpret_cast<const float2*>(c->scales);
+  p.page_b = c->page_stride * size;
+  p.token_b = c->token_stride * size;
+  p.head_b = c->head_stride * size;
+  p.pages = c->pages;
+  p.page_shift = log2_of(c->page_size);
+  p.kv_heads = c->kv_heads;
+  p.q = static_cast<const __nv_bfloat16*>(q->q);
+  p.q_batch = q->q_batch_stride;
+  p.q_token = q->q_token_stride;
+  p.q_head = q->q_head_stride;
+  p.out = static_cast<__nv_bfloat16*>(q->out);
+  p.lse = q->lse;
+  p.batch = q->batch;
+  p.tokens = q->tokens;
+  p.q_heads = q->q_heads;
+  p.group = q->q_heads / c->kv_heads;
+  p.table = q->page_table;
+  p.table_stride = q->table_stride;
+  p.table_pages = q->table_pages;
+  p.scale_log2 = (float)((double)q->softmax_scale * 1.4426950408889634);
+  return p;
+}
+
+// Queues the attention kernel and the one that joins its partials.
+int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
+  Device d;
+  Workspace ws;
+  const int rc = prepare(stream, &d, &ws);
+  if (rc != TKS_OK) return rc;
+  p.status = reinterpret_cast<unsigned*>(ws.ptr);
+  p.parts = reinterpret_cast<float*>(ws.ptr + kHeaderBytes);
+  const bool i8 = c->held == TKS_I8;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const int grid = d.sms * kRowsBlocksPerSm;
+  p.row_tiles = (p.rows + kRowsTile - 1) / kRowsTile;
+  cudaError_t e = launch_rows(p, c->head_dim, i8, selected, grid, s);
+  if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}
+
+CacheParams cache_params(const tks_cache* c, const int32_t* slots, int32_t n, unsigned* status) {
+  CacheParams p{};
+  const long long size = c->held == TKS_I8 ? 1 : 2;
+  p.k = static_cast<unsigned char*>(c->k);
+  p.v = static_cast<unsigned char*>(c->v);
+  p.scales = c->scales;
+  p.page_b = c->page_stride * size;
+  p.token_b = c->token_stride * size;
+  p.head_b = c->head_stride * size;
+  p.page_shift = log2_of(c->page_size);
+  p.kv_heads = c->kv_heads;
+  p.slots_held = c->pages * c->page_size;
+  p.slots = slots;
+  p.n = n;
+  p.status = status;
+  return p;
+}
+
+}  // namespace
+}  // namespace attn
+
+int attn_status(int dev, void* stream) {
+  using namespace attn;
+  Workspace w;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    auto it = g_ws.find(std::make_pair(dev, stream));
+    if (it == g_ws.end()) return TKS_OK;
+    w = it->second;
+  }
+  unsigned st = 0;
+  if (cudaMemcpyAsync(&st, w.ptr, sizeof st, cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess ||
+      cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  if (st == 0) return TKS_OK;
+  if (cudaMemsetAsync(w.ptr, 0, kHeaderBytes, (cudaStream_t)stream) != cudaSuccess ||
+      cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  if (st & kStatTimeoutBit) return TKS_E_TIMEOUT;
+  return st & kStatIndexBit ? TKS_E_INDEX : TKS_E_ROW_LEN;
+}
+
+int attn_release() {
+  using namespace attn;
+  std::lock_guard<std::mutex> lock(g_mu);
+  int rc = TKS_OK, cur = 0;
+  cudaGetDevice(&cur);
+  for (auto& kv : g_ws) {
+    cudaSetDevice(kv.first.first);
+    if (cudaFree(kv.second.ptr) != cudaSuccess) rc = TKS_E_CUDA;
+  }
+  cudaSetDevice(cur);
+  cudaGetLastError();
+  g_ws.clear();
+  return rc;
+}
+
+}  // namespace tks
+
+using namespace tks;
+using namespace tks::attn;
+
+extern "C" int tks_cache_write(const tks_cache* cache, const void* k, const void* v, int32_t n,
+                               int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,
+                               int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                               void* stream) {
+  if (check_cache(cache) != TKS_OK || n < 0 || (dtype != TKS_BF16 && dtype != TKS_F32)) return TKS_E_INVAL;
+  if (n == 0) return TKS_OK;
+  const int64_t size = dtype == TKS_F32 ? 4 : 2;
+  if (!k || !v || !slots || !aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 4)) return TKS_E_INVAL;
+  if (!strides_ok(size, n, k_token_stride, cache->kv_heads, k_head_stride) ||
+      !strides_ok(size, n, v_token_stride, cache->kv_heads, v_head_stride))
+    return TKS_E_INVAL;
+  if ((int64_t)n * cache->kv_heads > INT32_MAX) return TKS_E_INVAL;
+  Device d;
+  Workspace ws;
+  const int rc = prepare(stream, &d, &ws);
+  if (rc != TKS_OK) return rc;
+  CacheParams p = cache_params(cache, slots, n, reinterpret_cast<unsigned*>(ws.ptr));
+  p.src_k = k;
+  p.src_v = v;
+  p.k_token = k_token_stride;
+  p.k_head = k_head_stride;
+  p.v_token = v_token_stride;
+  p.v_head = v_head_stride;
+  if (launch_cache_write(p, cache->head_dim, cache->held == TKS_I8, dtype == TKS_F32, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}
+
+extern "C" int tks_cache_read(const tks_cache* cache, const int32_t* slots, int32_t n, void* k_out,
+                              void* v_out, int32_t dtype, void* stream) {
+  if (check_cache(cache) != TKS_OK || n < 0 || (dtype != TKS_BF16 && dtype != TKS_F32)) return TKS_E_INVAL;
+  if (n == 0) return TKS_OK;
+  if (!slots || !k_out || !v_out || !aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16)) return TKS_E_INVAL;
+  if ((int64_t)n * cache->kv_heads > INT32_MAX) return TKS_E_INVAL;
+  Device d;
+  Workspace ws;
+  const int rc = prepare(stream, &d, &ws);
+  if (rc != TKS_OK) return rc;
+  CacheParams p = cache_params(cache, slots, n, reinterpret_cast<unsigned*>(ws.ptr));
+  p.out_k = k_out;
+  p.out_v = v_out;
+  if (launch_cache_read(p, cache->head_dim, cache->held == TKS_I8, dtype == TKS_F32, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}
+
+extern "C" int tks_tree_attention(const tks_cache* cache, const tks_queries* queries,
+                                  const int32_t* ctx_len, const int32_t* draft_len,
+                                  const int32_t* tree, void* stream) {
+  if (check_cache(cache) != TKS_OK || check_queries(cache, queries) != TKS_OK) return TKS_E_INVAL;
+  if (queries->tokens > TKS_DRAFTS_MAX) return TKS_E_INVAL;
+  if (queries->batch == 0 || queries->tokens == 0) return TKS_OK;
+  if (!ctx_len || !aligned(ctx_len, 4) || !aligned(draft_len, 4) || !aligned(tree, 4)) return TKS_E_INVAL;
+  Params p = params_of(cache, queries);
+  p.ctx_len = ctx_len;
+  p.draft_len = draft_len;
+  p.tree = tree;
+  p.tree_words = (queries->tokens + 31) / 32;
+  p.seqs = queries->batch;
+  p.rows = queries->tokens * p.group;
+  return launch(p, cache, false, stream);
+}
+
+extern "C" int tks_selected_attention(const tks_cache* cache, const tks_queries* queries,
+                                      const int32_t* indices, int32_t k, const int32_t* kv_len,
+                                      void* stream) {
+  if (check_cache(cache) != TKS_OK || check_queries(cache, queries) != TKS_OK) return TKS_E_INVAL;
+  if (k < 0 || k > TKS_K_MAX) return TKS_E_INVAL;
+  if (queries->batch == 0 || queries->tokens == 0) return TKS_OK;
+  if ((k > 0 && !indices) || !aligned(indices, 4) || !aligned(kv_len, 4)) return TKS_E_INVAL;
+  Params p = params_of(cache, queries);
+  p.indices = indices;
+  p.k_sel = k;
+  p.kv_len = kv_len;
+  p.seqs = queries->batch * queries->tokens;
+  p.rows = p.group;
+  return launch(p, cache, true, stream);
+}

@@ -1,0 +1,79 @@
+// Internal interface between the cache and attention translation units of
+// libtks (not part of the C ABI).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace tks {
+namespace attn {
+
+// Status bits of the workspace's first word.
+constexpr unsigned kStatTimeoutBit = 1u << 0;
+constexpr unsigned kStatRowLenBit = 1u << 1;
+constexpr unsigned kStatIndexBit = 1u << 3;
+
+// Most positions of a sequence: indices of keys stay below 2^31 with a tile to spare.
+constexpr int kMaxPositions = 0x7fff0000;
+
+// Arguments of the cache kernels.
+struct CacheParams {
+  unsigned char *k, *v;
+  float* scales;
+  long long page_b, token_b, head_b;  // strides of the cache in bytes
+  int page_shift, kv_heads;
+  int slots_held;  // pages * page_size
+  const int32_t* slots;
+  int n;
+  const void *src_k, *src_v;                   // write: rows to put in,
+  long long k_token, k_head, v_token, v_head;  // and their strides in elements
+  void *out_k, *out_v;                         // read: where rows go
+  unsigned* status;
+};
+cudaError_t launch_cache_write(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s);
+cudaError_t launch_cache_read(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s);
+
+// Arguments of the attention kernels.
+struct Params {
+  const unsigned char *k, *v;
+  const float2* scales;
+  long long page_b, token_b, head_b;  // strides of the cache in bytes
+  int pages, page_shift, kv_heads;
+  const __nv_bfloat16* q;
+  long long q_batch, q_token, q_head;  // elements
+  __nv_bfloat16* out;
+  float* lse;
+  int batch, tokens, q_heads, group;
+  const int32_t* table;
+  long long table_stride;
+  int table_pages;
+  const int32_t *ctx_len, *draft_len, *tree;  // tree attention
+  int tree_words;
+  const int32_t *indices, *kv_len;  // selected attention
+  int k_sel;
+  float scale_log2;  // softmax_scale * log2(e)
+  int seqs;          // tree: batch; selected: batch * tokens
+  int rows;          // query rows of one (sequence, head)
+  int row_tiles;
+  unsigned* status;
+  float* parts;
+  long long spin_limit_ns;
+};
+
+// The kernels for few rows (16 a block; mma.sync).
+constexpr int kRowsTile = 16;  // query rows of a block
+constexpr int kRowsKeys = 64;  // keys of a tile
+cudaError_t setup_rows();
+constexpr int kRowsBlocksPerSm = 2;
+cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,
+                        cudaStream_t stream);
+
+}  // namespace attn
+
+// The workspace of the cache and attention calls on a stream: a status word
+// (256 bytes) and the partial results.  Host side, tks_attn.cu.
+int attn_status(int dev, void* stream);  // a tks_status; the stream has been synchronised
+int attn_release();
+
+}  // namespace tks

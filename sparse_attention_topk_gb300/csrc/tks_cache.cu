@@ -1,0 +1,214 @@
+// Writing the keys and values of new tokens into the paged cache, and reading
+// rows of it back.
+//
+// Mathematics.  A row x of head_dim values (one token, one head) is held in 8
+// bits as code_d = rint(x_d / scale) with scale = amax / 127, amax = max |x_d|
+// held to [2^-40, 2^80]: the error of a value is at most scale / 2.  Both
+// divisions are products with a correctly rounded reciprocal, in 32 bits.
+//
+// What bounds it: bytes.  Nothing is read twice: a row is split over
+// head_dim / 8 neighbouring lanes (eight elements each: one or two 16-byte
+// loads, one 8- or 16-byte store), its maximum goes round them by shuffles, and
+// a lane has kRowsPerLane rows in flight.
+
+#include "tks_attn.cuh"
+
+namespace tks {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerLane = 4;
+
+// Eight elements of a row in 32 bits.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(u[i] << 16);
+    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                                            pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
+  return ((uint32_t)(int)a & 0xffu) | (((uint32_t)(int)b & 0xffu) << 8) |
+         (((uint32_t)(int)c & 0xffu) << 16) | ((uint32_t)(int)d << 24);
+}
+
+// Rows are counted head fastest, then token; blockIdx.y is 0 for keys, 1 for values.
+template <typename T, bool I8, int D>
+__global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__ CacheParams p) {
+  constexpr int kLanes = D / 8, kPerPass = kThreads / kLanes;
+  const int g = threadIdx.x / kLanes, e = (threadIdx.x % kLanes) * 8;
+  const bool value = blockIdx.y != 0;
+  const T* src = static_cast<const T*>(value ? p.src_v : p.src_k);
+  const long long s_token = value ? p.v_token : p.k_token, s_head = value ? p.v_head : p.k_head;
+  unsigned char* dst = value ? p.v : p.k;
+  const unsigned total = (unsigned)p.n * (unsigned)p.kv_heads;
+  const unsigned row0 = blockIdx.x * (kPerPass * kRowsPerLane) + g;
+  grid_wait();
+  grid_launch_dependents();
+
+  float x[kRowsPerLane][8];
+  int slot[kRowsPerLane];
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const unsigned row = row0 + i * kPerPass;
+    slot[i] = -1;
+    if (row < total) {
+      const unsigned token = row / (unsigned)p.kv_heads, head = row - token * p.kv_heads;
+      slot[i] = __ldg(p.slots + token);
+      load8(src + token * s_token + head * s_head + e, x[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const unsigned row = row0 + i * kPerPass;
+    const unsigned token = row / (unsigned)p.kv_heads, head = row - token * p.kv_heads;
+    const bool ok = slot[i] >= 0 && slot[i] < p.slots_held;
+    if (slot[i] >= p.slots_held) report(p.status, kStatIndexBit);
+    const long long at = (slot[i] >> p.page_shift) * p.page_b +
+                         (slot[i] & ((1 << p.page_shift) - 1)) * p.token_b + head * p.head_b;
+    if (!I8) {
+      if (ok) store8(reinterpret_cast<__nv_bfloat16*>(dst + at) + e, x[i]);
+      continue;
+    }
+    float amax = 0.f;
+    bool nan = false;
+    if (ok)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        amax = fmaxf(amax, fabsf(x[i][j]));
+        nan |= x[i][j] != x[i][j];
+      }
+    if (nan) amax = __int_as_float(0x7fffffff);
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) {
+      // unsigned order of non-negative floats is theirs, with NaN on top
+      const unsigned y = __shfl_xor_sync(0xffffffffu, __float_as_uint(amax), o);
+      amax = __uint_as_float(max(__float_as_uint(amax), y));
+    }
+    if (!ok) continue;
+    const float lo = 9.094947017729282e-13f, hi = 1.2089258196146292e24f;  // 2^-40, 2^80
+    amax = amax < lo ? lo : amax > hi ? hi : amax;
+    const float scale = __fmul_rn(amax, 1.0f / 127.0f), inv = __frcp_rn(scale);
+    float q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      q[j] = fminf(fmaxf(rintf(__fmul_rn(x[i][j], inv)), -127.f), 127.f);
+    *reinterpret_cast<uint2*>(dst + at + e) =
+        make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+    if (e == 0) p.scales[2 * ((long long)slot[i] * p.kv_heads + head) + (value ? 1 : 0)] = scale;
+  }
+}
+
+template <typename T, bool I8, int D>
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ CacheParams p) {
+  constexpr int kLanes = D / 8, kPerPass = kThreads / kLanes;
+  const int g = threadIdx.x / kLanes, e = (threadIdx.x % kLanes) * 8;
+  const bool value = blockIdx.y != 0;
+  T* dst = static_cast<T*>(value ? p.out_v : p.out_k);
+  const unsigned char* src = value ? p.v : p.k;
+  const unsigned total = (unsigned)p.n * (unsigned)p.kv_heads;
+  const unsigned row0 = blockIdx.x * (kPerPass * kRowsPerLane) + g;
+  grid_wait();
+  grid_launch_dependents();
+
+  int slot[kRowsPerLane];
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const unsigned row = row0 + i * kPerPass;
+    slot[i] = row < total ? __ldg(p.slots + row / (unsigned)p.kv_heads) : -1;
+    if (slot[i] >= p.slots_held) {
+      report(p.status, kStatIndexBit);
+      slot[i] = -1;
+    }
+  }
+  uint4 w[kRowsPerLane];
+  float scale[kRowsPerLane];
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const unsigned row = row0 + i * kPerPass;
+    const unsigned head = row - (row / (unsigned)p.kv_heads) * p.kv_heads;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    scale[i] = 0.f;
+    if (slot[i] < 0) continue;
+    const unsigned char* at = src + (slot[i] >> p.page_shift) * p.page_b +
+                              (slot[i] & ((1 << p.page_shift) - 1)) * p.token_b + head * p.head_b;
+    if (I8) {
+      const uint2 y = *reinterpret_cast<const uint2*>(at + e);
+      w[i].x = y.x;
+      w[i].y = y.y;
+      scale[i] = p.scales[2 * ((long long)slot[i] * p.kv_heads + head) + (value ? 1 : 0)];
+    } else {
+      w[i] = *reinterpret_cast<const uint4*>(at + 2 * e);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerLane; ++i) {
+    const unsigned row = row0 + i * kPerPass;
+    if (row >= total) continue;
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (I8)
+        x[j] = (float)(int)(signed char)(u[j >> 2] >> (8 * (j & 3))) * scale[i];
+      else
+        x[j] = __uint_as_float(j & 1 ? u[j >> 1] & 0xffff0000u : u[j >> 1] << 16);
+    }
+    store8(dst + (long long)row * D + e, x);
+  }
+}
+
+template <typename K>
+cudaError_t run(K kernel, const CacheParams& p, int head_dim, cudaStream_t stream) {
+  const unsigned per = kThreads / (head_dim / 8) * kRowsPerLane;
+  const unsigned long long rows = (unsigned long long)p.n * p.kv_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((rows + per - 1) / per), 2);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1] = {};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s) {
+  if (head_dim == 64) {
+    if (i8) return f32 ? run(write_kernel<float, true, 64>, p, 64, s) : run(write_kernel<__nv_bfloat16, true, 64>, p, 64, s);
+    return f32 ? run(write_kernel<float, false, 64>, p, 64, s) : run(write_kernel<__nv_bfloat16, false, 64>, p, 64, s);
+  }
+  if (i8) return f32 ? run(write_kernel<float, true, 128>, p, 128, s) : run(write_kernel<__nv_bfloat16, true, 128>, p, 128, s);
+  return f32 ? run(write_kernel<float, false, 128>, p, 128, s) : run(write_kernel<__nv_bfloat16, false, 128>, p, 128, s);
+}
+
+cudaError_t launch_cache_read(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s) {
+  if (head_dim == 64) {
+    if (i8) return f32 ? run(read_kernel<float, true, 64>, p, 64, s) : run(read_kernel<__nv_bfloat16, true, 64>, p, 64, s);
+    return f32 ? run(read_kernel<float, false, 64>, p, 64, s) : run(read_kernel<__nv_bfloat16, false, 64>, p, 64, s);
+  }
+  if (i8) return f32 ? run(read_kernel<float, true, 128>, p, 128, s) : run(read_kernel<__nv_bfloat16, true, 128>, p, 128, s);
+  return f32 ? run(read_kernel<float, false, 128>, p, 128, s) : run(read_kernel<__nv_bfloat16, false, 128>, p, 128, s);
+}
+
+}  // namespace attn
+}  // namespace tks

@@ -48,6 +48,7 @@
 #include "tks.h"
 #include "tks_kernel.cuh"  // the 256-thread kernel, namespace tks::k256
 #include "tks_internal.h"
+#include "tks_attn_internal.h"
 
 namespace tks {
 using namespace k256;  // shared-memory, workspace and status constants (equal for k512)
@@ -439,7 +440,7 @@ extern "C" int tks_device_status(void* stream) {
   {
     std::lock_guard<std::mutex> lock(g_mu);
     auto it = g_ws.find(std::make_pair(dev, stream));
-    if (it == g_ws.end()) return TKS_OK;
+    if (it == g_ws.end()) return attn_status(dev, stream);  // (no selection on this stream)
     w = it->second;
   }
   unsigned st = 0;
@@ -449,7 +450,7 @@ extern "C" int tks_device_status(void* stream) {
     cudaGetLastError();
     return TKS_E_CUDA;
   }
-  if (st == 0) return TKS_OK;
+  if (st == 0) return attn_status(dev, stream);
   if (workspace_clear(w, w.slots, (cudaStream_t)stream) != cudaSuccess ||
       cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
@@ -470,6 +471,7 @@ extern "C" const char* tks_status_string(int status) {
     case TKS_E_INTERNAL: return "device-side consistency check failed";
     case TKS_E_ROW_LEN: return "a row length was outside [0, row_stride] and was clamped";
     case TKS_E_TOO_LARGE: return "more rows than the allocation-free entry point's fixed scratch holds";
+    case TKS_E_INDEX: return "a slot, page or position lay outside the cache and was skipped";
     default: return "unknown status";
   }
 }
@@ -488,7 +490,8 @@ extern "C" int tks_release(void) {
   cudaSetDevice(cur);
   cudaGetLastError();
   g_ws.clear();
-  return rc;
+  const int arc = attn_release();
+  return rc != TKS_OK ? rc : arc;
 }
 
 extern "C" int tks_set_option(int option, int64_t value) {

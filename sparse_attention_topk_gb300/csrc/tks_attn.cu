@@ -1,6 +1,7 @@
 // Host side of the cache and attention calls (include/tks_attention.h), and
 // the kernel that joins partial results.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -172,7 +173,9 @@ std::map<int, Device> g_dev;
 std::map<std::pair<int, void*>, Workspace> g_ws;
 
 size_t part_bytes(const Device& d) {
-  return (size_t)d.sms * kRowsBlocksPerSm * 2 * kPartFloats<kRowsTile, 128> * sizeof(float);
+  const size_t few = (size_t)d.sms * kRowsBlocksPerSm * 2 * kPartFloats<kRowsTile, 128>;
+  const size_t many = (size_t)d.sms * 2 * kPartFloats<kTilesRows, 128>;
+  return (few > many ? few : many) * sizeof(float);
 }
 
 // The current device and its workspace for `stream`, allocated on first use.
@@ -190,7 +193,7 @@ int prepare(void* stream, Device* dev, Workspace* ws) {
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, id) == cudaSuccess &&
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, id) == cudaSuccess &&
         cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id) == cudaSuccess)
-      d.ok = major == 10 && minor == 3 && setup_rows() == cudaSuccess;
+      d.ok = major == 10 && minor == 3 && setup_rows() == cudaSuccess && setup_tiles() == cudaSuccess;
     cudaGetLastError();
     di = g_dev.emplace(id, d).first;
   }
@@ -303,10 +306,22 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   p.parts = reinterpret_cast<float*>(ws.ptr + kHeaderBytes);
   const bool i8 = c->held == TKS_I8;
   const cudaStream_t s = (cudaStream_t)stream;
-  const int grid = d.sms * kRowsBlocksPerSm;
-  p.row_tiles = (p.rows + kRowsTile - 1) / kRowsTile;
-  cudaError_t e = launch_rows(p, c->head_dim, i8, selected, grid, s);
-  if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
+  p.spin_limit_ns = spin_limit_ns();
+  p.test_skip_arrive = test_skip_arrive();
+  cudaError_t e;
+  if (p.rows <= kRowsTile) {
+    const int grid = d.sms * kRowsBlocksPerSm;
+    p.row_tiles = (p.rows + kRowsTile - 1) / kRowsTile;
+    e = launch_rows(p, c->head_dim, i8, selected, grid, s);
+    if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
+  } else {
+    const int grid = d.sms;
+    p.row_tiles = (p.rows + kTilesRows - 1) / kTilesRows;
+    const int64_t keys = selected ? p.k_sel : std::min((int64_t)p.table_pages << p.page_shift, (int64_t)kMaxPositions);
+    if ((keys / kTilesKeys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
+    e = launch_tiles(p, c->head_dim, i8, selected, grid, s);
+    if (e == cudaSuccess) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

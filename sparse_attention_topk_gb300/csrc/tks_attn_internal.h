@@ -59,17 +59,30 @@ struct Params {
   unsigned* status;
   float* parts;
   long long spin_limit_ns;
+  int test_skip_arrive;
 };
 
 // The kernels for few rows (16 a block; mma.sync).
 constexpr int kRowsTile = 16;  // query rows of a block
 constexpr int kRowsKeys = 64;  // keys of a tile
-cudaError_t setup_rows();
 constexpr int kRowsBlocksPerSm = 2;
+cudaError_t setup_rows();
 cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,
                         cudaStream_t stream);
 
+// The kernels for many rows (128 a block, one block an SM; tcgen05).
+constexpr int kTilesRows = 128;
+constexpr int kTilesKeys = 128;
+cudaError_t setup_tiles();
+cudaError_t launch_tiles(const Params& p, int head_dim, bool i8, bool selected, int grid,
+                         cudaStream_t stream);
+
 }  // namespace attn
+
+// The time limit of device-side waits, and the test option that makes one run
+// out (tks_set_option; host side, tks_select.cu).
+long long spin_limit_ns();
+int test_skip_arrive();
 
 // The workspace of the cache and attention calls on a stream: a status word
 // (256 bytes) and the partial results.  Host side, tks_attn.cu.

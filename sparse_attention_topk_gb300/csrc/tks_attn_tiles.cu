@@ -1,0 +1,1068 @@
+// Attention over a paged cache for many query rows of each key/value head:
+// trees, wide head groups and selected positions of many heads, on the
+// tcgen05 tensor cores.
+//
+// Mathematics: that of tks_attn_rows.cu (running maximum and sum; codes of an
+// 8-bit cache exact in half precision, both scales folded into one
+// multiply-add per score, weights relative to the largest contribution).
+// Each row's queries get their own power of two. The running maximum follows
+// only when a row's has grown by more than 2^8: weights then reach 2^8 at
+// most, well inside a half, and the output in tensor memory is rarely rescaled.
+//
+// Layout.  A block is one SM: 128 query rows (a lane of tensor memory each)
+// against tiles of 128 keys. Warps 0-7 keep the rows: they take scores into
+// registers and write the weights back over them, as the next product's
+// operand, so neither touches shared memory. Warp 8 issues the products, S = Q K^T of tile i + 1 before O += P V
+// of tile i, into two score buffers, so they run while tile i's weights are
+// made. Warps 9-11 look up where the tile's keys lie (list, page table, scales)
+// some tiles ahead. Warps 12-19 bring the rows: 16-byte loads, codes widened to
+// halves, stored as 128-byte-swizzled operand tiles (keys K-major for the first
+// product; values, in the same form, read transposed by the second); a
+// bfloat16 cache goes there by cp.async. Rows are gathered one by one, so
+// pages, lists and the order of positions do not matter.
+//
+// What bounds it: up to 128 rows the cache's bytes (32 KB of int8 a tile, 1400
+// cycles at the memory's rate, against 1024 of tensor work for a full 128
+// rows); beyond, the products and, beside them, shared memory: operand reads,
+// the widened rows' stores and the scales' reads share its 128 bytes a cycle.
+//
+// Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
+// warp's role, which makes the waits on that warp run out; when all roles have
+// ended the block frees its tensor memory and returns.
+
+#include "tks_attn.cuh"
+
+namespace tks {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 640;
+constexpr int kRowWarps = 8, kMulWarp = 8, kMetaWarp0 = 9;  // then the producers
+constexpr int kKeys = kTilesKeys;  // keys of a tile
+constexpr int kMetas = 6;          // tiles whose lookups may be ahead
+constexpr int kProducers = 256, kProducer0 = 384;
+
+// Where a tile's keys lie, and what their scores are scaled with.
+struct Meta {
+  long long off[kKeys];  // byte offset of the row in the cache, or -1
+  // for each pair of keys: key scale * softmax scale * log2(e) of both (0 for no key),
+  // and log2 of the value scale of both (-inf for no key)
+  float kl[kKeys / 2][4];
+  float inv[kKeys];      // 1 / value scale; 0 for no key
+  unsigned valid[4];     // which keys there are
+  int draft0;            // the first drafted token's place in the tile (kKeys: none)
+  int pad[3];
+};
+
+template <int D, bool I8>
+struct Shape {
+  static constexpr int kBlock = kKeys * 128;              // 64 elements of every row
+  static constexpr int kMat = (D / 64) * kBlock;          // a tile's keys, or its values
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kMetaOff = kStages * 2 * kMat;
+  static constexpr int kBarOff = kMetaOff + kMetas * (int)sizeof(Meta);
+  static constexpr int kSmem = kBarOff + 512 + 1024;      // and room to align the base
+  static constexpr int kRow = D * (I8 ? 1 : 2);
+  static constexpr int kPieces = kRow / 16;               // 16-byte pieces of a row in the cache
+  static constexpr int kPer = kKeys * kPieces / kProducers;  // pieces of a matrix that a thread brings
+  // tensor memory columns
+  static constexpr int kS = 0, kO = 256, kQ = 384;
+};
+
+// Barriers, in 8-byte words behind the metas.
+enum Bar { kMetaFull = 0, kMetaEmpty = kMetaFull + kMetas, kKFull = kMetaEmpty + kMetas, kVFull = kKFull + 6, kEmpty = kVFull + 6,
+           kSFull = kEmpty + 6, kPReady = kSFull + 2, kPvDone = kPReady + 2, kQReady = kPvDone + 2, kFinal = kQReady + 1, kPair = kFinal + 1, kBars = kPair + 4 };
+static_assert(kBars * 8 <= 400, "barriers fit");
+
+__device__ __forceinline__ void bar_init(uint32_t a, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(n) : "memory");
+}
+// Barrier and tensor instructions take their addresses from uniform registers: with an address
+// that the compiler cannot see to be the same for the whole warp, each becomes a loop over its
+// lanes (some 200 cycles). So whole warps come here, with addresses made of uniform values, and
+// one elected lane acts.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// One arrival for the warp.
+__device__ __forceinline__ void bar_arrive(uint32_t a) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(a)
+      : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t a, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tmbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok) : "r"(a), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ long long now_ns() {
+  long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+
+// A place in a ring of N, and the parity of its use: (x mod N, x / N mod 2) for x = 0, 1, ...
+template <int N>
+struct Ring {
+  int i = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++i == N) {
+      i = 0;
+      parity ^= 1;
+    }
+  }
+};
+
+// What every role of the block shares.
+struct Block {
+  unsigned char* smem;  // stages
+  uint32_t stage, bars; // shared-memory addresses
+  volatile unsigned* poisoned;
+  unsigned* status;
+  long long limit;
+  Meta* metas;
+
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+  // Whether a barrier's phase of this parity is over, waiting for it up to the time limit.
+  // The answer is the same for all lanes of the warp. NAP: a wait that may be answered
+  // late sleeps between its looks, and leaves the issue slots to the others.
+  template <bool NAP = false>
+  __device__ __forceinline__ bool wait(int i, uint32_t parity) const {
+    const uint32_t a = bar(i);
+    long long t0 = 0;
+    for (unsigned looks = 1; !__all_sync(0xffffffffu, bar_try(a, parity)); ++looks) {
+      if (NAP) __nanosleep(100);
+      if (looks % 64 == 0) {  // (the clock is read now and then)
+        const long long t = now_ns();
+        if (t0 == 0) t0 = t;
+        if (__any_sync(0xffffffffu, t - t0 > limit)) {
+          if ((threadIdx.x & 31) == 0) report(status, kStatTimeoutBit);
+          return false;
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// ---- tensor memory and products ---------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
+}
+// D (tensor memory) = A (tensor memory) x B (shared memory) (+ D)
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+      : "memory");
+}
+#define TKS_R32(M) M(0), M(1), M(2), M(3), M(4), M(5), M(6), M(7), M(8), M(9), M(10), M(11), M(12), M(13), M(14), M(15), \
+                   M(16), M(17), M(18), M(19), M(20), M(21), M(22), M(23), M(24), M(25), M(26), M(27), M(28), M(29), M(30), M(31)
+// 32 columns of the warp's 32 lanes: a thread's lane, one register each.
+__device__ __forceinline__ void tc_ld32(uint32_t (&r)[32], uint32_t addr) {
+#define TKS_OUT(i) "=r"(r[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : TKS_R32(TKS_OUT) : "r"(addr) : "memory");
+#undef TKS_OUT
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+// 16 lanes by 64 (32) columns: register 4j + 2i + e is lane n + 8i, column 8j + 2c + e, of
+// thread 4n + c.
+__device__ __forceinline__ void tc_ld_frag(uint32_t (&r)[32], uint32_t addr) {
+#define TKS_OUT(i) "=r"(r[i])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : TKS_R32(TKS_OUT) : "r"(addr) : "memory");
+#undef TKS_OUT
+}
+// 16 lanes by 32 columns: register 2j + i is lane n + 8i, column 4j + c.
+__device__ __forceinline__ void tc_st_frag(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
+// 16 lanes by 8 (4) columns.
+__device__ __forceinline__ void tc_ld_piece(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_st_piece(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%2], {%0, %1};" ::"r"(a), "r"(b), "r"(addr) : "memory");
+}
+
+// A shared-memory operand of 128-byte rows, 128-byte swizzled. K-major (keys): 8-row
+// groups 1024 bytes apart. MN-major (values, transposed): 64-element blocks of the
+// row `lead` bytes apart, 8-key groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
+  return (uint64_t)((addr & 0x3ffffu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// 32-bit accumulators; both inputs half or bfloat16; B K-major or transposed; M = 128.
+__device__ __forceinline__ constexpr uint32_t instr(bool half, bool trans_b, int n) {
+  return (1u << 4) | ((half ? 0u : 1u) << 7) | ((half ? 0u : 1u) << 10) | ((trans_b ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+// ---- pairs of 32-bit floats ---------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// ---- a block's segments ---------------------------------------------------------
+struct Segment {
+  int seq, head, row_tile, b;
+  int t0, t1;
+  bool whole, first;
+  Seq len;
+};
+template <bool SEL>
+struct Segments {
+  long long w, w_first, w_end, cum;
+  int seq;
+  __device__ __forceinline__ void begin(const Start& st) {
+    w_first = block_start(st.total, blockIdx.x, gridDim.x);
+    w_end = block_start(st.total, blockIdx.x + 1, gridDim.x);
+    w = w_first;
+    cum = st.cum;
+    seq = st.seq;
+  }
+  __device__ __forceinline__ bool next(const Params& p, Segment& s) {
+    if (w >= w_end) return false;
+    s.len = seq_of<SEL>(p, seq);
+    const int tiles = tiles_of<kKeys>(s.len.len);
+    const unsigned rel = (unsigned)(w - cum);  // (a sequence's tiles over all heads fit: checked by the host)
+    const int unit = (int)(rel / (unsigned)tiles);
+    s.seq = seq;
+    s.b = SEL ? seq / p.tokens : seq;
+    s.head = unit / p.row_tiles;
+    s.row_tile = unit % p.row_tiles;
+    s.t0 = (int)(rel - (unsigned)unit * (unsigned)tiles);
+    s.t1 = (int)min((long long)tiles, s.t0 + (w_end - w));
+    s.whole = s.t0 == 0 && s.t1 == tiles;
+    s.first = w == w_first;
+    w += s.t1 - s.t0;
+    if (unit == p.kv_heads * p.row_tiles - 1 && s.t1 == tiles) {
+      cum += (long long)tiles * p.kv_heads * p.row_tiles;
+      ++seq;
+    }
+    return true;
+  }
+};
+
+// 32 bits of row t's view of the drafted tokens j0 .. j0 + 31 (those before 0 are context: seen).
+__device__ __forceinline__ unsigned draft_bits(const Params& p, int b, int t, int j0) {
+  if (j0 + 31 < 0) return ~0u;
+  if (!p.tree) {
+    const int n = t - j0;  // the last one seen
+    return n >= 31 ? ~0u : n < 0 ? 0u : (2u << n) - 1u;
+  }
+  const int32_t* row = p.tree + ((long long)b * p.tokens + t) * p.tree_words;
+  auto word = [&](int w) -> unsigned { return w < p.tree_words ? (unsigned)row[w] : 0u; };
+  if (j0 < 0) return (word(0) << -j0) | ((1u << -j0) - 1u);
+  const int w = j0 >> 5, sh = j0 & 31;
+  return sh ? (word(w) >> sh) | (word(w + 1) << (32 - sh)) : word(w);
+}
+
+// ---------------------------------------------------------------------------
+// Roles
+// ---------------------------------------------------------------------------
+
+// Warps 9-11: the lookups of every third tile.
+template <int D, bool I8, bool SEL>
+__device__ __forceinline__ void look_up(const Params& p, const Block& k, const Start& start, int who) {
+  const int lane = threadIdx.x & 31;
+  Segments<SEL> it;
+  it.begin(start);
+  Segment s;
+  unsigned g = 0;  // the tile's number in this block
+  while (it.next(p, s)) {
+    const int32_t* table = p.table + s.b * p.table_stride;
+    const int32_t* list = SEL ? p.indices + (long long)s.seq * p.k_sel : nullptr;
+    const int limit = SEL ? kv_limit(p, s.b) : 0;
+    const int end = (int)min((long long)s.len.len, (long long)s.t1 * kKeys);
+    auto entry = [&](int t, int i) -> int {  // key i of tile t: its list entry, or its position
+      const int j = t * kKeys + i;
+      if (t >= s.t1 || j >= end) return -1;
+      return SEL ? list[j] : j;
+    };
+    int t = uniform(s.t0 + (int)((who + 3u - g % 3u) % 3u));
+    const int t1 = uniform(s.t1);
+    int e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = entry(t, lane + 32 * i);
+    for (; t < t1; t += 3) {
+      int pos[4], pg[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        pos[i] = e[i];
+        if (SEL && pos[i] >= limit) {
+          report(p.status, kStatIndexBit);
+          pos[i] = -1;
+        }
+        pos[i] = max(pos[i], -1);
+        pg[i] = pos[i] < 0 ? -1 : table[pos[i] >> p.page_shift];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = entry(t + 3, lane + 32 * i);
+      float2 sc[4];
+      long long off[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool ok = pos[i] >= 0 && (unsigned)pg[i] < (unsigned)p.pages;
+        if (pos[i] >= 0 && !ok) report(p.status, kStatIndexBit);
+        const int in_page = pos[i] & ((1 << p.page_shift) - 1);
+        off[i] = ok ? pg[i] * p.page_b + in_page * p.token_b + s.head * p.head_b : -1;
+        sc[i] = make_float2(0.f, 1.f);
+        if (I8 && ok) sc[i] = p.scales[(((long long)pg[i] << p.page_shift) + in_page) * p.kv_heads + s.head];
+      }
+      const unsigned tile = uniform(g + (unsigned)(t - s.t0)), slot = tile % kMetas;
+      if (tile >= kMetas && !k.wait<true>(kMetaEmpty + slot, (tile / kMetas & 1) ^ 1)) return;
+      Meta& m = k.metas[slot];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int key = lane + 32 * i;
+        const bool ok = off[i] >= 0;
+        const unsigned bits = __ballot_sync(0xffffffffu, ok);
+        m.off[key] = off[i];
+        if (I8) {
+          const float lo = 7.105427357601002e-15f;  // 2^-47: a NaN stays one
+          const float vs = sc[i].y < lo ? lo : sc[i].y;
+          m.kl[key >> 1][key & 1] = ok ? sc[i].x * p.scale_log2 : 0.f;
+          m.kl[key >> 1][2 + (key & 1)] = ok ? lg2(vs) : -INFINITY;
+          m.inv[key] = !ok ? 0.f : vs == vs ? __fdividef(1.f, vs) : 1.f;  // (finite: a weight of 0 times it is 0)
+        }
+        if (lane == 0) m.valid[i] = bits;
+      }
+      if (lane == 0) {
+        const long long d = SEL ? kKeys : (long long)s.len.ctx - (long long)t * kKeys;
+        m.draft0 = d >= kKeys ? kKeys : (int)max(d, 0LL);
+      }
+      __syncwarp();
+      if (!(p.test_skip_arrive && tile == 0)) bar_arrive(k.bar(kMetaFull + slot));
+    }
+    g += (unsigned)(s.t1 - s.t0);
+  }
+}
+
+// Warps 12-19: the rows of every tile into its stage.
+template <int D, bool I8>
+__device__ __forceinline__ void produce(const Params& p, const Block& k, int tiles) {
+  using S = Shape<D, I8>;
+  const int t = threadIdx.x - kProducer0, lane = threadIdx.x & 31;
+  constexpr int kRows = kProducers / S::kPieces;  // rows that a pass covers
+  // A thread's piece of a row, and its first row. Eight neighbouring lanes take half of two rows
+  // of int8 (two 16-byte stores a piece), or a row's half of bfloat16: no bank conflicts.
+  const bool split = I8 && S::kPieces == 8;
+  const int piece = split ? (t & 3) | (t >> 2 & 4) : t % S::kPieces;
+  const int row0 = split ? (t >> 5) * 4 + (t >> 2 & 3) : t / S::kPieces;
+
+  if (I8) {
+    // A matrix's rows of the next tile are loaded as soon as this tile's have been stored.
+    const int blk = (piece >> 2) * S::kBlock, first = (piece & 3) * 2;
+    uint4 w[2][S::kPer];
+    auto load = [&](const Meta& m, int kv, uint4 (&x)[S::kPer]) {
+      const unsigned char* base = (kv ? p.v : p.k) + piece * 16;
+#pragma unroll
+      for (int i = 0; i < S::kPer; ++i) {
+        const long long off = m.off[row0 + i * kRows];
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (off >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(base + off));
+      }
+    };
+    auto store = [&](int st, int kv, const uint4 (&x)[S::kPer]) {
+      unsigned char* base = k.smem + (2 * st + kv) * S::kMat + blk;
+#pragma unroll
+      for (int i = 0; i < S::kPer; ++i) {
+        const int r = row0 + i * kRows;
+        const uint32_t a[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<uint4*>(base + r * 128 + (((first + j) ^ (r & 7)) << 4)) =
+              make_uint4(codes_to_half2<0x4140>(a[2 * j]), codes_to_half2<0x4342>(a[2 * j]),
+                         codes_to_half2<0x4140>(a[2 * j + 1]), codes_to_half2<0x4342>(a[2 * j + 1]));
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      bar_arrive(k.bar((kv ? kVFull : kKFull) + st));
+    };
+    Ring<kMetas> meta;
+    Ring<S::kStages> st;
+    auto leave = [&] {
+      __syncwarp();
+      bar_arrive(k.bar(kMetaEmpty + meta.i));
+      meta.next();
+    };
+    if (tiles == 0 || !k.wait(kMetaFull, 0)) return;
+    load(k.metas[0], 0, w[0]);
+    load(k.metas[0], 1, w[1]);
+    leave();
+    for (int g = 0; g < tiles; ++g) {
+      const bool more = g + 1 < tiles;
+      if (more && !k.wait(kMetaFull + meta.i, meta.parity)) return;
+      if (g >= S::kStages && !k.wait<true>(kEmpty + st.i, st.parity ^ 1)) return;
+      store(st.i, 0, w[0]);
+      if (more) load(k.metas[meta.i], 0, w[0]);
+      store(st.i, 1, w[1]);
+      if (more) {
+        load(k.metas[meta.i], 1, w[1]);
+        leave();
+      }
+      st.next();
+    }
+    return;
+  }
+
+  // bfloat16: cp.async straight into the stage; a tile is announced when the next one's copies are under way.
+  const int blk = (piece >> 3) * S::kBlock, at = piece & 7;
+  auto announce = [&](int st) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    bar_arrive(k.bar(kKFull + st));
+    bar_arrive(k.bar(kVFull + st));
+  };
+  Ring<kMetas> meta;
+  Ring<S::kStages> ring;
+  int last = 0;
+  for (int g = 0; g < tiles; ++g) {
+    const int st = ring.i;
+    if (!k.wait(kMetaFull + meta.i, meta.parity) || (g >= S::kStages && !k.wait<true>(kEmpty + st, ring.parity ^ 1))) {
+      cp_wait<0>();
+      return;
+    }
+    const Meta& m = k.metas[meta.i];
+    const int draft0 = m.draft0;
+    const uint32_t kd = k.stage + 2 * st * S::kMat + blk, vd = kd + S::kMat;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < S::kPer; ++i) {
+      const int r = row0 + i * kRows;
+      const long long off = m.off[r];
+      const long long src = off < 0 ? 0 : off + piece * 16;
+      const int dst = r * 128 + ((at ^ (r & 7)) << 4);
+      cp16(kd + dst, p.k + src, off < 0 ? 0 : 16);
+      if (r < draft0) {
+        cp16(vd + dst, p.v + src, off < 0 ? 0 : 16);
+      } else {
+        // a drafted token: infinities and NaNs must not meet the zero weights of rows that do not see it
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (off >= 0) x = *reinterpret_cast<const uint4*>(p.v + src);
+        uint32_t u[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((u[j] & 0x7f80u) == 0x7f80u) { u[j] &= 0xffff0000u; bad = true; }
+          if ((u[j] & 0x7f800000u) == 0x7f800000u) { u[j] &= 0x0000ffffu; bad = true; }
+        }
+        *reinterpret_cast<uint4*>(k.smem + (2 * st + 1) * S::kMat + blk + dst) = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+    if (bad) *k.poisoned = 1;
+    cp_commit();
+    __syncwarp();
+    bar_arrive(k.bar(kMetaEmpty + meta.i));
+    if (g > 0) {
+      cp_wait<1>();
+      announce(last);
+    }
+    last = st;
+    meta.next();
+    ring.next();
+  }
+  cp_wait<0>();
+  if (tiles > 0) announce(last);
+}
+
+// Warp 8: the products.
+template <int D, bool I8, bool SEL>
+__device__ __forceinline__ void multiply(const Params& p, const Block& k, const Start& start, uint32_t tmem) {
+  using S = Shape<D, I8>;
+  constexpr uint32_t kQk = instr(I8, false, kKeys), kPv = instr(I8, true, D);
+  Segments<SEL> it;
+  it.begin(start);
+  Segment s;
+  Ring<S::kStages> kr, vr;  // the stages of the first and of the second product
+  Ring<kMetas> mr;          // the second's lookups, which are done with, too
+  uint32_t gk = 0, gv = 0;  // their tiles, whose lowest bit is the score buffer
+  uint32_t seg = 0;
+  const uint64_t keys0 = operand(k.stage, 16), values0 = operand(k.stage + S::kMat, S::kBlock);
+  bool ok = true;
+  // O (+)= P V of the next tile; `fresh`: the segment's first
+  auto second = [&](bool fresh) -> bool {
+    if (!k.wait(kVFull + vr.i, vr.parity) || !k.wait(kPReady + (gv & 1), gv >> 1 & 1)) return false;
+    tc_fence_after();
+    const uint64_t v = values0 + (uint32_t)(vr.i * (2 * S::kMat >> 4));
+    const uint32_t a = tmem + S::kS + (gv & 1) * 128;
+#pragma unroll
+    for (int i = 0; i < kKeys / 16; ++i)
+      tc_mma(tmem + S::kO, a + (i >> 2) * 64 + (i & 3) * 8, v + i * (16 * 128 >> 4), kPv, !fresh || i > 0);
+    tc_commit(k.bar(kEmpty + vr.i));
+    tc_commit(k.bar(kMetaEmpty + mr.i));
+    tc_commit(k.bar(kPvDone + (gv & 1)));
+    mr.next();
+    vr.next();
+    ++gv;
+    return true;
+  };
+  while (ok && it.next(p, s)) {
+    if (!k.wait(kQReady, seg & 1)) break;
+    const int n = uniform(s.t1 - s.t0);
+    for (int i = 0; ok && i < n; ++i) {
+      if (!k.wait(kKFull + kr.i, kr.parity)) { ok = false; break; }
+      tc_fence_after();
+      const uint64_t b = keys0 + (uint32_t)(kr.i * (2 * S::kMat >> 4));
+      const uint32_t d = tmem + S::kS + (gk & 1) * 128;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+        tc_mma(d, tmem + S::kQ + 8 * j, b + (j >> 2) * (S::kBlock >> 4) + (j & 3) * 2, kQk, j > 0);
+      tc_commit(k.bar(kSFull + (gk & 1)));
+      kr.next();
+      ++gk;
+      if (i > 0) ok = second(i == 1);
+    }
+    if (ok) ok = second(n == 1);
+    ++seg;
+  }
+  // nothing may be under way when tensor memory is freed
+  tc_commit(k.bar(kFinal));
+  k.wait(kFinal, 0);
+}
+
+// What the two warps of a quarter of the rows tell each other, by row n + 8 * i of the
+// quarter at [n][i].
+struct PairRows {
+  float top[2][2][8][4];  // a tile's maxima: [tile & 1][half of the keys]
+  float sum[2][8][4];     // a segment's sums
+  float m[8][4];          // and maxima
+  float fac[8][4];        // what undoes the shifts of the rows' queries
+  unsigned seen[2][2][8][4];  // the keys that a row sees: [half of the keys][32 keys]
+};
+// Scales 16 lanes by 32 columns: lanes n by fa, lanes n + 8 by fb.
+__device__ __forceinline__ void rescale(uint32_t addr, float fa, float fb) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+        "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * (i & 2 ? fb : fa));
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
+// The segments of a row warp, kept in shared memory: its registers hold scores.
+template <bool SEL>
+struct RowSegments {
+  Segments<SEL> it;
+  Segment s[2];
+};
+
+// Warps 0-7: warps w and w + 4 have query rows 32w .. 32w + 31, warp w the first 64 keys of
+// every tile, warp w + 4 the others. Scores come in the layout of matrix fragments: thread
+// 4n + c has rows n, n + 8, n + 16, n + 24 and keys 8j + 2c, 8j + 2c + 1, so the scales that it
+// needs are an eighth of the tile's. Queries and outputs go by whole rows, a thread each, and
+// half the elements for each warp.
+template <int D, bool I8, bool SEL>
+__device__ __forceinline__ void rows(const Params& p, const Block& k, const Start& start, uint32_t tmem, RowSegments<SEL>& segs, PairRows& pr) {
+  using S = Shape<D, I8>;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
+  const int n = lane >> 2, c = lane & 3, r = quarter * 32 + lane;
+  const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);
+  if (lane == 0) segs.it.begin(start);
+  // the next segment, into place `at`
+  auto advance = [&](int at) -> bool {
+    int more = 0;
+    if (lane == 0) more = segs.it.next(p, segs.s[at]) ? 1 : 0;
+    return __shfl_sync(0xffffffffu, more, 0) != 0;
+  };
+  // Whether the second product of tile i is done. (That of tile i - 2, its barrier's phase
+  // before, is: tile i's scores came after it.)
+  auto outputs_done = [&](uint32_t i) -> bool {
+    if (!k.wait(kPvDone + (i & 1), i >> 1 & 1)) return false;
+    tc_fence_after();
+    return true;
+  };
+  uint32_t meetings = 0;
+  // Both warps of the quarter have come this far, their shared- and tensor-memory accesses done.
+  auto meet = [&]() -> bool {
+    tc_fence_before();
+    __syncwarp();
+    bar_arrive(k.bar(kPair + quarter));
+    if (!k.wait(kPair + quarter, meetings++ & 1)) return false;
+    tc_fence_after();
+    return true;
+  };
+  bool shifted = false;   // some row's queries are not as they were
+  float next_back = 1.f;  // what undoes the shift of row `lane`
+  uint32_t g = 0;  // the tile's number in this block
+  Ring<kMetas> mr;
+  int at = 0;
+
+  // Puts segment s's queries into tensor memory; fac undoes the rows' shifts.
+  auto queries = [&](const Segment& s) {
+    const int R = s.row_tile * kTilesRows + r;
+    const __nv_bfloat16* q = R < p.rows ? q_row<SEL>(p, s.seq, s.head, R) : nullptr;
+    float up = 1.f, back = 1.f;
+    if (I8) {
+      float top = 0.f;
+#pragma unroll 4
+      for (int i = 0; i < D / 8; ++i) {
+        const uint4 x = q ? *reinterpret_cast<const uint4*>(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float a = fabsf(__uint_as_float(w[j] << 16)), b = fabsf(__uint_as_float(w[j] & 0xffff0000u));
+          top = a < INFINITY ? fmaxf(top, a) : top;
+          top = b < INFINITY ? fmaxf(top, b) : top;
+        }
+      }
+      // a row whose largest finite magnitude is in [2^-7, 2^14) goes as it is, another is shifted to 1
+      if (top > 0.f && (top < 0.0078125f || top >= 16384.f)) {
+        const int shift = max(-120, min(120, -ilogbf(top)));
+        up = __int_as_float((shift + 127) << 23);
+        back = __int_as_float((127 - shift) << 23);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {  // 32 elements a step
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x = q ? *reinterpret_cast<const uint4*>(q + half * (D / 2) + 32 * i + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
+      }
+      if (I8)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          w[j] = pack_half(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+      tc_st16(mine + S::kQ + half * (D / 4) + 16 * i, w);
+    }
+    tc_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    bar_arrive(k.bar(kQReady));
+    shifted = __any_sync(0xffffffffu, back != 1.f);
+    next_back = back;
+  };
+
+  // Scores of keys 8j + 2c, 8j + 2c + 1 for the thread's four rows, -inf where a row does not see
+  // the key: the way of tiles with missing keys or drafted tokens, and of shifted rows.
+  auto masked = [&](uint32_t sb, const Meta& meta, int j, float2 (&a)[4]) {
+    uint32_t x[2][4];
+    tc_ld_piece(x[0], sb + half * 64 + 8 * j);
+    tc_ld_piece(x[1], sb + half * 64 + 8 * j + (16u << 16));
+    tc_wait_ld();
+    const float4 kl = I8 ? *reinterpret_cast<const float4*>(meta.kl[32 * half + 4 * j + c]) : make_float4(p.scale_log2, p.scale_log2, 0.f, 0.f);
+    const uint4 seen = *reinterpret_cast<const uint4*>(pr.seen[half][j >> 2][n]);
+    const float4 fac = *reinterpret_cast<const float4*>(pr.fac[n]);
+    const unsigned sn[4] = {seen.x, seen.y, seen.z, seen.w};
+    const float f[4] = {fac.x, fac.y, fac.z, fac.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned bits = sn[i] >> (8 * (j & 3) + 2 * c);
+      a[i].x = bits & 1u ? fmaf(__uint_as_float(x[i >> 1][2 * (i & 1)]) * f[i], kl.x, kl.z) : -INFINITY;
+      a[i].y = bits & 2u ? fmaf(__uint_as_float(x[i >> 1][2 * (i & 1) + 1]) * f[i], kl.y, kl.w) : -INFINITY;
+    }
+  };
+
+  bool more = advance(0);
+  if (more) queries(segs.s[0]);
+  while (more) {
+    const Segment& s = segs.s[at];
+    const int R0 = s.row_tile * kTilesRows + quarter * 32;
+    const float back = next_back;
+    const bool warp_live = uniform((int)(R0 < p.rows)) != 0;
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    uint64_t sum[4] = {0, 0, 0, 0};
+
+    const int t0 = uniform(s.t0), t1 = uniform(s.t1);
+    for (int t = t0; t < t1; ++t, ++g) {
+      const uint32_t sb = mine + S::kS + (g & 1) * 128;
+      if (!k.wait(kSFull + (g & 1), g >> 1 & 1)) return;
+      if (warp_live) {
+        tc_fence_after();
+        // (scores exist, so the tile's lookups do)
+        const Meta& meta = k.metas[mr.i];
+        const uint2 valid = *reinterpret_cast<const uint2*>(meta.valid + 2 * half);
+        const bool plain = uniform((int)((valid.x & valid.y) == ~0u && meta.draft0 == kKeys)) != 0 && !shifted;
+        uint64_t v[4][8];  // scores of rows n + 8i, in pairs of keys 8j + 2c, 8j + 2c + 1
+        float top[4];
+        if (plain) {
+          uint32_t x[2][32];
+          tc_ld_frag(x[0], sb + half * 64);
+          tc_ld_frag(x[1], sb + half * 64 + (16u << 16));
+          tc_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const ulonglong2 kl = I8 ? *reinterpret_cast<const ulonglong2*>(meta.kl[32 * half + 4 * j + c]) : make_ulonglong2(pair(p.scale_log2, p.scale_log2), 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t a = pair(__uint_as_float(x[i >> 1][4 * j + 2 * (i & 1)]), __uint_as_float(x[i >> 1][4 * j + 2 * (i & 1) + 1]));
+              v[i][j] = I8 ? fma2(a, kl.x, kl.y) : mul2(a, kl.x);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 a = unpair(v[i][0]);
+            float x0 = fmaxf(a.x, a.y), x1 = -INFINITY;
+#pragma unroll
+            for (int j = 1; j < 8; ++j) {
+              a = unpair(v[i][j]);
+              if (j & 1) x1 = fmaxf(x1, fmaxf(a.x, a.y));
+              else x0 = fmaxf(x0, fmaxf(a.x, a.y));
+            }
+            top[i] = fmaxf(x0, x1);
+          }
+        } else {
+          // what row `lane` of the quarter sees
+          const int tr = SEL ? 0 : min((R0 + lane) / p.group, p.tokens - 1), j0 = t * kKeys + 64 * half - s.len.ctx;
+          const bool drafts = !SEL && meta.draft0 < kKeys;
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < 2; ++i)
+            pr.seen[half][i][lane & 7][lane >> 3] = (i ? valid.y : valid.x) & (drafts ? draft_bits(p, s.b, tr, j0 + 32 * i) : ~0u);
+          if (half == 0) pr.fac[lane & 7][lane >> 3] = back;
+          if (!meet()) return;
+          top[0] = top[1] = top[2] = top[3] = -INFINITY;
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            float2 a[4];
+            masked(sb, meta, j, a);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fmaxf(a[i].x, a[i].y));
+          }
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+        pr.top[g & 1][half][n][c] = c == 0 ? top[0] : c == 1 ? top[1] : c == 2 ? top[2] : top[3];
+        if (!meet()) return;
+        {
+          const float4 y = *reinterpret_cast<const float4*>(pr.top[g & 1][half ^ 1][n]);
+          top[0] = fmaxf(top[0], y.x); top[1] = fmaxf(top[1], y.y);
+          top[2] = fmaxf(top[2], y.z); top[3] = fmaxf(top[3], y.w);
+        }
+
+        // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
+        const bool grow = top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || top[2] > m[2] + 8.f || top[3] > m[3] + 8.f;
+        if (__any_sync(0xffffffffu, grow)) {
+          float f[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bool up = top[i] > m[i] + 8.f;
+            f[i] = up ? ex2(m[i] - top[i]) : 1.f;  // (m = -inf: 0)
+            if (up) m[i] = top[i];
+            sum[i] = mul2(sum[i], pair(f[i], f[i]));
+          }
+          if (t > t0) {
+            if (!outputs_done(g - 1)) return;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t ob = mine + S::kO + half * (D / 2) + ((uint32_t)(16 * h) << 16);
+              const float fa = h ? f[2] : f[0], fb = h ? f[3] : f[1];
+#pragma unroll 1
+              for (int i = 0; i < D / 64; ++i) rescale(ob + 32 * i, fa, fb);
+            }
+            tc_wait_st();
+          }
+        }
+        uint64_t neg[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float u = m[i] == -INFINITY ? 0.f : -m[i];
+          neg[i] = pair(u, u);
+        }
+
+        // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
+        const uint32_t pb = sb + half * 64;
+        if (plain) {
+          uint32_t w[2][16];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 a = unpair(add2(v[i][j], neg[i]));
+              const float e0 = ex2(a.x), e1 = ex2(a.y);
+              sum[i] = I8 ? fma2(pair(e0, e1), inv, sum[i]) : add2(sum[i], pair(e0, e1));
+              w[i >> 1][2 * j + (i & 1)] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+            }
+          }
+          tc_st_frag(pb, w[0]);
+          tc_st_frag(pb + (16u << 16), w[1]);
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            float2 a[4];
+            masked(sb, meta, j, a);
+            const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 b = unpair(neg[i]);
+              const float e0 = ex2(a[i].x + b.x), e1 = ex2(a[i].y + b.y);
+              sum[i] = I8 ? fma2(pair(e0, e1), inv, sum[i]) : add2(sum[i], pair(e0, e1));
+              w[i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+            }
+            tc_wait_ld();
+            tc_st_piece(pb + 4 * j, w[0], w[1]);
+            tc_st_piece(pb + 4 * j + (16u << 16), w[2], w[3]);
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+      }
+      __syncwarp();
+      bar_arrive(k.bar(kPReady + (g & 1)));
+      mr.next();
+    }
+
+    // The next segment's queries first (its scores can begin), then this one's output.
+    const Segment& done = s;
+    more = advance(at ^ 1);
+    if (more) queries(segs.s[at ^ 1]);
+    if (!outputs_done(g - 1)) return;
+    if (warp_live) {
+      float l[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = unpair(sum[i]);
+        l[i] = a.x + a.y;
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      }
+      pr.sum[half][n][c] = c == 0 ? l[0] : c == 1 ? l[1] : c == 2 ? l[2] : l[3];
+      if (half == 0) pr.m[n][c] = c == 0 ? m[0] : c == 1 ? m[1] : c == 2 ? m[2] : m[3];
+      if (!meet()) return;
+      const int R = R0 + lane;
+      const int t_row = SEL ? 0 : min(R / p.group, p.tokens - 1);
+      const bool live = R < p.rows && (SEL || R / p.group < done.len.drafts);
+      const float lr = pr.sum[0][lane & 7][lane >> 3] + pr.sum[1][lane & 7][lane >> 3], top = pr.m[lane & 7][lane >> 3];
+      const bool empty = !live || lr == 0.f;
+      const float inv = empty ? 0.f : 1.f / lr;
+      const bool fix = !I8 && !SEL && *k.poisoned != 0;
+      const long long row = out_row<SEL>(p, done.seq, done.head, min(R, p.rows - 1));
+      float* part = p.parts + (2LL * blockIdx.x + (done.first ? 0 : 1)) * kPartFloats<kTilesRows, D>;
+#pragma unroll 1
+      for (int i = 0; i < D / 64; ++i) {
+        const int d = half * (D / 2) + 32 * i;
+        uint32_t o[32];
+        tc_ld32(o, mine + S::kO + d);
+        tc_wait_ld();
+        if (R < p.rows) {
+          float f[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = empty ? 0.f : __uint_as_float(o[j]);
+          if (fix && !empty) {  // infinities and NaNs of drafts that this row attends to
+            const int32_t* table = p.table + done.b * p.table_stride;
+            const int end = (int)min((long long)done.len.len, (long long)done.t1 * kKeys);
+            for (int j = max(done.len.ctx, done.t0 * kKeys); j < end; ++j) {
+              const int pg = table[j >> p.page_shift];
+              if ((unsigned)pg >= (unsigned)p.pages || !sees_draft(p, done.b, t_row, j - done.len.ctx)) continue;
+              const __nv_bfloat16* v = reinterpret_cast<const __nv_bfloat16*>(
+                  p.v + pg * p.page_b + (j & ((1 << p.page_shift) - 1)) * p.token_b + done.head * p.head_b) + d;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                const float y = __bfloat162float(v[c]);
+                if (!(fabsf(y) < INFINITY)) f[c] += y;
+              }
+            }
+          }
+          if (done.whole) {
+            uint4* out = reinterpret_cast<uint4*>(p.out + row * D + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              out[j] = make_uint4(pack_bf16(f[8 * j] * inv, f[8 * j + 1] * inv), pack_bf16(f[8 * j + 2] * inv, f[8 * j + 3] * inv),
+                                  pack_bf16(f[8 * j + 4] * inv, f[8 * j + 5] * inv), pack_bf16(f[8 * j + 6] * inv, f[8 * j + 7] * inv));
+          } else {
+            float4* out = reinterpret_cast<float4*>(part + r * D + d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) out[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (R < p.rows && half == 0) {
+        if (!done.whole)
+          *reinterpret_cast<float2*>(part + kTilesRows * D + 2 * r) = make_float2(top, empty ? 0.f : lr);
+        else if (p.lse)
+          p.lse[row] = empty ? -INFINITY : (top + lg2(lr)) * 0.6931471805599453f;
+      }
+    }
+    tc_fence_before();  // these reads come before the next segment's products (through kPReady)
+    at ^= 1;
+    __syncwarp();
+  }
+}
+
+template <int D, bool I8, bool SEL>
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D, I8>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Start start;
+  __shared__ unsigned poisoned_s;
+  __shared__ uint32_t tmem_s;
+  __shared__ RowSegments<SEL> segs[kRowWarps];
+  __shared__ __align__(16) PairRows pair_rows[4];
+
+  unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  Block k;
+  k.smem = smem;
+  k.stage = smem_addr(smem);
+  k.bars = smem_addr(smem + S::kBarOff);
+  k.poisoned = &poisoned_s;
+  k.status = p.status;
+  k.limit = p.spin_limit_ns;
+  k.metas = reinterpret_cast<Meta*>(smem + S::kMetaOff);
+  const int warp = uniform((int)threadIdx.x >> 5);
+
+  if (warp == kMulWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    poisoned_s = 0;
+    for (int i = 0; i < kMetas; ++i) {
+      bar_init(k.bar(kMetaFull + i), 1);
+      bar_init(k.bar(kMetaEmpty + i), 9);
+    }
+    for (int i = 0; i < S::kStages; ++i) {
+      bar_init(k.bar(kKFull + i), 8);
+      bar_init(k.bar(kVFull + i), 8);
+      bar_init(k.bar(kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(k.bar(kSFull + i), 1);
+      bar_init(k.bar(kPReady + i), kRowWarps);
+      bar_init(k.bar(kPvDone + i), 1);
+    }
+    for (int i = 0; i < 4; ++i) bar_init(k.bar(kPair + i), 2);
+    bar_init(k.bar(kQReady), kRowWarps);
+    bar_init(k.bar(kFinal), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  grid_wait();
+  grid_launch_dependents();
+  if (warp == kMetaWarp0) find_start<SEL, kKeys>(p, blockIdx.x, gridDim.x, &start);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(tmem_s);
+  const int tiles = uniform((int)(block_start(start.total, blockIdx.x + 1, gridDim.x) - block_start(start.total, blockIdx.x, gridDim.x)));
+
+  // registers: 2 * 152 + 48 + 2 * 64 of the launch's 5 * 96
+  if (warp < kRowWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    rows<D, I8, SEL>(p, k, start, tmem, segs[warp], pair_rows[warp & 3]);
+  } else if (warp < kRowWarps + 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == kMulWarp) {
+      multiply<D, I8, SEL>(p, k, start, tmem);
+    } else {
+      look_up<D, I8, SEL>(p, k, start, warp - kMetaWarp0);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    produce<D, I8>(p, k, tiles);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D, bool I8, bool SEL>
+cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<D, I8>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute a[1] = {};
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL>, p);
+}
+
+template <int D, bool I8, bool SEL>
+cudaError_t opt_in() {
+  return cudaFuncSetAttribute(tiles_kernel<D, I8, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Shape<D, I8>::kSmem);
+}
+
+}  // namespace
+
+cudaError_t setup_tiles() {
+  cudaError_t e = opt_in<64, false, false>();
+  if (e == cudaSuccess) e = opt_in<64, false, true>();
+  if (e == cudaSuccess) e = opt_in<64, true, false>();
+  if (e == cudaSuccess) e = opt_in<64, true, true>();
+  if (e == cudaSuccess) e = opt_in<128, false, false>();
+  if (e == cudaSuccess) e = opt_in<128, false, true>();
+  if (e == cudaSuccess) e = opt_in<128, true, false>();
+  if (e == cudaSuccess) e = opt_in<128, true, true>();
+  return e;
+}
+
+cudaError_t launch_tiles(const Params& p, int head_dim, bool i8, bool selected, int grid,
+                         cudaStream_t stream) {
+  if (head_dim == 64) {
+    if (i8) return selected ? launch<64, true, true>(p, grid, stream) : launch<64, true, false>(p, grid, stream);
+    return selected ? launch<64, false, true>(p, grid, stream) : launch<64, false, false>(p, grid, stream);
+  }
+  if (i8) return selected ? launch<128, true, true>(p, grid, stream) : launch<128, true, false>(p, grid, stream);
+  return selected ? launch<128, false, true>(p, grid, stream) : launch<128, false, false>(p, grid, stream);
+}
+
+}  // namespace attn
+}  // namespace tks

@@ -246,6 +246,9 @@ int get_workspace(int dev, void* stream, const DeviceInfo& d, Workspace* out) {
 }
 
 }  // namespace
+
+long long spin_limit_ns() { return g_spin_limit_ns.load(); }
+int test_skip_arrive() { return g_test_skip_arrive.load() ? 1 : 0; }
 }  // namespace tks
 
 using namespace tks;

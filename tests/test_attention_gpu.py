@@ -501,3 +501,20 @@ def test_refusals():
     with pytest.raises(ValueError):
         many = torch.zeros(1, tks.TKS_DRAFTS_MAX + 1, 8, 64, dtype=torch.bfloat16, device="cuda")
         tks.tree_attention(many, cache.k, cache.v, table, ctx, scales=cache.scales)
+
+
+@pytest.mark.parametrize("held", HELD)
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_sound(held):
+    """The lookups of each block's first tile are never announced, so its other warps' waits run out."""
+    cache, table, q, ctx = _small(held, heads=64)
+    want = tks.tree_attention(q, cache.k, cache.v, table, ctx, scales=cache.scales)
+    assert tks.device_status() == tks.TKS_OK
+    tks.set_option(tks.TKS_OPT_SPIN_LIMIT_NS, 20_000_000)
+    tks.set_option(tks.TKS_OPT_TEST_SKIP_ARRIVE, 1)
+    try:
+        tks.tree_attention(q, cache.k, cache.v, table, ctx, scales=cache.scales)
+        assert tks.device_status() == tks.TKS_E_TIMEOUT
+    finally:
+        tks.set_option(tks.TKS_OPT_TEST_SKIP_ARRIVE, 0)
+        tks.set_option(tks.TKS_OPT_SPIN_LIMIT_NS, 1_000_000_000)
+    assert torch.equal(tks.tree_attention(q, cache.k, cache.v, table, ctx, scales=cache.scales), want)

@@ -730,8 +730,9 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
         tc_fence_after();
         // (scores exist, so the tile's lookups do)
         const Meta& meta = k.metas[mr.i];
-        const uint2 valid = *reinterpret_cast<const uint2*>(meta.valid + 2 * half);
-        const bool plain = uniform((int)((valid.x & valid.y) == ~0u && meta.draft0 == kKeys)) != 0 && !shifted;
+        const uint4 all = *reinterpret_cast<const uint4*>(meta.valid);
+        // (the same answer for both warps of the quarter: they meet once more if it is no)
+        const bool plain = uniform((int)((all.x & all.y & all.z & all.w) == ~0u && meta.draft0 == kKeys)) != 0 && !shifted;
         uint64_t v[4][8];  // scores of rows n + 8i, in pairs of keys 8j + 2c, 8j + 2c + 1
         float top[4];
         if (plain) {
@@ -767,7 +768,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
           __syncwarp();
 #pragma unroll 1
           for (int i = 0; i < 2; ++i)
-            pr.seen[half][i][lane & 7][lane >> 3] = (i ? valid.y : valid.x) & (drafts ? draft_bits(p, s.b, tr, j0 + 32 * i) : ~0u);
+            pr.seen[half][i][lane & 7][lane >> 3] = meta.valid[2 * half + i] & (drafts ? draft_bits(p, s.b, tr, j0 + 32 * i) : ~0u);
           if (half == 0) pr.fac[lane & 7][lane >> 3] = back;
           if (!meet()) return;
           top[0] = top[1] = top[2] = top[3] = -INFINITY;

@@ -94,6 +94,7 @@ def load(path: str | None = None):
             fn.argtypes = args
         if path is None:
             _lib = lib
+            _attention.bound(lib)
         return lib
 
 
@@ -104,6 +105,7 @@ def use(path: str):
     lib = load(path)
     with _lock:
         _lib = lib
+        _attention.bound(lib)
     return lib
 
 

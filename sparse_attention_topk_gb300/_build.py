@@ -1,4 +1,5 @@
-"""Builds libtks.so (the CUDA selection library) in-tree with nvcc, for sm_103a."""
+"""Builds libtks.so (the CUDA library) in-tree with nvcc, for sm_103a, and the C++ binding
+of the cache and attention calls with the host compiler."""
 
 from __future__ import annotations
 
@@ -84,6 +85,57 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str = LIB_PATH,
     return out
 
 
+# The C++ step between Python and the cache and attention calls: an extension
+# module built by the host compiler against torch's headers.
+BINDING_SOURCE = os.path.join(CSRC, "tks_binding.cpp")
+BINDING_PATH = os.path.join(BUILD_DIR, "tks_binding.so")
+
+
+def _binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING_PATH):
+        return False
+    t = os.path.getmtime(BINDING_PATH)
+    return all(os.path.getmtime(s) <= t for s in (BINDING_SOURCE, os.path.join(INCLUDE, "tks.h"),
+                                                  os.path.join(INCLUDE, "tks_attention.h")))
+
+
+def start_binding(force: bool = False):
+    """Starts compiling the binding unless it is up to date; finish_binding() takes what this returns."""
+    if not force and _binding_up_to_date():
+        return None
+    import sysconfig
+
+    import torch
+
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    tmp = f"{BINDING_PATH}.tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SOURCE, "-o", tmp,
+           f"-I{INCLUDE}", f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+           f"-I{os.path.join(cuda, 'include')}", f"-I{sysconfig.get_paths()['include']}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-L{lib}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}"]
+    return subprocess.Popen(cmd), tmp
+
+
+def finish_binding(started) -> str:
+    if started is not None:
+        proc, tmp = started
+        if proc.wait() != 0:
+            raise subprocess.CalledProcessError(proc.returncode, f"g++ {BINDING_SOURCE}")
+        os.replace(tmp, BINDING_PATH)
+    return BINDING_PATH
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the binding unless it is newer than its sources; returns its path."""
+    return finish_binding(start_binding(force))
+
+
 if __name__ == "__main__":
     import sys
+    started = start_binding("--force" in sys.argv)
     print(build(force="--force" in sys.argv, verbose_ptxas="-v" in sys.argv))
+    print(finish_binding(started))

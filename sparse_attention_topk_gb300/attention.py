@@ -1,6 +1,7 @@
 """The paged key/value cache and the attention that reads it (``include/tks_attention.h``).
 
-What stands around the selector in a decode step, as thin calls over ``libtks.so``:
+What stands around the selector in a decode step, as thin calls over ``libtks.so`` (tensors
+are checked, and outputs allocated, by a small C++ module, ``csrc/tks_binding.cpp``):
 
     tks.cache_write(k, v, k_cache, v_cache, slots, scales=scales)      # the new tokens
     idx = tks.topk_indices(logits, 2048, row_len=lens)                 # the selector
@@ -47,80 +48,38 @@ SIGNATURES = {
 }
 
 
-def _call(device, stream, fn):
-    """fn(stream handle) with `device` current, and `stream` too (the device's current one if
-    None), so that what fn allocates belongs to the stream that writes it."""
-    import torch
-
-    if stream is None and device.index == torch.cuda.current_device():
-        return fn(torch.cuda.current_stream().cuda_stream)
-    with torch.cuda.device(device):
-        if stream is None:
-            return fn(torch.cuda.current_stream().cuda_stream)
-        s = stream
-        if isinstance(stream, int):
-            s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
-        with torch.cuda.stream(s):
-            return fn(s.cuda_stream)
+_binding = None
 
 
-def _check(rc, what):
-    if rc:
+def bound(lib):
+    """Makes the calls go to the entry points of `lib` (called when the package loads a library)."""
+    if _binding is not None:
         from . import TksError
-        raise TksError(rc, what)
+        _binding.set_library(TksError, *(ctypes.cast(getattr(lib, name), _VP).value for name in SIGNATURES))
 
 
-def _cache(k_cache, v_cache, scales):
-    import torch
+def _native():
+    """The C++ module that checks the tensors and makes the calls, built and loaded on first use."""
+    global _binding
+    if _binding is None:
+        import importlib.util
 
-    if k_cache.dim() != 4 or not k_cache.is_cuda:
-        raise ValueError("caches must be CUDA tensors [pages, page_size, kv_heads, head_dim]")
-    shape, stride, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
-    if v_cache.shape != shape or v_cache.dtype != dtype or v_cache.stride() != stride or v_cache.device != k_cache.device:
-        raise ValueError("k_cache and v_cache must have one shape, strides, dtype and device")
-    pages, page_size, heads, dim = shape
-    if dim not in (64, 128) or stride[3] != 1:
-        raise ValueError("head_dim must be 64 or 128, and contiguous")
-    if page_size < 1 or page_size & (page_size - 1):
-        raise ValueError("page_size must be a power of two")
-    if dtype is torch.int8:
-        if scales is None or scales.shape != (pages, page_size, heads, 2) or scales.dtype is not torch.float32 \
-                or not scales.is_contiguous() or scales.device != k_cache.device:
-            raise ValueError("an int8 cache needs scales: a contiguous float32 CUDA tensor [pages, page_size, kv_heads, 2]")
-        held, sc = TKS_I8, scales.data_ptr()
-    elif dtype is torch.bfloat16:
-        if scales is not None:
-            raise ValueError("a bfloat16 cache has no scales")
-        held, sc = 1, None
-    else:
-        raise ValueError(f"unsupported cache dtype {dtype}")
-    return Cache(k_cache.data_ptr(), v_cache.data_ptr(), sc, held, pages, page_size, heads, dim, stride[0], stride[1], stride[2])
+        import torch  # noqa: F401  (its libraries come first)
+
+        from . import load
+        from ._build import build_binding
+
+        spec = importlib.util.spec_from_file_location("tks_binding", build_binding())
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        lib = load()
+        _binding = module
+        bound(lib)
+    return _binding
 
 
-def _ints(t, shape, device, what):
-    import torch
-
-    if t.dtype is not torch.int32 or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 CUDA tensor {list(shape)} on the cache's device")
-    return t.data_ptr()
-
-
-def _rows_ok(t, size):
-    """Whether the kernels can read t as it is: a contiguous last dimension, and 16-byte
-    pieces everywhere else (an extent of one is never stepped over)."""
-    unit = 16 // size
-    return t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and \
-        all(s >= 0 and s % unit == 0 for s, n in zip(t.stride()[:-1], t.shape[:-1]) if n > 1)
-
-
-def _dtype(t, what):
-    import torch
-
-    if t is torch.bfloat16:
-        return 1
-    if t is torch.float32:
-        return 0
-    raise ValueError(f"{what} must be bfloat16 or float32, not {t}")
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def cache_write(k, v, k_cache, v_cache, slots, scales=None, stream=None):
@@ -131,28 +90,7 @@ def cache_write(k, v, k_cache, v_cache, slots, scales=None, stream=None):
     negative slot skips its token.  An int8 cache takes each row as codes with a scale of
     max|x| / 127, written to ``scales``; a bfloat16 cache takes the values rounded.
     """
-    import torch
-
-    c = _cache(k_cache, v_cache, scales)
-    n, dev = slots.numel(), k_cache.device
-    if k.shape != (n, c.kv_heads, c.head_dim) or v.shape != k.shape or v.dtype != k.dtype or k.device != dev or v.device != dev:
-        raise ValueError(f"k and v must be CUDA tensors [{n}, {c.kv_heads}, {c.head_dim}] of one dtype on the cache's device")
-    dt = _dtype(k.dtype, "k and v")
-    at = _ints(slots, (n,), dev, "slots")
-    if n == 0:
-        return
-    size = 4 if dt == 0 else 2
-
-    def go(handle):
-        a = k if _rows_ok(k, size) else k.contiguous()
-        b = v if _rows_ok(v, size) else v.contiguous()
-        if a.data_ptr() % 16 or b.data_ptr() % 16:
-            a, b = a.clone(), b.clone()
-        unit = 16 // size
-        ks, vs = ([s if e > 1 else 0 for s, e in zip(t.stride(), t.shape)] for t in (a, b))
-        return _lib().tks_cache_write(ctypes.byref(c), a.data_ptr(), b.data_ptr(), n, dt, ks[0], ks[1], vs[0], vs[1], at, handle)
-
-    _check(_call(dev, stream, go), "tks_cache_write")
+    (_binding or _native()).write(k, v, k_cache, v_cache, slots, scales, _handle(stream))
 
 
 def cache_read(k_cache, v_cache, slots, scales=None, dtype=None, out=None, stream=None):
@@ -163,62 +101,12 @@ def cache_read(k_cache, v_cache, slots, scales=None, dtype=None, out=None, strea
     """
     import torch
 
-    c = _cache(k_cache, v_cache, scales)
-    n, dev = slots.numel(), k_cache.device
-    at = _ints(slots, (n,), dev, "slots")
-    shape = (n, c.kv_heads, c.head_dim)
     if out is not None:
         dtype = out[0].dtype if dtype is None else dtype
-        for t in out:
-            if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous() or t.data_ptr() % 16:
-                raise ValueError(f"out must be two contiguous, 16-byte aligned {dtype} CUDA tensors {list(shape)}")
-    dtype = torch.bfloat16 if dtype is None else dtype
-    dt = _dtype(dtype, "dtype")
-    result = []
-
-    def go(handle):
-        result.extend(out if out is not None else torch.empty((2,) + shape, dtype=dtype, device=dev))
-        if n == 0:
-            return 0
-        return _lib().tks_cache_read(ctypes.byref(c), at, n, result[0].data_ptr(), result[1].data_ptr(), dt, handle)
-
-    _check(_call(dev, stream, go), "tks_cache_read")
-    return result[0], result[1]
-
-
-def _attend(q, c, dev, page_table, softmax_scale, out, return_lse, stream, what, call):
-    import torch
-
-    if q.dim() != 4 or q.dtype is not torch.bfloat16 or q.device != dev or q.shape[3] != c.head_dim:
-        raise ValueError(f"q must be a bfloat16 CUDA tensor [batch, tokens, q_heads, {c.head_dim}] on the cache's device")
-    batch, tokens, heads, dim = q.shape
-    if heads < 1 or heads % c.kv_heads:
-        raise ValueError("q_heads must be a multiple of kv_heads")
-    if page_table.dim() != 2 or page_table.shape[0] != batch or page_table.dtype is not torch.int32 \
-            or page_table.device != dev or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be an int32 CUDA tensor [batch, pages of a sequence] with contiguous rows")
-    if out is not None and (out.shape != q.shape or out.dtype is not torch.bfloat16 or out.device != dev
-                            or not out.is_contiguous() or out.data_ptr() % 16):
-        raise ValueError("out must be a contiguous, 16-byte aligned bfloat16 CUDA tensor of q's shape")
-    scale = dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    if not abs(scale) < float("inf"):
-        raise ValueError("softmax_scale must be finite")
-    result = []
-
-    def go(handle):
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
-        lse = torch.empty(q.shape[:3], dtype=torch.float32, device=dev) if return_lse else None
-        result.extend((o, lse))
-        x = q if _rows_ok(q, 2) else q.contiguous()
-        if x.data_ptr() % 16:
-            x = x.clone()
-        st = [s if e > 1 else 0 for s, e in zip(x.stride(), x.shape)]
-        queries = Queries(x.data_ptr(), st[0], st[1], st[2], o.data_ptr(), lse.data_ptr() if return_lse else None, batch, tokens, heads,
-                          page_table.data_ptr(), page_table.stride(0) if batch > 1 else 0, page_table.shape[1], scale)
-        return call(ctypes.byref(c), ctypes.byref(queries), handle)
-
-    _check(_call(dev, stream, go), what)
-    return tuple(result) if return_lse else result[0]
+    if dtype is not None and dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise ValueError(f"dtype must be bfloat16 or float32, not {dtype}")
+    k_out, v_out = (None, None) if out is None else out
+    return (_binding or _native()).read(k_cache, v_cache, slots, scales, dtype is torch.float32, k_out, v_out, _handle(stream))
 
 
 def tree_attention(q, k_cache, v_cache, page_table, ctx_len, tree=None, draft_len=None, scales=None,
@@ -238,15 +126,8 @@ def tree_attention(q, k_cache, v_cache, page_table, ctx_len, tree=None, draft_le
     the log-sum-exp of the attended, scaled scores.  A query that attends to nothing (one
     beyond ``draft_len`` too) gives zeros and -inf.
     """
-    c, dev = _cache(k_cache, v_cache, scales), k_cache.device
-    batch, tokens = q.shape[0], q.shape[1]
-    if tokens > TKS_DRAFTS_MAX:
-        raise ValueError(f"at most {TKS_DRAFTS_MAX} drafted tokens")
-    ctx = _ints(ctx_len, (batch,), dev, "ctx_len")
-    count = None if draft_len is None else _ints(draft_len, (batch,), dev, "draft_len")
-    bits = None if tree is None else _ints(tree, (batch, tokens, (tokens + 31) // 32), dev, "tree")
-    return _attend(q, c, dev, page_table, softmax_scale, out, return_lse, stream, "tks_tree_attention",
-                   lambda cache, queries, handle: _lib().tks_tree_attention(cache, queries, ctx, count, bits, handle))
+    return (_binding or _native()).tree(q, k_cache, v_cache, page_table, ctx_len, tree, draft_len, scales, softmax_scale, out,
+                                        bool(return_lse), _handle(stream))
 
 
 def selected_attention(q, k_cache, v_cache, page_table, indices, kv_len=None, scales=None,
@@ -258,15 +139,8 @@ def selected_attention(q, k_cache, v_cache, page_table, indices, kv_len=None, sc
     skipped, entries at or beyond ``kv_len[b]`` (int32 [batch], optional) are skipped and
     reported by ``device_status``.  Returns as ``tree_attention`` does.
     """
-    c, dev = _cache(k_cache, v_cache, scales), k_cache.device
-    batch, tokens = q.shape[0], q.shape[1]
-    if indices.dim() != 3:
-        raise ValueError("indices must be an int32 CUDA tensor [batch, tokens, k]")
-    k = indices.shape[2]
-    idx = _ints(indices, (batch, tokens, k), dev, "indices")
-    limit = None if kv_len is None else _ints(kv_len, (batch,), dev, "kv_len")
-    return _attend(q, c, dev, page_table, softmax_scale, out, return_lse, stream, "tks_selected_attention",
-                   lambda cache, queries, handle: _lib().tks_selected_attention(cache, queries, idx, k, limit, handle))
+    return (_binding or _native()).selected(q, k_cache, v_cache, page_table, indices, kv_len, scales, softmax_scale, out,
+                                            bool(return_lse), _handle(stream))
 
 
 def tree_mask(parents):
@@ -291,8 +165,3 @@ def tree_mask(parents):
         table.append([[((m >> (32 * w)) & 0xFFFFFFFF) for w in range(words)] for m in seen])
     bits = torch.tensor(table, dtype=torch.int64).reshape(len(rows), parents.shape[1], words)
     return torch.where(bits >= 1 << 31, bits - (1 << 32), bits).to(torch.int32).to(parents.device)
-
-
-def _lib():
-    from . import load
-    return load()

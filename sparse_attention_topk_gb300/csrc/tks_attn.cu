@@ -16,17 +16,19 @@ namespace attn {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Joining the partial results of units that were split over blocks:
-//     out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s,  m = max_s m_s.
+// Joining the partial results of units that were split over blocks.
 // A unit's partials are few (most units are whole, and return at once) or, for
 // a lone long sequence, many; in the first case a warp takes a row (PER_BLOCK =
 // 8), in the second the block's warps share one row's partials.
 // ---------------------------------------------------------------------------
 template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Params p, int blocks) {
-  constexpr int kVec = D / 32, kStep = PER_BLOCK == 8 ? 1 : 8;
-  __shared__ long long total_s, cum_s;
-  __shared__ float acc_s[8][D], l_s[8];
+  constexpr int kVec = D / 32;
+  __shared__ struct {
+    int c0, c1, slot0;
+  } span;
+  __shared__ float acc_s[8][D];
+  __shared__ float2 ml_s[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per = p.kv_heads * p.row_tiles;
   const int seq = blockIdx.x / per, in = blockIdx.x % per;
@@ -38,94 +40,68 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
   const Seq len = seq_of<SEL>(p, seq);
   const int tiles = tiles_of<TK>(len.len);
   if (warp == 0) {
-    if (SEL) {
+    unsigned tiles0;
+    const Split sp = make_split<SEL, TK>(p, blocks, tiles0);
+    if (sp.share) {
       if (lane == 0) {
-        total_s = (long long)per * tiles * p.seqs;
-        cum_s = (long long)per * tiles * seq;
+        span.c0 = blockIdx.x * sp.share;
+        span.c1 = span.c0 + (int)min(sp.share, (unsigned)tiles) - 1;
+        span.slot0 = 0;
       }
     } else {
-      long long all = 0, before = 0;
-      for (int s = lane; s < p.seqs; s += 32) {
-        const int t = tiles_of<TK>(seq_of<SEL>(p, s).len);
-        all += t;
-        before += s < seq ? t : 0;
-      }
+      long long before = 0;  // tiles of a unit of each sequence before this one
+      if (!SEL) {
+        before = lane < seq ? (long long)tiles0 : 0;
+        for (int s = lane + 32; s < seq; s += 32) before += tiles_of<TK>(seq_of<SEL>(p, s).len);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
+        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
       }
       if (lane == 0) {
-        total_s = all * per;
-        cum_s = before * per;
+        const long long w0 = (SEL ? (long long)tiles * seq : before) * per + (long long)in * tiles;
+        span.c0 = sp.block_of(w0);
+        span.c1 = sp.block_of(w0 + tiles - 1);  // (those between have tiles, too)
+        span.slot0 = sp.start(span.c0) != w0 ? 1 : 0;
       }
     }
   }
   __syncthreads();
-  const long long W = total_s, w0 = cum_s + (long long)in * tiles;
-  const int c0 = block_of(W, w0, blocks), c1 = block_of(W, w0 + tiles - 1, blocks);
+  const int c0 = span.c0, c1 = span.c1, slot0 = span.slot0;
   if (c0 == c1) return;  // whole: its block has written the output
 
   const int r = first - row_tile * ROWS + (PER_BLOCK == 8 ? warp : 0);  // row in its tile
   const int R = row_tile * ROWS + r;
   const bool live = r < ROWS && R < p.rows;
-  auto part_of = [&](int c) -> const float* {
-    const int slot = c == c0 && block_start(W, c, blocks) != w0 ? 1 : 0;
-    return p.parts + (2LL * c + slot) * kPartFloats<ROWS, D>;
-  };
-  auto used = [&](int c) { return block_start(W, c, blocks) < block_start(W, c + 1, blocks); };
-
-  float m = -INFINITY;
-  if (live)
-    for (int c = c0 + lane; c <= c1; c += 32)
-      if (used(c)) {
-        const float2 q = *reinterpret_cast<const float2*>(part_of(c) + ROWS * D + 2 * r);
-        if (q.y != 0.f) m = fmaxf(m, q.x);
-      }
+  if (PER_BLOCK == 8) {
+    if (!live) return;
+    float m, l, acc[kVec];
+    join_row<ROWS, D>(p.parts, c0, c1, slot0, r, 0, 1, acc, m, l);
+    store_joined<D>(p, out_row<SEL>(p, seq, head, R), acc, m, l);
+    return;
+  }
+  // (one row a block, and it is live)
+  float m, l, acc[kVec];
+  join_row<ROWS, D>(p.parts, c0, c1, slot0, r, warp, 8, acc, m, l);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float l = 0.f, acc[kVec];
+  for (int i = 0; i < kVec; ++i) acc_s[warp][lane * kVec + i] = acc[i];
+  if (lane == 0) ml_s[warp] = make_float2(m, l);
+  __syncthreads();
+  if (warp != 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = fmaxf(top, ml_s[k].x);
+  l = 0.f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
-  if (live) {
-#pragma unroll 4
-    for (int c = c0 + (kStep == 1 ? 0 : warp); c <= c1; c += kStep) {
-      if (!used(c)) continue;
-      const float* part = part_of(c);
-      const float2 q = *reinterpret_cast<const float2*>(part + ROWS * D + 2 * r);
-      float o[kVec];
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) o[i] = part[r * D + lane * kVec + i];
-      if (q.y == 0.f) continue;  // saw nothing
-      const float f = q.x == m ? 1.f : ex2(q.x - m);
-      l += f * q.y;
+  for (int k = 0; k < 8; ++k) {
+    const float2 q = ml_s[k];
+    if (q.y == 0.f) continue;
+    const float f = q.x == top ? 1.f : ex2(q.x - top);
+    l += f * q.y;
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] += f * o[i];
-    }
+    for (int i = 0; i < kVec; ++i) acc[i] += f * acc_s[k][lane * kVec + i];
   }
-  if (PER_BLOCK != 8) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) acc_s[warp][lane * kVec + i] = acc[i];
-    if (lane == 0) l_s[warp] = l;
-    __syncthreads();
-    if (warp != 0) return;
-    l = 0.f;
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      l += l_s[k];
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] += acc_s[k][lane * kVec + i];
-    }
-  }
-  if (!live) return;
-  const float g = l == 0.f ? 0.f : 1.f / l;
-  const long long row = out_row<SEL>(p, seq, head, R);
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * kVec);
-#pragma unroll
-  for (int i = 0; i < kVec / 2; ++i) out[i] = pack_bf16(acc[2 * i] * g, acc[2 * i + 1] * g);
-  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
+  store_joined<D>(p, out_row<SEL>(p, seq, head, R), acc, top, l);
 }
 
 template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
@@ -296,7 +272,9 @@ Params params_of(const tks_cache* c, const tks_queries* q) {
   return p;
 }
 
-// Queues the attention kernel and the one that joins its partials.
+// Queues the attention kernel and the one that joins its partials. (A unit's last block joining
+// them instead, by a count of the blocks that are done, saved 3 us of host time and cost more on
+// the GPU: one token over 2048 selected positions 11.7 us against 10.5.)
 int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   Device d;
   Workspace ws;
@@ -304,21 +282,24 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   if (rc != TKS_OK) return rc;
   p.status = reinterpret_cast<unsigned*>(ws.ptr);
   p.parts = reinterpret_cast<float*>(ws.ptr + kHeaderBytes);
+  const int64_t keys = selected ? p.k_sel : std::min((int64_t)p.table_pages << p.page_shift, (int64_t)kMaxPositions);
   const bool i8 = c->held == TKS_I8;
   const cudaStream_t s = (cudaStream_t)stream;
   p.spin_limit_ns = spin_limit_ns();
   p.test_skip_arrive = test_skip_arrive();
   cudaError_t e;
-  if (p.rows <= kRowsTile) {
+  const bool few = p.rows <= kRowsTile;
+  const int tile = few ? kRowsTile : kTilesRows, tile_keys = few ? kRowsKeys : kTilesKeys;
+  p.row_tiles = (p.rows + tile - 1) / tile;
+  if ((keys / tile_keys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
+  const long long units = (long long)p.seqs * p.kv_heads * p.row_tiles;
+  if (units > INT32_MAX) return TKS_E_TOO_LARGE;
+  if (few) {
     const int grid = d.sms * kRowsBlocksPerSm;
-    p.row_tiles = (p.rows + kRowsTile - 1) / kRowsTile;
     e = launch_rows(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
   } else {
     const int grid = d.sms;
-    p.row_tiles = (p.rows + kTilesRows - 1) / kTilesRows;
-    const int64_t keys = selected ? p.k_sel : std::min((int64_t)p.table_pages << p.page_shift, (int64_t)kMaxPositions);
-    if ((keys / kTilesKeys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
     e = launch_tiles(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);
   }
@@ -340,6 +321,7 @@ CacheParams cache_params(const tks_cache* c, const int32_t* slots, int32_t n, un
   p.head_b = c->head_stride * size;
   p.page_shift = log2_of(c->page_size);
   p.kv_heads = c->kv_heads;
+  p.head_shift = (c->kv_heads & (c->kv_heads - 1)) == 0 ? log2_of(c->kv_heads) : -1;
   p.slots_held = c->pages * c->page_size;
   p.slots = slots;
   p.n = n;

@@ -2,14 +2,19 @@
 // over blocks, where a key lives in the paged cache, and PTX helpers.
 //
 // Work is counted in tiles of keys.  A unit is (sequence, key/value head, tile
-// of query rows); its tiles are the keys that its rows attend to.  All units'
-// tiles, in order, form one axis of W tiles, and block c of G takes tiles
-// [W*c/G, W*(c+1)/G): every block has the same work however ragged the
-// sequences are, a long unit is split over many blocks and short ones share a
-// block.  A block that holds all of a unit writes its output; otherwise it
+// of query rows); its tiles are the keys that its rows attend to.  Two ways:
+//  * even shares: every unit is split over the same number of blocks.  A block
+//    has one segment of one unit.
+//  * one run: all units' tiles, in order, form one axis, and every block takes an
+//    equal run of it, whatever units it crosses: every block has the same work
+//    however ragged the sequences are.
+// Starting a segment costs a block as much as kSegmentTiles tiles (lookups and
+// queries come first, and the joining and the output last), so even shares are
+// taken where the longest of them is not longer than an equal run and that (one
+// token over 4096 positions of 8 heads: 15.6 us as a run, 10.9 in even shares).  A block that holds all of a unit writes its output; otherwise it
 // writes a partial result (unnormalised output, running maximum, sum) to its
-// slot of the workspace and combine_kernel joins the unit's partials in block
-// order, so results do not depend on timing.  A block has at most two partial
+// slot of the workspace, and the unit's partials are joined in block order, so
+// results do not depend on timing.  A block has at most two partial
 // segments, its first (slot 0) and its last (slot 1).
 #pragma once
 
@@ -128,44 +133,109 @@ __device__ __forceinline__ int tiles_of(int len) {
   return len <= TK ? 1 : (int)(((unsigned)len + TK - 1) / TK);
 }
 
-// First tile of block c, and the block that holds tile w.
-__device__ __forceinline__ long long block_start(long long W, int c, int G) { return W * c / G; }
-__device__ __forceinline__ int block_of(long long W, long long w, int G) {
-  return (int)((G * (w + 1) - 1) / W);
-}
+constexpr int kSegmentTiles = 6;
 
-// Where a block starts: filled by warp 0, read by all after a barrier.
-struct Start {
-  long long total;  // W
-  long long cum;    // first tile of sequence `seq`
-  int seq;
+// How W tiles are split over G blocks.
+struct Split {
+  long long W;
+  unsigned share;  // blocks of a unit (even shares), or 0 (one run)
+  unsigned q, r;   // one run: tiles of a block, q or, for the first r blocks, q + 1
+
+  __device__ __forceinline__ void set(long long w, unsigned longest, long long units, int G) {
+    W = w;
+    if (w >> 31) {
+      q = (unsigned)(w / G);
+      r = (unsigned)(w % G);
+    } else {
+      q = (unsigned)w / (unsigned)G;
+      r = (unsigned)w - q * (unsigned)G;
+    }
+    share = 0;
+    if (units <= G) {
+      const unsigned s = (unsigned)G / (unsigned)units;
+      if ((longest + s - 1) / s <= q + (r > 0) + kSegmentTiles) share = s;
+    }
+  }
+  __device__ __forceinline__ long long start(int c) const { return (long long)c * q + min((unsigned)c, r); }
+  // One run: the block that holds tile w.
+  __device__ __forceinline__ int block_of(long long w) const {
+    const long long more = (long long)r * (q + 1);
+    if (w < more) return W >> 31 ? (int)(w / (q + 1)) : (int)((unsigned)w / (q + 1));
+    return (int)r + (W >> 31 ? (int)((w - more) / q) : (int)((unsigned)(w - more) / q));
+  }
 };
 
-// All tiles of all sequences, and the sequence that holds tile `w` (w is
-// given as block index times total over blocks).  Called by one warp.
+// The split, for all lanes of a warp; `tiles0`: the tiles of a unit of sequence `lane`.
 template <bool SEL, int TK>
-__device__ __forceinline__ void find_start(const Params& p, int block, int blocks, Start* st) {
+__device__ __forceinline__ Split make_split(const Params& p, int blocks, unsigned& tiles0) {
   const int lane = threadIdx.x & 31;
-  const long long per = (long long)p.kv_heads * p.row_tiles;
+  const unsigned per = (unsigned)(p.kv_heads * p.row_tiles);
+  Split split;
   if (SEL) {
-    const long long each = per * tiles_of<TK>(p.k_sel);
-    const long long W = each * p.seqs, w = block_start(W, block, blocks);
+    tiles0 = (unsigned)tiles_of<TK>(p.k_sel);
+    split.set((long long)per * tiles0 * p.seqs, tiles0, (long long)per * p.seqs, blocks);
+    return split;
+  }
+  tiles0 = lane < p.seqs ? (unsigned)tiles_of<TK>(seq_of<SEL>(p, lane).len) : 0;
+  long long sum = tiles0;
+  unsigned longest = tiles0;
+  for (int s = lane + 32; s < p.seqs; s += 32) {
+    const unsigned t = (unsigned)tiles_of<TK>(seq_of<SEL>(p, s).len);
+    sum += t;
+    longest = max(longest, t);
+  }
+  longest = __reduce_max_sync(0xffffffffu, longest);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  split.set(sum * per, longest, (long long)per * p.seqs, blocks);
+  return split;
+}
+
+// Where a block starts: filled by one warp, read by all after a barrier.
+struct Start {
+  int seq;        // the sequence of the block's first tile
+  unsigned rel;   // the tile's number among the sequence's (they fit: the host checks)
+  unsigned left;  // the block's tiles
+};
+
+template <bool SEL, int TK>
+__device__ __forceinline__ void find_start(const Params& p, Start* st) {
+  const int lane = threadIdx.x & 31, block = blockIdx.x;
+  const unsigned per = (unsigned)(p.kv_heads * p.row_tiles);
+  unsigned tiles0;
+  const Split split = make_split<SEL, TK>(p, gridDim.x, tiles0);
+  if (split.share) {
     if (lane == 0) {
-      st->total = W;
-      st->seq = (int)(w / each);
-      st->cum = (w / each) * each;
+      const unsigned unit = (unsigned)block / split.share, i = (unsigned)block - unit * split.share;
+      const unsigned seq = unit / per, in = unit - seq * per;
+      st->seq = (int)seq;
+      st->rel = st->left = 0;
+      if (seq < (unsigned)p.seqs) {
+        const unsigned tiles = (unsigned)tiles_of<TK>(seq_of<SEL>(p, (int)seq).len), n = min(split.share, tiles);
+        if (i < n) {
+          const unsigned tq = tiles / n, tr = tiles - tq * n;
+          st->rel = in * tiles + i * tq + min(i, tr);
+          st->left = tq + (i < tr ? 1 : 0);
+        }
+      }
     }
     return;
   }
-  long long sum = 0;
-  for (int s = lane; s < p.seqs; s += 32) sum += tiles_of<TK>(seq_of<SEL>(p, s).len);
-#pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const long long W = sum * per, w = block_start(W, block, blocks);
+  const long long w = split.start(block);
+  const unsigned left = split.q + ((unsigned)block < split.r ? 1 : 0);
+  if (SEL) {
+    if (lane == 0) {
+      const unsigned each = per * tiles0;
+      st->seq = w >> 31 ? (int)(w / each) : (int)((unsigned)w / each);
+      st->rel = (unsigned)(w - (long long)st->seq * each);
+      st->left = left;
+    }
+    return;
+  }
   long long base = 0;
   for (int s0 = 0; s0 < p.seqs; s0 += 32) {
     const int s = s0 + lane;
-    const long long mine = s < p.seqs ? per * tiles_of<TK>(seq_of<SEL>(p, s).len) : 0;
+    const long long mine = (long long)per * (s0 == 0 ? (int)tiles0 : s < p.seqs ? tiles_of<TK>(seq_of<SEL>(p, s).len) : 0);
     long long end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -176,20 +246,62 @@ __device__ __forceinline__ void find_start(const Params& p, int block, int block
     const unsigned m = __ballot_sync(0xffffffffu, s < p.seqs && w < end);
     if (m) {
       if (lane == __ffs(m) - 1) {
-        st->total = W;
         st->seq = s;
-        st->cum = end - mine;
+        st->rel = (unsigned)(w - (end - mine));
+        st->left = left;
       }
       return;
     }
     base = __shfl_sync(0xffffffffu, end, 31);
   }
-  if (lane == 0) {  // an empty tail: no tile of this block's
-    st->total = W;
+  if (lane == 0) {  // past the last tile: a block without work
     st->seq = p.seqs;
-    st->cum = W;
+    st->rel = st->left = 0;
   }
 }
+
+// A block's segments: runs of tiles of one unit.
+struct Segment {
+  int seq, head, row_tile, b;
+  int t0, t1, tiles;  // tiles [t0, t1) of the unit's
+  bool first;         // of the block
+  Seq len;
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+template <bool SEL, int TK>
+struct Segments {
+  unsigned left, rel;
+  int seq;
+  bool first;
+  __device__ __forceinline__ void begin(const Start& st) {
+    left = st.left;
+    rel = st.rel;
+    seq = st.seq;
+    first = true;
+  }
+  __device__ __forceinline__ bool next(const Params& p, Segment& s) {
+    if (left == 0) return false;
+    s.len = seq_of<SEL>(p, seq);
+    const unsigned tiles = (unsigned)tiles_of<TK>(s.len.len);
+    const unsigned unit = rel / tiles, t0 = rel - unit * tiles, n = min(tiles - t0, left);
+    s.seq = seq;
+    s.b = SEL ? seq / p.tokens : seq;
+    s.head = (int)(unit / (unsigned)p.row_tiles);
+    s.row_tile = (int)(unit - (unsigned)s.head * p.row_tiles);
+    s.t0 = (int)t0;
+    s.t1 = (int)(t0 + n);
+    s.tiles = (int)tiles;
+    s.first = first;
+    first = false;
+    left -= n;
+    rel += n;
+    if (rel == tiles * (unsigned)(p.kv_heads * p.row_tiles)) {
+      rel = 0;
+      ++seq;
+    }
+    return true;
+  }
+};
 
 // Whether query row t sees drafted token j.
 __device__ __forceinline__ bool sees_draft(const Params& p, int b, int t, int j) {
@@ -210,6 +322,79 @@ __device__ __forceinline__ const __nv_bfloat16* q_row(const Params& p, int seq, 
   const int b = SEL ? seq / p.tokens : seq, t = SEL ? seq % p.tokens : R / p.group;
   const int h = head * p.group + (SEL ? R : R % p.group);
   return p.q + b * p.q_batch + t * p.q_token + h * p.q_head;
+}
+
+// Block c's partial of a unit whose first block is c0; `slot0`: which of that block's slots is the unit's.
+template <int ROWS, int D>
+__device__ __forceinline__ const float* part_of(const float* parts, int c, int c0, int slot0) {
+  return parts + (2LL * c + (c == c0 ? slot0 : 0)) * (ROWS * (D + 2));
+}
+
+// One warp joins partials c0 + from, c0 + from + step, ... <= c1 of row r of a unit's tile:
+//     out = sum_s 2^(m_s - m) o_s,  l = sum_s 2^(m_s - m) l_s,  m = max_s m_s
+// (partials that saw nothing have l_s = 0 and count for nothing). A lane has D / 32 elements.
+// 32 partials' weights are made at once, a lane each; their rows are read eight at a time.
+template <int ROWS, int D>
+__device__ __forceinline__ void join_row(const float* parts, int c0, int c1, int slot0, int r,
+                                         int from, int step, float (&acc)[D / 32], float& m, float& l) {
+  constexpr int kVec = D / 32;
+  const int lane = threadIdx.x & 31;
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = 0.f;
+  for (int b = c0 + from; b <= c1; b += 32 * step) {
+    const int c = b + lane * step;
+    const float* mine = part_of<ROWS, D>(parts, min(c, c1), c0, slot0) + r * D;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (c <= c1) ml = __ldcg(reinterpret_cast<const float2*>(mine + (ROWS - r) * D + 2 * r));
+    float top = ml.y != 0.f ? ml.x : -INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    top = fmaxf(top, m);
+    const float back = m == top ? 1.f : ex2(m - top);
+    const float w = ml.y == 0.f ? 0.f : ml.x == top ? 1.f : ex2(ml.x - top);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    l = l * back + sum;
+    m = top;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] *= back;
+    const int n = min(32, (c1 - b) / step + 1);
+    for (int j = 0; j < n; j += 8) {
+      float v[8][kVec];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float* row = part_of<ROWS, D>(parts, min(b + (j + e) * step, c1), c0, slot0) + r * D + lane * kVec;
+        if (kVec == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(row));
+          v[e][0] = x.x; v[e][1] = x.y; v[e][2 % kVec] = x.z; v[e][3 % kVec] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(row));
+          v[e][0] = x.x; v[e][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = __shfl_sync(0xffffffffu, w, (j + e) & 31);
+        if (j + e < n && f != 0.f)
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] += f * v[e][i];
+      }
+    }
+  }
+}
+
+// A lane's part of an output row, and the row's log-sum-exp.
+template <int D>
+__device__ __forceinline__ void store_joined(const Params& p, long long row, const float (&acc)[D / 32], float m, float l) {
+  const int lane = threadIdx.x & 31;
+  const float g = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + row * D + lane * (D / 32));
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) out[i] = pack_bf16(acc[2 * i] * g, acc[2 * i + 1] * g);
+  if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
 }
 
 // Floats of a partial slot: ROWS x D of output, then ROWS pairs (maximum, sum).

@@ -23,6 +23,7 @@ struct CacheParams {
   float* scales;
   long long page_b, token_b, head_b;  // strides of the cache in bytes
   int page_shift, kv_heads;
+  int head_shift;  // log2 of kv_heads where it is a power of two, else -1
   int slots_held;  // pages * page_size
   const int32_t* slots;
   int n;

@@ -108,21 +108,16 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 
   grid_wait();
   grid_launch_dependents();
-  if (warp == 0) find_start<SEL, kRowsKeys>(p, blockIdx.x, gridDim.x, &start);
+  if (warp == 0) find_start<SEL, kRowsKeys>(p, &start);
   __syncthreads();
-  const long long W = start.total, w_first = block_start(W, blockIdx.x, gridDim.x),
-                  w_end = block_start(W, blockIdx.x + 1, gridDim.x);
-  long long w = w_first, cum = start.cum;
-  int seq = start.seq;
+  Segments<SEL, kRowsKeys> segments;
+  segments.begin(start);
+  Segment sg;
 
-  while (w < w_end) {
+  while (segments.next(p, sg)) {
     // ---- the segment ------------------------------------------------------
-    const Seq len = seq_of<SEL>(p, seq);
-    const int tiles = tiles_of<kRowsKeys>(len.len);
-    const int unit = (int)((w - cum) / tiles), t0 = (int)((w - cum) % tiles);
-    const int t1 = (int)min((long long)tiles, t0 + (w_end - w));
-    const int head = unit / p.row_tiles, row_tile = unit % p.row_tiles;
-    const int b = SEL ? seq / p.tokens : seq;
+    const Seq len = sg.len;
+    const int seq = sg.seq, head = sg.head, row_tile = sg.row_tile, b = sg.b, t0 = sg.t0, t1 = sg.t1;
     const int k_beg = t0 * kRowsKeys;  // tiles * kRowsKeys stays below 2^31: len does, rounded up once
     const int k_end = (int)min((long long)len.len, (long long)t1 * kRowsKeys);
     const int chunks = (k_end - k_beg + kChunk - 1) / kChunk;
@@ -466,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       ml_s[warp][n + 8] = make_float2(m[1], l[1]);
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    float* part = p.parts + (2LL * blockIdx.x + (w == w_first ? 0 : 1)) * kPartFloats<kRowsTile, D>;
+    const bool whole = sg.whole();
+    float* part = p.parts + (2LL * blockIdx.x + (sg.first ? 0 : 1)) * kPartFloats<kRowsTile, D>;
     const float* om0 = reinterpret_cast<const float*>(smem);
     for (int x = threadIdx.x; x < 16 * D / 4; x += kThreads) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4, R = row_tile * kRowsTile + r;
@@ -492,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       if (whole) {
         const float g = ll == 0.f ? 0.f : 1.f / ll;
         const long long row = out_row<SEL>(p, seq, head, R);
-        uint2 y = make_uint2(pack_bf16(o.x * g, o.y * g), pack_bf16(o.z * g, o.w * g));
-        *reinterpret_cast<uint2*>(p.out + row * D + d) = y;
+        *reinterpret_cast<uint2*>(p.out + row * D + d) = make_uint2(pack_bf16(o.x * g, o.y * g), pack_bf16(o.z * g, o.w * g));
         if (p.lse && d == 0) p.lse[row] = ll == 0.f ? -INFINITY : (mm + lg2(ll)) * 0.6931471805599453f;
       } else {
         *reinterpret_cast<float4*>(part + r * D + d) = o;
@@ -501,12 +495,6 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       }
     }
     __syncthreads();  // the ring is free for the next segment
-
-    w += t1 - t0;
-    if (unit == p.kv_heads * p.row_tiles - 1 && t1 == tiles) {
-      cum += (long long)tiles * p.kv_heads * p.row_tiles;
-      ++seq;
-    }
   }
 }
 

@@ -251,47 +251,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// ---- a block's segments ---------------------------------------------------------
-struct Segment {
-  int seq, head, row_tile, b;
-  int t0, t1;
-  bool whole, first;
-  Seq len;
-};
-template <bool SEL>
-struct Segments {
-  long long w, w_first, w_end, cum;
-  int seq;
-  __device__ __forceinline__ void begin(const Start& st) {
-    w_first = block_start(st.total, blockIdx.x, gridDim.x);
-    w_end = block_start(st.total, blockIdx.x + 1, gridDim.x);
-    w = w_first;
-    cum = st.cum;
-    seq = st.seq;
-  }
-  __device__ __forceinline__ bool next(const Params& p, Segment& s) {
-    if (w >= w_end) return false;
-    s.len = seq_of<SEL>(p, seq);
-    const int tiles = tiles_of<kKeys>(s.len.len);
-    const unsigned rel = (unsigned)(w - cum);  // (a sequence's tiles over all heads fit: checked by the host)
-    const int unit = (int)(rel / (unsigned)tiles);
-    s.seq = seq;
-    s.b = SEL ? seq / p.tokens : seq;
-    s.head = unit / p.row_tiles;
-    s.row_tile = unit % p.row_tiles;
-    s.t0 = (int)(rel - (unsigned)unit * (unsigned)tiles);
-    s.t1 = (int)min((long long)tiles, s.t0 + (w_end - w));
-    s.whole = s.t0 == 0 && s.t1 == tiles;
-    s.first = w == w_first;
-    w += s.t1 - s.t0;
-    if (unit == p.kv_heads * p.row_tiles - 1 && s.t1 == tiles) {
-      cum += (long long)tiles * p.kv_heads * p.row_tiles;
-      ++seq;
-    }
-    return true;
-  }
-};
-
 // 32 bits of row t's view of the drafted tokens j0 .. j0 + 31 (those before 0 are context: seen).
 __device__ __forceinline__ unsigned draft_bits(const Params& p, int b, int t, int j0) {
   if (j0 + 31 < 0) return ~0u;
@@ -314,7 +273,7 @@ __device__ __forceinline__ unsigned draft_bits(const Params& p, int b, int t, in
 template <int D, bool I8, bool SEL>
 __device__ __forceinline__ void look_up(const Params& p, const Block& k, const Start& start, int who) {
   const int lane = threadIdx.x & 31;
-  Segments<SEL> it;
+  Segments<SEL, kKeys> it;
   it.begin(start);
   Segment s;
   unsigned g = 0;  // the tile's number in this block
@@ -391,7 +350,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
 template <int D, bool I8>
 __device__ __forceinline__ void produce(const Params& p, const Block& k, int tiles) {
   using S = Shape<D, I8>;
-  const int t = threadIdx.x - kProducer0, lane = threadIdx.x & 31;
+  const int t = threadIdx.x - kProducer0;
   constexpr int kRows = kProducers / S::kPieces;  // rows that a pass covers
   // A thread's piece of a row, and its first row. Eight neighbouring lanes take half of two rows
   // of int8 (two 16-byte stores a piece), or a row's half of bfloat16: no bank conflicts.
@@ -519,7 +478,7 @@ template <int D, bool I8, bool SEL>
 __device__ __forceinline__ void multiply(const Params& p, const Block& k, const Start& start, uint32_t tmem) {
   using S = Shape<D, I8>;
   constexpr uint32_t kQk = instr(I8, false, kKeys), kPv = instr(I8, true, D);
-  Segments<SEL> it;
+  Segments<SEL, kKeys> it;
   it.begin(start);
   Segment s;
   Ring<S::kStages> kr, vr;  // the stages of the first and of the second product
@@ -600,7 +559,7 @@ __device__ __forceinline__ void rescale(uint32_t addr, float fa, float fb) {
 // The segments of a row warp, kept in shared memory: its registers hold scores.
 template <bool SEL>
 struct RowSegments {
-  Segments<SEL> it;
+  Segments<SEL, kKeys> it;
   Segment s[2];
 };
 
@@ -917,7 +876,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
               }
             }
           }
-          if (done.whole) {
+          if (done.whole()) {
             uint4* out = reinterpret_cast<uint4*>(p.out + row * D + d);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -932,7 +891,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
         __syncwarp();
       }
       if (R < p.rows && half == 0) {
-        if (!done.whole)
+        if (!done.whole())
           *reinterpret_cast<float2*>(part + kTilesRows * D + 2 * r) = make_float2(top, empty ? 0.f : lr);
         else if (p.lse)
           p.lse[row] = empty ? -INFINITY : (top + lg2(lr)) * 0.6931471805599453f;
@@ -992,12 +951,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   }
   grid_wait();
   grid_launch_dependents();
-  if (warp == kMetaWarp0) find_start<SEL, kKeys>(p, blockIdx.x, gridDim.x, &start);
+  if (warp == kMetaWarp0) find_start<SEL, kKeys>(p, &start);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(tmem_s);
-  const int tiles = uniform((int)(block_start(start.total, blockIdx.x + 1, gridDim.x) - block_start(start.total, blockIdx.x, gridDim.x)));
+  const int tiles = uniform((int)start.left);
 
   // registers: 2 * 152 + 48 + 2 * 64 of the launch's 5 * 96
   if (warp < kRowWarps) {

@@ -20,20 +20,58 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsPerLane = 4;
 
-// Eight elements of a row in 32 bits.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// Eight elements of a row as they lie in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint32_t u[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
+    u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  // The largest magnitude over the row's LANES lanes. Magnitudes are compared as unsigned
+  // numbers, two at a time: their order, with NaN on top.
+  template <int LANES>
+  __device__ __forceinline__ float amax() const {
+    uint32_t m = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu), __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return __uint_as_float(max(m & 0xffff0000u, m << 16));
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  float v[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  template <int LANES>
+  __device__ __forceinline__ float amax() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return __uint_as_float(m);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = v[i];
+  }
+};
+// A row's token; rows are counted head fastest.
+__device__ __forceinline__ unsigned token_of(const CacheParams& p, unsigned row) {
+  return p.head_shift >= 0 ? row >> p.head_shift : row / (unsigned)p.kv_heads;
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
@@ -43,9 +81,13 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
+// Four values rounded to nearest even, as codes. Adding 1.5 * 2^23 leaves the rounded number in
+// the low bits of the sum.
 __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d) {
-  return ((uint32_t)(int)a & 0xffu) | (((uint32_t)(int)b & 0xffu) << 8) |
-         (((uint32_t)(int)c & 0xffu) << 16) | ((uint32_t)(int)d << 24);
+  const float k = 12582912.f;
+  const uint32_t x = __float_as_uint(__fadd_rn(a, k)), y = __float_as_uint(__fadd_rn(b, k));
+  const uint32_t z = __float_as_uint(__fadd_rn(c, k)), w = __float_as_uint(__fadd_rn(d, k));
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 
 // Rows are counted head fastest, then token; blockIdx.y is 0 for keys, 1 for values.
@@ -62,55 +104,43 @@ __global__ void __launch_bounds__(kThreads) write_kernel(const __grid_constant__
   grid_wait();
   grid_launch_dependents();
 
-  float x[kRowsPerLane][8];
+  Raw<T> raw[kRowsPerLane];
   int slot[kRowsPerLane];
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
     const unsigned row = row0 + i * kPerPass;
     slot[i] = -1;
     if (row < total) {
-      const unsigned token = row / (unsigned)p.kv_heads, head = row - token * p.kv_heads;
+      const unsigned token = token_of(p, row), head = row - token * p.kv_heads;
       slot[i] = __ldg(p.slots + token);
-      load8(src + token * s_token + head * s_head + e, x[i]);
+      raw[i].load(src + token * s_token + head * s_head + e);
     }
   }
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
     const unsigned row = row0 + i * kPerPass;
-    const unsigned token = row / (unsigned)p.kv_heads, head = row - token * p.kv_heads;
+    const unsigned head = row - token_of(p, row) * p.kv_heads;
     const bool ok = slot[i] >= 0 && slot[i] < p.slots_held;
     if (slot[i] >= p.slots_held) report(p.status, kStatIndexBit);
-    const long long at = (slot[i] >> p.page_shift) * p.page_b +
-                         (slot[i] & ((1 << p.page_shift) - 1)) * p.token_b + head * p.head_b;
+    float amax = I8 ? raw[i].template amax<kLanes>() : 0.f;
+    if (!ok) continue;
+    unsigned char* at = dst + (slot[i] >> p.page_shift) * p.page_b + (slot[i] & ((1 << p.page_shift) - 1)) * p.token_b + head * p.head_b;
+    float x[8];
+    raw[i].get(x);
     if (!I8) {
-      if (ok) store8(reinterpret_cast<__nv_bfloat16*>(dst + at) + e, x[i]);
+      store8(reinterpret_cast<__nv_bfloat16*>(at) + e, x);
       continue;
     }
-    float amax = 0.f;
-    bool nan = false;
-    if (ok)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        amax = fmaxf(amax, fabsf(x[i][j]));
-        nan |= x[i][j] != x[i][j];
-      }
-    if (nan) amax = __int_as_float(0x7fffffff);
-#pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) {
-      // unsigned order of non-negative floats is theirs, with NaN on top
-      const unsigned y = __shfl_xor_sync(0xffffffffu, __float_as_uint(amax), o);
-      amax = __uint_as_float(max(__float_as_uint(amax), y));
-    }
-    if (!ok) continue;
     const float lo = 9.094947017729282e-13f, hi = 1.2089258196146292e24f;  // 2^-40, 2^80
-    amax = amax < lo ? lo : amax > hi ? hi : amax;
+    const bool beyond = amax > hi;
+    amax = amax < lo ? lo : beyond ? hi : amax;  // (a NaN stays one)
     const float scale = __fmul_rn(amax, 1.0f / 127.0f), inv = __frcp_rn(scale);
-    float q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      q[j] = fminf(fmaxf(rintf(__fmul_rn(x[i][j], inv)), -127.f), 127.f);
-    *reinterpret_cast<uint2*>(dst + at + e) =
-        make_uint2(pack_codes(q[0], q[1], q[2], q[3]), pack_codes(q[4], q[5], q[6], q[7]));
+    for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(x[j], inv);
+    if (beyond)  // (otherwise no value is beyond 127)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = fminf(fmaxf(x[j], -127.f), 127.f);
+    *reinterpret_cast<uint2*>(at + e) = make_uint2(pack_codes(x[0], x[1], x[2], x[3]), pack_codes(x[4], x[5], x[6], x[7]));
     if (e == 0) p.scales[2 * ((long long)slot[i] * p.kv_heads + head) + (value ? 1 : 0)] = scale;
   }
 }
@@ -131,7 +161,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
     const unsigned row = row0 + i * kPerPass;
-    slot[i] = row < total ? __ldg(p.slots + row / (unsigned)p.kv_heads) : -1;
+    slot[i] = row < total ? __ldg(p.slots + token_of(p, row)) : -1;
     if (slot[i] >= p.slots_held) {
       report(p.status, kStatIndexBit);
       slot[i] = -1;
@@ -142,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
     const unsigned row = row0 + i * kPerPass;
-    const unsigned head = row - (row / (unsigned)p.kv_heads) * p.kv_heads;
+    const unsigned head = row - token_of(p, row) * p.kv_heads;
     w[i] = make_uint4(0u, 0u, 0u, 0u);
     scale[i] = 0.f;
     if (slot[i] < 0) continue;

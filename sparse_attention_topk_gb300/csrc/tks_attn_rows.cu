@@ -19,11 +19,12 @@
 // works on 16 rows, so up to 16 rows of a head cost the same; 16 keys of int8
 // (4 KB) take 32 of them, a third of their rate at the memory's pace.
 //
-// Layout.  A block is four warps; each takes every fourth chunk of 16 keys of
-// the block's segment, keeps its own maximum, sum and output in registers and
-// its own ring of cp.async stages in shared memory, so warps meet only at a
-// segment's end.  Key positions are looked up (list, page table) one and two
-// chunks ahead of their copies.  The order of the 16-wide k index inside a
+// Layout.  A block is four warps; each takes every fourth chunk of the block's
+// segment (32 keys of int8, 16 of bfloat16: 8 KB), keeps its own maximum, sum and
+// output in registers and its own ring of cp.async stages in shared memory, so
+// warps meet only at a segment's end.  Key positions are looked up (list, page
+// table) one and two chunks ahead of their copies; a chunk that lies in one page
+// takes one lookup.  The order of the 16-wide k index inside a
 // product is free as long as both operands agree, so a lane takes whole
 // 16-byte pieces of its key's row for the first product and of its four
 // value rows for the second; bytes are paired by byte permutes, and the rows'
@@ -37,7 +38,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 16;  // keys of a stage
 
 template <int D, bool I8>
 struct Shape {
@@ -48,12 +48,16 @@ struct Shape {
   static constexpr int kKH = kPieces / 4;              // pieces a lane takes of a key
   static constexpr int kEV = (I8 && D == 64) ? 8 : kE; // elements a lane takes of a value at once
   static constexpr int kVH = D / (8 * kEV);            // how often
+  static constexpr int kChunk = I8 ? 32 : 16;          // keys of a stage
   static constexpr int kOps = 2 * kChunk * kRow;       // keys, then values
   static constexpr int kScales = I8 ? kChunk * 8 : 0;
   static constexpr int kStage = kOps + kScales + 16;   // and the mask of valid keys
-  static constexpr int kStages = I8 ? (D == 128 ? 5 : 6) : (D == 128 ? 3 : 5);
-  static constexpr int kSmem = kWarps * kStages * kStage;
-  static_assert(kSmem >= kWarps * (16 * D * 4 + 16 * 8), "the merge fits the ring");
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kQs = D / 16 * 32 * 16;         // query fragments, behind the rings
+  static constexpr int kConst = I8 ? kWarps * 32 * 16 : 0;  // and each warp's scales as they are used
+  static constexpr int kRings = kWarps * kStages * kStage;
+  static constexpr int kSmem = kRings + kQs + kConst;
+  static_assert(kRings >= kWarps * (16 * D * 4 + 16 * 8), "the merge fits the ring");
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
   static __device__ __forceinline__ int ksw(int r) { return kPieces >= 8 ? (r & 1) << 2 : 0; }
@@ -63,17 +67,17 @@ struct Shape {
 };
 
 template <bool HALF>
-__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   if (HALF)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
@@ -103,8 +107,17 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;  // the lane's key, row or column, and its quarter
+  constexpr int kChunk = S::kChunk, kNT = kChunk / 8;  // key columns of a chunk, in eights
   unsigned char* ring = smem + warp * S::kStages * S::kStage;
-  const uint32_t ring_a = smem_addr(ring);
+  uint4* qs = reinterpret_cast<uint4*>(smem + S::kRings);
+  float4* consts = reinterpret_cast<float4*>(smem + S::kRings + S::kQs) + warp * 32;
+  // the lane's piece of a row, its first row, and where that goes in a stage
+  constexpr int kPer = 32 / S::kPieces;  // rows that 32 lanes cover
+  const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
+  const uint32_t k_dst = smem_addr(ring) + row0 * S::kRow + ((piece ^ S::ksw(row0)) << 4);
+  const uint32_t v_dst = smem_addr(ring) + (kChunk + row0) * S::kRow;
+  const int v_piece = piece ^ S::vsw(row0);  // (the swizzles of row0 and of i * kPer combine by XOR)
+  const bool paged = !SEL && (1 << p.page_shift) >= kChunk;
 
   grid_wait();
   grid_launch_dependents();
@@ -128,9 +141,10 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     const unsigned char* kb = p.k + head * p.head_b;
     const unsigned char* vb = p.v + head * p.head_b;
 
-    // Position of this lane's key (lane & 15) of the warp's chunk `it`, or -1.
+    // Position of this lane's key (lane % kChunk) of the warp's chunk `it`, or -1; where chunks lie
+    // in one page, of the chunk's first key.
     auto position = [&](int it) -> int {
-      const long long j = (long long)k_beg + ((long long)it * kWarps + warp) * kChunk + (lane & 15);
+      const long long j = (long long)k_beg + ((long long)it * kWarps + warp) * kChunk + (paged ? 0 : lane % kChunk);
       if (j >= k_end) return -1;
       if (!SEL) return (int)j;
       const int idx = list[j];
@@ -138,32 +152,50 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       return idx < limit ? idx : -1;
     };
     auto page = [&](int pos) -> int { return pos < 0 ? -1 : table[pos >> p.page_shift]; };
-    // Starts the copies of chunk `it` into its stage, given its lane's position and page.
-    auto issue = [&](int it, int pos, int pg) {
+    // Starts the copies of chunk `it` into stage `st`, given its lane's position and page.
+    auto issue = [&](int it, int st, int pos, int pg) {
       if (it < iters) {
         const bool ok = pos >= 0 && (unsigned)pg < (unsigned)p.pages;
         if (pos >= 0 && !ok) report(p.status, kStatIndexBit);
         const int in_page = pos & ((1 << p.page_shift) - 1);
-        const long long off = ok ? pg * p.page_b + in_page * p.token_b : -1;
-        const unsigned valid = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-        unsigned char* st = ring + (it % S::kStages) * S::kStage;
-        const uint32_t st_a = ring_a + (it % S::kStages) * S::kStage;
-        constexpr int kPer = 32 / S::kPieces;  // rows that 32 lanes cover
-        const int piece = lane % S::kPieces;
+        const uint32_t to = st * S::kStage;
+        unsigned valid;
+        if (paged) {
+          const int n_valid = ok ? min(kChunk, k_end - pos) : 0;
+          const long long off = ok ? pg * p.page_b + in_page * p.token_b : 0;
+          const unsigned char* ks = kb + off + row0 * p.token_b + piece * 16;
+          const unsigned char* vs = vb + off + row0 * p.token_b + piece * 16;
+          const long long step = kPer * p.token_b;
 #pragma unroll
-        for (int i = 0; i < kChunk / kPer; ++i) {
-          const int r = lane / S::kPieces + i * kPer;
-          const long long o = __shfl_sync(0xffffffffu, off, r);
-          const int bytes = o >= 0 ? 16 : 0;
-          const long long at = (o >= 0 ? o : 0) + piece * 16;
-          cp16(st_a + r * S::kRow + ((piece ^ S::ksw(r)) << 4), kb + (bytes ? at : 0), bytes);
-          cp16(st_a + kChunk * S::kRow + r * S::kRow + ((piece ^ S::vsw(r)) << 4), vb + (bytes ? at : 0), bytes);
+          for (int i = 0; i < kChunk / kPer; ++i) {
+            const int bytes = row0 + i * kPer < n_valid ? 16 : 0;
+            cp16(k_dst + to + i * kPer * S::kRow, ks, bytes);
+            cp16(v_dst + to + i * kPer * S::kRow + ((v_piece ^ S::vsw(i * kPer)) << 4), vs, bytes);
+            ks += step;
+            vs += step;
+          }
+          if (I8) {
+            const long long row = ok ? (((long long)pg << p.page_shift) + in_page) * p.kv_heads + head : 0;
+            cp8(smem_addr(ring) + to + S::kOps + lane * 8, p.scales + row + (lane < n_valid ? (long long)lane * p.kv_heads : 0), lane < n_valid ? 8 : 0);
+          }
+          valid = n_valid >= 32 ? ~0u : (1u << n_valid) - 1u;
+        } else {
+          const long long off = ok ? pg * p.page_b + in_page * p.token_b : -1;
+          valid = __ballot_sync(0xffffffffu, ok) & (kChunk == 32 ? ~0u : (1u << (kChunk & 31)) - 1u);
+#pragma unroll
+          for (int i = 0; i < kChunk / kPer; ++i) {
+            const long long o = __shfl_sync(0xffffffffu, off, row0 + i * kPer);
+            const int bytes = o >= 0 ? 16 : 0;
+            const long long at = o >= 0 ? o + piece * 16 : 0;
+            cp16(k_dst + to + i * kPer * S::kRow, kb + at, bytes);
+            cp16(v_dst + to + i * kPer * S::kRow + ((v_piece ^ S::vsw(i * kPer)) << 4), vb + at, bytes);
+          }
+          if (I8) {
+            const long long row = ok ? (((long long)pg << p.page_shift) + in_page) * p.kv_heads + head : 0;
+            cp8(smem_addr(ring) + to + S::kOps + lane * 8, p.scales + row, ok ? 8 : 0);
+          }
         }
-        if (I8 && lane < kChunk) {
-          const long long row = ok ? ((long long)(((long long)pg << p.page_shift) + in_page) * p.kv_heads + head) : 0;
-          cp8(st_a + S::kOps + lane * 8, p.scales + row, ok ? 8 : 0);
-        }
-        if (lane == 0) *reinterpret_cast<unsigned*>(st + S::kOps + S::kScales) = valid;
+        if (lane == 0) *reinterpret_cast<unsigned*>(ring + to + S::kOps + S::kScales) = valid;
       }
       cp_commit();
     };
@@ -181,15 +213,15 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       for (int i = 0; i < kAhead; ++i) pg[i] = page(ps[i]);
       pg_n = page(pos_n);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) issue(i, ps[i], pg[i]);
+      for (int i = 0; i < kAhead; ++i) issue(i, i, ps[i], pg[i]);
     }
 
     // Query fragments: rows n and n + 8; for product step (h, j) of a lane,
     // elements kE * (c + 4h) + 4j + {0,1} and {2,3}.
-    uint32_t qf[D / 16][4];
     const int rows_left = p.rows - row_tile * kRowsTile;
     float fac = p.scale_log2;
     {
+      uint32_t qf[D / 16][4];
       const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
       const __nv_bfloat16* q0 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in0 ? n : 0));
       const __nv_bfloat16* q1 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in1 ? n + 8 : 0));
@@ -221,6 +253,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             qf[s][r] = pack_half(f.x * up, f.y * up);
           }
       }
+      // all warps have the same rows: each puts down a quarter of the steps
+#pragma unroll
+      for (int s = 0; s < D / 16; ++s)
+        if ((s & 3) == warp) qs[s * 32 + lane] = make_uint4(qf[s][0], qf[s][1], qf[s][2], qf[s][3]);
+      __syncthreads();
     }
 
     float acc[D / 8][4];
@@ -232,11 +269,12 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     bool poisoned = false;  // a draft's value held an infinity or NaN (bfloat16)
 
     // ---- the warp's chunks ------------------------------------------------
+    int stage = 0, ahead = kAhead;  // of this chunk, and of the one whose copies start
     for (int it = 0; it < iters; ++it) {
       cp_wait<kAhead - 1>();
       __syncwarp();
       {  // the next copies go into the stage that the previous chunk has left
-        issue(it + kAhead, pos_n, pg_n);
+        issue(it + kAhead, ahead, pos_n, pg_n);
         if (SEL) {
           pos_n = pos_nn;
           pg_n = page(pos_n);
@@ -246,91 +284,103 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
           pg_n = page(pos_n);
         }
       }
-      const unsigned char* st = ring + (it % S::kStages) * S::kStage;
+      const unsigned char* st = ring + stage * S::kStage;
+      ahead = stage;
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
       const unsigned valid = *reinterpret_cast<const unsigned*>(st + S::kOps + S::kScales);
+      if (I8) {  // the scales of key `lane` as they are used: a factor, a summand, and the sum's factor
+        const float2 sc = *reinterpret_cast<const float2*>(st + S::kOps + lane * 8);
+        const float lo = 7.105427357601002e-15f;  // 2^-47: a NaN stays one
+        const float x = sc.y < lo ? lo : sc.y;
+        // (the last is finite: a weight of 0 times it is 0)
+        consts[lane] = make_float4(sc.x * fac, lg2(x), x == x ? __fdividef(1.f, x) : 1.f, 0.f);
+      }
 
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[kNT][4];
+#pragma unroll
+      for (int t = 0; t < kNT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
       for (int h = 0; h < S::kKH; ++h) {
-        const int piece = ((c + 4 * h) ^ S::ksw(n)) << 4;
-        uint4 ka = *reinterpret_cast<const uint4*>(st + n * S::kRow + piece);
-        uint4 kc = *reinterpret_cast<const uint4*>(st + (n + 8) * S::kRow + piece);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wc[4] = {kc.x, kc.y, kc.z, kc.w};
+        uint4 kw[kNT];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t)
+          kw[t] = *reinterpret_cast<const uint4*>(st + (n + 8 * t) * S::kRow + (((c + 4 * h) ^ S::ksw(n)) << 4));
         if (I8) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a = wa[j] ^ 0x80808080u, e = wc[j] ^ 0x80808080u;
-            mma<true>(s[0], qf[h * 4 + j], codes_to_half2<0x4140>(a), codes_to_half2<0x4342>(a));
-            mma<true>(s[1], qf[h * 4 + j], codes_to_half2<0x4140>(e), codes_to_half2<0x4342>(e));
+            const uint4 q = qs[(h * 4 + j) * 32 + lane];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) {
+              const uint32_t a = (j == 0 ? kw[t].x : j == 1 ? kw[t].y : j == 2 ? kw[t].z : kw[t].w) ^ 0x80808080u;
+              mma<true>(s[t], q, codes_to_half2<0x4140>(a), codes_to_half2<0x4342>(a));
+            }
           }
         } else {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            mma<false>(s[0], qf[h * 2 + j], wa[2 * j], wa[2 * j + 1]);
-            mma<false>(s[1], qf[h * 2 + j], wc[2 * j], wc[2 * j + 1]);
+            const uint4 q = qs[(h * 2 + j) * 32 + lane];
+#pragma unroll
+            for (int t = 0; t < kNT; ++t) mma<false>(s[t], q, j ? kw[t].z : kw[t].x, j ? kw[t].w : kw[t].y);
           }
         }
       }
 
-      // Scores: rows n (s[.][0..1]) and n + 8 (s[.][2..3]), keys 2c, 2c+1 and those + 8.
-      float inv[4];
+      // Scores: rows n (s[.][0..1]) and n + 8 (s[.][2..3]), keys 8t + 2c and the next.
+      float inv[2 * kNT];
       if (I8) {
-        const float4 s0 = *reinterpret_cast<const float4*>(st + S::kOps + 16 * c);
-        const float4 s1 = *reinterpret_cast<const float4*>(st + S::kOps + 64 + 16 * c);
-        const float ks[4] = {s0.x * fac, s0.z * fac, s1.x * fac, s1.z * fac};
-        const float vs[4] = {s0.y, s0.w, s1.y, s1.w};
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lo = 7.105427357601002e-15f;  // 2^-47: a NaN stays one
-          const float x = vs[e] < lo ? lo : vs[e], lv = lg2(x);
-          inv[e] = __fdividef(1.f, x);
-          s[e >> 1][e & 1] = fmaf(s[e >> 1][e & 1], ks[e], lv);
-          s[e >> 1][2 + (e & 1)] = fmaf(s[e >> 1][2 + (e & 1)], ks[e], lv);
-        }
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float4 k = consts[8 * t + 2 * c + e];
+            s[t][e] = fmaf(s[t][e], k.x, k.y);
+            s[t][2 + e] = fmaf(s[t][2 + e], k.x, k.y);
+            inv[2 * t + e] = k.z;
+          }
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[e >> 1][e & 1] *= fac;
-          s[e >> 1][2 + (e & 1)] *= fac;
-        }
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] *= fac;
       }
       const int j0 = k_beg + (it * kWarps + warp) * kChunk;  // the chunk's first key
-      unsigned seen0 = 15u, seen1 = 15u;                      // of this lane's four keys
       const bool drafts = !SEL && j0 + kChunk > len.ctx;
-      if (valid != 0xffffu || drafts) {
-        seen0 = ((valid >> (2 * c)) & 3u) | (((valid >> (2 * c + 8)) & 3u) << 2);
-        seen1 = seen0;
-        if (drafts) {
-          const int R = row_tile * kRowsTile + n;
-          const int ta = min(R / p.group, p.tokens - 1), tc = min((R + 8) / p.group, p.tokens - 1);
+      if (valid != (kChunk == 32 ? ~0u : 0xffffu) || drafts) {
+        const int R = row_tile * kRowsTile + n;
+        const int ta = min(R / p.group, p.tokens - 1), tc = min((R + 8) / p.group, p.tokens - 1);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = j0 + 2 * c + (e & 1) + 8 * (e >> 1) - len.ctx;
-            if (j >= 0 && j < len.drafts) {
-              if (!sees_draft(p, b, ta, j)) seen0 &= ~(1u << e);
-              if (!sees_draft(p, b, tc, j)) seen1 &= ~(1u << e);
+        for (int t = 0; t < kNT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = 8 * t + 2 * c + e, j = j0 + key - len.ctx;
+            bool seen0 = (valid >> key) & 1u, seen1 = seen0;
+            if (drafts && j >= 0 && j < len.drafts) {
+              seen0 = seen0 && sees_draft(p, b, ta, j);
+              seen1 = seen1 && sees_draft(p, b, tc, j);
             }
+            if (!seen0) s[t][e] = -INFINITY;
+            if (!seen1) s[t][2 + e] = -INFINITY;
           }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (!((seen0 >> e) & 1u)) s[e >> 1][e & 1] = -INFINITY;
-          if (!((seen1 >> e) & 1u)) s[e >> 1][2 + (e & 1)] = -INFINITY;
-        }
       }
 
-      // Running maximum; the output is rescaled only when one has grown.
-      float t0m = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-      float t1m = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+      // The maxima that weights are relative to follow when one has grown by more than 2^8.
+      float t0m = fmaxf(s[0][0], s[0][1]), t1m = fmaxf(s[0][2], s[0][3]);
+#pragma unroll
+      for (int t = 1; t < kNT; ++t) {
+        t0m = fmaxf(t0m, fmaxf(s[t][0], s[t][1]));
+        t1m = fmaxf(t1m, fmaxf(s[t][2], s[t][3]));
+      }
 #pragma unroll
       for (int o = 1; o < 4; o <<= 1) {
         t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, o));
         t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, o));
       }
-      if (__any_sync(0xffffffffu, t0m > m[0] || t1m > m[1])) {
-        const float n0 = fmaxf(m[0], t0m), n1 = fmaxf(m[1], t1m);
-        const float f0 = m[0] == n0 ? 1.f : ex2(m[0] - n0), f1 = m[1] == n1 ? 1.f : ex2(m[1] - n1);
-        m[0] = n0; m[1] = n1;
+      if (__any_sync(0xffffffffu, t0m > m[0] + 8.f || t1m > m[1] + 8.f)) {
+        const bool up0 = t0m > m[0] + 8.f, up1 = t1m > m[1] + 8.f;
+        const float f0 = up0 ? ex2(m[0] - t0m) : 1.f, f1 = up1 ? ex2(m[1] - t1m) : 1.f;
+        if (up0) m[0] = t0m;
+        if (up1) m[1] = t1m;
         l[0] *= f0; l[1] *= f1;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -340,70 +390,65 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       }
       const float u0 = m[0] == -INFINITY ? 0.f : m[0], u1 = m[1] == -INFINITY ? 0.f : m[1];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = ex2(s[e >> 1][e & 1] - u0), d = ex2(s[e >> 1][2 + (e & 1)] - u1);
-        s[e >> 1][e & 1] = a;
-        s[e >> 1][2 + (e & 1)] = d;
-        if (I8) {  // (an unseen key's scale may be NaN)
-          l[0] += (seen0 >> e) & 1u ? a * inv[e] : 0.f;
-          l[1] += (seen1 >> e) & 1u ? d * inv[e] : 0.f;
-        } else {
-          l[0] += a;
-          l[1] += d;
+      for (int t = 0; t < kNT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float a = ex2(s[t][e] - u0), d = ex2(s[t][2 + e] - u1);
+          s[t][e] = a;
+          s[t][2 + e] = d;
+          l[0] = I8 ? fmaf(a, inv[2 * t + e], l[0]) : l[0] + a;
+          l[1] = I8 ? fmaf(d, inv[2 * t + e], l[1]) : l[1] + d;
         }
-      }
-      uint32_t pf[4];
-      if (I8) {
-        pf[0] = pack_half(s[0][0], s[0][1]); pf[1] = pack_half(s[0][2], s[0][3]);
-        pf[2] = pack_half(s[1][0], s[1][1]); pf[3] = pack_half(s[1][2], s[1][3]);
-      } else {
-        pf[0] = pack_bf16(s[0][0], s[0][1]); pf[1] = pack_bf16(s[0][2], s[0][3]);
-        pf[2] = pack_bf16(s[1][0], s[1][1]); pf[3] = pack_bf16(s[1][2], s[1][3]);
-      }
 
-      // Values: keys 2c, 2c+1 (b0) and those + 8 (b1), element kEV * (n + 8h) + j in tile (h, j).
+      // Values, 16 keys at a time: keys 2c, 2c+1 (b0) and those + 8 (b1), element kEV * (n + 8h) + j in tile (h, j).
       const unsigned char* vst = st + kChunk * S::kRow;
 #pragma unroll
-      for (int h = 0; h < S::kVH; ++h) {
-        uint32_t vw[4][S::kEV * S::kElem / 4];
+      for (int g = 0; g < kNT / 2; ++g) {
+        const float(&sa)[4] = s[2 * g];
+        const float(&sb)[4] = s[2 * g + 1];
+        const uint4 pf = I8 ? make_uint4(pack_half(sa[0], sa[1]), pack_half(sa[2], sa[3]), pack_half(sb[0], sb[1]), pack_half(sb[2], sb[3]))
+                            : make_uint4(pack_bf16(sa[0], sa[1]), pack_bf16(sa[2], sa[3]), pack_bf16(sb[0], sb[1]), pack_bf16(sb[2], sb[3]));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 2 * c + (e & 1) + 8 * (e >> 1);
-          if (S::kEV * S::kElem == 16) {
-            const uint4 x = *reinterpret_cast<const uint4*>(vst + r * S::kRow + (((n + 8 * h) ^ S::vsw(r)) << 4));
-            vw[e][0] = x.x; vw[e][1] = x.y; vw[e][2 % (S::kEV * S::kElem / 4)] = x.z; vw[e][3 % (S::kEV * S::kElem / 4)] = x.w;
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(vst + r * S::kRow + (((n >> 1) ^ S::vsw(r)) << 4) + (n & 1) * 8);
-            vw[e][0] = x.x; vw[e][1] = x.y;
-          }
-        }
-        if (!I8 && drafts) {
-          bool bad = false;
+        for (int h = 0; h < S::kVH; ++h) {
+          constexpr int kW = S::kEV * S::kElem / 4;
+          uint32_t vw[4][kW];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int r = 2 * c + (e & 1) + 8 * (e >> 1);
-            if (j0 + r >= len.ctx)
-#pragma unroll
-              for (int x = 0; x < S::kEV * S::kElem / 4; ++x) bad |= clear_nonfinite(vw[e][x]);
+            const int r = 16 * g + 2 * c + (e & 1) + 8 * (e >> 1);
+            if (kW == 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(vst + r * S::kRow + (((n + 8 * h) ^ S::vsw(r)) << 4));
+              vw[e][0] = x.x; vw[e][1] = x.y; vw[e][2 % kW] = x.z; vw[e][3 % kW] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(vst + r * S::kRow + (((n >> 1) ^ S::vsw(r)) << 4) + (n & 1) * 8);
+              vw[e][0] = x.x; vw[e][1] = x.y;
+            }
           }
-          poisoned |= __any_sync(0xffffffffu, bad);
-        }
+          if (!I8 && drafts) {
+            bool bad = false;
 #pragma unroll
-        for (int x = 0; x < S::kEV * S::kElem / 4; ++x) {
-          if (I8) {
-            const uint32_t a0 = vw[0][x] ^ 0x80808080u, a1 = vw[1][x] ^ 0x80808080u;
-            const uint32_t a2 = vw[2][x] ^ 0x80808080u, a3 = vw[3][x] ^ 0x80808080u;
-            const uint32_t lo0 = __byte_perm(a0, a1, 0x5140), hi0 = __byte_perm(a0, a1, 0x7362);
-            const uint32_t lo1 = __byte_perm(a2, a3, 0x5140), hi1 = __byte_perm(a2, a3, 0x7362);
-            const int i = h * S::kEV + 4 * x;
-            mma<true>(acc[i], pf, codes_to_half2<0x4140>(lo0), codes_to_half2<0x4140>(lo1));
-            mma<true>(acc[i + 1], pf, codes_to_half2<0x4342>(lo0), codes_to_half2<0x4342>(lo1));
-            mma<true>(acc[i + 2], pf, codes_to_half2<0x4140>(hi0), codes_to_half2<0x4140>(hi1));
-            mma<true>(acc[i + 3], pf, codes_to_half2<0x4342>(hi0), codes_to_half2<0x4342>(hi1));
-          } else {
-            const int i = h * S::kEV + 2 * x;
-            mma<false>(acc[i], pf, __byte_perm(vw[0][x], vw[1][x], 0x5410), __byte_perm(vw[2][x], vw[3][x], 0x5410));
-            mma<false>(acc[i + 1], pf, __byte_perm(vw[0][x], vw[1][x], 0x7632), __byte_perm(vw[2][x], vw[3][x], 0x7632));
+            for (int e = 0; e < 4; ++e)
+              if (j0 + 16 * g + 2 * c + (e & 1) + 8 * (e >> 1) >= len.ctx)
+#pragma unroll
+                for (int x = 0; x < kW; ++x) bad |= clear_nonfinite(vw[e][x]);
+            poisoned |= __any_sync(0xffffffffu, bad);
+          }
+#pragma unroll
+          for (int x = 0; x < kW; ++x) {
+            if (I8) {
+              const uint32_t a0 = vw[0][x] ^ 0x80808080u, a1 = vw[1][x] ^ 0x80808080u;
+              const uint32_t a2 = vw[2][x] ^ 0x80808080u, a3 = vw[3][x] ^ 0x80808080u;
+              const uint32_t lo0 = __byte_perm(a0, a1, 0x5140), hi0 = __byte_perm(a0, a1, 0x7362);
+              const uint32_t lo1 = __byte_perm(a2, a3, 0x5140), hi1 = __byte_perm(a2, a3, 0x7362);
+              const int i = h * S::kEV + 4 * x;
+              mma<true>(acc[i], pf, codes_to_half2<0x4140>(lo0), codes_to_half2<0x4140>(lo1));
+              mma<true>(acc[i + 1], pf, codes_to_half2<0x4342>(lo0), codes_to_half2<0x4342>(lo1));
+              mma<true>(acc[i + 2], pf, codes_to_half2<0x4140>(hi0), codes_to_half2<0x4140>(hi1));
+              mma<true>(acc[i + 3], pf, codes_to_half2<0x4342>(hi0), codes_to_half2<0x4342>(hi1));
+            } else {
+              const int i = h * S::kEV + 2 * x;
+              mma<false>(acc[i], pf, __byte_perm(vw[0][x], vw[1][x], 0x5410), __byte_perm(vw[2][x], vw[3][x], 0x5410));
+              mma<false>(acc[i + 1], pf, __byte_perm(vw[0][x], vw[1][x], 0x7632), __byte_perm(vw[2][x], vw[3][x], 0x7632));
+            }
           }
         }
       }

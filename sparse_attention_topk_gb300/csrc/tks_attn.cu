@@ -22,7 +22,7 @@ namespace {
 // 8), in the second the block's warps share one row's partials.
 // ---------------------------------------------------------------------------
 template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Params p, int blocks) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Params p) {
   constexpr int kVec = D / 32;
   __shared__ struct {
     int c0, c1, slot0;
@@ -37,31 +37,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
   grid_wait();
   grid_launch_dependents();
   if (first >= p.rows) return;
-  const Seq len = seq_of<SEL>(p, seq);
-  const int tiles = tiles_of<TK>(len.len);
-  if (warp == 0) {
-    unsigned tiles0;
-    const Split sp = make_split<SEL, TK>(p, blocks, tiles0);
-    if (sp.share) {
-      if (lane == 0) {
-        span.c0 = blockIdx.x * sp.share;
-        span.c1 = span.c0 + (int)min(sp.share, (unsigned)tiles) - 1;
-        span.slot0 = 0;
-      }
-    } else {
-      long long before = 0;  // tiles of a unit of each sequence before this one
-      if (!SEL) {
-        before = lane < seq ? (long long)tiles0 : 0;
-        for (int s = lane + 32; s < seq; s += 32) before += tiles_of<TK>(seq_of<SEL>(p, s).len);
+  const Split sp = SEL ? p.split : *p.plan;
+  const int tiles = tiles_of<TK>(seq_of<SEL>(p, seq).len);
+  if (sp.share) {
+    if (threadIdx.x == 0) {
+      span.c0 = blockIdx.x * sp.share;
+      span.c1 = span.c0 + (int)min(sp.share, (unsigned)tiles) - 1;
+      span.slot0 = 0;
+    }
+  } else if (warp == 0) {
+    long long before = 0;  // tiles of a unit of each sequence before this one
+    if (!SEL) {
+      for (int s = lane; s < seq; s += 32) before += tiles_of<TK>(seq_of<SEL>(p, s).len);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-      }
-      if (lane == 0) {
-        const long long w0 = (SEL ? (long long)tiles * seq : before) * per + (long long)in * tiles;
-        span.c0 = sp.block_of(w0);
-        span.c1 = sp.block_of(w0 + tiles - 1);  // (those between have tiles, too)
-        span.slot0 = sp.start(span.c0) != w0 ? 1 : 0;
-      }
+      for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    if (lane == 0) {
+      const long long w0 = (SEL ? (long long)tiles * seq : before) * per + (long long)in * tiles;
+      span.c0 = sp.block_of(w0);
+      span.c1 = sp.block_of(w0 + tiles - 1);  // (those between have tiles, too)
+      span.slot0 = sp.start(span.c0) != w0 ? 1 : 0;
     }
   }
   __syncthreads();
@@ -105,7 +100,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ Pa
 }
 
 template <int ROWS, int D, int TK, bool SEL, int PER_BLOCK>
-cudaError_t combine(const Params& p, int blocks, cudaStream_t stream) {
+cudaError_t combine(const Params& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   const int rows = p.rows < ROWS ? p.rows : ROWS;
   cfg.gridDim = dim3((unsigned)(p.seqs * p.kv_heads * p.row_tiles), (unsigned)((rows + PER_BLOCK - 1) / PER_BLOCK));
@@ -116,7 +111,7 @@ cudaError_t combine(const Params& p, int blocks, cudaStream_t stream) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<ROWS, D, TK, SEL, PER_BLOCK>, p, blocks);
+  return cudaLaunchKernelEx(&cfg, combine_kernel<ROWS, D, TK, SEL, PER_BLOCK>, p);
 }
 
 template <int ROWS, int TK>
@@ -124,11 +119,11 @@ cudaError_t launch_combine(const Params& p, int head_dim, bool selected, int blo
   // many partials for a unit, or few
   const bool many = (long long)p.seqs * p.kv_heads * p.row_tiles * 8 < blocks;
   if (head_dim == 64) {
-    if (selected) return many ? combine<ROWS, 64, TK, true, 1>(p, blocks, s) : combine<ROWS, 64, TK, true, 8>(p, blocks, s);
-    return many ? combine<ROWS, 64, TK, false, 1>(p, blocks, s) : combine<ROWS, 64, TK, false, 8>(p, blocks, s);
+    if (selected) return many ? combine<ROWS, 64, TK, true, 1>(p, s) : combine<ROWS, 64, TK, true, 8>(p, s);
+    return many ? combine<ROWS, 64, TK, false, 1>(p, s) : combine<ROWS, 64, TK, false, 8>(p, s);
   }
-  if (selected) return many ? combine<ROWS, 128, TK, true, 1>(p, blocks, s) : combine<ROWS, 128, TK, true, 8>(p, blocks, s);
-  return many ? combine<ROWS, 128, TK, false, 1>(p, blocks, s) : combine<ROWS, 128, TK, false, 8>(p, blocks, s);
+  if (selected) return many ? combine<ROWS, 128, TK, true, 1>(p, s) : combine<ROWS, 128, TK, true, 8>(p, s);
+  return many ? combine<ROWS, 128, TK, false, 1>(p, s) : combine<ROWS, 128, TK, false, 8>(p, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -139,10 +134,10 @@ struct Device {
   bool ok = false;
 };
 struct Workspace {
-  unsigned char* ptr = nullptr;  // status word (256 bytes), then partial slots
+  unsigned char* ptr = nullptr;  // status word, the last call's split, then (at 256 bytes) partial slots
 };
 
-constexpr size_t kHeaderBytes = 256;
+constexpr size_t kPlanOffset = 64, kHeaderBytes = 256;
 
 std::mutex g_mu;
 std::map<int, Device> g_dev;
@@ -294,12 +289,16 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   if ((keys / tile_keys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
   const long long units = (long long)p.seqs * p.kv_heads * p.row_tiles;
   if (units > INT32_MAX) return TKS_E_TOO_LARGE;
+  const int grid = few ? d.sms * kRowsBlocksPerSm : d.sms;
+  p.plan = reinterpret_cast<Split*>(ws.ptr + kPlanOffset);
+  if (selected) {
+    const long long tiles = std::max(1, (p.k_sel + tile_keys - 1) / tile_keys);
+    p.split.set(units * tiles, (unsigned)tiles, units, grid);
+  }
   if (few) {
-    const int grid = d.sms * kRowsBlocksPerSm;
     e = launch_rows(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
   } else {
-    const int grid = d.sms;
     e = launch_tiles(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);
   }

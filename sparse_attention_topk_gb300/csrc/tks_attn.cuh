@@ -100,8 +100,9 @@ __device__ __forceinline__ int capacity(const Params& p) {
   return room > kMaxPositions ? kMaxPositions : (int)room;
 }
 
+// (lengths out of range are reported by the warps that read all of them: make_split)
 template <bool SEL>
-__device__ __forceinline__ Seq seq_of(const Params& p, int s) {
+__device__ __forceinline__ Seq seq_of(const Params& p, int s, bool* bad = nullptr) {
   Seq q;
   if (SEL) {
     q.ctx = p.k_sel;
@@ -110,20 +111,19 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int s) {
     return q;
   }
   const int cap = capacity(p);
-  const int c = p.ctx_len[s], d = p.draft_len ? p.draft_len[s] : p.tokens;
+  const int c = __ldg(p.ctx_len + s), d = p.draft_len ? __ldg(p.draft_len + s) : p.tokens;
   q.ctx = min(max(c, 0), cap);
   q.drafts = min(min(max(d, 0), p.tokens), cap - q.ctx);
   q.len = q.ctx + q.drafts;
-  if (q.ctx != c || q.drafts != d) report(p.status, kStatRowLenBit);
+  if (bad) *bad |= q.ctx != c || q.drafts != d;
   return q;
 }
 
-// The number of positions that a list's entries may name.
-__device__ __forceinline__ int kv_limit(const Params& p, int b) {
-  const int cap = capacity(p);
-  if (!p.kv_len) return cap;
-  const int n = p.kv_len[b], r = min(max(n, 0), cap);
-  if (r != n) report(p.status, kStatRowLenBit);
+// The number of positions that a list's entries may name; `given`: kv_len[b], or INT_MAX.
+__device__ __forceinline__ int kv_given(const Params& p, int b) { return p.kv_len ? __ldg(p.kv_len + b) : 0x7fffffff; }
+__device__ __forceinline__ int kv_limit(const Params& p, int given) {
+  const int r = min(max(given, 0), capacity(p));
+  if (r != given && p.kv_len) report(p.status, kStatRowLenBit);
   return r;
 }
 
@@ -133,61 +133,40 @@ __device__ __forceinline__ int tiles_of(int len) {
   return len <= TK ? 1 : (int)(((unsigned)len + TK - 1) / TK);
 }
 
-constexpr int kSegmentTiles = 6;
-
-// How W tiles are split over G blocks.
-struct Split {
-  long long W;
-  unsigned share;  // blocks of a unit (even shares), or 0 (one run)
-  unsigned q, r;   // one run: tiles of a block, q or, for the first r blocks, q + 1
-
-  __device__ __forceinline__ void set(long long w, unsigned longest, long long units, int G) {
-    W = w;
-    if (w >> 31) {
-      q = (unsigned)(w / G);
-      r = (unsigned)(w % G);
-    } else {
-      q = (unsigned)w / (unsigned)G;
-      r = (unsigned)w - q * (unsigned)G;
-    }
-    share = 0;
-    if (units <= G) {
-      const unsigned s = (unsigned)G / (unsigned)units;
-      if ((longest + s - 1) / s <= q + (r > 0) + kSegmentTiles) share = s;
-    }
-  }
-  __device__ __forceinline__ long long start(int c) const { return (long long)c * q + min((unsigned)c, r); }
-  // One run: the block that holds tile w.
-  __device__ __forceinline__ int block_of(long long w) const {
-    const long long more = (long long)r * (q + 1);
-    if (w < more) return W >> 31 ? (int)(w / (q + 1)) : (int)((unsigned)w / (q + 1));
-    return (int)r + (W >> 31 ? (int)((w - more) / q) : (int)((unsigned)(w - more) / q));
-  }
-};
-
-// The split, for all lanes of a warp; `tiles0`: the tiles of a unit of sequence `lane`.
+// The split, for all lanes of a warp, and the lengths of sequence `lane`. Selected: the host has made
+// it. Trees: it depends on the lengths, and block 0 leaves it for the kernel that joins.
 template <bool SEL, int TK>
-__device__ __forceinline__ Split make_split(const Params& p, int blocks, unsigned& tiles0) {
+__device__ __forceinline__ Split make_split(const Params& p, Seq& mine) {
+  if (SEL) {
+    mine = seq_of<SEL>(p, 0);
+    return p.split;
+  }
   const int lane = threadIdx.x & 31;
   const unsigned per = (unsigned)(p.kv_heads * p.row_tiles);
-  Split split;
-  if (SEL) {
-    tiles0 = (unsigned)tiles_of<TK>(p.k_sel);
-    split.set((long long)per * tiles0 * p.seqs, tiles0, (long long)per * p.seqs, blocks);
-    return split;
-  }
-  tiles0 = lane < p.seqs ? (unsigned)tiles_of<TK>(seq_of<SEL>(p, lane).len) : 0;
-  long long sum = tiles0;
-  unsigned longest = tiles0;
+  bool bad = false;
+  mine.ctx = mine.drafts = mine.len = 0;
+  if (lane < p.seqs) mine = seq_of<SEL>(p, lane, &bad);
+  unsigned longest = lane < p.seqs ? (unsigned)tiles_of<TK>(mine.len) : 0;
+  long long sum = longest;
   for (int s = lane + 32; s < p.seqs; s += 32) {
-    const unsigned t = (unsigned)tiles_of<TK>(seq_of<SEL>(p, s).len);
+    const unsigned t = (unsigned)tiles_of<TK>(seq_of<SEL>(p, s, &bad).len);
     sum += t;
     longest = max(longest, t);
   }
-  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (p.seqs > 1) {
+    longest = __reduce_max_sync(0xffffffffu, longest);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  split.set(sum * per, longest, (long long)per * p.seqs, blocks);
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  } else {
+    longest = __shfl_sync(0xffffffffu, longest, 0);
+    sum = longest;
+  }
+  Split split;
+  split.set(sum * per, longest, (long long)per * p.seqs, gridDim.x);
+  if (blockIdx.x == 0) {
+    if (bad) report(p.status, kStatRowLenBit);
+    if (lane == 0) *p.plan = split;
+  }
   return split;
 }
 
@@ -196,27 +175,37 @@ struct Start {
   int seq;        // the sequence of the block's first tile
   unsigned rel;   // the tile's number among the sequence's (they fit: the host checks)
   unsigned left;  // the block's tiles
+  Seq len;        // of that sequence
 };
 
 template <bool SEL, int TK>
 __device__ __forceinline__ void find_start(const Params& p, Start* st) {
   const int lane = threadIdx.x & 31, block = blockIdx.x;
   const unsigned per = (unsigned)(p.kv_heads * p.row_tiles);
-  unsigned tiles0;
-  const Split split = make_split<SEL, TK>(p, gridDim.x, tiles0);
+  Seq mine;
+  const Split split = make_split<SEL, TK>(p, mine);
   if (split.share) {
+    const unsigned unit = (unsigned)block / split.share, i = (unsigned)block - unit * split.share;
+    const unsigned seq = unit / per, in = unit - seq * per;
+    Seq len = mine;
+    if (!SEL) {
+      if (seq < 32) {
+        len.ctx = __shfl_sync(0xffffffffu, mine.ctx, (int)seq);
+        len.drafts = __shfl_sync(0xffffffffu, mine.drafts, (int)seq);
+        len.len = len.ctx + len.drafts;
+      } else if (seq < (unsigned)p.seqs) {
+        len = seq_of<SEL>(p, (int)seq);
+      }
+    }
     if (lane == 0) {
-      const unsigned unit = (unsigned)block / split.share, i = (unsigned)block - unit * split.share;
-      const unsigned seq = unit / per, in = unit - seq * per;
       st->seq = (int)seq;
       st->rel = st->left = 0;
-      if (seq < (unsigned)p.seqs) {
-        const unsigned tiles = (unsigned)tiles_of<TK>(seq_of<SEL>(p, (int)seq).len), n = min(split.share, tiles);
-        if (i < n) {
-          const unsigned tq = tiles / n, tr = tiles - tq * n;
-          st->rel = in * tiles + i * tq + min(i, tr);
-          st->left = tq + (i < tr ? 1 : 0);
-        }
+      st->len = len;
+      const unsigned tiles = (unsigned)tiles_of<TK>(len.len), n = min(split.share, tiles);
+      if (seq < (unsigned)p.seqs && i < n) {
+        const unsigned tq = tiles / n, tr = tiles - tq * n;
+        st->rel = in * tiles + i * tq + min(i, tr);
+        st->left = tq + (i < tr ? 1 : 0);
       }
     }
     return;
@@ -225,18 +214,20 @@ __device__ __forceinline__ void find_start(const Params& p, Start* st) {
   const unsigned left = split.q + ((unsigned)block < split.r ? 1 : 0);
   if (SEL) {
     if (lane == 0) {
-      const unsigned each = per * tiles0;
+      const unsigned each = per * (unsigned)tiles_of<TK>(p.k_sel);
       st->seq = w >> 31 ? (int)(w / each) : (int)((unsigned)w / each);
       st->rel = (unsigned)(w - (long long)st->seq * each);
       st->left = left;
+      st->len = mine;
     }
     return;
   }
   long long base = 0;
   for (int s0 = 0; s0 < p.seqs; s0 += 32) {
     const int s = s0 + lane;
-    const long long mine = (long long)per * (s0 == 0 ? (int)tiles0 : s < p.seqs ? tiles_of<TK>(seq_of<SEL>(p, s).len) : 0);
-    long long end = mine;
+    if (s0 > 0 && s < p.seqs) mine = seq_of<SEL>(p, s);
+    const long long tiles = s < p.seqs ? (long long)per * tiles_of<TK>(mine.len) : 0;
+    long long end = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, end, o);
@@ -247,8 +238,9 @@ __device__ __forceinline__ void find_start(const Params& p, Start* st) {
     if (m) {
       if (lane == __ffs(m) - 1) {
         st->seq = s;
-        st->rel = (unsigned)(w - (end - mine));
+        st->rel = (unsigned)(w - (end - tiles));
         st->left = left;
+        st->len = mine;
       }
       return;
     }
@@ -272,22 +264,24 @@ template <bool SEL, int TK>
 struct Segments {
   unsigned left, rel;
   int seq;
+  Seq len0;  // of the first segment's sequence
   bool first;
   __device__ __forceinline__ void begin(const Start& st) {
     left = st.left;
     rel = st.rel;
     seq = st.seq;
+    len0 = st.len;
     first = true;
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
     if (left == 0) return false;
-    s.len = seq_of<SEL>(p, seq);
+    s.len = first ? len0 : seq_of<SEL>(p, seq);
     const unsigned tiles = (unsigned)tiles_of<TK>(s.len.len);
     const unsigned unit = rel / tiles, t0 = rel - unit * tiles, n = min(tiles - t0, left);
     s.seq = seq;
     s.b = SEL ? seq / p.tokens : seq;
-    s.head = (int)(unit / (unsigned)p.row_tiles);
-    s.row_tile = (int)(unit - (unsigned)s.head * p.row_tiles);
+    s.head = TK == kRowsKeys ? (int)unit : (int)(unit / (unsigned)p.row_tiles);  // (few rows: one tile)
+    s.row_tile = TK == kRowsKeys ? 0 : (int)(unit - (unsigned)s.head * p.row_tiles);
     s.t0 = (int)t0;
     s.t1 = (int)(t0 + n);
     s.tiles = (int)tiles;
@@ -308,6 +302,20 @@ __device__ __forceinline__ bool sees_draft(const Params& p, int b, int t, int j)
   if (!p.tree) return j <= t;
   const int w = p.tree[((long long)b * p.tokens + t) * p.tree_words + (j >> 5)];
   return (w >> (j & 31)) & 1;
+}
+
+// 32 bits of row t's view of the drafted tokens j0 .. j0 + 31 (those before 0 are context: seen).
+__device__ __forceinline__ unsigned draft_bits(const Params& p, int b, int t, int j0) {
+  if (j0 + 31 < 0) return ~0u;
+  if (!p.tree) {
+    const int n = t - j0;  // the last one seen
+    return n >= 31 ? ~0u : n < 0 ? 0u : (2u << n) - 1u;
+  }
+  const int32_t* row = p.tree + ((long long)b * p.tokens + t) * p.tree_words;
+  auto word = [&](int w) -> unsigned { return w < p.tree_words ? (unsigned)row[w] : 0u; };
+  if (j0 < 0) return (word(0) << -j0) | ((1u << -j0) - 1u);
+  const int w = j0 >> 5, sh = j0 & 31;
+  return sh ? (word(w) >> sh) | (word(w + 1) << (32 - sh)) : word(w);
 }
 
 // The place of query row R of a unit among the rows of out and lse.

@@ -35,6 +35,39 @@ struct CacheParams {
 cudaError_t launch_cache_write(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s);
 cudaError_t launch_cache_read(const CacheParams& p, int head_dim, bool i8, bool f32, cudaStream_t s);
 
+// A segment costs a block as much as this many tiles, beside its own.
+constexpr int kSegmentTiles = 6;
+
+// How W tiles are split over G blocks.
+struct Split {
+  long long W;
+  unsigned share;  // blocks of a unit (even shares), or 0 (one run)
+  unsigned q, r;   // one run: tiles of a block, q or, for the first r blocks, q + 1
+
+  __host__ __device__ void set(long long w, unsigned longest, long long units, int G) {
+    W = w;
+    if (w >> 31) {
+      q = (unsigned)(w / G);
+      r = (unsigned)(w % G);
+    } else {
+      q = (unsigned)w / (unsigned)G;
+      r = (unsigned)w - q * (unsigned)G;
+    }
+    share = 0;
+    if (units <= G) {
+      const unsigned s = (unsigned)G / (unsigned)units;
+      if ((longest + s - 1) / s <= q + (r > 0) + kSegmentTiles) share = s;
+    }
+  }
+  __host__ __device__ long long start(int c) const { return (long long)c * q + ((unsigned)c < r ? (unsigned)c : r); }
+  // One run: the block that holds tile w.
+  __host__ __device__ int block_of(long long w) const {
+    const long long more = (long long)r * (q + 1);
+    if (w < more) return W >> 31 ? (int)(w / (q + 1)) : (int)((unsigned)w / (q + 1));
+    return (int)r + (W >> 31 ? (int)((w - more) / q) : (int)((unsigned)(w - more) / q));
+  }
+};
+
 // Arguments of the attention kernels.
 struct Params {
   const unsigned char *k, *v;
@@ -59,6 +92,8 @@ struct Params {
   int row_tiles;
   unsigned* status;
   float* parts;
+  Split* plan;  // trees: the split, for the kernel that joins
+  Split split;  // selected: the split
   long long spin_limit_ns;
   int test_skip_arrive;
 };

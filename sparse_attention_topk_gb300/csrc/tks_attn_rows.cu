@@ -22,9 +22,11 @@
 // Layout.  A block is four warps; each takes every fourth chunk of the block's
 // segment (32 keys of int8, 16 of bfloat16: 8 KB), keeps its own maximum, sum and
 // output in registers and its own ring of cp.async stages in shared memory, so
-// warps meet only at a segment's end.  Key positions are looked up (list, page
-// table) one and two chunks ahead of their copies; a chunk that lies in one page
-// takes one lookup.  The order of the 16-wide k index inside a
+// warps meet only at a segment's end.  Where the keys lie is looked up (list, page
+// table) for 1024 of them at once, the block's threads side by side, before their
+// copies start (one chunk ahead, it bound a gather of rows: 64 tokens over 2048
+// selected positions of bfloat16, 35.0 us against GATHER_US); chunks that lie in one
+// page each take one lookup, a chunk ahead.  The order of the 16-wide k index inside a
 // product is free as long as both operands agree, so a lane takes whole
 // 16-byte pieces of its key's row for the first product and of its four
 // value rows for the second; bytes are paired by byte permutes, and the rows'
@@ -56,7 +58,8 @@ struct Shape {
   static constexpr int kQs = D / 16 * 32 * 16;         // query fragments, behind the rings
   static constexpr int kConst = I8 ? kWarps * 32 * 16 : 0;  // and each warp's scales as they are used
   static constexpr int kRings = kWarps * kStages * kStage;
-  static constexpr int kSmem = kRings + kQs + kConst;
+  static constexpr int kSlots = 1024 * 4;              // and where keys lie
+  static constexpr int kSmem = kRings + kQs + kConst + kSlots;
   static_assert(kRings >= kWarps * (16 * D * 4 + 16 * 8), "the merge fits the ring");
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
@@ -111,6 +114,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   unsigned char* ring = smem + warp * S::kStages * S::kStage;
   uint4* qs = reinterpret_cast<uint4*>(smem + S::kRings);
   float4* consts = reinterpret_cast<float4*>(smem + S::kRings + S::kQs) + warp * 32;
+  int* slots = reinterpret_cast<int*>(smem + S::kRings + S::kQs + S::kConst);
+  constexpr int kSlots = S::kSlots / 4;
   // the lane's piece of a row, its first row, and where that goes in a stage
   constexpr int kPer = 32 / S::kPieces;  // rows that 32 lanes cover
   const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
@@ -133,35 +138,41 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     const int seq = sg.seq, head = sg.head, row_tile = sg.row_tile, b = sg.b, t0 = sg.t0, t1 = sg.t1;
     const int k_beg = t0 * kRowsKeys;  // tiles * kRowsKeys stays below 2^31: len does, rounded up once
     const int k_end = (int)min((long long)len.len, (long long)t1 * kRowsKeys);
-    const int chunks = (k_end - k_beg + kChunk - 1) / kChunk;
-    const int iters = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     const int32_t* table = p.table + b * p.table_stride;
     const int32_t* list = SEL ? p.indices + (long long)seq * p.k_sel : nullptr;
-    const int limit = SEL ? kv_limit(p, b) : 0;
+    const int given = SEL ? kv_given(p, b) : 0;
     const unsigned char* kb = p.k + head * p.head_b;
     const unsigned char* vb = p.v + head * p.head_b;
 
-    // Position of this lane's key (lane % kChunk) of the warp's chunk `it`, or -1; where chunks lie
-    // in one page, of the chunk's first key.
-    auto position = [&](int it) -> int {
-      const long long j = (long long)k_beg + ((long long)it * kWarps + warp) * kChunk + (paged ? 0 : lane % kChunk);
-      if (j >= k_end) return -1;
-      if (!SEL) return (int)j;
-      const int idx = list[j];
-      if (idx >= limit) report(p.status, kStatIndexBit);
-      return idx < limit ? idx : -1;
-    };
-    auto page = [&](int pos) -> int { return pos < 0 ? -1 : table[pos >> p.page_shift]; };
-    // Starts the copies of chunk `it` into stage `st`, given its lane's position and page.
-    auto issue = [&](int it, int st, int pos, int pg) {
-      if (it < iters) {
-        const bool ok = pos >= 0 && (unsigned)pg < (unsigned)p.pages;
-        if (pos >= 0 && !ok) report(p.status, kStatIndexBit);
-        const int in_page = pos & ((1 << p.page_shift) - 1);
+    // Query fragments: rows n and n + 8; for product step (h, j) of a lane,
+    // elements kE * (c + 4h) + 4j + {0,1} and {2,3}.
+    const int rows_left = p.rows - row_tile * kRowsTile;
+    float fac = p.scale_log2;
+    uint32_t qf[D / 16][4];
+    const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
+    const __nv_bfloat16* q0 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in0 ? n : 0));
+    const __nv_bfloat16* q1 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in1 ? n + 8 : 0));
+#pragma unroll
+    for (int h = 0; h < S::kKH; ++h)
+#pragma unroll
+      for (int j = 0; j < S::kE / 4; ++j) {
+        const int d = S::kE * (c + 4 * h) + 4 * j, s = h * (S::kE / 4) + j;
+        const uint2 a = in0 ? *reinterpret_cast<const uint2*>(q0 + d) : make_uint2(0u, 0u);
+        const uint2 e = in1 ? *reinterpret_cast<const uint2*>(q1 + d) : make_uint2(0u, 0u);
+        qf[s][0] = a.x; qf[s][1] = e.x; qf[s][2] = a.y; qf[s][3] = e.y;
+      }
+
+    // The page of the warp's chunk that starts at key j.
+    auto page = [&](int j) -> int { return paged && j < k_end ? table[j >> p.page_shift] : -1; };
+    // Starts the copies of the chunk at key j into stage `st`; pg: its page; beg: the key of slots[0].
+    auto issue = [&](int j, int st, int pg, int beg, int end) {
+      if (j < end) {
         const uint32_t to = st * S::kStage;
         unsigned valid;
         if (paged) {
-          const int n_valid = ok ? min(kChunk, k_end - pos) : 0;
+          const bool ok = (unsigned)pg < (unsigned)p.pages;
+          if (!ok) report(p.status, kStatIndexBit);
+          const int n_valid = ok ? min(kChunk, end - j) : 0, in_page = j & ((1 << p.page_shift) - 1);
           const long long off = ok ? pg * p.page_b + in_page * p.token_b : 0;
           const unsigned char* ks = kb + off + row0 * p.token_b + piece * 16;
           const unsigned char* vs = vb + off + row0 * p.token_b + piece * 16;
@@ -180,64 +191,39 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
           }
           valid = n_valid >= 32 ? ~0u : (1u << n_valid) - 1u;
         } else {
-          const long long off = ok ? pg * p.page_b + in_page * p.token_b : -1;
-          valid = __ballot_sync(0xffffffffu, ok) & (kChunk == 32 ? ~0u : (1u << (kChunk & 31)) - 1u);
+          const int* sl = slots + (j - beg);
+          const int mine = lane < kChunk ? sl[lane] : -1;
+          // all offsets before the first copy: the copies are not to be moved across
+          long long at[kChunk / kPer];
 #pragma unroll
           for (int i = 0; i < kChunk / kPer; ++i) {
-            const long long o = __shfl_sync(0xffffffffu, off, row0 + i * kPer);
-            const int bytes = o >= 0 ? 16 : 0;
-            const long long at = o >= 0 ? o + piece * 16 : 0;
-            cp16(k_dst + to + i * kPer * S::kRow, kb + at, bytes);
-            cp16(v_dst + to + i * kPer * S::kRow + ((v_piece ^ S::vsw(i * kPer)) << 4), vb + at, bytes);
+            const int slot = sl[row0 + i * kPer];
+            at[i] = slot < 0 ? -1 : (slot >> p.page_shift) * p.page_b + (slot & ((1 << p.page_shift) - 1)) * p.token_b + piece * 16;
           }
-          if (I8) {
-            const long long row = ok ? (((long long)pg << p.page_shift) + in_page) * p.kv_heads + head : 0;
-            cp8(smem_addr(ring) + to + S::kOps + lane * 8, p.scales + row, ok ? 8 : 0);
+#pragma unroll
+          for (int i = 0; i < kChunk / kPer; ++i) {
+            const int bytes = at[i] >= 0 ? 16 : 0;
+            const long long o = at[i] >= 0 ? at[i] : 0;
+            cp16(k_dst + to + i * kPer * S::kRow, kb + o, bytes);
+            cp16(v_dst + to + i * kPer * S::kRow + ((v_piece ^ S::vsw(i * kPer)) << 4), vb + o, bytes);
           }
+          if (I8)
+            cp8(smem_addr(ring) + to + S::kOps + lane * 8, p.scales + (mine >= 0 ? (long long)mine * p.kv_heads + head : 0), mine >= 0 ? 8 : 0);
+          valid = __ballot_sync(0xffffffffu, mine >= 0);
         }
         if (lane == 0) *reinterpret_cast<unsigned*>(ring + to + S::kOps + S::kScales) = valid;
       }
       cp_commit();
     };
+    constexpr int kAhead = S::kStages - 1, kStep = kWarps * kChunk;
 
-    // ---- first copies; then the queries, while they are under way -----------
-    constexpr int kAhead = S::kStages - 1;
-    int pos_n, pg_n, pos_nn = -1;
-    {
-      int ps[kAhead], pg[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) ps[i] = position(i);
-      pos_n = position(kAhead);
-      if (SEL) pos_nn = position(kAhead + 1);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) pg[i] = page(ps[i]);
-      pg_n = page(pos_n);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) issue(i, i, ps[i], pg[i]);
-    }
-
-    // Query fragments: rows n and n + 8; for product step (h, j) of a lane,
-    // elements kE * (c + 4h) + 4j + {0,1} and {2,3}.
-    const int rows_left = p.rows - row_tile * kRowsTile;
-    float fac = p.scale_log2;
-    {
-      uint32_t qf[D / 16][4];
-      const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
-      const __nv_bfloat16* q0 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in0 ? n : 0));
-      const __nv_bfloat16* q1 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in1 ? n + 8 : 0));
-      float top = 0.f;
-#pragma unroll
-      for (int h = 0; h < S::kKH; ++h)
-#pragma unroll
-        for (int j = 0; j < S::kE / 4; ++j) {
-          const int d = S::kE * (c + 4 * h) + 4 * j, s = h * (S::kE / 4) + j;
-          const uint2 a = in0 ? *reinterpret_cast<const uint2*>(q0 + d) : make_uint2(0u, 0u);
-          const uint2 e = in1 ? *reinterpret_cast<const uint2*>(q1 + d) : make_uint2(0u, 0u);
-          qf[s][0] = a.x; qf[s][1] = e.x; qf[s][2] = a.y; qf[s][3] = e.y;
-          if (I8)
-            top = finite_max(finite_max(finite_max(finite_max(top, a.x), a.y), e.x), e.y);
-        }
+    auto put_queries = [&] {
       if (I8) {
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) top = finite_max(top, qf[s][r]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         // the largest finite magnitude goes to [2^14, 2^15): halves keep 11 bits
@@ -258,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       for (int s = 0; s < D / 16; ++s)
         if ((s & 3) == warp) qs[s * 32 + lane] = make_uint4(qf[s][0], qf[s][1], qf[s][2], qf[s][3]);
       __syncthreads();
-    }
+    };
 
     float acc[D / 8][4];
 #pragma unroll
@@ -268,22 +254,53 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     bool poisoned = false;  // a draft's value held an infinity or NaN (bfloat16)
 
-    // ---- the warp's chunks ------------------------------------------------
+    // ---- the warp's chunks: of the whole segment, or of the keys looked up at once ----
+    for (int beg = k_beg; beg < k_end; beg += paged ? k_end - k_beg : kSlots) {
+    const int end = paged ? k_end : (int)min((long long)k_end, (long long)beg + kSlots);
+    if (!paged) {
+      // all list entries, then all pages: two waits, not one for each key
+      constexpr int kMine = kSlots / kThreads;
+      int pos[kMine], pg[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int j = beg + threadIdx.x + i * kThreads;
+        pos[i] = j >= end ? -1 : SEL ? __ldg(list + j) : j;
+      }
+      bool bad = false;
+      const int limit = SEL ? kv_limit(p, given) : 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        bad |= SEL && pos[i] >= limit;
+        if (SEL && pos[i] >= limit) pos[i] = -1;
+        pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
+      }
+      __syncthreads();  // the previous keys' copies have started
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const bool ok = pos[i] >= 0 && (unsigned)pg[i] < (unsigned)p.pages;
+        bad |= pos[i] >= 0 && !ok;
+        slots[threadIdx.x + i * kThreads] = ok ? (int)(((unsigned)pg[i] << p.page_shift) + (pos[i] & ((1 << p.page_shift) - 1))) : -1;
+      }
+      if (bad) report(p.status, kStatIndexBit);
+      __syncthreads();
+    }
+    int pg_n;
+    {
+      int pg[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) pg[i] = page(beg + warp * kChunk + i * kStep);
+      pg_n = page(beg + warp * kChunk + kAhead * kStep);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) issue(beg + warp * kChunk + i * kStep, i, pg[i], beg, end);
+    }
+    if (beg == k_beg) put_queries();
     int stage = 0, ahead = kAhead;  // of this chunk, and of the one whose copies start
-    for (int it = 0; it < iters; ++it) {
+    for (int j0 = beg + warp * kChunk; j0 < end; j0 += kStep) {  // (j0 + (kAhead + 1) * kStep stays below 2^31: kMaxPositions)
       cp_wait<kAhead - 1>();
       __syncwarp();
-      {  // the next copies go into the stage that the previous chunk has left
-        issue(it + kAhead, ahead, pos_n, pg_n);
-        if (SEL) {
-          pos_n = pos_nn;
-          pg_n = page(pos_n);
-          pos_nn = position(it + kAhead + 2);
-        } else {
-          pos_n = position(it + kAhead + 1);
-          pg_n = page(pos_n);
-        }
-      }
+      // the next copies go into the stage that the previous chunk has left
+      issue(j0 + kAhead * kStep, ahead, pg_n, beg, end);
+      pg_n = page(j0 + (kAhead + 1) * kStep);
       const unsigned char* st = ring + stage * S::kStage;
       ahead = stage;
       stage = stage + 1 == S::kStages ? 0 : stage + 1;
@@ -344,23 +361,20 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[t][e] *= fac;
       }
-      const int j0 = k_beg + (it * kWarps + warp) * kChunk;  // the chunk's first key
       const bool drafts = !SEL && j0 + kChunk > len.ctx;
       if (valid != (kChunk == 32 ? ~0u : 0xffffu) || drafts) {
-        const int R = row_tile * kRowsTile + n;
-        const int ta = min(R / p.group, p.tokens - 1), tc = min((R + 8) / p.group, p.tokens - 1);
+        unsigned seen0 = valid, seen1 = valid;  // the keys that rows n and n + 8 see
+        if (drafts) {
+          const int R = row_tile * kRowsTile + n;
+          seen0 &= draft_bits(p, b, min(R / p.group, p.tokens - 1), j0 - len.ctx);
+          seen1 &= draft_bits(p, b, min((R + 8) / p.group, p.tokens - 1), j0 - len.ctx);
+        }
 #pragma unroll
         for (int t = 0; t < kNT; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int key = 8 * t + 2 * c + e, j = j0 + key - len.ctx;
-            bool seen0 = (valid >> key) & 1u, seen1 = seen0;
-            if (drafts && j >= 0 && j < len.drafts) {
-              seen0 = seen0 && sees_draft(p, b, ta, j);
-              seen1 = seen1 && sees_draft(p, b, tc, j);
-            }
-            if (!seen0) s[t][e] = -INFINITY;
-            if (!seen1) s[t][2 + e] = -INFINITY;
+            if (!(seen0 >> (8 * t + 2 * c + e) & 1u)) s[t][e] = -INFINITY;
+            if (!(seen1 >> (8 * t + 2 * c + e) & 1u)) s[t][2 + e] = -INFINITY;
           }
       }
 
@@ -455,12 +469,12 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       __syncwarp();  // all lanes have read the stage before it is filled again
     }
     cp_wait<0>();
+    }
 
     // Infinities and NaNs of drafted tokens' values reach only the rows that
     // attend to them (rare: the product above took them as zeros).
     if (!I8 && !SEL && poisoned) {
-      for (int it = 0; it < iters; ++it) {
-        const int j0 = k_beg + (it * kWarps + warp) * kChunk;
+      for (int j0 = k_beg + warp * kChunk; j0 < k_end; j0 += kStep) {
         for (int j = max(j0, len.ctx); j < min(j0 + kChunk, k_end); ++j) {
           const int pg = table[j >> p.page_shift];
           if ((unsigned)pg >= (unsigned)p.pages) continue;

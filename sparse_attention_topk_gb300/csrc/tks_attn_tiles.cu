@@ -251,20 +251,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// 32 bits of row t's view of the drafted tokens j0 .. j0 + 31 (those before 0 are context: seen).
-__device__ __forceinline__ unsigned draft_bits(const Params& p, int b, int t, int j0) {
-  if (j0 + 31 < 0) return ~0u;
-  if (!p.tree) {
-    const int n = t - j0;  // the last one seen
-    return n >= 31 ? ~0u : n < 0 ? 0u : (2u << n) - 1u;
-  }
-  const int32_t* row = p.tree + ((long long)b * p.tokens + t) * p.tree_words;
-  auto word = [&](int w) -> unsigned { return w < p.tree_words ? (unsigned)row[w] : 0u; };
-  if (j0 < 0) return (word(0) << -j0) | ((1u << -j0) - 1u);
-  const int w = j0 >> 5, sh = j0 & 31;
-  return sh ? (word(w) >> sh) | (word(w + 1) << (32 - sh)) : word(w);
-}
-
 // ---------------------------------------------------------------------------
 // Roles
 // ---------------------------------------------------------------------------
@@ -280,7 +266,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
   while (it.next(p, s)) {
     const int32_t* table = p.table + s.b * p.table_stride;
     const int32_t* list = SEL ? p.indices + (long long)s.seq * p.k_sel : nullptr;
-    const int limit = SEL ? kv_limit(p, s.b) : 0;
+    const int limit = SEL ? kv_limit(p, kv_given(p, s.b)) : 0;
     const int end = (int)min((long long)s.len.len, (long long)s.t1 * kKeys);
     auto entry = [&](int t, int i) -> int {  // key i of tile t: its list entry, or its position
       const int j = t * kKeys + i;

@@ -101,12 +101,14 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-template <int D, bool I8, bool SEL>
+// PAGED: every chunk lies in one page (positions in order, pages of at least a chunk).
+template <int D, bool I8, bool SEL, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, I8>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Start start;
   __shared__ float2 ml_s[kWarps][16];
+  __shared__ float top_s[kWarps];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;  // the lane's key, row or column, and its quarter
@@ -122,7 +124,6 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   const uint32_t k_dst = smem_addr(ring) + row0 * S::kRow + ((piece ^ S::ksw(row0)) << 4);
   const uint32_t v_dst = smem_addr(ring) + (kChunk + row0) * S::kRow;
   const int v_piece = piece ^ S::vsw(row0);  // (the swizzles of row0 and of i * kPer combine by XOR)
-  const bool paged = !SEL && (1 << p.page_shift) >= kChunk;
 
   grid_wait();
   grid_launch_dependents();
@@ -144,32 +145,33 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     const unsigned char* kb = p.k + head * p.head_b;
     const unsigned char* vb = p.v + head * p.head_b;
 
-    // Query fragments: rows n and n + 8; for product step (h, j) of a lane,
-    // elements kE * (c + 4h) + 4j + {0,1} and {2,3}.
+    // Query fragments: rows n and n + 8; for product step (h, j) of a lane, elements
+    // kE * (c + 4h) + 4j + {0,1} and {2,3}. All warps have the same rows, and each brings every
+    // fourth step.
+    constexpr int kMySteps = D / 16 / kWarps;
     const int rows_left = p.rows - row_tile * kRowsTile;
     float fac = p.scale_log2;
-    uint32_t qf[D / 16][4];
-    const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
-    const __nv_bfloat16* q0 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in0 ? n : 0));
-    const __nv_bfloat16* q1 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in1 ? n + 8 : 0));
+    uint2 qa[kMySteps], qe[kMySteps];
+    {
+      const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
+      const __nv_bfloat16* q0 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in0 ? n : 0));
+      const __nv_bfloat16* q1 = q_row<SEL>(p, seq, head, row_tile * kRowsTile + (in1 ? n + 8 : 0));
 #pragma unroll
-    for (int h = 0; h < S::kKH; ++h)
-#pragma unroll
-      for (int j = 0; j < S::kE / 4; ++j) {
-        const int d = S::kE * (c + 4 * h) + 4 * j, s = h * (S::kE / 4) + j;
-        const uint2 a = in0 ? *reinterpret_cast<const uint2*>(q0 + d) : make_uint2(0u, 0u);
-        const uint2 e = in1 ? *reinterpret_cast<const uint2*>(q1 + d) : make_uint2(0u, 0u);
-        qf[s][0] = a.x; qf[s][1] = e.x; qf[s][2] = a.y; qf[s][3] = e.y;
+      for (int i = 0; i < kMySteps; ++i) {
+        const int s = warp + i * kWarps, d = S::kE * (c + 4 * (s / (S::kE / 4))) + 4 * (s % (S::kE / 4));
+        qa[i] = in0 ? __ldg(reinterpret_cast<const uint2*>(q0 + d)) : make_uint2(0u, 0u);
+        qe[i] = in1 ? __ldg(reinterpret_cast<const uint2*>(q1 + d)) : make_uint2(0u, 0u);
       }
+    }
 
     // The page of the warp's chunk that starts at key j.
-    auto page = [&](int j) -> int { return paged && j < k_end ? table[j >> p.page_shift] : -1; };
+    auto page = [&](int j) -> int { return PAGED && j < k_end ? table[j >> p.page_shift] : -1; };
     // Starts the copies of the chunk at key j into stage `st`; pg: its page; beg: the key of slots[0].
     auto issue = [&](int j, int st, int pg, int beg, int end) {
       if (j < end) {
         const uint32_t to = st * S::kStage;
         unsigned valid;
-        if (paged) {
+        if (PAGED) {
           const bool ok = (unsigned)pg < (unsigned)p.pages;
           if (!ok) report(p.status, kStatIndexBit);
           const int n_valid = ok ? min(kChunk, end - j) : 0, in_page = j & ((1 << p.page_shift) - 1);
@@ -218,31 +220,30 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     constexpr int kAhead = S::kStages - 1, kStep = kWarps * kChunk;
 
     auto put_queries = [&] {
+      float up = 1.f;
       if (I8) {
         float top = 0.f;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) top = finite_max(top, qf[s][r]);
+        for (int i = 0; i < kMySteps; ++i)
+          top = finite_max(finite_max(finite_max(finite_max(top, qa[i].x), qa[i].y), qe[i].x), qe[i].y);
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) top_s[warp] = top;
+        __syncthreads();
+        top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
         // the largest finite magnitude goes to [2^14, 2^15): halves keep 11 bits
         // over 2^28 below it
         const int shift = top > 0.f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
-        const float up = __int_as_float((shift + 127) << 23);
+        up = __int_as_float((shift + 127) << 23);
         fac *= __int_as_float((127 - shift) << 23);
-#pragma unroll
-        for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float2 f = bf16_pair(qf[s][r]);
-            qf[s][r] = pack_half(f.x * up, f.y * up);
-          }
       }
-      // all warps have the same rows: each puts down a quarter of the steps
+      auto held = [&](uint32_t w) -> uint32_t {
+        const float2 f = bf16_pair(w);
+        return I8 ? pack_half(f.x * up, f.y * up) : w;
+      };
 #pragma unroll
-      for (int s = 0; s < D / 16; ++s)
-        if ((s & 3) == warp) qs[s * 32 + lane] = make_uint4(qf[s][0], qf[s][1], qf[s][2], qf[s][3]);
+      for (int i = 0; i < kMySteps; ++i)
+        qs[(warp + i * kWarps) * 32 + lane] = make_uint4(held(qa[i].x), held(qe[i].x), held(qa[i].y), held(qe[i].y));
       __syncthreads();
     };
 
@@ -255,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     bool poisoned = false;  // a draft's value held an infinity or NaN (bfloat16)
 
     // ---- the warp's chunks: of the whole segment, or of the keys looked up at once ----
-    for (int beg = k_beg; beg < k_end; beg += paged ? k_end - k_beg : kSlots) {
-    const int end = paged ? k_end : (int)min((long long)k_end, (long long)beg + kSlots);
-    if (!paged) {
+    for (int beg = k_beg; beg < k_end; beg += PAGED ? k_end - k_beg : kSlots) {
+    const int end = PAGED ? k_end : (int)min((long long)k_end, (long long)beg + kSlots);
+    if (!PAGED) {
       // all list entries, then all pages: two waits, not one for each key
       constexpr int kMine = kSlots / kThreads;
       int pos[kMine], pg[kMine];
@@ -284,15 +285,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       if (bad) report(p.status, kStatIndexBit);
       __syncthreads();
     }
-    int pg_n;
-    {
-      int pg[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) pg[i] = page(beg + warp * kChunk + i * kStep);
-      pg_n = page(beg + warp * kChunk + kAhead * kStep);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) issue(beg + warp * kChunk + i * kStep, i, pg[i], beg, end);
-    }
+    // the first chunks' pages, a lane each (loops that run once or twice are not unrolled: a block
+    // runs most of this code once, and fetches its instructions first)
+    const int pgs = lane <= kAhead ? page(beg + warp * kChunk + lane * kStep) : -1;
+    int pg_n = __shfl_sync(0xffffffffu, pgs, kAhead);
+#pragma unroll 1
+    for (int i = 0; i < kAhead; ++i)
+      issue(beg + warp * kChunk + i * kStep, i, __shfl_sync(0xffffffffu, pgs, i), beg, end);
     if (beg == k_beg) put_queries();
     int stage = 0, ahead = kAhead;  // of this chunk, and of the one whose copies start
     for (int j0 = beg + warp * kChunk; j0 < end; j0 += kStep) {  // (j0 + (kAhead + 1) * kStep stays below 2^31: kMaxPositions)
@@ -523,9 +522,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     const bool whole = sg.whole();
     float* part = p.parts + (2LL * blockIdx.x + (sg.first ? 0 : 1)) * kPartFloats<kRowsTile, D>;
     const float* om0 = reinterpret_cast<const float*>(smem);
-    for (int x = threadIdx.x; x < 16 * D / 4; x += kThreads) {
+#pragma unroll 1
+    for (int x = threadIdx.x; x < min(rows_left, 16) * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = (x % (D / 4)) * 4, R = row_tile * kRowsTile + r;
-      if (r >= rows_left) continue;
       float2 q[kWarps];
       float mm = -INFINITY, ll = 0.f;
 #pragma unroll
@@ -557,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   }
 }
 
-template <int D, bool I8, bool SEL>
+template <int D, bool I8, bool SEL, bool PAGED>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -569,37 +568,38 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL>, p);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED>, p);
+}
+template <int D, bool I8>
+cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream) {
+  if (selected) return launch<D, I8, true, false>(p, grid, stream);
+  return (1 << p.page_shift) >= Shape<D, I8>::kChunk ? launch<D, I8, false, true>(p, grid, stream)
+                                                     : launch<D, I8, false, false>(p, grid, stream);
 }
 
-template <int D, bool I8, bool SEL>
+template <int D, bool I8>
 cudaError_t opt_in() {
-  return cudaFuncSetAttribute(rows_kernel<D, I8, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Shape<D, I8>::kSmem);
+  const auto what = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, I8, true, false>, what, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D, I8, false, true>, what, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D, I8, false, false>, what, Shape<D, I8>::kSmem);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t setup_rows() {
-  cudaError_t e = opt_in<64, false, false>();
-  if (e == cudaSuccess) e = opt_in<64, false, true>();
-  if (e == cudaSuccess) e = opt_in<64, true, false>();
-  if (e == cudaSuccess) e = opt_in<64, true, true>();
-  if (e == cudaSuccess) e = opt_in<128, false, false>();
-  if (e == cudaSuccess) e = opt_in<128, false, true>();
-  if (e == cudaSuccess) e = opt_in<128, true, false>();
-  if (e == cudaSuccess) e = opt_in<128, true, true>();
+  cudaError_t e = opt_in<64, false>();
+  if (e == cudaSuccess) e = opt_in<64, true>();
+  if (e == cudaSuccess) e = opt_in<128, false>();
+  if (e == cudaSuccess) e = opt_in<128, true>();
   return e;
 }
 
 cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,
                         cudaStream_t stream) {
-  if (head_dim == 64) {
-    if (i8) return selected ? launch<64, true, true>(p, grid, stream) : launch<64, true, false>(p, grid, stream);
-    return selected ? launch<64, false, true>(p, grid, stream) : launch<64, false, false>(p, grid, stream);
-  }
-  if (i8) return selected ? launch<128, true, true>(p, grid, stream) : launch<128, true, false>(p, grid, stream);
-  return selected ? launch<128, false, true>(p, grid, stream) : launch<128, false, false>(p, grid, stream);
+  if (head_dim == 64) return i8 ? launch<64, true>(p, selected, grid, stream) : launch<64, false>(p, selected, grid, stream);
+  return i8 ? launch<128, true>(p, selected, grid, stream) : launch<128, false>(p, selected, grid, stream);
 }
 
 }  // namespace attn

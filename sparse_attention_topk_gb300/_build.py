@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(BUILD_DIR, "libtks.so")
 SOURCES = [os.path.join(CSRC, "tks_select.cu"), os.path.join(CSRC, "tks_select512.cu"),
            os.path.join(CSRC, "tks_order.cu"), os.path.join(CSRC, "tks_cache.cu"),
            os.path.join(CSRC, "tks_attn.cu"), os.path.join(CSRC, "tks_attn_rows.cu"),
-           os.path.join(CSRC, "tks_attn_tiles.cu")]
+           os.path.join(CSRC, "tks_attn_tiles.cu"), os.path.join(CSRC, "tks_attn_tiles_bf16.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "tks_device.cuh"), os.path.join(CSRC, "tks_kernel.cuh"),
                      os.path.join(CSRC, "tks_internal.h"), os.path.join(CSRC, "tks_attn.cuh"),
                      os.path.join(CSRC, "tks_attn_internal.h"), os.path.join(INCLUDE, "tks.h"),

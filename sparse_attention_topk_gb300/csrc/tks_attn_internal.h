@@ -110,6 +110,8 @@ cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, i
 constexpr int kTilesRows = 128;
 constexpr int kTilesKeys = 128;
 cudaError_t setup_tiles();
+cudaError_t setup_tiles_bf16();  // (tks_attn_tiles_bf16.cu, called by setup_tiles and launch_tiles)
+cudaError_t launch_tiles_bf16(const Params& p, int head_dim, bool selected, int grid, cudaStream_t stream);
 cudaError_t launch_tiles(const Params& p, int head_dim, bool i8, bool selected, int grid,
                          cudaStream_t stream);
 

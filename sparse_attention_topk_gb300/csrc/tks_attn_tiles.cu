@@ -158,6 +158,10 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
+// Between the producers' ordinary stores to a stage and the products' reads of it. The warp that
+// issues the products executes it, after the barrier: a producer's own would also wait for the
+// loads that it has under way for the next tile (which took the wide tree from 224 us to FENCE_US).
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // D (tensor memory) = A (tensor memory) x B (shared memory) (+ D)
 __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -202,13 +206,14 @@ __device__ __forceinline__ void tc_st_frag(uint32_t addr, const uint32_t (&r)[16
       : "memory");
 }
 
-// 16 lanes by 8 (4) columns.
+// 16 lanes by 8 columns.
 __device__ __forceinline__ void tc_ld_piece(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-__device__ __forceinline__ void tc_st_piece(uint32_t addr, uint32_t a, uint32_t b) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%2], {%0, %1};" ::"r"(a), "r"(b), "r"(addr) : "memory");
+__device__ __forceinline__ void tc_st_scores(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%4], {%0, %1, %2, %3};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(addr)
+               : "memory");
 }
 
 // A shared-memory operand of 128-byte rows, 128-byte swizzled. K-major (keys): 8-row
@@ -263,7 +268,8 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
   it.begin(start);
   Segment s;
   unsigned g = 0;  // the tile's number in this block
-  while (it.next(p, s)) {
+  bool bad = false;
+  while (uniform((int)it.next(p, s))) {
     const int32_t* table = p.table + s.b * p.table_stride;
     const int32_t* list = SEL ? p.indices + (long long)s.seq * p.k_sel : nullptr;
     const int limit = SEL ? kv_limit(p, kv_given(p, s.b)) : 0;
@@ -271,7 +277,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
     auto entry = [&](int t, int i) -> int {  // key i of tile t: its list entry, or its position
       const int j = t * kKeys + i;
       if (t >= s.t1 || j >= end) return -1;
-      return SEL ? list[j] : j;
+      return SEL ? __ldg(list + j) : j;
     };
     int t = uniform(s.t0 + (int)((who + 3u - g % 3u) % 3u));
     const int t1 = uniform(s.t1);
@@ -283,12 +289,9 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         pos[i] = e[i];
-        if (SEL && pos[i] >= limit) {
-          report(p.status, kStatIndexBit);
-          pos[i] = -1;
-        }
-        pos[i] = max(pos[i], -1);
-        pg[i] = pos[i] < 0 ? -1 : table[pos[i] >> p.page_shift];
+        bad |= SEL && pos[i] >= limit;
+        if (SEL && pos[i] >= limit) pos[i] = -1;
+        pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) e[i] = entry(t + 3, lane + 32 * i);
@@ -297,7 +300,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool ok = pos[i] >= 0 && (unsigned)pg[i] < (unsigned)p.pages;
-        if (pos[i] >= 0 && !ok) report(p.status, kStatIndexBit);
+        bad |= pos[i] >= 0 && !ok;
         const int in_page = pos[i] & ((1 << p.page_shift) - 1);
         off[i] = ok ? pg[i] * p.page_b + in_page * p.token_b + s.head * p.head_b : -1;
         sc[i] = make_float2(0.f, 1.f);
@@ -330,6 +333,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
     }
     g += (unsigned)(s.t1 - s.t0);
   }
+  if (bad) report(p.status, kStatIndexBit);
 }
 
 // Warps 12-19: the rows of every tile into its stage.
@@ -348,54 +352,47 @@ __device__ __forceinline__ void produce(const Params& p, const Block& k, int til
     // A matrix's rows of the next tile are loaded as soon as this tile's have been stored.
     const int blk = (piece >> 2) * S::kBlock, first = (piece & 3) * 2;
     uint4 w[2][S::kPer];
-    auto load = [&](const Meta& m, int kv, uint4 (&x)[S::kPer]) {
-      const unsigned char* base = (kv ? p.v : p.k) + piece * 16;
-#pragma unroll
-      for (int i = 0; i < S::kPer; ++i) {
-        const long long off = m.off[row0 + i * kRows];
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (off >= 0) x[i] = __ldg(reinterpret_cast<const uint4*>(base + off));
-      }
-    };
-    auto store = [&](int st, int kv, const uint4 (&x)[S::kPer]) {
-      unsigned char* base = k.smem + (2 * st + kv) * S::kMat + blk;
-#pragma unroll
-      for (int i = 0; i < S::kPer; ++i) {
-        const int r = row0 + i * kRows;
-        const uint32_t a[4] = {x[i].x ^ 0x80808080u, x[i].y ^ 0x80808080u, x[i].z ^ 0x80808080u, x[i].w ^ 0x80808080u};
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<uint4*>(base + r * 128 + (((first + j) ^ (r & 7)) << 4)) =
-              make_uint4(codes_to_half2<0x4140>(a[2 * j]), codes_to_half2<0x4342>(a[2 * j]),
-                         codes_to_half2<0x4140>(a[2 * j + 1]), codes_to_half2<0x4342>(a[2 * j + 1]));
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      bar_arrive(k.bar((kv ? kVFull : kKFull) + st));
-    };
     Ring<kMetas> meta;
     Ring<S::kStages> st;
-    auto leave = [&] {
-      __syncwarp();
-      bar_arrive(k.bar(kMetaEmpty + meta.i));
-      meta.next();
-    };
-    if (tiles == 0 || !k.wait(kMetaFull, 0)) return;
-    load(k.metas[0], 0, w[0]);
-    load(k.metas[0], 1, w[1]);
-    leave();
-    for (int g = 0; g < tiles; ++g) {
+#pragma unroll 1
+    for (int g = -1; g < tiles; ++g) {  // (-1: only loads)
       const bool more = g + 1 < tiles;
       if (more && !k.wait(kMetaFull + meta.i, meta.parity)) return;
       if (g >= S::kStages && !k.wait<true>(kEmpty + st.i, st.parity ^ 1)) return;
-      store(st.i, 0, w[0]);
-      if (more) load(k.metas[meta.i], 0, w[0]);
-      store(st.i, 1, w[1]);
-      if (more) {
-        load(k.metas[meta.i], 1, w[1]);
-        leave();
+      const Meta& m = k.metas[meta.i];
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (g >= 0) {
+          unsigned char* base = k.smem + (2 * st.i + kv) * S::kMat + blk;
+#pragma unroll
+          for (int i = 0; i < S::kPer; ++i) {
+            const int r = row0 + i * kRows;
+            const uint32_t a[4] = {w[kv][i].x ^ 0x80808080u, w[kv][i].y ^ 0x80808080u, w[kv][i].z ^ 0x80808080u, w[kv][i].w ^ 0x80808080u};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<uint4*>(base + r * 128 + (((first + j) ^ (r & 7)) << 4)) =
+                  make_uint4(codes_to_half2<0x4140>(a[2 * j]), codes_to_half2<0x4342>(a[2 * j]),
+                             codes_to_half2<0x4140>(a[2 * j + 1]), codes_to_half2<0x4342>(a[2 * j + 1]));
+          }
+          __syncwarp();
+          bar_arrive(k.bar((kv ? kVFull : kKFull) + st.i));
+        }
+        if (more) {
+          const unsigned char* base = (kv ? p.v : p.k) + piece * 16;
+#pragma unroll
+          for (int i = 0; i < S::kPer; ++i) {
+            const long long off = m.off[row0 + i * kRows];
+            w[kv][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (off >= 0) w[kv][i] = __ldg(reinterpret_cast<const uint4*>(base + off));
+          }
+        }
       }
-      st.next();
+      if (more) {
+        __syncwarp();
+        bar_arrive(k.bar(kMetaEmpty + meta.i));
+        meta.next();
+      }
+      if (g >= 0) st.next();
     }
     return;
   }
@@ -403,7 +400,6 @@ __device__ __forceinline__ void produce(const Params& p, const Block& k, int til
   // bfloat16: cp.async straight into the stage; a tile is announced when the next one's copies are under way.
   const int blk = (piece >> 3) * S::kBlock, at = piece & 7;
   auto announce = [&](int st) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     bar_arrive(k.bar(kKFull + st));
     bar_arrive(k.bar(kVFull + st));
@@ -420,7 +416,6 @@ __device__ __forceinline__ void produce(const Params& p, const Block& k, int til
     const Meta& m = k.metas[meta.i];
     const int draft0 = m.draft0;
     const uint32_t kd = k.stage + 2 * st * S::kMat + blk, vd = kd + S::kMat;
-    bool bad = false;
 #pragma unroll
     for (int i = 0; i < S::kPer; ++i) {
       const int r = row0 + i * kRows;
@@ -428,22 +423,28 @@ __device__ __forceinline__ void produce(const Params& p, const Block& k, int til
       const long long src = off < 0 ? 0 : off + piece * 16;
       const int dst = r * 128 + ((at ^ (r & 7)) << 4);
       cp16(kd + dst, p.k + src, off < 0 ? 0 : 16);
-      if (r < draft0) {
-        cp16(vd + dst, p.v + src, off < 0 ? 0 : 16);
-      } else {
-        // a drafted token: infinities and NaNs must not meet the zero weights of rows that do not see it
+      if (r < draft0) cp16(vd + dst, p.v + src, off < 0 ? 0 : 16);
+    }
+    if (draft0 < kKeys) {
+      // drafted tokens: infinities and NaNs must not meet the zero weights of rows that do not see them
+      bool bad = false;
+#pragma unroll 1
+      for (int i = 0; i < S::kPer; ++i) {
+        const int r = row0 + i * kRows;
+        if (r < draft0) continue;
+        const long long off = m.off[r];
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (off >= 0) x = *reinterpret_cast<const uint4*>(p.v + src);
+        if (off >= 0) x = *reinterpret_cast<const uint4*>(p.v + off + piece * 16);
         uint32_t u[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if ((u[j] & 0x7f80u) == 0x7f80u) { u[j] &= 0xffff0000u; bad = true; }
           if ((u[j] & 0x7f800000u) == 0x7f800000u) { u[j] &= 0x0000ffffu; bad = true; }
         }
-        *reinterpret_cast<uint4*>(k.smem + (2 * st + 1) * S::kMat + blk + dst) = make_uint4(u[0], u[1], u[2], u[3]);
+        *reinterpret_cast<uint4*>(k.smem + (2 * st + 1) * S::kMat + blk + r * 128 + ((at ^ (r & 7)) << 4)) = make_uint4(u[0], u[1], u[2], u[3]);
       }
+      if (bad) *k.poisoned = 1;
     }
-    if (bad) *k.poisoned = 1;
     cp_commit();
     __syncwarp();
     bar_arrive(k.bar(kMetaEmpty + meta.i));
@@ -473,40 +474,41 @@ __device__ __forceinline__ void multiply(const Params& p, const Block& k, const 
   uint32_t seg = 0;
   const uint64_t keys0 = operand(k.stage, 16), values0 = operand(k.stage + S::kMat, S::kBlock);
   bool ok = true;
-  // O (+)= P V of the next tile; `fresh`: the segment's first
-  auto second = [&](bool fresh) -> bool {
-    if (!k.wait(kVFull + vr.i, vr.parity) || !k.wait(kPReady + (gv & 1), gv >> 1 & 1)) return false;
-    tc_fence_after();
-    const uint64_t v = values0 + (uint32_t)(vr.i * (2 * S::kMat >> 4));
-    const uint32_t a = tmem + S::kS + (gv & 1) * 128;
-#pragma unroll
-    for (int i = 0; i < kKeys / 16; ++i)
-      tc_mma(tmem + S::kO, a + (i >> 2) * 64 + (i & 3) * 8, v + i * (16 * 128 >> 4), kPv, !fresh || i > 0);
-    tc_commit(k.bar(kEmpty + vr.i));
-    tc_commit(k.bar(kMetaEmpty + mr.i));
-    tc_commit(k.bar(kPvDone + (gv & 1)));
-    mr.next();
-    vr.next();
-    ++gv;
-    return true;
-  };
-  while (ok && it.next(p, s)) {
+  while (ok && uniform((int)it.next(p, s))) {
     if (!k.wait(kQReady, seg & 1)) break;
     const int n = uniform(s.t1 - s.t0);
-    for (int i = 0; ok && i < n; ++i) {
-      if (!k.wait(kKFull + kr.i, kr.parity)) { ok = false; break; }
-      tc_fence_after();
-      const uint64_t b = keys0 + (uint32_t)(kr.i * (2 * S::kMat >> 4));
-      const uint32_t d = tmem + S::kS + (gk & 1) * 128;
+#pragma unroll 1
+    for (int i = 0; i <= n; ++i) {
+      if (i < n) {  // S = Q K^T of tile i
+        if (!k.wait(kKFull + kr.i, kr.parity)) { ok = false; break; }
+        proxy_fence();
+        tc_fence_after();
+        const uint64_t b = keys0 + (uint32_t)(kr.i * (2 * S::kMat >> 4));
+        const uint32_t d = tmem + S::kS + (gk & 1) * 128;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-        tc_mma(d, tmem + S::kQ + 8 * j, b + (j >> 2) * (S::kBlock >> 4) + (j & 3) * 2, kQk, j > 0);
-      tc_commit(k.bar(kSFull + (gk & 1)));
-      kr.next();
-      ++gk;
-      if (i > 0) ok = second(i == 1);
+        for (int j = 0; j < D / 16; ++j)
+          tc_mma(d, tmem + S::kQ + 8 * j, b + (j >> 2) * (S::kBlock >> 4) + (j & 3) * 2, kQk, j > 0);
+        tc_commit(k.bar(kSFull + (gk & 1)));
+        kr.next();
+        ++gk;
+      }
+      if (i > 0) {  // O (+)= P V of tile i - 1
+        if (!k.wait(kVFull + vr.i, vr.parity) || !k.wait(kPReady + (gv & 1), gv >> 1 & 1)) { ok = false; break; }
+        proxy_fence();
+        tc_fence_after();
+        const uint64_t v = values0 + (uint32_t)(vr.i * (2 * S::kMat >> 4));
+        const uint32_t a = tmem + S::kS + (gv & 1) * 128;
+#pragma unroll
+        for (int j = 0; j < kKeys / 16; ++j)
+          tc_mma(tmem + S::kO, a + (j >> 2) * 64 + (j & 3) * 8, v + j * (16 * 128 >> 4), kPv, i > 1 || j > 0);
+        tc_commit(k.bar(kEmpty + vr.i));
+        tc_commit(k.bar(kMetaEmpty + mr.i));
+        tc_commit(k.bar(kPvDone + (gv & 1)));
+        mr.next();
+        vr.next();
+        ++gv;
+      }
     }
-    if (ok) ok = second(n == 1);
     ++seg;
   }
   // nothing may be under way when tensor memory is freed
@@ -514,14 +516,14 @@ __device__ __forceinline__ void multiply(const Params& p, const Block& k, const 
   k.wait(kFinal, 0);
 }
 
-// What the two warps of a quarter of the rows tell each other, by row n + 8 * i of the
-// quarter at [n][i].
+// What the two warps of a quarter of the rows tell each other, and themselves. Rows of a quarter
+// are lanes: row 16h + n of it, and row 16h + n + 8, at [h][n].
 struct PairRows {
-  float top[2][2][8][4];  // a tile's maxima: [tile & 1][half of the keys]
-  float sum[2][8][4];     // a segment's sums
-  float m[8][4];          // and maxima
-  float fac[8][4];        // what undoes the shifts of the rows' queries
-  unsigned seen[2][2][8][4];  // the keys that a row sees: [half of the keys][32 keys]
+  float2 top[2][2][2][8];    // a tile's maxima: [tile & 1][half of the keys]
+  float2 sum[2][2][8];       // a segment's sums, by half of the keys
+  float2 m[2][8];            // and maxima
+  float fac[2][32];          // what undoes the shifts of the rows' queries (a copy for each warp)
+  unsigned seen[2][2][32];   // the keys that a row sees: [half of the keys][32 keys]
 };
 // Scales 16 lanes by 32 columns: lanes n by fa, lanes n + 8 by fb.
 __device__ __forceinline__ void rescale(uint32_t addr, float fa, float fb) {
@@ -549,16 +551,21 @@ struct RowSegments {
   Segment s[2];
 };
 
-// Warps 0-7: warps w and w + 4 have query rows 32w .. 32w + 31, warp w the first 64 keys of
-// every tile, warp w + 4 the others. Scores come in the layout of matrix fragments: thread
-// 4n + c has rows n, n + 8, n + 16, n + 24 and keys 8j + 2c, 8j + 2c + 1, so the scales that it
-// needs are an eighth of the tile's. Queries and outputs go by whole rows, a thread each, and
-// half the elements for each warp.
-template <int D, bool I8, bool SEL>
-__device__ __forceinline__ void rows(const Params& p, const Block& k, const Start& start, uint32_t tmem, RowSegments<SEL>& segs, PairRows& pr) {
+// Warps 0-7: warps w and w + 4 have the rows of lanes 32w .. 32w + 31, warp w the first 64 keys of
+// every tile, warp w + 4 the others. Scores come in the layout of matrix fragments, 16 rows a
+// step: thread 4n + c has rows n and n + 8 and keys 8j + 2c, 8j + 2c + 1, so the scales that it
+// needs are an eighth of the tile's. A step's scores are read twice from tensor memory, for the
+// maxima and for the weights: the loops stay short (instructions not fetched in time were what
+// bound them), and few registers wait. Queries and outputs go by whole rows, a thread each, and
+// half the elements for each warp. Up to 64 rows lie in the first 16 lanes of each quarter, so
+// that all the warps share them.
+template <int D, bool I8, bool SEL, int STEPS>
+__device__ __forceinline__ void rows(const Params& p, const Block& k, const Start& start, uint32_t tmem, RowSegments<SEL>& segs, PairRows& pr,
+                                     const float4* plain_kl) {
   using S = Shape<D, I8>;
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
-  const int n = lane >> 2, c = lane & 3, r = quarter * 32 + lane;
+  const int n = lane >> 2, c = lane & 3;
+  const int row_lane = lane < 16 * STEPS ? quarter * 16 * STEPS + lane : 1 << 20;  // this lane's row in the tile
   const uint32_t mine = tmem + ((uint32_t)(quarter * 32) << 16);
   if (lane == 0) segs.it.begin(start);
   // the next segment, into place `at`
@@ -585,21 +592,21 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
     return true;
   };
   bool shifted = false;   // some row's queries are not as they were
-  float next_back = 1.f;  // what undoes the shift of row `lane`
+  float next_back = 1.f;  // what undoes the shift of this lane's row
   uint32_t g = 0;  // the tile's number in this block
   Ring<kMetas> mr;
   int at = 0;
 
-  // Puts segment s's queries into tensor memory; fac undoes the rows' shifts.
+  // Puts segment s's queries into tensor memory.
   auto queries = [&](const Segment& s) {
-    const int R = s.row_tile * kTilesRows + r;
+    const int R = s.row_tile * kTilesRows + row_lane;
     const __nv_bfloat16* q = R < p.rows ? q_row<SEL>(p, s.seq, s.head, R) : nullptr;
     float up = 1.f, back = 1.f;
     if (I8) {
       float top = 0.f;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
-        const uint4 x = q ? *reinterpret_cast<const uint4*>(q + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = q ? __ldg(reinterpret_cast<const uint4*>(q + 8 * i)) : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -615,12 +622,12 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
         back = __int_as_float((127 - shift) << 23);
       }
     }
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < D / 64; ++i) {  // 32 elements a step
       uint32_t w[16];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint4 x = q ? *reinterpret_cast<const uint4*>(q + half * (D / 2) + 32 * i + 8 * j) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = q ? __ldg(reinterpret_cast<const uint4*>(q + half * (D / 2) + 32 * i + 8 * j)) : make_uint4(0u, 0u, 0u, 0u);
         w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
       }
       if (I8)
@@ -637,23 +644,19 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
     next_back = back;
   };
 
-  // Scores of keys 8j + 2c, 8j + 2c + 1 for the thread's four rows, -inf where a row does not see
-  // the key: the way of tiles with missing keys or drafted tokens, and of shifted rows.
-  auto masked = [&](uint32_t sb, const Meta& meta, int j, float2 (&a)[4]) {
-    uint32_t x[2][4];
-    tc_ld_piece(x[0], sb + half * 64 + 8 * j);
-    tc_ld_piece(x[1], sb + half * 64 + 8 * j + (16u << 16));
+  // The scores of 16 rows, scaled, in pairs of keys: v[i][j] of row n + 8i, keys 8j + 2c, 8j + 2c + 1.
+  auto scores = [&](uint32_t addr, const float4* kl, float f, uint64_t (&v)[2][8]) {
+    uint32_t x[32];
+    tc_ld_frag(x, addr);
     tc_wait_ld();
-    const float4 kl = I8 ? *reinterpret_cast<const float4*>(meta.kl[32 * half + 4 * j + c]) : make_float4(p.scale_log2, p.scale_log2, 0.f, 0.f);
-    const uint4 seen = *reinterpret_cast<const uint4*>(pr.seen[half][j >> 2][n]);
-    const float4 fac = *reinterpret_cast<const float4*>(pr.fac[n]);
-    const unsigned sn[4] = {seen.x, seen.y, seen.z, seen.w};
-    const float f[4] = {fac.x, fac.y, fac.z, fac.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned bits = sn[i] >> (8 * (j & 3) + 2 * c);
-      a[i].x = bits & 1u ? fmaf(__uint_as_float(x[i >> 1][2 * (i & 1)]) * f[i], kl.x, kl.z) : -INFINITY;
-      a[i].y = bits & 2u ? fmaf(__uint_as_float(x[i >> 1][2 * (i & 1) + 1]) * f[i], kl.y, kl.w) : -INFINITY;
+    for (int j = 0; j < 8; ++j) {
+      const ulonglong2 e = I8 ? *reinterpret_cast<const ulonglong2*>(kl + 4 * j) : make_ulonglong2(pair(f, f), 0);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t a = pair(__uint_as_float(x[4 * j + 2 * i]), __uint_as_float(x[4 * j + 2 * i + 1]));
+        v[i][j] = I8 ? fma2(a, e.x, e.y) : mul2(a, e.x);
+      }
     }
   };
 
@@ -661,147 +664,132 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
   if (more) queries(segs.s[0]);
   while (more) {
     const Segment& s = segs.s[at];
-    const int R0 = s.row_tile * kTilesRows + quarter * 32;
+    const int R0 = s.row_tile * kTilesRows + quarter * 16 * STEPS;
     const float back = next_back;
     const bool warp_live = uniform((int)(R0 < p.rows)) != 0;
-    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    uint64_t sum[4] = {0, 0, 0, 0};
+    float m[STEPS][2];
+    uint64_t sum[STEPS][2];
+#pragma unroll
+    for (int h = 0; h < STEPS; ++h) {
+      m[h][0] = m[h][1] = -INFINITY;
+      sum[h][0] = sum[h][1] = 0;
+    }
 
     const int t0 = uniform(s.t0), t1 = uniform(s.t1);
     for (int t = t0; t < t1; ++t, ++g) {
-      const uint32_t sb = mine + S::kS + (g & 1) * 128;
-      if (!k.wait(kSFull + (g & 1), g >> 1 & 1)) return;
-      if (warp_live) {
+      const uint32_t sb = mine + S::kS + (g & 1) * 128 + half * 64;
+      if (!warp_live) {
+        if (!k.wait<true>(kSFull + (g & 1), g >> 1 & 1)) return;
+      } else {
+        if (!k.wait(kSFull + (g & 1), g >> 1 & 1)) return;
         tc_fence_after();
         // (scores exist, so the tile's lookups do)
         const Meta& meta = k.metas[mr.i];
         const uint4 all = *reinterpret_cast<const uint4*>(meta.valid);
-        // (the same answer for both warps of the quarter: they meet once more if it is no)
         const bool plain = uniform((int)((all.x & all.y & all.z & all.w) == ~0u && meta.draft0 == kKeys)) != 0 && !shifted;
-        uint64_t v[4][8];  // scores of rows n + 8i, in pairs of keys 8j + 2c, 8j + 2c + 1
-        float top[4];
-        if (plain) {
-          uint32_t x[2][32];
-          tc_ld_frag(x[0], sb + half * 64);
-          tc_ld_frag(x[1], sb + half * 64 + (16u << 16));
-          tc_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const ulonglong2 kl = I8 ? *reinterpret_cast<const ulonglong2*>(meta.kl[32 * half + 4 * j + c]) : make_ulonglong2(pair(p.scale_log2, p.scale_log2), 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint64_t a = pair(__uint_as_float(x[i >> 1][4 * j + 2 * (i & 1)]), __uint_as_float(x[i >> 1][4 * j + 2 * (i & 1) + 1]));
-              v[i][j] = I8 ? fma2(a, kl.x, kl.y) : mul2(a, kl.x);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 a = unpair(v[i][0]);
-            float x0 = fmaxf(a.x, a.y), x1 = -INFINITY;
-#pragma unroll
-            for (int j = 1; j < 8; ++j) {
-              a = unpair(v[i][j]);
-              if (j & 1) x1 = fmaxf(x1, fmaxf(a.x, a.y));
-              else x0 = fmaxf(x0, fmaxf(a.x, a.y));
-            }
-            top[i] = fmaxf(x0, x1);
-          }
-        } else {
-          // what row `lane` of the quarter sees
+        const float4* kl = reinterpret_cast<const float4*>(meta.kl) + 32 * half + c;
+        float f = p.scale_log2;
+        if (!plain) {
+          // Missing keys, drafted tokens, shifted rows: the scores are scaled and masked in tensor
+          // memory first, and what follows takes them as they are.
           const int tr = SEL ? 0 : min((R0 + lane) / p.group, p.tokens - 1), j0 = t * kKeys + 64 * half - s.len.ctx;
           const bool drafts = !SEL && meta.draft0 < kKeys;
           __syncwarp();
 #pragma unroll 1
           for (int i = 0; i < 2; ++i)
-            pr.seen[half][i][lane & 7][lane >> 3] = meta.valid[2 * half + i] & (drafts ? draft_bits(p, s.b, tr, j0 + 32 * i) : ~0u);
-          if (half == 0) pr.fac[lane & 7][lane >> 3] = back;
-          if (!meet()) return;
-          top[0] = top[1] = top[2] = top[3] = -INFINITY;
+            pr.seen[half][i][lane] = meta.valid[2 * half + i] & (drafts ? draft_bits(p, s.b, tr, j0 + 32 * i) : ~0u);
+          pr.fac[half][lane] = back;
+          __syncwarp();
 #pragma unroll 1
-          for (int j = 0; j < 8; ++j) {
-            float2 a[4];
-            masked(sb, meta, j, a);
+          for (int e = 0; e < 8 * STEPS; ++e) {
+            const int h = e >> 3, j = e & 7;
+            uint32_t x[4];
+            tc_ld_piece(x, sb + 8 * j + ((uint32_t)(16 * h) << 16));
+            tc_wait_ld();
+            const float4 e4 = I8 ? kl[4 * j] : make_float4(f, f, 0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], fmaxf(a[i].x, a[i].y));
-          }
-        }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-        pr.top[g & 1][half][n][c] = c == 0 ? top[0] : c == 1 ? top[1] : c == 2 ? top[2] : top[3];
-        if (!meet()) return;
-        {
-          const float4 y = *reinterpret_cast<const float4*>(pr.top[g & 1][half ^ 1][n]);
-          top[0] = fmaxf(top[0], y.x); top[1] = fmaxf(top[1], y.y);
-          top[2] = fmaxf(top[2], y.z); top[3] = fmaxf(top[3], y.w);
-        }
-
-        // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
-        const bool grow = top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || top[2] > m[2] + 8.f || top[3] > m[3] + 8.f;
-        if (__any_sync(0xffffffffu, grow)) {
-          float f[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool up = top[i] > m[i] + 8.f;
-            f[i] = up ? ex2(m[i] - top[i]) : 1.f;  // (m = -inf: 0)
-            if (up) m[i] = top[i];
-            sum[i] = mul2(sum[i], pair(f[i], f[i]));
-          }
-          if (t > t0) {
-            if (!outputs_done(g - 1)) return;
-#pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t ob = mine + S::kO + half * (D / 2) + ((uint32_t)(16 * h) << 16);
-              const float fa = h ? f[2] : f[0], fb = h ? f[3] : f[1];
-#pragma unroll 1
-              for (int i = 0; i < D / 64; ++i) rescale(ob + 32 * i, fa, fb);
+            for (int i = 0; i < 2; ++i) {
+              const int row = 16 * h + n + 8 * i;
+              const unsigned bits = pr.seen[half][j >> 2][row] >> (8 * (j & 3) + 2 * c);
+              const float b = pr.fac[half][row];
+              x[2 * i] = __float_as_uint(bits & 1u ? fmaf(__uint_as_float(x[2 * i]) * b, e4.x, e4.z) : -INFINITY);
+              x[2 * i + 1] = __float_as_uint(bits & 2u ? fmaf(__uint_as_float(x[2 * i + 1]) * b, e4.y, e4.w) : -INFINITY);
             }
-            tc_wait_st();
+            tc_st_scores(sb + 8 * j + ((uint32_t)(16 * h) << 16), x);
           }
-        }
-        uint64_t neg[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = m[i] == -INFINITY ? 0.f : -m[i];
-          neg[i] = pair(u, u);
+          tc_wait_st();
+          kl = plain_kl + c;
+          f = 1.f;
         }
 
-        // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
-        const uint32_t pb = sb + half * 64;
-        if (plain) {
-          uint32_t w[2][16];
+#pragma unroll
+        for (int h = 0; h < STEPS; ++h) {
+          uint64_t v[2][8];
+          scores(sb + ((uint32_t)(16 * h) << 16), kl, f, v);
+          float top[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float2 a = unpair(v[i][0]), b = unpair(v[i][1]);
+            float x0 = fmaxf(a.x, a.y), x1 = fmaxf(b.x, b.y);
+#pragma unroll
+            for (int j = 2; j < 8; j += 2) {
+              a = unpair(v[i][j]);
+              b = unpair(v[i][j + 1]);
+              x0 = fmaxf(x0, fmaxf(a.x, a.y));
+              x1 = fmaxf(x1, fmaxf(b.x, b.y));
+            }
+            top[i] = fmaxf(x0, x1);
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+          if (c == 0) pr.top[g & 1][half][h][n] = make_float2(top[0], top[1]);
+        }
+        if (!meet()) return;
+
+#pragma unroll
+        for (int h = 0; h < STEPS; ++h) {
+          const float2 ta = pr.top[g & 1][0][h][n], tb = pr.top[g & 1][1][h][n];
+          const float top[2] = {fmaxf(ta.x, tb.x), fmaxf(ta.y, tb.y)};
+          // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
+          if (__any_sync(0xffffffffu, top[0] > m[h][0] + 8.f || top[1] > m[h][1] + 8.f)) {
+            float back2[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool up = top[i] > m[h][i] + 8.f;
+              back2[i] = up ? ex2(m[h][i] - top[i]) : 1.f;  // (m = -inf: 0)
+              if (up) m[h][i] = top[i];
+              sum[h][i] = mul2(sum[h][i], pair(back2[i], back2[i]));
+            }
+            if (t > t0) {
+              if (!outputs_done(g - 1)) return;
+#pragma unroll 1
+              for (int i = 0; i < D / 64; ++i)
+                rescale(mine + S::kO + half * (D / 2) + 32 * i + ((uint32_t)(16 * h) << 16), back2[0], back2[1]);
+            }
+          }
+          uint64_t v[2][8], neg[2];
+          scores(sb + ((uint32_t)(16 * h) << 16), kl, f, v);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float u = m[h][i] == -INFINITY ? 0.f : -m[h][i];
+            neg[i] = pair(u, u);
+          }
+          // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
+          uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               const float2 a = unpair(add2(v[i][j], neg[i]));
               const float e0 = ex2(a.x), e1 = ex2(a.y);
-              sum[i] = I8 ? fma2(pair(e0, e1), inv, sum[i]) : add2(sum[i], pair(e0, e1));
-              w[i >> 1][2 * j + (i & 1)] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+              sum[h][i] = I8 ? fma2(pair(e0, e1), inv, sum[h][i]) : add2(sum[h][i], pair(e0, e1));
+              w[2 * j + i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
             }
           }
-          tc_st_frag(pb, w[0]);
-          tc_st_frag(pb + (16u << 16), w[1]);
-        } else {
-#pragma unroll 1
-          for (int j = 0; j < 8; ++j) {
-            float2 a[4];
-            masked(sb, meta, j, a);
-            const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 b = unpair(neg[i]);
-              const float e0 = ex2(a[i].x + b.x), e1 = ex2(a[i].y + b.y);
-              sum[i] = I8 ? fma2(pair(e0, e1), inv, sum[i]) : add2(sum[i], pair(e0, e1));
-              w[i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
-            }
-            tc_wait_ld();
-            tc_st_piece(pb + 4 * j, w[0], w[1]);
-            tc_st_piece(pb + 4 * j + (16u << 16), w[2], w[3]);
-          }
+          tc_st_frag(sb + ((uint32_t)(16 * h) << 16), w);
         }
         tc_wait_st();
         tc_fence_before();
@@ -817,21 +805,28 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
     if (more) queries(segs.s[at ^ 1]);
     if (!outputs_done(g - 1)) return;
     if (warp_live) {
-      float l[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a = unpair(sum[i]);
-        l[i] = a.x + a.y;
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      for (int h = 0; h < STEPS; ++h) {
+        float l[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float2 a = unpair(sum[h][i]);
+          l[i] = a.x + a.y;
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+          l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+        }
+        if (c == 0) {
+          pr.sum[half][h][n] = make_float2(l[0], l[1]);
+          if (half == 0) pr.m[h][n] = make_float2(m[h][0], m[h][1]);
+        }
       }
-      pr.sum[half][n][c] = c == 0 ? l[0] : c == 1 ? l[1] : c == 2 ? l[2] : l[3];
-      if (half == 0) pr.m[n][c] = c == 0 ? m[0] : c == 1 ? m[1] : c == 2 ? m[2] : m[3];
       if (!meet()) return;
-      const int R = R0 + lane;
+      const int R = done.row_tile * kTilesRows + row_lane, hl = lane >> 4, nl = lane & 7;
+      const bool low = (lane & 8) == 0;
       const int t_row = SEL ? 0 : min(R / p.group, p.tokens - 1);
       const bool live = R < p.rows && (SEL || R / p.group < done.len.drafts);
-      const float lr = pr.sum[0][lane & 7][lane >> 3] + pr.sum[1][lane & 7][lane >> 3], top = pr.m[lane & 7][lane >> 3];
+      const float2 la = pr.sum[0][hl][nl], lb = pr.sum[1][hl][nl], mm = pr.m[hl][nl];
+      const float lr = low ? la.x + lb.x : la.y + lb.y, top = low ? mm.x : mm.y;
       const bool empty = !live || lr == 0.f;
       const float inv = empty ? 0.f : 1.f / lr;
       const bool fix = !I8 && !SEL && *k.poisoned != 0;
@@ -869,7 +864,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
               out[j] = make_uint4(pack_bf16(f[8 * j] * inv, f[8 * j + 1] * inv), pack_bf16(f[8 * j + 2] * inv, f[8 * j + 3] * inv),
                                   pack_bf16(f[8 * j + 4] * inv, f[8 * j + 5] * inv), pack_bf16(f[8 * j + 6] * inv, f[8 * j + 7] * inv));
           } else {
-            float4* out = reinterpret_cast<float4*>(part + r * D + d);
+            float4* out = reinterpret_cast<float4*>(part + row_lane * D + d);
 #pragma unroll
             for (int j = 0; j < 8; ++j) out[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
           }
@@ -878,7 +873,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
       }
       if (R < p.rows && half == 0) {
         if (!done.whole())
-          *reinterpret_cast<float2*>(part + kTilesRows * D + 2 * r) = make_float2(top, empty ? 0.f : lr);
+          *reinterpret_cast<float2*>(part + kTilesRows * D + 2 * row_lane) = make_float2(top, empty ? 0.f : lr);
         else if (p.lse)
           p.lse[row] = empty ? -INFINITY : (top + lg2(lr)) * 0.6931471805599453f;
       }
@@ -889,7 +884,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
   }
 }
 
-template <int D, bool I8, bool SEL>
+template <int D, bool I8, bool SEL, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, I8>;
   extern __shared__ unsigned char raw[];
@@ -898,6 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   __shared__ uint32_t tmem_s;
   __shared__ RowSegments<SEL> segs[kRowWarps];
   __shared__ __align__(16) PairRows pair_rows[4];
+  __shared__ float4 plain_kl[32];  // the scales of scores that are scaled already
 
   unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   Block k;
@@ -914,6 +910,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  if (threadIdx.x < 32) plain_kl[threadIdx.x] = make_float4(1.f, 1.f, 0.f, 0.f);
   if (threadIdx.x == 0) {
     poisoned_s = 0;
     for (int i = 0; i < kMetas; ++i) {
@@ -944,19 +941,19 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const uint32_t tmem = uniform(tmem_s);
   const int tiles = uniform((int)start.left);
 
-  // registers: 2 * 152 + 48 + 2 * 64 of the launch's 5 * 96
+  // registers: 2 * 128 + 64 + 2 * 80 of the launch's 5 * 96
   if (warp < kRowWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    rows<D, I8, SEL>(p, k, start, tmem, segs[warp], pair_rows[warp & 3]);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    rows<D, I8, SEL, STEPS>(p, k, start, tmem, segs[warp], pair_rows[warp & 3], plain_kl);
   } else if (warp < kRowWarps + 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kMulWarp) {
       multiply<D, I8, SEL>(p, k, start, tmem);
     } else {
       look_up<D, I8, SEL>(p, k, start, warp - kMetaWarp0);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     produce<D, I8>(p, k, tiles);
   }
   tc_fence_before();
@@ -965,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D, bool I8, bool SEL>
+template <int D, bool I8, bool SEL, int STEPS>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -977,38 +974,51 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   a[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = a;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL>, p);
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL, STEPS>, p);
+}
+template <bool I8>
+cudaError_t launch_held(const Params& p, int head_dim, bool selected, int grid, cudaStream_t stream) {
+  const bool one = p.rows <= 64;
+  if (head_dim == 64) {
+    if (selected) return one ? launch<64, I8, true, 1>(p, grid, stream) : launch<64, I8, true, 2>(p, grid, stream);
+    return one ? launch<64, I8, false, 1>(p, grid, stream) : launch<64, I8, false, 2>(p, grid, stream);
+  }
+  if (selected) return one ? launch<128, I8, true, 1>(p, grid, stream) : launch<128, I8, true, 2>(p, grid, stream);
+  return one ? launch<128, I8, false, 1>(p, grid, stream) : launch<128, I8, false, 2>(p, grid, stream);
 }
 
 template <int D, bool I8, bool SEL>
 cudaError_t opt_in() {
-  return cudaFuncSetAttribute(tiles_kernel<D, I8, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Shape<D, I8>::kSmem);
+  const auto what = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, I8, SEL, 1>, what, Shape<D, I8>::kSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(tiles_kernel<D, I8, SEL, 2>, what, Shape<D, I8>::kSmem);
+}
+template <bool I8>
+cudaError_t setup_held() {
+  cudaError_t e = opt_in<64, I8, false>();
+  if (e == cudaSuccess) e = opt_in<64, I8, true>();
+  if (e == cudaSuccess) e = opt_in<128, I8, false>();
+  if (e == cudaSuccess) e = opt_in<128, I8, true>();
+  return e;
 }
 
 }  // namespace
 
-cudaError_t setup_tiles() {
-  cudaError_t e = opt_in<64, false, false>();
-  if (e == cudaSuccess) e = opt_in<64, false, true>();
-  if (e == cudaSuccess) e = opt_in<64, true, false>();
-  if (e == cudaSuccess) e = opt_in<64, true, true>();
-  if (e == cudaSuccess) e = opt_in<128, false, false>();
-  if (e == cudaSuccess) e = opt_in<128, false, true>();
-  if (e == cudaSuccess) e = opt_in<128, true, false>();
-  if (e == cudaSuccess) e = opt_in<128, true, true>();
-  return e;
+#ifdef TKS_TILES_BF16
+cudaError_t setup_tiles_bf16() { return setup_held<false>(); }
+cudaError_t launch_tiles_bf16(const Params& p, int head_dim, bool selected, int grid, cudaStream_t stream) {
+  return launch_held<false>(p, head_dim, selected, grid, stream);
 }
-
+#else
+cudaError_t setup_tiles() {
+  const cudaError_t e = setup_held<true>();
+  return e != cudaSuccess ? e : setup_tiles_bf16();
+}
 cudaError_t launch_tiles(const Params& p, int head_dim, bool i8, bool selected, int grid,
                          cudaStream_t stream) {
-  if (head_dim == 64) {
-    if (i8) return selected ? launch<64, true, true>(p, grid, stream) : launch<64, true, false>(p, grid, stream);
-    return selected ? launch<64, false, true>(p, grid, stream) : launch<64, false, false>(p, grid, stream);
-  }
-  if (i8) return selected ? launch<128, true, true>(p, grid, stream) : launch<128, true, false>(p, grid, stream);
-  return selected ? launch<128, false, true>(p, grid, stream) : launch<128, false, false>(p, grid, stream);
+  return i8 ? launch_held<true>(p, head_dim, selected, grid, stream) : launch_tiles_bf16(p, head_dim, selected, grid, stream);
 }
+#endif
 
 }  // namespace attn
 }  // namespace tks

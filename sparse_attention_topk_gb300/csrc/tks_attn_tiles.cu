@@ -553,10 +553,10 @@ struct RowSegments {
 
 // Warps 0-7: warps w and w + 4 have the rows of lanes 32w .. 32w + 31, warp w the first 64 keys of
 // every tile, warp w + 4 the others. Scores come in the layout of matrix fragments, 16 rows a
-// step: thread 4n + c has rows n and n + 8 and keys 8j + 2c, 8j + 2c + 1, so the scales that it
-// needs are an eighth of the tile's. A step's scores are read twice from tensor memory, for the
-// maxima and for the weights: the loops stay short (instructions not fetched in time were what
-// bound them), and few registers wait. Queries and outputs go by whole rows, a thread each, and
+// step (STEPS of them): thread 4n + c has rows n and n + 8 and keys 8j + 2c, 8j + 2c + 1, so the scales that it
+// needs are an eighth of the tile's. What few tiles need (masks, shifted rows) is done in tensor
+// memory ahead of the common way, which stays short: instructions not fetched in time bound a
+// longer one. Queries and outputs go by whole rows, a thread each, and
 // half the elements for each warp. Up to 64 rows lie in the first 16 lanes of each quarter, so
 // that all the warps share them.
 template <int D, bool I8, bool SEL, int STEPS>
@@ -644,19 +644,22 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
     next_back = back;
   };
 
-  // The scores of 16 rows, scaled, in pairs of keys: v[i][j] of row n + 8i, keys 8j + 2c, 8j + 2c + 1.
-  auto scores = [&](uint32_t addr, const float4* kl, float f, uint64_t (&v)[2][8]) {
-    uint32_t x[32];
-    tc_ld_frag(x, addr);
+  // The scores, scaled, in pairs of keys: v[h][i][j] of row 16h + n + 8i, keys 8j + 2c, 8j + 2c + 1.
+  auto scores = [&](uint32_t addr, const float4* kl, float f, uint64_t (&v)[STEPS][2][8]) {
+    uint32_t x[STEPS][32];
+#pragma unroll
+    for (int h = 0; h < STEPS; ++h) tc_ld_frag(x[h], addr + ((uint32_t)(16 * h) << 16));
     tc_wait_ld();
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const ulonglong2 e = I8 ? *reinterpret_cast<const ulonglong2*>(kl + 4 * j) : make_ulonglong2(pair(f, f), 0);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint64_t a = pair(__uint_as_float(x[4 * j + 2 * i]), __uint_as_float(x[4 * j + 2 * i + 1]));
-        v[i][j] = I8 ? fma2(a, e.x, e.y) : mul2(a, e.x);
-      }
+      for (int h = 0; h < STEPS; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t a = pair(__uint_as_float(x[h][4 * j + 2 * i]), __uint_as_float(x[h][4 * j + 2 * i + 1]));
+          v[h][i][j] = I8 ? fma2(a, e.x, e.y) : mul2(a, e.x);
+        }
     }
   };
 
@@ -722,75 +725,81 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
           f = 1.f;
         }
 
+        uint64_t v[STEPS][2][8];
+        scores(sb, kl, f, v);
+        float top[STEPS][2];
 #pragma unroll
-        for (int h = 0; h < STEPS; ++h) {
-          uint64_t v[2][8];
-          scores(sb + ((uint32_t)(16 * h) << 16), kl, f, v);
-          float top[2];
+        for (int h = 0; h < STEPS; ++h)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float2 a = unpair(v[i][0]), b = unpair(v[i][1]);
+            float2 a = unpair(v[h][i][0]), b = unpair(v[h][i][1]);
             float x0 = fmaxf(a.x, a.y), x1 = fmaxf(b.x, b.y);
 #pragma unroll
             for (int j = 2; j < 8; j += 2) {
-              a = unpair(v[i][j]);
-              b = unpair(v[i][j + 1]);
+              a = unpair(v[h][i][j]);
+              b = unpair(v[h][i][j + 1]);
               x0 = fmaxf(x0, fmaxf(a.x, a.y));
               x1 = fmaxf(x1, fmaxf(b.x, b.y));
             }
-            top[i] = fmaxf(x0, x1);
+            top[h][i] = fmaxf(x0, x1);
           }
 #pragma unroll
-          for (int o = 1; o < 4; o <<= 1)
+        for (int o = 1; o < 4; o <<= 1)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-          if (c == 0) pr.top[g & 1][half][h][n] = make_float2(top[0], top[1]);
-        }
+          for (int h = 0; h < STEPS; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) top[h][i] = fmaxf(top[h][i], __shfl_xor_sync(0xffffffffu, top[h][i], o));
+        if (c == 0)
+#pragma unroll
+          for (int h = 0; h < STEPS; ++h) pr.top[g & 1][half][h][n] = make_float2(top[h][0], top[h][1]);
         if (!meet()) return;
 
+        // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
+        bool grow = false;
 #pragma unroll
         for (int h = 0; h < STEPS; ++h) {
-          const float2 ta = pr.top[g & 1][0][h][n], tb = pr.top[g & 1][1][h][n];
-          const float top[2] = {fmaxf(ta.x, tb.x), fmaxf(ta.y, tb.y)};
-          // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
-          if (__any_sync(0xffffffffu, top[0] > m[h][0] + 8.f || top[1] > m[h][1] + 8.f)) {
+          const float2 y = pr.top[g & 1][half ^ 1][h][n];
+          top[h][0] = fmaxf(top[h][0], y.x);
+          top[h][1] = fmaxf(top[h][1], y.y);
+          grow |= top[h][0] > m[h][0] + 8.f || top[h][1] > m[h][1] + 8.f;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          if (t > t0 && !outputs_done(g - 1)) return;
+#pragma unroll
+          for (int h = 0; h < STEPS; ++h) {
             float back2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool up = top[i] > m[h][i] + 8.f;
-              back2[i] = up ? ex2(m[h][i] - top[i]) : 1.f;  // (m = -inf: 0)
-              if (up) m[h][i] = top[i];
+              const bool up = top[h][i] > m[h][i] + 8.f;
+              back2[i] = up ? ex2(m[h][i] - top[h][i]) : 1.f;  // (m = -inf: 0)
+              if (up) m[h][i] = top[h][i];
               sum[h][i] = mul2(sum[h][i], pair(back2[i], back2[i]));
             }
-            if (t > t0) {
-              if (!outputs_done(g - 1)) return;
+            if (t > t0)
 #pragma unroll 1
               for (int i = 0; i < D / 64; ++i)
                 rescale(mine + S::kO + half * (D / 2) + 32 * i + ((uint32_t)(16 * h) << 16), back2[0], back2[1]);
-            }
           }
-          uint64_t v[2][8], neg[2];
-          scores(sb + ((uint32_t)(16 * h) << 16), kl, f, v);
+        }
+
+        // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
+        uint32_t w[STEPS][16];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float u = m[h][i] == -INFINITY ? 0.f : -m[h][i];
-            neg[i] = pair(u, u);
-          }
-          // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
-          uint32_t w[16];
+        for (int j = 0; j < 8; ++j) {
+          const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
+          for (int h = 0; h < STEPS; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float2 a = unpair(add2(v[i][j], neg[i]));
+              const float u = m[h][i] == -INFINITY ? 0.f : -m[h][i];
+              const float2 a = unpair(add2(v[h][i][j], pair(u, u)));
               const float e0 = ex2(a.x), e1 = ex2(a.y);
               sum[h][i] = I8 ? fma2(pair(e0, e1), inv, sum[h][i]) : add2(sum[h][i], pair(e0, e1));
-              w[2 * j + i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+              w[h][2 * j + i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
             }
-          }
-          tc_st_frag(sb + ((uint32_t)(16 * h) << 16), w);
         }
+#pragma unroll
+        for (int h = 0; h < STEPS; ++h) tc_st_frag(sb + ((uint32_t)(16 * h) << 16), w[h]);
         tc_wait_st();
         tc_fence_before();
       }

@@ -57,6 +57,7 @@ struct Meta {
 template <int D, bool I8>
 struct Shape {
   static constexpr int kBlock = kKeys * 128;              // 64 elements of every row
+  static_assert(kBlock >> 4 == 1024 && 16 * 128 >> 4 == 128, "the steps of tc_scores and tc_outputs");
   static constexpr int kMat = (D / 64) * kBlock;          // a tile's keys, or its values
   static constexpr int kStages = D == 128 ? 3 : 6;
   static constexpr int kMetaOff = kStages * 2 * kMat;
@@ -160,14 +161,36 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 // Between the producers' ordinary stores to a stage and the products' reads of it. The warp that
 // issues the products executes it, after the barrier: a producer's own would also wait for the
-// loads that it has under way for the next tile (which took the wide tree from 224 us to FENCE_US).
+// loads that it has under way for the next tile (the wide tree of 64 drafts: 224 us, so 218).
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-// D (tensor memory) = A (tensor memory) x B (shared memory) (+ D)
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
-      : "memory");
+// A tile's product, D (tensor memory) (+)= A (tensor memory) x B (shared memory), sixteen of the
+// summed index an instruction, and the arrivals at barriers when it is done: one lane issues all of
+// it in one go, so that the tensor cores do not run dry between instructions. Step j's operands
+// lie ja columns of A and jb 16-byte pieces of B behind the first's.
+#define TKS_MMA(ja, jb) \
+  "add.s32 a, %1, " ja ";\n\tadd.s64 b, %2, " jb ";\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+#define TKS_COMMIT(n) "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%" n "];\n\t"
+#define TKS_MMA_BEGIN \
+  "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\t" \
+  "setp.eq.u32 t, 0, 0;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+// S = Q K^T: K-major keys, 32 bytes of a 128-byte row a step, blocks of 64 elements 16 KB apart.
+template <int D>
+__device__ __forceinline__ void tc_scores(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t bar) {
+  if (D == 128)
+    asm volatile(TKS_MMA_BEGIN TKS_MMA("8", "2") TKS_MMA("16", "4") TKS_MMA("24", "6") TKS_MMA("32", "1024") TKS_MMA("40", "1026")
+                     TKS_MMA("48", "1028") TKS_MMA("56", "1030") TKS_COMMIT("5") "}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(0), "r"(bar)
+                 : "memory");
+  else
+    asm volatile(TKS_MMA_BEGIN TKS_MMA("8", "2") TKS_MMA("16", "4") TKS_MMA("24", "6") TKS_COMMIT("5") "}" ::"r"(d), "r"(a), "l"(b),
+                 "r"(idesc), "r"(0), "r"(bar)
+                 : "memory");
+}
+// O (+)= P V: 16 keys' rows a step; the weights of the second 64 keys lie 64 columns behind the first's.
+__device__ __forceinline__ void tc_outputs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t bar0, uint32_t bar1, uint32_t bar2) {
+  asm volatile(TKS_MMA_BEGIN TKS_MMA("8", "128") TKS_MMA("16", "256") TKS_MMA("24", "384") TKS_MMA("64", "512") TKS_MMA("72", "640")
+                   TKS_MMA("80", "768") TKS_MMA("88", "896") TKS_COMMIT("5") TKS_COMMIT("6") TKS_COMMIT("7") "}" ::"r"(d), "r"(a), "l"(b),
+               "r"(idesc), "r"((unsigned)add), "r"(bar0), "r"(bar1), "r"(bar2)
+               : "memory");
 }
 #define TKS_R32(M) M(0), M(1), M(2), M(3), M(4), M(5), M(6), M(7), M(8), M(9), M(10), M(11), M(12), M(13), M(14), M(15), \
                    M(16), M(17), M(18), M(19), M(20), M(21), M(22), M(23), M(24), M(25), M(26), M(27), M(28), M(29), M(30), M(31)
@@ -485,10 +508,7 @@ __device__ __forceinline__ void multiply(const Params& p, const Block& k, const 
         tc_fence_after();
         const uint64_t b = keys0 + (uint32_t)(kr.i * (2 * S::kMat >> 4));
         const uint32_t d = tmem + S::kS + (gk & 1) * 128;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          tc_mma(d, tmem + S::kQ + 8 * j, b + (j >> 2) * (S::kBlock >> 4) + (j & 3) * 2, kQk, j > 0);
-        tc_commit(k.bar(kSFull + (gk & 1)));
+        tc_scores<D>(d, tmem + S::kQ, b, kQk, k.bar(kSFull + (gk & 1)));
         kr.next();
         ++gk;
       }
@@ -498,12 +518,7 @@ __device__ __forceinline__ void multiply(const Params& p, const Block& k, const 
         tc_fence_after();
         const uint64_t v = values0 + (uint32_t)(vr.i * (2 * S::kMat >> 4));
         const uint32_t a = tmem + S::kS + (gv & 1) * 128;
-#pragma unroll
-        for (int j = 0; j < kKeys / 16; ++j)
-          tc_mma(tmem + S::kO, a + (j >> 2) * 64 + (j & 3) * 8, v + j * (16 * 128 >> 4), kPv, i > 1 || j > 0);
-        tc_commit(k.bar(kEmpty + vr.i));
-        tc_commit(k.bar(kMetaEmpty + mr.i));
-        tc_commit(k.bar(kPvDone + (gv & 1)));
+        tc_outputs(tmem + S::kO, a, v, kPv, i > 1, k.bar(kEmpty + vr.i), k.bar(kMetaEmpty + mr.i), k.bar(kPvDone + (gv & 1)));
         mr.next();
         vr.next();
         ++gv;

@@ -694,6 +694,13 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
     }
 
     const int t0 = uniform(s.t0), t1 = uniform(s.t1);
+    // the next segment's queries are brought near while this one's tiles run
+    more = advance(at ^ 1);
+    if (more) {
+      const Segment& next = segs.s[at ^ 1];
+      const int Rn = next.row_tile * kTilesRows + row_lane;
+      if (Rn < p.rows) prefetch_l2(q_row<SEL>(p, next.seq, next.head, Rn) + half * (D / 2));
+    }
     for (int t = t0; t < t1; ++t, ++g) {
       const uint32_t sb = mine + S::kS + (g & 1) * 128 + half * 64;
       if (!warp_live) {
@@ -825,7 +832,6 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
 
     // The next segment's queries first (its scores can begin), then this one's output.
     const Segment& done = s;
-    more = advance(at ^ 1);
     if (more) queries(segs.s[at ^ 1]);
     if (!outputs_done(g - 1)) return;
     if (warp_live) {

@@ -267,6 +267,19 @@ Params params_of(const tks_cache* c, const tks_queries* q) {
   return p;
 }
 
+// The cluster size that a unit of at most `tiles` tiles is split over, or 0. Clusters pay where the
+// device holds all units at once and shares are short: up to 1024 keys where the blocks fill more
+// than half of the device (4 sequences of 7000 positions, 8 heads: 19.3 us, 21.5 with a second
+// kernel), up to 640 where more blocks would help (one sequence of 7000: 14.4 us in a cluster of 8,
+// 13.1 over 304 blocks; of 2048: 9.3 and 12.1). Selected positions of many rows keep the second
+// kernel: one query of 64 heads over 256 takes 11.6 us with a cluster and 9.5 without.
+int cluster_of(long long units, int64_t tiles, int tile_keys, int blocks) {
+  int n = 1;
+  while (n < kClusterMax && 2 * n * units <= blocks && n < tiles) n *= 2;
+  const int64_t keys = 2 * n * units > blocks ? 1024 : 640;
+  return units <= blocks && tiles <= n * (keys / tile_keys) ? n : 0;
+}
+
 // Queues the attention kernel and the one that joins its partials. (A unit's last block joining
 // them instead, by a count of the blocks that are done, saved 3 us of host time and cost more on
 // the GPU: one token over 2048 selected positions 11.7 us against 10.5.)
@@ -289,18 +302,24 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   if ((keys / tile_keys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
   const long long units = (long long)p.seqs * p.kv_heads * p.row_tiles;
   if (units > INT32_MAX) return TKS_E_TOO_LARGE;
-  const int grid = few ? d.sms * kRowsBlocksPerSm : d.sms;
+  int grid = few ? d.sms * kRowsBlocksPerSm : d.sms;
   p.plan = reinterpret_cast<Split*>(ws.ptr + kPlanOffset);
   if (selected) {
     const long long tiles = std::max(1, (p.k_sel + tile_keys - 1) / tile_keys);
     p.split.set(units * tiles, (unsigned)tiles, units, grid);
   }
+  const int cluster = selected && !few ? 0 : cluster_of(units, (keys + tile_keys - 1) / tile_keys, tile_keys, grid);
+  if (cluster > 0) {
+    p.cluster = cluster;
+    p.split.share = (unsigned)cluster;
+    grid = (int)units * cluster;
+  }
   if (few) {
     e = launch_rows(p, c->head_dim, i8, selected, grid, s);
-    if (e == cudaSuccess) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
+    if (e == cudaSuccess && !cluster) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
   } else {
     e = launch_tiles(p, c->head_dim, i8, selected, grid, s);
-    if (e == cudaSuccess) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);
+    if (e == cudaSuccess && !cluster) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -92,8 +92,9 @@ struct Params {
   int row_tiles;
   unsigned* status;
   float* parts;
+  int cluster;  // > 0: the blocks of a unit are one thread-block cluster of this size, which joins itself
   Split* plan;  // trees: the split, for the kernel that joins
-  Split split;  // selected: the split
+  Split split;  // selected, and clusters: the split
   long long spin_limit_ns;
   int test_skip_arrive;
 };
@@ -101,6 +102,7 @@ struct Params {
 // The kernels for few rows (16 a block; mma.sync).
 constexpr int kRowsTile = 16;  // query rows of a block
 constexpr int kRowsKeys = 64;  // keys of a tile
+constexpr int kClusterMax = 8;  // (portable; clusters of 16 start later: 10.6 us where 8 take 9.0)
 constexpr int kRowsBlocksPerSm = 2;
 cudaError_t setup_rows();
 cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,

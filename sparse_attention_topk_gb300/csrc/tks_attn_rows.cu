@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kRings = kWarps * kStages * kStage;
   static constexpr int kSlots = 1024 * 4;              // and where keys lie
   static constexpr int kSmem = kRings + kQs + kConst + kSlots;
-  static_assert(kRings >= kWarps * (16 * D * 4 + 16 * 8), "the merge fits the ring");
+  static_assert(kRings >= (kWarps + 1) * (16 * D * 4 + 16 * 8), "the merge fits the ring");
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
   static __device__ __forceinline__ int ksw(int r) { return kPieces >= 8 ? (r & 1) << 2 : 0; }
@@ -129,6 +129,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   grid_launch_dependents();
   if (warp == 0) find_start<SEL, kRowsKeys>(p, &start);
   __syncthreads();
+  // clusters: this block's partial, behind the warps' outputs
+  float* part_s = reinterpret_cast<float*>(smem) + kWarps * 16 * D;
+  float2* part_ml = reinterpret_cast<float2*>(part_s + 16 * D);
   Segments<SEL, kRowsKeys> segments;
   segments.begin(start);
   Segment sg;
@@ -519,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       ml_s[warp][n + 8] = make_float2(m[1], l[1]);
     }
     __syncthreads();
-    const bool whole = sg.whole();
-    float* part = p.parts + (2LL * blockIdx.x + (sg.first ? 0 : 1)) * kPartFloats<kRowsTile, D>;
+    const bool whole = sg.whole() && !p.cluster;
+    float* part = p.cluster ? part_s : p.parts + (2LL * blockIdx.x + (sg.first ? 0 : 1)) * kPartFloats<kRowsTile, D>;
     const float* om0 = reinterpret_cast<const float*>(smem);
 #pragma unroll 1
     for (int x = threadIdx.x; x < min(rows_left, 16) * (D / 4); x += kThreads) {
@@ -554,6 +557,10 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     }
     __syncthreads();  // the ring is free for the next segment
   }
+  if (p.cluster) {
+    if (start.left == 0 && threadIdx.x < 16) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    join_cluster<kRowsTile, D, SEL>(p, smem_addr(part_s), smem_addr(part_ml), kThreads);
+  }
 }
 
 template <int D, bool I8, bool SEL, bool PAGED>
@@ -563,11 +570,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<D, I8>::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute a[1] = {};
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = launch_attributes(a, p.cluster);
   return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED>, p);
 }
 template <int D, bool I8>
@@ -579,10 +584,9 @@ cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream
 
 template <int D, bool I8>
 cudaError_t opt_in() {
-  const auto what = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, I8, true, false>, what, Shape<D, I8>::kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D, I8, false, true>, what, Shape<D, I8>::kSmem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(rows_kernel<D, I8, false, false>, what, Shape<D, I8>::kSmem);
+  cudaError_t e = allow(rows_kernel<D, I8, true, false>, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, true>, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, false>, Shape<D, I8>::kSmem);
   return e;
 }
 

@@ -861,7 +861,9 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
       const float inv = empty ? 0.f : 1.f / lr;
       const bool fix = !I8 && !SEL && *k.poisoned != 0;
       const long long row = out_row<SEL>(p, done.seq, done.head, min(R, p.rows - 1));
-      float* part = p.parts + (2LL * blockIdx.x + (done.first ? 0 : 1)) * kPartFloats<kTilesRows, D>;
+      // (in a cluster, the block's one partial takes the place of its stages, which are done with)
+      const bool whole = done.whole() && !p.cluster;
+      float* part = p.cluster ? reinterpret_cast<float*>(k.smem) : p.parts + (2LL * blockIdx.x + (done.first ? 0 : 1)) * kPartFloats<kTilesRows, D>;
 #pragma unroll 1
       for (int i = 0; i < D / 64; ++i) {
         const int d = half * (D / 2) + 32 * i;
@@ -887,7 +889,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
               }
             }
           }
-          if (done.whole()) {
+          if (whole) {
             uint4* out = reinterpret_cast<uint4*>(p.out + row * D + d);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -902,7 +904,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
         __syncwarp();
       }
       if (R < p.rows && half == 0) {
-        if (!done.whole())
+        if (!whole)
           *reinterpret_cast<float2*>(part + kTilesRows * D + 2 * row_lane) = make_float2(top, empty ? 0.f : lr);
         else if (p.lse)
           p.lse[row] = empty ? -INFINITY : (top + lg2(lr)) * 0.6931471805599453f;
@@ -989,6 +991,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.cluster) {
+    float2* ml = reinterpret_cast<float2*>(smem + kTilesRows * D * 4);
+    if (start.left == 0 && threadIdx.x < kTilesRows) ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    join_cluster<kTilesRows, D, SEL>(p, smem_addr(smem), smem_addr(ml), kRowWarps * 32);  // (the others have given registers up)
+  }
   if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
@@ -999,11 +1006,9 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = Shape<D, I8>::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute a[1] = {};
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = launch_attributes(a, p.cluster);
   return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL, STEPS>, p);
 }
 template <bool I8>
@@ -1019,9 +1024,8 @@ cudaError_t launch_held(const Params& p, int head_dim, bool selected, int grid, 
 
 template <int D, bool I8, bool SEL>
 cudaError_t opt_in() {
-  const auto what = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  const cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, I8, SEL, 1>, what, Shape<D, I8>::kSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(tiles_kernel<D, I8, SEL, 2>, what, Shape<D, I8>::kSmem);
+  const cudaError_t e = allow(tiles_kernel<D, I8, SEL, 1>, Shape<D, I8>::kSmem);
+  return e != cudaSuccess ? e : allow(tiles_kernel<D, I8, SEL, 2>, Shape<D, I8>::kSmem);
 }
 template <bool I8>
 cudaError_t setup_held() {

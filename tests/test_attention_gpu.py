@@ -44,14 +44,14 @@ def ancestors(parents):
 
 
 def tree_case(ctx, drafts, q_heads, kv_heads, dim, held, page, layout="tokens", tree="random", counts=None, seed=0, scale=None,
-              spread=1.5):
+              spread=1.5, room=1):
     g = gen(seed)
     batch = len(ctx)
     counts = [drafts] * batch if counts is None else counts
     lens = [c + d for c, d in zip(ctx, counts)]
     pages = sum(-(-n // page) for n in lens) + 2
     cache = PagedCache(pages, page, kv_heads, dim, held, layout, seed)
-    width = max(1, max(-(-n // page) for n in lens) + 1)
+    width = max(1, max(-(-n // page) for n in lens) + room)  # (`room`: columns of the page table without a page)
     tables, held_rows = [], []
     for n in lens:
         t, k, v = cache.fill(rand_rows(n, kv_heads, dim, g), rand_rows(n, kv_heads, dim, g), width)
@@ -137,6 +137,21 @@ def test_long_contexts_are_split(held):
     tree_case([50003], 1, 8, 1, 128, held, 64)
     tree_case([30011, 17], 8, 16, 1, 64, held, 64)
     tree_case([30011], 20, 16, 1, 128, held, 64)
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("drafts, heads, kv_heads", [(1, 8, 2), (3, 4, 4), (30, 8, 2), (70, 4, 2)])
+def test_page_tables_with_room_to_spare(drafts, heads, kv_heads, held):
+    """Short sequences that could be long: blocks split by the lengths on the device."""
+    tree_case([700, 0, 33, 1, 450], drafts, heads, kv_heads, 64, held, 16, counts=[drafts, drafts, 0, 1, drafts], room=2000)
+    tree_case([130], drafts, heads, kv_heads, 128, held, 16, room=2000)
+
+
+@pytest.mark.parametrize("held", HELD)
+def test_more_units_than_blocks(held):
+    tree_case([(61 * i) % 200 for i in range(90)], 1, 8, 4, 64, held, 16, room=600)
+    tree_case([(61 * i) % 200 for i in range(45)], 9, 16, 4, 64, held, 16)
+    tree_case([3000, 5] + [1] * 60, 9, 8, 4, 64, held, 64, room=300)
 
 
 @pytest.mark.parametrize("held", HELD)
@@ -347,6 +362,14 @@ def test_selected_padding_and_short_rows(q_heads, held):
 def test_selected_many_tokens(held):
     selected_case([1000], 100, 64, 8, 1, 64, held, 16)
     selected_case([1000], 60, 200, 64, 1, 128, held, 16)
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("q_heads, kv_heads", [(4, 2), (40, 1)])
+def test_selected_long_lists_and_many_units(q_heads, kv_heads, held):
+    selected_case([12000], 1, 9001, q_heads, kv_heads, 64, held, 64)
+    selected_case([12000, 700], 2, 5000, q_heads, kv_heads, 128, held, 64)
+    selected_case([300], 170, 70, q_heads, kv_heads, 64, held, 16)
 
 
 @pytest.mark.parametrize("q_heads", [4, 64])

@@ -862,8 +862,8 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
       const bool fix = !I8 && !SEL && *k.poisoned != 0;
       const long long row = out_row<SEL>(p, done.seq, done.head, min(R, p.rows - 1));
       // (in a cluster, the block's one partial takes the place of its stages, which are done with)
-      const bool whole = done.whole() && !p.cluster;
-      float* part = p.cluster ? reinterpret_cast<float*>(k.smem) : p.parts + (2LL * blockIdx.x + (done.first ? 0 : 1)) * kPartFloats<kTilesRows, D>;
+      const bool whole = done.whole() && (SEL || !p.cluster);
+      float* part = !SEL && p.cluster ? reinterpret_cast<float*>(k.smem) : p.parts + (2LL * blockIdx.x + (done.first ? 0 : 1)) * kPartFloats<kTilesRows, D>;
 #pragma unroll 1
       for (int i = 0; i < D / 64; ++i) {
         const int d = half * (D / 2) + 32 * i;
@@ -977,6 +977,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   if (warp < kRowWarps) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
     rows<D, I8, SEL, STEPS>(p, k, start, tmem, segs[warp], pair_rows[warp & 3], plain_kl);
+    if (!SEL && p.cluster) {  // (the other warps have given registers up)
+      float2* ml = reinterpret_cast<float2*>(smem + kTilesRows * D * 4);
+      if (start.left == 0 && threadIdx.x < kTilesRows) ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+      __syncwarp();
+      join_cluster<kTilesRows, D, SEL>(p, smem_addr(smem), smem_addr(ml), kRowWarps * 32);
+    }
   } else if (warp < kRowWarps + 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kMulWarp) {
@@ -988,14 +994,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     produce<D, I8>(p, k, tiles);
   }
+  if (!SEL && p.cluster && warp >= kRowWarps) {  // join_cluster's two meetings
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.cluster) {
-    float2* ml = reinterpret_cast<float2*>(smem + kTilesRows * D * 4);
-    if (start.left == 0 && threadIdx.x < kTilesRows) ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
-    join_cluster<kTilesRows, D, SEL>(p, smem_addr(smem), smem_addr(ml), kRowWarps * 32);  // (the others have given registers up)
-  }
   if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 

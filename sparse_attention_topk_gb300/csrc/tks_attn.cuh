@@ -76,6 +76,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+// Two weights as sums of two bfloat16 each: `first`, cut off a little below the weight, and what is
+// left, rounded. Both parts of a positive weight are positive, so that an infinite value times
+// them is that infinity.
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& first, uint32_t& rest) {
+  const uint32_t x = __float_as_uint(a * 0.99609375f), y = __float_as_uint(b * 0.99609375f);
+  first = __byte_perm(x, y, 0x7632);
+  rest = pack_bf16(a - __uint_as_float(x & 0xffff0000u), b - __uint_as_float(y & 0xffff0000u));
+}
 
 // Two codes as a pair of halves, exactly: `biased` holds codes + 128 as bytes
 // (code ^ 0x80), a byte u under the exponent 0x64 is 1024 + u, and 1152 is

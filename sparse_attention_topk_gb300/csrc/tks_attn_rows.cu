@@ -12,8 +12,9 @@
 // precision, one multiply-add applies both scales to a score, and the weights
 // are rounded (to 11 bits) relative to the largest contribution to the output.
 // Queries are bfloat16; they enter as halves, exactly, after a shift by a
-// power of two that is common to the block's rows.  Over a bfloat16 cache the
-// weights are rounded to bfloat16 (the products want one type).
+// power of two that is common to the block's rows.  Over a bfloat16 cache, whose
+// products want bfloat16 weights, a weight goes in as the sum of two (rounded to
+// one, weights made outputs 1.4 times less exact).
 //
 // What bounds it: the cache's bytes, each read once.  One matrix instruction
 // works on 16 rows, so up to 16 rows of a head cost the same; 16 keys of int8
@@ -422,8 +423,15 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       for (int g = 0; g < kNT / 2; ++g) {
         const float(&sa)[4] = s[2 * g];
         const float(&sb)[4] = s[2 * g + 1];
-        const uint4 pf = I8 ? make_uint4(pack_half(sa[0], sa[1]), pack_half(sa[2], sa[3]), pack_half(sb[0], sb[1]), pack_half(sb[2], sb[3]))
-                            : make_uint4(pack_bf16(sa[0], sa[1]), pack_bf16(sa[2], sa[3]), pack_bf16(sb[0], sb[1]), pack_bf16(sb[2], sb[3]));
+        uint4 pf, rest;
+        if (I8) {
+          pf = make_uint4(pack_half(sa[0], sa[1]), pack_half(sa[2], sa[3]), pack_half(sb[0], sb[1]), pack_half(sb[2], sb[3]));
+        } else {
+          split_bf16(sa[0], sa[1], pf.x, rest.x);
+          split_bf16(sa[2], sa[3], pf.y, rest.y);
+          split_bf16(sb[0], sb[1], pf.z, rest.z);
+          split_bf16(sb[2], sb[3], pf.w, rest.w);
+        }
 #pragma unroll
         for (int h = 0; h < S::kVH; ++h) {
           constexpr int kW = S::kEV * S::kElem / 4;
@@ -462,8 +470,12 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
               mma<true>(acc[i + 3], pf, codes_to_half2<0x4342>(hi0), codes_to_half2<0x4342>(hi1));
             } else {
               const int i = h * S::kEV + 2 * x;
-              mma<false>(acc[i], pf, __byte_perm(vw[0][x], vw[1][x], 0x5410), __byte_perm(vw[2][x], vw[3][x], 0x5410));
-              mma<false>(acc[i + 1], pf, __byte_perm(vw[0][x], vw[1][x], 0x7632), __byte_perm(vw[2][x], vw[3][x], 0x7632));
+              const uint32_t a0 = __byte_perm(vw[0][x], vw[1][x], 0x5410), a1 = __byte_perm(vw[2][x], vw[3][x], 0x5410);
+              const uint32_t b0 = __byte_perm(vw[0][x], vw[1][x], 0x7632), b1 = __byte_perm(vw[2][x], vw[3][x], 0x7632);
+              mma<false>(acc[i], pf, a0, a1);
+              mma<false>(acc[i + 1], pf, b0, b1);
+              mma<false>(acc[i], rest, a0, a1);
+              mma<false>(acc[i + 1], rest, b0, b1);
             }
           }
         }

@@ -186,6 +186,11 @@ __device__ __forceinline__ void tc_scores(uint32_t d, uint32_t a, uint64_t b, ui
                  : "memory");
 }
 // O (+)= P V: 16 keys' rows a step; the weights of the second 64 keys lie 64 columns behind the first's.
+__device__ __forceinline__ void tc_outputs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(TKS_MMA_BEGIN TKS_MMA("8", "128") TKS_MMA("16", "256") TKS_MMA("24", "384") TKS_MMA("64", "512") TKS_MMA("72", "640")
+                   TKS_MMA("80", "768") TKS_MMA("88", "896") "}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+               : "memory");
+}
 __device__ __forceinline__ void tc_outputs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, uint32_t bar0, uint32_t bar1, uint32_t bar2) {
   asm volatile(TKS_MMA_BEGIN TKS_MMA("8", "128") TKS_MMA("16", "256") TKS_MMA("24", "384") TKS_MMA("64", "512") TKS_MMA("72", "640")
                    TKS_MMA("80", "768") TKS_MMA("88", "896") TKS_COMMIT("5") TKS_COMMIT("6") TKS_COMMIT("7") "}" ::"r"(d), "r"(a), "l"(b),
@@ -518,7 +523,8 @@ __device__ __forceinline__ void multiply(const Params& p, const Block& k, const 
         tc_fence_after();
         const uint64_t v = values0 + (uint32_t)(vr.i * (2 * S::kMat >> 4));
         const uint32_t a = tmem + S::kS + (gv & 1) * 128;
-        tc_outputs(tmem + S::kO, a, v, kPv, i > 1, k.bar(kEmpty + vr.i), k.bar(kMetaEmpty + mr.i), k.bar(kPvDone + (gv & 1)));
+        if (!I8) tc_outputs(tmem + S::kO, a + 32, v, kPv, i > 1);  // the weights' second parts
+        tc_outputs(tmem + S::kO, a, v, kPv, !I8 || i > 1, k.bar(kEmpty + vr.i), k.bar(kMetaEmpty + mr.i), k.bar(kPvDone + (gv & 1)));
         mr.next();
         vr.next();
         ++gv;
@@ -804,8 +810,9 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
           }
         }
 
-        // Weights and their sums; their halves go over the scores' first 32 columns of these 64 keys.
-        uint32_t w[STEPS][16];
+        // Weights and their sums. Rounded, they go over the scores' first 32 columns of these 64 keys
+        // (bfloat16: their second parts over the other 32).
+        uint32_t w[STEPS][16], rest[I8 ? 1 : STEPS][16];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const uint64_t inv = I8 ? *reinterpret_cast<const uint64_t*>(meta.inv + 64 * half + 8 * j + 2 * c) : 0;
@@ -817,11 +824,15 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
               const float2 a = unpair(add2(v[h][i][j], pair(u, u)));
               const float e0 = ex2(a.x), e1 = ex2(a.y);
               sum[h][i] = I8 ? fma2(pair(e0, e1), inv, sum[h][i]) : add2(sum[h][i], pair(e0, e1));
-              w[h][2 * j + i] = I8 ? pack_half(e0, e1) : pack_bf16(e0, e1);
+              if (I8) w[h][2 * j + i] = pack_half(e0, e1);
+              else split_bf16(e0, e1, w[h][2 * j + i], rest[I8 ? 0 : h][2 * j + i]);
             }
         }
 #pragma unroll
-        for (int h = 0; h < STEPS; ++h) tc_st_frag(sb + ((uint32_t)(16 * h) << 16), w[h]);
+        for (int h = 0; h < STEPS; ++h) {
+          tc_st_frag(sb + ((uint32_t)(16 * h) << 16), w[h]);
+          if (!I8) tc_st_frag(sb + 32 + ((uint32_t)(16 * h) << 16), rest[I8 ? 0 : h]);
+        }
         tc_wait_st();
         tc_fence_before();
       }

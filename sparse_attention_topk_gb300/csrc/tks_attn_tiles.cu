@@ -984,9 +984,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const uint32_t tmem = uniform(tmem_s);
   const int tiles = uniform((int)start.left);
 
-  // registers: 2 * 128 + 64 + 2 * 80 of the launch's 5 * 96
+  // Registers, of the launch's 5 * 96: 2 * 128 + 64 + 2 * 80, or, where weights are split in two and
+  // rows go straight to shared memory, 2 * 144 + 64 + 2 * 64.
   if (warp < kRowWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(I8 ? 128 : 144));
     rows<D, I8, SEL, STEPS>(p, k, start, tmem, segs[warp], pair_rows[warp & 3], plain_kl);
     if (!SEL && p.cluster) {  // (the other warps have given registers up)
       float2* ml = reinterpret_cast<float2*>(smem + kTilesRows * D * 4);
@@ -1002,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       look_up<D, I8, SEL>(p, k, start, warp - kMetaWarp0);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(I8 ? 80 : 64));
     produce<D, I8>(p, k, tiles);
   }
   if (!SEL && p.cluster && warp >= kRowWarps) {  // join_cluster's two meetings

@@ -13,10 +13,18 @@
  * Status codes, streams, workspaces and device-side errors are those of tks.h:
  * calls are asynchronous on `stream`, argument errors return TKS_E_INVAL and
  * launch nothing, and errors found on the device are read with
- * tks_device_status(stream).  The library allocates one workspace for each
- * (device, stream) on the first of these calls on it (make that call before
- * any CUDA-graph capture); later calls allocate nothing and never synchronise.
+ * tks_device_status(stream) (which reports one at a time: first those of the
+ * selection, then, at its next call, those of the calls below).  The library
+ * allocates one workspace for each (device, stream) on the first of these calls
+ * on it (make that call before any CUDA-graph capture); later calls allocate
+ * nothing and never synchronise, and tks_release frees it with the others.
  * The caller owns every buffer, which must stay valid until the work completes.
+ *
+ * Results do not depend on timing: the same call gives the same bits.  Waits
+ * inside the attention kernels are bounded by TKS_OPT_SPIN_LIMIT_NS; one that
+ * runs out is reported as TKS_E_TIMEOUT, and the outputs of that call are then
+ * undefined.  (TKS_OPT_TEST_SKIP_ARRIVE makes one run out where a call has more
+ * than 16 query rows for a key/value head.)
  */
 #ifndef TKS_ATTENTION_H
 #define TKS_ATTENTION_H
@@ -75,6 +83,8 @@ typedef struct {
  *     code  = x * (1/scale), rounded to nearest even, held to [-127, 127]
  * so infinities count as the largest value, and a row with a NaN gets a NaN
  * scale: every query that attends to it has a NaN result, and no other.
+ * (2^-40 / 127 lies above 2^-47, below which the attention calls take a value's
+ * scale for 2^-47.)
  */
 int tks_cache_write(const tks_cache *cache, const void *k, const void *v, int32_t n,
                     int32_t dtype, int64_t k_token_stride, int64_t k_head_stride,
@@ -96,6 +106,9 @@ int tks_cache_read(const tks_cache *cache, const int32_t *slots, int32_t n, void
  * (q_heads / kv_heads).  Position p of sequence b is token p % page_size of
  * page page_table[b * table_stride + p / page_size].  A position whose page is
  * outside [0, pages) counts as not attended and is reported as TKS_E_INDEX.
+ * Sizes whose work cannot be counted in 32 bits (key/value heads times the
+ * longest sequence's positions / 64, or sequences times heads, beyond 2^31)
+ * return TKS_E_TOO_LARGE and launch nothing.
  */
 typedef struct {
     const void *q;              /* 16-byte aligned; strides in elements, multiples of 8 */
@@ -125,9 +138,8 @@ typedef struct {
  *              draft j < draft_len[b] where bit j % 32 of word j / 32 is set
  *
  * ctx_len is held to [0, table_pages * page_size] (a sequence has at most 2^31 -
- * 65536 positions), draft_len to [0, tokens]
- * and to what is left of the page table; a length that had to be changed is
- * reported as TKS_E_ROW_LEN.  A query that attends to nothing gives zeros, and
+ * 65536 positions), draft_len to [0, tokens] and to what is left of the page
+ * table; a length that had to be changed is reported as TKS_E_ROW_LEN.  A query that attends to nothing gives zeros, and
  * -inf in lse.  What the cache holds where a query does not attend has no
  * influence on it, NaN and infinities included.  tokens <= TKS_DRAFTS_MAX;
  * tokens = 1 is the attention of an ordinary decode step.

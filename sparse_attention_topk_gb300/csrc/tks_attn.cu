@@ -3,8 +3,9 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
+#include <exception>
 #include <map>
+#include <memory>
 #include <mutex>
 #include <utility>
 
@@ -116,7 +117,9 @@ cudaError_t combine(const Params& p, cudaStream_t stream) {
 
 template <int ROWS, int TK>
 cudaError_t launch_combine(const Params& p, int head_dim, bool selected, int blocks, cudaStream_t s) {
-  // many partials for a unit, or few
+  // Many partials for a unit, or few: one token over 1M positions of 4 heads (76 partials a unit) takes
+  // 194 us with a block for each row and 207 with a warp; four of 64 heads over 2048 selected ones
+  // (16) 12.4 and 15.2; 8 ragged sequences of 8 heads (2 or 3) 203 and 195.
   const bool many = (long long)p.seqs * p.kv_heads * p.row_tiles * 8 < blocks;
   if (head_dim == 64) {
     if (selected) return many ? combine<ROWS, 64, TK, true, 1>(p, s) : combine<ROWS, 64, TK, true, 8>(p, s);
@@ -135,6 +138,8 @@ struct Device {
 };
 struct Workspace {
   unsigned char* ptr = nullptr;  // status word, the last call's split, then (at 256 bytes) partial slots
+  // A call's two kernels follow each other on the stream, without another thread's between them.
+  std::shared_ptr<std::mutex> order;
 };
 
 constexpr size_t kPlanOffset = 64, kHeaderBytes = 256;
@@ -150,7 +155,7 @@ size_t part_bytes(const Device& d) {
 }
 
 // The current device and its workspace for `stream`, allocated on first use.
-int prepare(void* stream, Device* dev, Workspace* ws) {
+int prepare(void* stream, Device* dev, Workspace* ws) try {
   int id = 0;
   if (cudaGetDevice(&id) != cudaSuccess) {
     cudaGetLastError();
@@ -174,6 +179,7 @@ int prepare(void* stream, Device* dev, Workspace* ws) {
   auto wi = g_ws.find(key);
   if (wi == g_ws.end()) {
     Workspace w;
+    w.order = std::make_shared<std::mutex>();
     if (cudaMalloc(&w.ptr, kHeaderBytes + part_bytes(*dev)) != cudaSuccess) {
       cudaGetLastError();
       return TKS_E_CUDA;
@@ -187,6 +193,8 @@ int prepare(void* stream, Device* dev, Workspace* ws) {
   }
   *ws = wi->second;
   return TKS_OK;
+} catch (const std::exception&) {  // (host memory ran out: no C++ exception leaves a C entry point)
+  return TKS_E_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -296,6 +304,10 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   p.spin_limit_ns = spin_limit_ns();
   p.test_skip_arrive = test_skip_arrive();
   cudaError_t e;
+  // Few rows: mma.sync with 16, else tcgen05 with 128 of them. With the latter for few rows too, one token
+  // over 1M positions takes 288 us instead of 194, 64 over 2048 selected ones of 2 heads 38.2 instead
+  // of 30.6: the operands' way through shared memory is paid for rows that are not there. (More than
+  // 16 would be read twice by the former.)
   const bool few = p.rows <= kRowsTile;
   const int tile = few ? kRowsTile : kTilesRows, tile_keys = few ? kRowsKeys : kTilesKeys;
   p.row_tiles = (p.rows + tile - 1) / tile;
@@ -314,6 +326,7 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
     p.split.share = (unsigned)cluster;
     grid = (int)units * cluster;
   }
+  std::lock_guard<std::mutex> lock(*ws.order);
   if (few) {
     e = launch_rows(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess && !cluster) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
@@ -355,7 +368,7 @@ int attn_status(int dev, void* stream) {
   Workspace w;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    auto it = g_ws.find(std::make_pair(dev, stream));
+    const auto it = g_ws.find(std::make_pair(dev, stream));
     if (it == g_ws.end()) return TKS_OK;
     w = it->second;
   }

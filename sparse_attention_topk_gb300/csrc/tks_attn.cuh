@@ -11,15 +11,16 @@
 // Starting a segment costs a block as much as kSegmentTiles tiles (lookups and
 // queries come first, and the joining and the output last), so even shares are
 // taken where the longest of them is not longer than an equal run and that (one
-// token over 4096 positions of 8 heads: 15.6 us as a run, 12.6 in even shares).  A block that holds all of a unit writes its output; otherwise it
-// writes a partial result (unnormalised output, running maximum, sum) to its
-// slot of the workspace, and the unit's partials are joined in block order, so
-// results do not depend on timing.  Where shares are even and short (the host can
+// token over 4096 positions of 8 heads: 15.6 us as a run, 12.6 in even shares).
+// A block that holds all of a unit writes its output; otherwise it writes a
+// partial result (unnormalised output, running maximum, sum) to its slot of the
+// workspace, and the unit's partials are joined in block order, so results do
+// not depend on timing.  A block has at most two partial segments, its first
+// (slot 0) and its last (slot 1).  Where shares are even and short (the host can
 // tell from the list's or the page table's length), the blocks of a unit are a
 // thread-block cluster: they leave their partials in their shared memory, and
 // join them from there without another kernel (one token over 2048 selected
-// positions: 10.8 us with the other kernel, 9.3 as clusters).  A block has at most two partial
-// segments, its first (slot 0) and its last (slot 1).
+// positions: 10.8 us with the other kernel, 9.3 as clusters).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -508,8 +509,7 @@ inline unsigned launch_attributes(cudaLaunchAttribute* a, int cluster) {
 }
 template <typename K>
 cudaError_t allow(K kernel, int smem) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 // Floats of a partial slot: ROWS x D of output, then ROWS pairs (maximum, sum).

@@ -19,6 +19,9 @@
 // What bounds it: the cache's bytes, each read once.  One matrix instruction
 // works on 16 rows, so up to 16 rows of a head cost the same; 16 keys of int8
 // (4 KB) take 32 of them, a third of their rate at the memory's pace.
+// Measured: one token over 1,048,576 positions of int8 (4 heads of 128, 1.11 GB)
+// 184-194 us, 5.7-6.0 TB/s; one over 4096 (8 heads, 8.7 MB) 11.6 us, bound by
+// the chain of lookups, copies and joins that a lone call cannot hide.
 //
 // Layout.  A block is four warps; each takes every fourth chunk of the block's
 // segment (32 keys of int8, 16 of bfloat16: 8 KB), keeps its own maximum, sum and
@@ -26,9 +29,10 @@
 // warps meet only at a segment's end.  Where the keys lie is looked up (list, page
 // table) for 1024 of them at once, the block's threads side by side, before their
 // copies start (one chunk ahead, it bound a gather of rows: 64 tokens over 2048
-// selected positions of bfloat16, 35.0 us against GATHER_US); chunks that lie in one
-// page each take one lookup, a chunk ahead.  The order of the 16-wide k index inside a
-// product is free as long as both operands agree, so a lane takes whole
+// selected positions of bfloat16 took 35.0 us so, and 30.6 now, 4.4 TB/s); chunks
+// that lie in one page each take one lookup, a chunk ahead (1M positions: 194 us so,
+// 220 with the lookups of the others).  The order of the 16-wide k index inside
+// a product is free as long as both operands agree, so a lane takes whole
 // 16-byte pieces of its key's row for the first product and of its four
 // value rows for the second; bytes are paired by byte permutes, and the rows'
 // pieces are XOR-swizzled so that neither read has bank conflicts.

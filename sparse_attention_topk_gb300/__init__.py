@@ -8,6 +8,8 @@ missing or the device is unsupported.
     import torch, sparse_attention_topk_gb300 as tks
     idx = tks.topk_indices(logits, k=2048)            # logits: cuda fp32/bf16 [batch, n]
     idx = tks.topk_indices(logits, 2048, row_len=lens)  # ragged rows (int32 cuda tensor)
+
+The paged cache that the indices point into, and the attention over it, are in ``attention.py``.
 """
 
 from __future__ import annotations

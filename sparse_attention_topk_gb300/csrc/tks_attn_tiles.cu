@@ -23,14 +23,14 @@
 //
 // What bounds it: up to 128 rows the cache's bytes (32 KB of int8 a tile, 1400
 // cycles at the memory's rate, against 1024 of tensor work for a full 128
-// rows); beyond, the products and, beside them, shared memory: operand reads,
-// the widened rows' stores and the scales' reads share its 128 bytes a cycle.
+// rows); beyond, the eight warps that make weights and the eight that widen
+// rows, which share an SM's issue slots and take about as long as each other.
 // Measured: 8 ragged trees of 8 drafts over up to 65,536 positions of bfloat16
 // (32 rows a head, 1.16 GB) 195 us, 5.9 TB/s; two trees of 64 drafts over 32,768
-// positions of int8 (512 rows a head, 137 Gflop) 196 us, 706 Tflop/s: a tile
-// takes the rows' chain (scores, maximum, weights) some 3500 cycles, 2000 beyond
-// the products; 512 queries of 64 heads over 2048 selected positions each 103 us,
-// of which a block's 3 or 4 changes of segment take some 4 us each.
+// positions of int8 (512 rows a head, 137 Gflop) 196 us, 700 Tflop/s, a tile in
+// some 3500 cycles (161 us without making weights, 178 without loading rows, 103
+// without both); 512 queries of 64 heads over 2048 selected positions each 103 us,
+// of which a block's four changes of segment take some 6 us each.
 //
 // Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
 // warp's role, which makes the waits on that warp run out; when all roles have

@@ -455,6 +455,7 @@ __device__ __forceinline__ void join_cluster(const Params& p, uint32_t part, uin
   const unsigned per = (unsigned)(p.kv_heads * p.row_tiles);
   const int seq = (int)(unit / per), in = (int)(unit % per);
   const int head = in / p.row_tiles, first = (in % p.row_tiles) * ROWS, live = min(p.rows - first, ROWS);
+  __syncwarp();  // (the cluster's barrier takes whole warps; some lanes may have written their partial's sums last)
   cluster_sync();
   for (unsigned x = rank * threads + threadIdx.x; threadIdx.x < threads && x < (unsigned)live * (D / 4); x += size * threads) {
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;

@@ -599,6 +599,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
   auto advance = [&](int at) -> bool {
     int more = 0;
     if (lane == 0) more = segs.it.next(p, segs.s[at]) ? 1 : 0;
+    __syncwarp();  // (a shuffle orders no memory: the other lanes read what lane 0 has written)
     return __shfl_sync(0xffffffffu, more, 0) != 0;
   };
   // Whether the second product of tile i is done. (That of tile i - 2, its barrier's phase
@@ -661,6 +662,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           w[j] = pack_half(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+      __syncwarp();  // (tensor memory is accessed by whole warps; lanes have rows to load, or none)
       tc_st16(mine + S::kQ + half * (D / 4) + 16 * i, w);
     }
     tc_wait_st();
@@ -752,6 +754,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
               x[2 * i] = __float_as_uint(bits & 1u ? fmaf(__uint_as_float(x[2 * i]) * b, e4.x, e4.z) : -INFINITY);
               x[2 * i + 1] = __float_as_uint(bits & 2u ? fmaf(__uint_as_float(x[2 * i + 1]) * b, e4.y, e4.w) : -INFINITY);
             }
+            __syncwarp();
             tc_st_scores(sb + 8 * j + ((uint32_t)(16 * h) << 16), x);
           }
           tc_wait_st();
@@ -998,7 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (!SEL && p.cluster) {  // (the other warps have given registers up)
       float2* ml = reinterpret_cast<float2*>(smem + kTilesRows * D * 4);
       if (start.left == 0 && threadIdx.x < kTilesRows) ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
-      __syncwarp();
       join_cluster<kTilesRows, D, SEL>(p, smem_addr(smem), smem_addr(ml), kRowWarps * 32);
     }
   } else if (warp < kRowWarps + 4) {

@@ -138,7 +138,8 @@ struct Device {
 };
 struct Workspace {
   unsigned char* ptr = nullptr;  // status word, the last call's split, then (at 256 bytes) partial slots
-  // A call's two kernels follow each other on the stream, without another thread's between them.
+  // A call's two kernels follow each other on the stream, without another thread's call or a status
+  // call's clear between them.
   std::shared_ptr<std::mutex> order;
 };
 
@@ -372,6 +373,9 @@ int attn_status(int dev, void* stream) {
     if (it == g_ws.end()) return TKS_OK;
     w = it->second;
   }
+  // Calls of other threads wait: none is queued between the read and the clear, which would lose its
+  // report, and none has its first kernel before the clear and its second behind.
+  std::lock_guard<std::mutex> lock(*w.order);
   unsigned st = 0;
   if (cudaMemcpyAsync(&st, w.ptr, sizeof st, cudaMemcpyDeviceToHost, (cudaStream_t)stream) != cudaSuccess ||
       cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
@@ -379,7 +383,8 @@ int attn_status(int dev, void* stream) {
     return TKS_E_CUDA;
   }
   if (st == 0) return TKS_OK;
-  if (cudaMemsetAsync(w.ptr, 0, kHeaderBytes, (cudaStream_t)stream) != cudaSuccess ||
+  // (the word alone: behind it lies the split that a call's second kernel reads)
+  if (cudaMemsetAsync(w.ptr, 0, sizeof st, (cudaStream_t)stream) != cudaSuccess ||
       cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
@@ -431,6 +436,7 @@ extern "C" int tks_cache_write(const tks_cache* cache, const void* k, const void
   p.k_head = k_head_stride;
   p.v_token = v_token_stride;
   p.v_head = v_head_stride;
+  std::lock_guard<std::mutex> lock(*ws.order);
   if (launch_cache_write(p, cache->head_dim, cache->held == TKS_I8, dtype == TKS_F32, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
@@ -451,6 +457,7 @@ extern "C" int tks_cache_read(const tks_cache* cache, const int32_t* slots, int3
   CacheParams p = cache_params(cache, slots, n, reinterpret_cast<unsigned*>(ws.ptr));
   p.out_k = k_out;
   p.out_v = v_out;
+  std::lock_guard<std::mutex> lock(*ws.order);
   if (launch_cache_read(p, cache->head_dim, cache->held == TKS_I8, dtype == TKS_F32, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

@@ -18,6 +18,9 @@
  * allocates one workspace for each (device, stream) on the first of these calls
  * on it (make that call before any CUDA-graph capture); later calls allocate
  * nothing and never synchronise, and tks_release frees it with the others.
+ * (cudaStreamPerThread is a stream of every host thread, so each thread that
+ * passes that handle to these calls gets a workspace, and asks for the errors
+ * of its own stream.)
  * The caller owns every buffer, which must stay valid until the work completes.
  *
  * Results do not depend on timing: the same call gives the same bits.  Waits

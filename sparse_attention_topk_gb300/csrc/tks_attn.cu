@@ -2,12 +2,13 @@
 // the kernel that joins partial results.
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <exception>
 #include <map>
 #include <memory>
 #include <mutex>
-#include <utility>
+#include <tuple>
 
 #include "tks_attention.h"
 #include "tks_attn.cuh"
@@ -147,7 +148,18 @@ constexpr size_t kPlanOffset = 64, kHeaderBytes = 256;
 
 std::mutex g_mu;
 std::map<int, Device> g_dev;
-std::map<std::pair<int, void*>, Workspace> g_ws;
+
+// Device, stream, and, where the handle stands for another stream in every host thread, the thread (by
+// a number of its own: the system's are used again).
+using Key = std::tuple<int, void*, unsigned long long>;
+Key key_of(int dev, void* stream) {
+  static std::atomic<unsigned long long> threads{0};
+  thread_local unsigned long long mine = 0;
+  if (stream != (void*)cudaStreamPerThread) return Key(dev, stream, 0);
+  if (mine == 0) mine = ++threads;
+  return Key(dev, stream, mine);
+}
+std::map<Key, Workspace> g_ws;
 
 size_t part_bytes(const Device& d) {
   const size_t few = (size_t)d.sms * kRowsBlocksPerSm * 2 * kPartFloats<kRowsTile, 128>;
@@ -176,7 +188,7 @@ int prepare(void* stream, Device* dev, Workspace* ws) try {
   }
   if (!di->second.ok) return TKS_E_UNSUPPORTED;
   *dev = di->second;
-  const auto key = std::make_pair(id, stream);
+  const Key key = key_of(id, stream);
   auto wi = g_ws.find(key);
   if (wi == g_ws.end()) {
     Workspace w;
@@ -369,7 +381,7 @@ int attn_status(int dev, void* stream) {
   Workspace w;
   {
     std::lock_guard<std::mutex> lock(g_mu);
-    const auto it = g_ws.find(std::make_pair(dev, stream));
+    const auto it = g_ws.find(key_of(dev, stream));
     if (it == g_ws.end()) return TKS_OK;
     w = it->second;
   }
@@ -399,7 +411,7 @@ int attn_release() {
   int rc = TKS_OK, cur = 0;
   cudaGetDevice(&cur);
   for (auto& kv : g_ws) {
-    cudaSetDevice(kv.first.first);
+    cudaSetDevice(std::get<0>(kv.first));
     if (cudaFree(kv.second.ptr) != cudaSuccess) rc = TKS_E_CUDA;
   }
   cudaSetDevice(cur);

@@ -106,3 +106,29 @@ def test_no_report_is_lost_between_status_calls():
     assert tks.load().tks_device_status(stream) == tks.TKS_OK
     torch.cuda.synchronize()
     assert torch.equal(case.out, case.want)
+
+
+@pytest.mark.parametrize("q_heads", [4, 80])
+def test_the_per_thread_stream(q_heads):
+    """One handle, a stream of its own in every thread: the calls run side by side, and each thread has its own errors."""
+    threads, calls, per_thread = 4, 50, 2  # (the handle's value: cudaStreamPerThread)
+    case = Split(q_heads, threads, calls)
+    bad = torch.tensor([case.slots], dtype=torch.int32, device="cuda")
+    rows = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    rcs, told = [], {}
+    begin = threading.Barrier(threads)
+
+    def run(i):
+        begin.wait()
+        rcs.extend(case.call(i, j, per_thread) for j in range(calls))
+        if i == 0:
+            rcs.append(tks.load().tks_cache_read(ctypes.byref(case.cache), bad.data_ptr(), 1, rows[0].data_ptr(), rows[1].data_ptr(), tks.TKS_BF16, per_thread))
+        begin.wait()
+        told[i] = tks.load().tks_device_status(per_thread)
+
+    together(*(lambda i=i: run(i) for i in range(threads)))
+    assert rcs == [tks.TKS_OK] * (threads * calls + 1)
+    assert told == {0: tks.TKS_E_INDEX, 1: tks.TKS_OK, 2: tks.TKS_OK, 3: tks.TKS_OK}
+    torch.cuda.synchronize()
+    assert torch.equal(case.out, case.want)

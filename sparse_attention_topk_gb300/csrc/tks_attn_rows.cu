@@ -11,10 +11,12 @@
 // so the codes go into the matrix products as they are, exact in half
 // precision, one multiply-add applies both scales to a score, and the weights
 // are rounded (to 11 bits) relative to the largest contribution to the output.
-// Queries are bfloat16; they enter as halves, exactly, after a shift by a
-// power of two that is common to the block's rows.  Over a bfloat16 cache, whose
-// products want bfloat16 weights, a weight goes in as the sum of two (rounded to
-// one, weights made outputs 1.4 times less exact).
+// Queries are bfloat16; they enter as halves, each row shifted by a power of
+// two of its own that brings its largest element to [2^14, 2^15): exactly, but
+// for elements more than 2^31 below that one.  (One shift for all 16 rows let a
+// large one, or a padded row's contents, take the others' bits away.)  Over a
+// bfloat16 cache, whose products want bfloat16 weights, a weight goes in as the
+// sum of two (rounded to one, weights made outputs 1.4 times less exact).
 //
 // What bounds it: the cache's bytes, each read once.  One matrix instruction
 // works on 16 rows, so up to 16 rows of a head cost the same; 16 keys of int8
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Start start;
   __shared__ float2 ml_s[kWarps][16];
-  __shared__ float top_s[kWarps];
+  __shared__ float top_s[kWarps][16];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = lane >> 2, c = lane & 3;  // the lane's key, row or column, and its quarter
@@ -158,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     // fourth step.
     constexpr int kMySteps = D / 16 / kWarps;
     const int rows_left = p.rows - row_tile * kRowsTile;
-    float fac = p.scale_log2;
+    const float fac = p.scale_log2;
+    float back0 = 1.f, back1 = 1.f;  // 8 bits: what undoes the shifts of rows n and n + 8
     uint2 qa[kMySteps], qe[kMySteps];
     {
       const bool in0 = n < rows_left, in1 = n + 8 < rows_left;
@@ -228,30 +231,42 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     constexpr int kAhead = S::kStages - 1, kStep = kWarps * kChunk;
 
     auto put_queries = [&] {
-      float up = 1.f;
+      float up0 = 1.f, up1 = 1.f;
       if (I8) {
-        float top = 0.f;
+        float a = 0.f, b = 0.f;  // the rows' largest finite magnitudes: this lane's, the warp's, the block's
 #pragma unroll
-        for (int i = 0; i < kMySteps; ++i)
-          top = finite_max(finite_max(finite_max(finite_max(top, qa[i].x), qa[i].y), qe[i].x), qe[i].y);
+        for (int i = 0; i < kMySteps; ++i) {
+          a = finite_max(finite_max(a, qa[i].x), qa[i].y);
+          b = finite_max(finite_max(b, qe[i].x), qe[i].y);
+        }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) top_s[warp] = top;
+        for (int o = 1; o < 4; o <<= 1) {
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
+        }
+        if (c == 0) {
+          top_s[warp][n] = a;
+          top_s[warp][n + 8] = b;
+        }
         __syncthreads();
-        top = fmaxf(fmaxf(top_s[0], top_s[1]), fmaxf(top_s[2], top_s[3]));
-        // the largest finite magnitude goes to [2^14, 2^15): halves keep 11 bits
-        // over 2^28 below it
-        const int shift = top > 0.f ? max(-120, min(120, 14 - ilogbf(top))) : 0;
-        up = __int_as_float((shift + 127) << 23);
-        fac *= __int_as_float((127 - shift) << 23);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          a = fmaxf(a, top_s[i][n]);
+          b = fmaxf(b, top_s[i][n + 8]);
+        }
+        const int s0 = a > 0.f ? max(-120, min(120, 14 - ilogbf(a))) : 0, s1 = b > 0.f ? max(-120, min(120, 14 - ilogbf(b))) : 0;
+        up0 = __int_as_float((s0 + 127) << 23);
+        up1 = __int_as_float((s1 + 127) << 23);
+        back0 = __int_as_float((127 - s0) << 23);
+        back1 = __int_as_float((127 - s1) << 23);
       }
-      auto held = [&](uint32_t w) -> uint32_t {
+      auto held = [&](uint32_t w, float up) -> uint32_t {
         const float2 f = bf16_pair(w);
         return I8 ? pack_half(f.x * up, f.y * up) : w;
       };
 #pragma unroll
       for (int i = 0; i < kMySteps; ++i)
-        qs[(warp + i * kWarps) * 32 + lane] = make_uint4(held(qa[i].x), held(qe[i].x), held(qa[i].y), held(qe[i].y));
+        qs[(warp + i * kWarps) * 32 + lane] = make_uint4(held(qa[i].x, up0), held(qe[i].x, up1), held(qa[i].y, up0), held(qe[i].y, up1));
       __syncthreads();
     };
 
@@ -358,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float4 k = consts[8 * t + 2 * c + e];
-            s[t][e] = fmaf(s[t][e], k.x, k.y);
-            s[t][2 + e] = fmaf(s[t][2 + e], k.x, k.y);
+            s[t][e] = fmaf(s[t][e] * back0, k.x, k.y);
+            s[t][2 + e] = fmaf(s[t][2 + e] * back1, k.x, k.y);
             inv[2 * t + e] = k.z;
           }
       } else {

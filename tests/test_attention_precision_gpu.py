@@ -1,0 +1,73 @@
+"""What the range and the rounding of queries and weights may do to a result, and what they may not.
+
+The bounds are derived beside each test, from the formats: a half keeps 11 bits of values from 2^-14
+up and steps of 2^-24 below; a bfloat16 keeps 8.
+"""
+
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import sparse_attention_topk_gb300 as tks  # noqa: E402
+from tests.attention_plain import PagedCache, check_rows  # noqa: E402
+from tests.test_attention_gpu import HELD, gen, rand_rows  # noqa: E402
+
+
+@pytest.fixture(autouse=True)
+def _clean_status():
+    yield
+    assert tks.device_status() == tks.TKS_OK
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ---------------------------------------------------------------------------
+# Queries: each row's result is its own
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("what", [2.0 ** 40, 1e30, 3e38, math.inf, math.nan])
+@pytest.mark.parametrize("drafts, count, heads", [(4, 3, 4), (9, 1, 1), (40, 7, 2)])
+def test_queries_beyond_the_drafts_have_no_influence(drafts, count, heads, what, held):
+    """A padded query row may hold anything."""
+    g = gen(11)
+    ctx = 150
+    cache = PagedCache(16, 16, 1, 64, held)
+    table, _, _ = cache.fill(rand_rows(ctx + count, 1, 64, g), rand_rows(ctx + count, 1, 64, g))
+    q = torch.randn(1, drafts, heads, 64, device="cuda", generator=g).to(torch.bfloat16)
+    call = lambda x: tks.tree_attention(x, cache.k, cache.v, table[None], ints(ctx), draft_len=ints(count), scales=cache.scales, return_lse=True)  # noqa: E731
+    q[:, count:] = 0
+    want, want_lse = call(q)
+    q[:, count:] = what
+    out, lse = call(q)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("apart", [2.0 ** 20, 2.0 ** 40, 2.0 ** 80])
+@pytest.mark.parametrize("heads", [2, 16, 48])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_of_very_different_queries(dim, heads, apart, held):
+    """Query rows far apart in size, over keys that make the small ones' scores ordinary: those rows as if they were alone.
+
+    check_rows' bounds hold for each row by itself: a score is off by dim * 2^-23 of the sum of its products'
+    magnitudes, which leaves room for the 2^-25 of its largest element by which a half may miss the rest of a row.
+    """
+    g = gen(12)
+    n = 200
+    cache = PagedCache(16, 16, 1, dim, held)
+    k = rand_rows(n, 1, dim, g) * apart ** 0.5
+    table, kh, vh = cache.fill(k, rand_rows(n, 1, dim, g))
+    q = torch.randn(1, 1, heads, dim, device="cuda", generator=g) * apart ** -0.5
+    q[:, :, 1::2] *= apart  # (their softmax has one key)
+    q = q.to(torch.bfloat16)
+    out, lse = tks.tree_attention(q, cache.k, cache.v, table[None], ints(n - 1), scales=cache.scales, return_lse=True)
+    ones = torch.ones(heads, n, dtype=torch.bool, device="cuda")
+    check_rows(out[0, 0, ::2], lse[0, 0, ::2], q[0, 0, ::2].double(), kh[:, 0], vh[:, 0], ones[::2], dim ** -0.5, held)
+    assert out.isfinite().all() and lse.isfinite().all()

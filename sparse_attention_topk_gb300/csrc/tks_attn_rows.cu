@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
           }
       }
 
-      // The maxima that weights are relative to follow when one has grown by more than 2^8.
+      // The maxima that weights are relative to follow when one has grown by more than 2^8: by its
+      // difference, which weights are powers of. (Where 32 bits go in steps of 16, m + 8 can be m + 16.)
       float t0m = fmaxf(s[0][0], s[0][1]), t1m = fmaxf(s[0][2], s[0][3]);
 #pragma unroll
       for (int t = 1; t < kNT; ++t) {
@@ -412,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, o));
         t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, o));
       }
-      if (__any_sync(0xffffffffu, t0m > m[0] + 8.f || t1m > m[1] + 8.f)) {
-        const bool up0 = t0m > m[0] + 8.f, up1 = t1m > m[1] + 8.f;
+      const bool up0 = t0m - m[0] > 8.f, up1 = t1m - m[1] > 8.f;  // (both -inf: no)
+      if (__any_sync(0xffffffffu, up0 || up1)) {
         const float f0 = up0 ? ex2(m[0] - t0m) : 1.f, f1 = up1 ? ex2(m[1] - t1m) : 1.f;
         if (up0) m[0] = t0m;
         if (up1) m[1] = t1m;

@@ -798,7 +798,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
           const float2 y = pr.top[g & 1][half ^ 1][h][n];
           top[h][0] = fmaxf(top[h][0], y.x);
           top[h][1] = fmaxf(top[h][1], y.y);
-          grow |= top[h][0] > m[h][0] + 8.f || top[h][1] > m[h][1] + 8.f;
+          grow |= top[h][0] - m[h][0] > 8.f || top[h][1] - m[h][1] > 8.f;  // (both -inf: no; see tks_attn_rows.cu)
         }
         if (__any_sync(0xffffffffu, grow)) {
           if (t > t0 && !outputs_done(g - 1)) return;
@@ -807,7 +807,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
             float back2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool up = top[h][i] > m[h][i] + 8.f;
+              const bool up = top[h][i] - m[h][i] > 8.f;
               back2[i] = up ? ex2(m[h][i] - top[h][i]) : 1.f;  // (m = -inf: 0)
               if (up) m[h][i] = top[h][i];
               sum[h][i] = mul2(sum[h][i], pair(back2[i], back2[i]));

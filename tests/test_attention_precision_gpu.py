@@ -71,3 +71,34 @@ def test_rows_of_very_different_queries(dim, heads, apart, held):
     ones = torch.ones(heads, n, dtype=torch.bool, device="cuda")
     check_rows(out[0, 0, ::2], lse[0, 0, ::2], q[0, 0, ::2].double(), kh[:, 0], vh[:, 0], ones[::2], dim ** -0.5, held)
     assert out.isfinite().all() and lse.isfinite().all()
+
+
+# ---------------------------------------------------------------------------
+# Weights
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("heads", [1, 16, 20, 80])
+def test_scores_so_large_that_they_differ_in_steps(heads, held):
+    """Scores near 2^28 (of powers of two), where 32 bits go in steps of 16, and each a step above the one before.
+
+    Such scores tell only which key is the largest, but a weight must not leave the range of its type: the result
+    is a mean of values, nearly those of the last keys.
+    """
+    n, dim, group = 12800, 64, 128
+    k = torch.zeros(n, 1, dim, device="cuda")
+    k[:, 0, 0] = 127.0
+    k[:, 0, 1] = torch.arange(n, device="cuda") // group  # 0 .. 99, a step each
+    v = torch.where(torch.arange(n, device="cuda") < n - group, 1.0, 2.0)[:, None, None].expand(n, 1, dim)
+    many = 320  # (sequences enough that a row's keys are not split over blocks)
+    q = torch.zeros(many, 1, heads, dim, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    q[..., 1] = 2.0 ** -17
+    cache = PagedCache(n // 16 + 1, 16, 1, dim, held)
+    table, _, _ = cache.fill(k, v)
+    for scale in (2.0 ** 20, 2.0 ** 21, 2.0 ** 22, 2.0 ** 30):
+        out, lse = tks.tree_attention(q, cache.k, cache.v, table[None].expand(many, -1), torch.full((many,), n - 1, dtype=torch.int32, device="cuda"),
+                                      scales=cache.scales, softmax_scale=scale * math.log(2.0), return_lse=True)
+        assert out.isfinite().all() and lse.isfinite().all()
+        assert out.min() >= 1.0 - 2.0 ** -7 and out.max() <= 2.0 + 2.0 ** -6

@@ -86,6 +86,15 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& first, ui
   rest = pack_bf16(a - __uint_as_float(x & 0xffff0000u), b - __uint_as_float(y & 0xffff0000u));
 }
 
+// Weights are 2^(x - m), m near a row's running maximum: when that has grown to more than this and 8
+// beyond m, m becomes the maximum less this. Over 8 bits weights go into the products as halves, so with
+// 11 bits down to 2^-14, in steps of 2^-24 below, and up to 2^16: with the largest at 2^7 to 2^15, a
+// weight is off by 2^-11 of itself or by 2^-32 of the largest. (With the largest at 1 to 2^8, those below
+// 2^-25 of it were 0 in the output, and not in the sum: a flat tail of 2^20 keys behind a dominant one
+// lost the 2.7 % that it is of the row.) Weights over bfloat16 have the range of 32 bits.
+template <bool I8>
+constexpr float kWeightLog2 = I8 ? 7.f : 0.f;
+
 // Two codes as a pair of halves, exactly: `biased` holds codes + 128 as bytes
 // (code ^ 0x80), a byte u under the exponent 0x64 is 1024 + u, and 1152 is
 // taken off again.  SEL picks the bytes: 0x4140 the lower two, 0x4342 the upper.

@@ -3,14 +3,15 @@
 //
 // Mathematics.  For a row i and the keys j it attends to, with x_ij = q_i.k_j
 // * scale * log2(e):
-//     out_i = sum_j 2^(x_ij - m) v_j / sum_j 2^(x_ij - m),   m the running
+//     out_i = sum_j 2^(x_ij - m) v_j / sum_j 2^(x_ij - m),   m near the running
 // maximum; all sums in 32 bits.  Of a cache in 8 bits, k_j = ks_j * a_j and
 // v_j = vs_j * b_j with integer codes a, b; then
 //     w_ij = 2^(q_i.a_j * ks_j * scale * log2(e) + log2(vs_j) - m'),
 //     out_i = sum_j w_ij b_j / sum_j w_ij / vs_j,
 // so the codes go into the matrix products as they are, exact in half
-// precision, one multiply-add applies both scales to a score, and the weights
-// are rounded (to 11 bits) relative to the largest contribution to the output.
+// precision, one multiply-add applies both scales to a score, and a weight is
+// rounded to 11 bits of itself (a small one in steps of 2^-31 of the largest,
+// which is the largest contribution to the output: kWeightLog2).
 // Queries are bfloat16; they enter as halves, each row shifted by a power of
 // two of its own that brings its largest element to [2^14, 2^15): exactly, but
 // for elements more than 2^31 below that one.  (One shift for all 16 rows let a
@@ -400,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
           }
       }
 
-      // The maxima that weights are relative to follow when one has grown by more than 2^8: by its
-      // difference, which weights are powers of. (Where 32 bits go in steps of 16, m + 8 can be m + 16.)
+      // What weights are relative to (kWeightLog2) follows when a maximum has grown by more than 2^8: by
+      // its difference, which weights are powers of. (Where 32 bits go in steps of 16, m + 8 can be m + 16.)
       float t0m = fmaxf(s[0][0], s[0][1]), t1m = fmaxf(s[0][2], s[0][3]);
 #pragma unroll
       for (int t = 1; t < kNT; ++t) {
@@ -413,8 +414,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         t0m = fmaxf(t0m, __shfl_xor_sync(0xffffffffu, t0m, o));
         t1m = fmaxf(t1m, __shfl_xor_sync(0xffffffffu, t1m, o));
       }
-      const bool up0 = t0m - m[0] > 8.f, up1 = t1m - m[1] > 8.f;  // (both -inf: no)
+      constexpr float kAbove = kWeightLog2<I8>;
+      const bool up0 = t0m - m[0] > 8.f + kAbove, up1 = t1m - m[1] > 8.f + kAbove;  // (both -inf: no)
       if (__any_sync(0xffffffffu, up0 || up1)) {
+        t0m -= kAbove;
+        t1m -= kAbove;
         const float f0 = up0 ? ex2(m[0] - t0m) : 1.f, f1 = up1 ? ex2(m[1] - t1m) : 1.f;
         if (up0) m[0] = t0m;
         if (up1) m[1] = t1m;

@@ -5,9 +5,9 @@
 // Mathematics: that of tks_attn_rows.cu (running maximum and sum; codes of an
 // 8-bit cache exact in half precision, both scales folded into one
 // multiply-add per score, weights relative to the largest contribution).
-// Each row's queries get their own power of two. The running maximum follows
-// only when a row's has grown by more than 2^8: weights then reach 2^8 at
-// most, well inside a half, and the output in tensor memory is rarely rescaled.
+// Each row's queries get their own power of two. What weights are relative to
+// follows only when a row's maximum has grown by more than 2^8, so the output in
+// tensor memory is rarely rescaled.
 //
 // Layout.  A block is one SM: 128 query rows (a lane of tensor memory each)
 // against tiles of 128 keys. Warps 0-7 keep the rows: they take scores into
@@ -791,14 +791,15 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
           for (int h = 0; h < STEPS; ++h) pr.top[g & 1][half][h][n] = make_float2(top[h][0], top[h][1]);
         if (!meet()) return;
 
-        // The maxima that the weights are relative to: -inf as long as a row has seen nothing.
+        // What the weights are relative to (kWeightLog2): -inf as long as a row has seen nothing.
+        constexpr float kAbove = kWeightLog2<I8>;
         bool grow = false;
 #pragma unroll
         for (int h = 0; h < STEPS; ++h) {
           const float2 y = pr.top[g & 1][half ^ 1][h][n];
           top[h][0] = fmaxf(top[h][0], y.x);
           top[h][1] = fmaxf(top[h][1], y.y);
-          grow |= top[h][0] - m[h][0] > 8.f || top[h][1] - m[h][1] > 8.f;  // (both -inf: no; see tks_attn_rows.cu)
+          grow |= top[h][0] - m[h][0] > 8.f + kAbove || top[h][1] - m[h][1] > 8.f + kAbove;  // (both -inf: no; see tks_attn_rows.cu)
         }
         if (__any_sync(0xffffffffu, grow)) {
           if (t > t0 && !outputs_done(g - 1)) return;
@@ -807,9 +808,10 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
             float back2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool up = top[h][i] - m[h][i] > 8.f;
-              back2[i] = up ? ex2(m[h][i] - top[h][i]) : 1.f;  // (m = -inf: 0)
-              if (up) m[h][i] = top[h][i];
+              const bool up = top[h][i] - m[h][i] > 8.f + kAbove;
+              const float next = top[h][i] - kAbove;
+              back2[i] = up ? ex2(m[h][i] - next) : 1.f;  // (m = -inf: 0)
+              if (up) m[h][i] = next;
               sum[h][i] = mul2(sum[h][i], pair(back2[i], back2[i]));
             }
             if (t > t0)

@@ -102,3 +102,44 @@ def test_scores_so_large_that_they_differ_in_steps(heads, held):
                                       scales=cache.scales, softmax_scale=scale * math.log(2.0), return_lse=True)
         assert out.isfinite().all() and lse.isfinite().all()
         assert out.min() >= 1.0 - 2.0 ** -7 and out.max() <= 2.0 + 2.0 ** -6
+
+
+def dominant_key_case(sequences, heads, held):
+    """One key 25.2 doublings above 2^20 equal ones: together they are 2.7 % of the row.
+
+    As many sequences as the device takes at once, all in the same pages, so that a row's keys are not split over
+    blocks. A weight is held to 2^-11 of itself (a bfloat16 cache: 2^-15) or, small, to 2^-32 of the largest, so
+    the output to n * 2^-32 of the largest value beside its own rounding. Sums of weights are held in 32 bits by
+    lanes that take every eighth key or fewer: the lane of the dominant one may lose its share of the tail. (A tail
+    that counts for nothing in the output would be 0.027.)
+    """
+    n, page, dim, below = 1 << 20, 64, 64, 25.2
+    shape = (n // page + 1, page, 1, dim)
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    k, v = torch.zeros(n, 1, dim, device="cuda"), torch.ones(n, 1, dim, device="cuda")
+    k[0, 0, 0] = 1.0
+    v[0, 0, dim // 2 :] = 0.0
+    if held == "int8":
+        kc, vc, scales = torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(shape, dtype=torch.int8, device="cuda"), torch.zeros(*shape[:3], 2, device="cuda")
+    else:
+        kc, vc, scales = torch.zeros(shape, dtype=torch.bfloat16, device="cuda"), torch.zeros(shape, dtype=torch.bfloat16, device="cuda"), None
+    tks.cache_write(k, v, kc, vc, slots, scales=scales)
+    q = torch.zeros(sequences, 1, heads, dim, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = below * math.log(2.0)
+    table = torch.arange(shape[0], dtype=torch.int32, device="cuda")[None].expand(sequences, -1)
+    out, lse = tks.tree_attention(q, kc, vc, table, torch.full((sequences,), n - 1, dtype=torch.int32, device="cuda"), scales=scales,
+                                  softmax_scale=scale, return_lse=True)
+    tail = (n - 1) * 2.0 ** -below
+    want = torch.ones(dim, dtype=torch.float64, device="cuda")
+    want[dim // 2 :] = tail / (1 + tail)
+    bound = 2.0 ** -8 * want + (2.0 ** -11 if held == "int8" else 2.0 ** -15) * want + want * tail / 8 + n * 2.0 ** -32 + 2.0 ** -18
+    assert (lse.double() - (scale + math.log1p(tail))).abs().max().item() <= tail / 8 + 2.0 ** -22 * scale + 2.0 ** -18
+    return (out.double() - want).abs() / bound
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("sequences, heads", [(304, 4), (152, 24), (152, 70)])
+def test_a_long_flat_tail_behind_a_dominant_key(sequences, heads, held):
+    """Where the dominant key has a value of zero, the tail is all there is."""
+    assert dominant_key_case(sequences, heads, held)[..., 32:].max().item() <= 1.0

@@ -16,7 +16,7 @@
 // partial result (unnormalised output, running maximum, sum) to its slot of the
 // workspace, and the unit's partials are joined in block order, so results do
 // not depend on timing.  A block has at most two partial segments, its first
-// (slot 0) and its last (slot 1).  Where shares are even and short (the host can
+// (slot 0) and its last (slot 1).  (A long run's pieces meet in these slots, too.)  Where shares are even and short (the host can
 // tell from the list's or the page table's length), the blocks of a unit are a
 // thread-block cluster: they leave their partials in their shared memory, and
 // join them from there without another kernel (one token over 2048 selected
@@ -280,41 +280,50 @@ __device__ __forceinline__ void find_start(const Params& p, Start* st) {
   }
 }
 
-// A block's segments: runs of tiles of one unit.
+// A block's segments: runs of tiles of one unit, or pieces of them.
 struct Segment {
   int seq, head, row_tile, b;
   int t0, t1, tiles;  // tiles [t0, t1) of the unit's
-  bool first;         // of the block
+  int from;           // where the block's run of the unit begins: t0, or in a piece before
+  bool first;         // of the block's runs
+  bool more;          // the run goes on behind this piece
   Seq len;
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  __device__ __forceinline__ bool whole() const { return from == 0 && t1 == tiles; }  // (the last piece)
+  __device__ __forceinline__ bool goes_on() const { return from != t0; }              // pieces came before
 };
 template <bool SEL, int TK>
 struct Segments {
   unsigned left, rel;
   int seq;
   Seq len0;  // of the first segment's sequence
-  bool first;
+  bool first, more;
+  int from;
   __device__ __forceinline__ void begin(const Start& st) {
     left = st.left;
     rel = st.rel;
     seq = st.seq;
     len0 = st.len;
     first = true;
+    more = false;
   }
   __device__ __forceinline__ bool next(const Params& p, Segment& s) {
     if (left == 0) return false;
     s.len = first ? len0 : seq_of<SEL>(p, seq);
     const unsigned tiles = (unsigned)tiles_of<TK>(s.len.len);
-    const unsigned unit = rel / tiles, t0 = rel - unit * tiles, n = min(tiles - t0, left);
+    const unsigned unit = rel / tiles, t0 = rel - unit * tiles, run = min(tiles - t0, left), n = min(run, (unsigned)(kPieceKeys / TK));
     s.seq = seq;
     s.b = SEL ? seq / p.tokens : seq;
     s.head = TK == kRowsKeys ? (int)unit : (int)(unit / (unsigned)p.row_tiles);  // (few rows: one tile)
     s.row_tile = TK == kRowsKeys ? 0 : (int)(unit - (unsigned)s.head * p.row_tiles);
+    if (!more) from = (int)t0;
+    more = n < run;
+    s.from = from;
     s.t0 = (int)t0;
     s.t1 = (int)(t0 + n);
     s.tiles = (int)tiles;
     s.first = first;
-    first = false;
+    s.more = more;
+    first = first && more;
     left -= n;
     rel += n;
     if (rel == tiles * (unsigned)(p.kv_heads * p.row_tiles)) {

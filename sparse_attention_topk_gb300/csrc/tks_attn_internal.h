@@ -17,6 +17,13 @@ constexpr unsigned kStatIndexBit = 1u << 3;
 // Most positions of a sequence: indices of keys stay below 2^31 with a tile to spare.
 constexpr int kMaxPositions = 0x7fff0000;
 
+// Most keys that an output is summed over in one go. The matrix instructions add products to a 32-bit
+// accumulator whose small ones, below 2^-24 of it, are dropped: of a flat tail of weights behind a
+// dominant one, n * 2^-24 at most. A longer run of a unit's keys is summed in pieces, joined as the
+// partials of blocks are; at 32,768 the dropped part is 2^-9 at most, half a step of the bfloat16 output,
+// and a piece's begin and end (some 6 us) come once in 0.2 to 0.4 ms.
+constexpr int kPieceKeys = 32768;
+
 // Arguments of the cache kernels.
 struct CacheParams {
   unsigned char *k, *v;

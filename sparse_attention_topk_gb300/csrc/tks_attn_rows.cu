@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
   using S = Shape<D, I8>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Start start;
-  __shared__ float2 ml_s[kWarps][16];
+  __shared__ float2 ml_s[kWarps + 1][16];  // maxima and sums: the warps', and those of a run's pieces before
   __shared__ float top_s[kWarps][16];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -571,6 +571,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         q[i] = ml_s[i][r];
         mm = fmaxf(mm, q[i].x);
       }
+      float2 qb = make_float2(-INFINITY, 0.f);  // the run's pieces before
+      if (sg.goes_on()) qb = ml_s[kWarps][r];
+      mm = fmaxf(mm, qb.x);
       const bool active = SEL || R / p.group < len.drafts;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -581,6 +584,12 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
           ll += f * q[i].y;
           o.x += f * a.x; o.y += f * a.y; o.z += f * a.z; o.w += f * a.w;
         }
+      if (active && qb.y != 0.f) {  // (this thread has put them there)
+        const float f = qb.x == mm ? 1.f : ex2(qb.x - mm);
+        const float4 a = *reinterpret_cast<const float4*>(part + r * D + d);
+        ll += f * qb.y;
+        o.x += f * a.x; o.y += f * a.y; o.z += f * a.z; o.w += f * a.w;
+      }
       if (whole) {
         const float g = ll == 0.f ? 0.f : 1.f / ll;
         const long long row = out_row<SEL>(p, seq, head, R);
@@ -592,6 +601,20 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
       }
     }
     __syncthreads();  // the ring is free for the next segment
+    if (sg.more && threadIdx.x < 16) {  // (read behind the next piece's barriers)
+      const int r = threadIdx.x;
+      float2 all = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i <= kWarps; ++i)
+        if (i < kWarps || sg.goes_on()) all.x = fmaxf(all.x, ml_s[i][r].x);
+#pragma unroll
+      for (int i = 0; i <= kWarps; ++i) {
+        if (i == kWarps && !sg.goes_on()) continue;
+        const float2 q = ml_s[i][r];
+        if (q.y != 0.f) all.y += (q.x == all.x ? 1.f : ex2(q.x - all.x)) * q.y;
+      }
+      ml_s[kWarps][r] = all;
+    }
   }
   if (p.cluster) {
     if (start.left == 0 && threadIdx.x < 16) part_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);

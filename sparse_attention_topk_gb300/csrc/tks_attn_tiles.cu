@@ -549,6 +549,7 @@ struct PairRows {
   float2 top[2][2][2][8];    // a tile's maxima: [tile & 1][half of the keys]
   float2 sum[2][2][8];       // a segment's sums, by half of the keys
   float2 m[2][8];            // and maxima
+  float2 before[2][32];      // maximum and sum of a run's pieces before this one, by row (a copy for each warp)
   float fac[2][32];          // what undoes the shifts of the rows' queries (a copy for each warp)
   unsigned seen[2][2][32];   // the keys that a row sees: [half of the keys][32 keys]
 };
@@ -878,8 +879,23 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
       const int t_row = SEL ? 0 : min(R / p.group, p.tokens - 1);
       const bool live = R < p.rows && (SEL || R / p.group < done.len.drafts);
       const float2 la = pr.sum[0][hl][nl], lb = pr.sum[1][hl][nl], mm = pr.m[hl][nl];
-      const float lr = low ? la.x + lb.x : la.y + lb.y, top = low ? mm.x : mm.y;
-      const bool empty = !live || lr == 0.f;
+      float lr = low ? la.x + lb.x : la.y + lb.y, top = low ? mm.x : mm.y;
+      bool empty = !live || lr == 0.f;
+      // What this piece and those before count for in the run so far; theirs is in the slot, where this
+      // thread has put it.
+      float now = empty ? 0.f : 1.f, past = 0.f;
+      if (done.goes_on()) {
+        const float2 q = pr.before[half][lane];
+        if (q.y != 0.f) {
+          const float most = empty ? q.x : fmaxf(top, q.x);
+          if (!empty) now = top == most ? 1.f : ex2(top - most);
+          past = q.x == most ? 1.f : ex2(q.x - most);
+          lr = (empty ? 0.f : now * lr) + past * q.y;
+          top = most;
+          empty = false;
+        }
+      }
+      if (done.more) pr.before[half][lane] = make_float2(top, empty ? 0.f : lr);
       const float inv = empty ? 0.f : 1.f / lr;
       const bool fix = !I8 && !SEL && *k.poisoned != 0;
       const long long row = out_row<SEL>(p, done.seq, done.head, min(R, p.rows - 1));
@@ -895,8 +911,8 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
         if (R < p.rows) {
           float f[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = empty ? 0.f : __uint_as_float(o[j]);
-          if (fix && !empty) {  // infinities and NaNs of drafts that this row attends to
+          for (int j = 0; j < 32; ++j) f[j] = now == 0.f ? 0.f : __uint_as_float(o[j]);
+          if (fix && now != 0.f) {  // infinities and NaNs of drafts that this row attends to
             const int32_t* table = p.table + done.b * p.table_stride;
             const int end = (int)min((long long)done.len.len, (long long)done.t1 * kKeys);
             for (int j = max(done.len.ctx, done.t0 * kKeys); j < end; ++j) {
@@ -909,6 +925,17 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
                 const float y = __bfloat162float(v[c]);
                 if (!(fabsf(y) < INFINITY)) f[c] += y;
               }
+            }
+          }
+          if (past != 0.f) {
+            const float4* was = reinterpret_cast<const float4*>(part + row_lane * D + d);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 x = was[j];
+              f[4 * j] = f[4 * j] * now + x.x * past;
+              f[4 * j + 1] = f[4 * j + 1] * now + x.y * past;
+              f[4 * j + 2] = f[4 * j + 2] * now + x.z * past;
+              f[4 * j + 3] = f[4 * j + 3] * now + x.w * past;
             }
           }
           if (whole) {

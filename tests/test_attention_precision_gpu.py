@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 import sparse_attention_topk_gb300 as tks  # noqa: E402
 from tests.attention_plain import PagedCache, check_rows  # noqa: E402
-from tests.test_attention_gpu import HELD, gen, rand_rows  # noqa: E402
+from tests.test_attention_gpu import HELD, ancestors, gen, rand_rows, random_parents  # noqa: E402
 
 
 @pytest.fixture(autouse=True)
@@ -143,3 +143,52 @@ def dominant_key_case(sequences, heads, held):
 def test_a_long_flat_tail_behind_a_dominant_key(sequences, heads, held):
     """Where the dominant key has a value of zero, the tail is all there is."""
     assert dominant_key_case(sequences, heads, held)[..., 32:].max().item() <= 1.0
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("sequences, heads", [(304, 4), (152, 24), (152, 70)])
+def test_a_dominant_key_before_a_long_flat_tail(sequences, heads, held):
+    """Where the dominant key has a value, the tail's are added to it, each less than 2^-24 of it."""
+    assert dominant_key_case(sequences, heads, held).max().item() <= 1.0
+
+
+@pytest.mark.parametrize("held", HELD)
+@pytest.mark.parametrize("heads, dim", [(3, 64), (3, 128), (9, 64), (24, 128)])
+def test_runs_of_several_pieces(heads, dim, held):
+    """Sequences of one cache, cut at many lengths around the pieces' ends, that fill the device several times."""
+    g = gen(13)
+    n, page, drafts, many = 70000, 64, 5, 340
+    cache = PagedCache(n // page + 2, page, 1, dim, held)
+    table, kh, vh = cache.fill(rand_rows(n, 1, dim, g), rand_rows(n, 1, dim, g))
+    lens = [69990, 1, 32768, 32763, 65536, 0, 65540, 32769, 50001, 40000, 69000]
+    ctx = [lens[i % len(lens)] for i in range(many)]
+    counts = [i % (drafts + 1) for i in range(many)]
+    q = torch.randn(many, drafts, heads, dim, device="cuda", generator=g).to(torch.bfloat16)
+    parents = random_parents(many, drafts, g)
+    out, lse = tks.tree_attention(q, cache.k, cache.v, table[None].expand(many, -1), ints(*ctx), tree=tks.tree_mask(parents), draft_len=ints(*counts),
+                                  scales=cache.scales, return_lse=True)
+    assert tks.device_status() == tks.TKS_OK
+    for b in range(0, many, 9):
+        seen = torch.zeros(drafts, ctx[b] + counts[b], dtype=torch.bool)
+        seen[:, : ctx[b]] = True
+        seen[:, ctx[b] :] = ancestors(parents[b].tolist())[:, : counts[b]]
+        seen[counts[b] :] = False
+        end = ctx[b] + counts[b]
+        check_rows(out[b].reshape(-1, dim), lse[b].reshape(-1), q[b].reshape(-1, dim).double(), kh[:end, 0], vh[:end, 0],
+                   seen.cuda().repeat_interleave(heads, 0), dim ** -0.5, held)
+
+
+@pytest.mark.parametrize("heads", [4, 40])
+def test_infinite_values_in_a_later_piece(heads):
+    """Values of drafts that lie in the second piece of a run reach the rows that attend, as they do in the first."""
+    g = gen(14)
+    n, many, dim = 40004, 320, 64
+    cache = PagedCache(n // 64 + 2, 64, 1, dim, "bf16")
+    table, _, _ = cache.fill(rand_rows(n, 1, dim, g), rand_rows(n, 1, dim, g))
+    for pos, d, x in ((10, 3, math.inf), (40002, 5, -math.inf), (40003, 6, math.nan)):  # one in the context, two among the drafts
+        cache.v[table[pos // 64], pos % 64, 0, d] = x
+    q = 0.1 * torch.randn(many, 4, heads, dim, device="cuda", generator=g)
+    out = tks.tree_attention(q.to(torch.bfloat16), cache.k, cache.v, table[None].expand(many, -1), torch.full((many,), n - 4, dtype=torch.int32, device="cuda"))
+    assert (out[..., 3] == math.inf).all()
+    assert (out[:, 2:, :, 5] == -math.inf).all() and out[:, :2, :, 5].isfinite().all()
+    assert out[:, 3, :, 6].isnan().all() and out[:, :3, :, 6].isfinite().all()

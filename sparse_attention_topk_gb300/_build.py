@@ -88,6 +88,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str = LIB_PATH,
 # The C++ step between Python and the cache and attention calls: an extension
 # module built by the host compiler against torch's headers.
 BINDING_SOURCE = os.path.join(CSRC, "tks_binding.cpp")
+
 BINDING_PATH = os.path.join(BUILD_DIR, "tks_binding.so")
 
 
@@ -104,6 +105,7 @@ def start_binding(force: bool = False):
     if not force and _binding_up_to_date():
         return None
     import sysconfig
+    import tempfile
 
     import torch
 
@@ -111,7 +113,9 @@ def start_binding(force: bool = False):
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
-    tmp = f"{BINDING_PATH}.tmp{os.getpid()}"
+    # (a name of its own for every build: threads and processes may come here together)
+    fd, tmp = tempfile.mkstemp(prefix="tks_binding.", suffix=".tmp", dir=BUILD_DIR)
+    os.close(fd)
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", BINDING_SOURCE, "-o", tmp,
            f"-I{INCLUDE}", f"-I{inc}", f"-I{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
            f"-I{os.path.join(cuda, 'include')}", f"-I{sysconfig.get_paths()['include']}",
@@ -124,7 +128,9 @@ def finish_binding(started) -> str:
     if started is not None:
         proc, tmp = started
         if proc.wait() != 0:
+            os.remove(tmp)
             raise subprocess.CalledProcessError(proc.returncode, f"g++ {BINDING_SOURCE}")
+        os.chmod(tmp, 0o755)
         os.replace(tmp, BINDING_PATH)
     return BINDING_PATH
 

@@ -16,6 +16,7 @@ value); slot ``s`` is token ``s % page_size`` of page ``s // page_size``.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 _I32, _I64, _VP, _F32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
 
@@ -48,33 +49,45 @@ SIGNATURES = {
 }
 
 
-_binding = None
+_binding = None  # the C++ module, once its calls have somewhere to go
+_library = None  # the library that the package's calls go to
+_first_use, _change = threading.Lock(), threading.Lock()
+
+
+def _point(module):
+    from . import TksError
+
+    module.set_library(TksError, *(ctypes.cast(getattr(_library, name), _VP).value for name in SIGNATURES))
 
 
 def bound(lib):
     """Makes the calls go to the entry points of `lib` (called when the package loads a library)."""
-    if _binding is not None:
-        from . import TksError
-        _binding.set_library(TksError, *(ctypes.cast(getattr(lib, name), _VP).value for name in SIGNATURES))
+    global _library
+    with _change:
+        _library = lib
+        if _binding is not None:
+            _point(_binding)
 
 
 def _native():
     """The C++ module that checks the tensors and makes the calls, built and loaded on first use."""
     global _binding
-    if _binding is None:
-        import importlib.util
+    with _first_use:
+        if _binding is None:
+            import importlib.util
 
-        import torch  # noqa: F401  (its libraries come first)
+            import torch  # noqa: F401  (its libraries come first)
 
-        from . import load
-        from ._build import build_binding
+            from . import load
+            from ._build import build_binding
 
-        spec = importlib.util.spec_from_file_location("tks_binding", build_binding())
-        module = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(module)
-        lib = load()
-        _binding = module
-        bound(lib)
+            spec = importlib.util.spec_from_file_location("tks_binding", build_binding())
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            load()
+            with _change:
+                _point(module)
+                _binding = module  # (other threads' calls take it from here on)
     return _binding
 
 

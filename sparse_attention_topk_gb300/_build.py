@@ -89,13 +89,22 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str = LIB_PATH,
 # module built by the host compiler against torch's headers.
 BINDING_SOURCE = os.path.join(CSRC, "tks_binding.cpp")
 
-BINDING_PATH = os.path.join(BUILD_DIR, "tks_binding.so")
+
+def binding_path() -> str:
+    """Where the binding for this Python and this torch is: one built for another does not fit."""
+    import sysconfig
+
+    import torch
+
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(BUILD_DIR, f"tks_binding.{tag}.so")
 
 
 def _binding_up_to_date() -> bool:
-    if not os.path.exists(BINDING_PATH):
+    path = binding_path()
+    if not os.path.exists(path):
         return False
-    t = os.path.getmtime(BINDING_PATH)
+    t = os.path.getmtime(path)
     return all(os.path.getmtime(s) <= t for s in (BINDING_SOURCE, os.path.join(INCLUDE, "tks.h"),
                                                   os.path.join(INCLUDE, "tks_attention.h")))
 
@@ -125,14 +134,15 @@ def start_binding(force: bool = False):
 
 
 def finish_binding(started) -> str:
+    path = binding_path()
     if started is not None:
         proc, tmp = started
         if proc.wait() != 0:
             os.remove(tmp)
             raise subprocess.CalledProcessError(proc.returncode, f"g++ {BINDING_SOURCE}")
         os.chmod(tmp, 0o755)
-        os.replace(tmp, BINDING_PATH)
-    return BINDING_PATH
+        os.replace(tmp, path)
+    return path
 
 
 def build_binding(force: bool = False) -> str:

@@ -1,4 +1,4 @@
-"""The C++ module behind the cache and attention calls: its first use by several threads."""
+"""The C++ module behind the cache and attention calls: its first use by several threads, and which build is taken."""
 
 import os
 import threading
@@ -80,6 +80,15 @@ def test_another_library_is_taken_up(monkeypatch, tmp_path):
         attention.bound(lib)
 
 
+def test_a_build_for_another_torch_or_abi_is_not_taken(monkeypatch):
+    assert os.path.exists(_build.build_binding()) and _build._binding_up_to_date()
+    for where, name, other in ((torch, "__version__", "0.0.0"), (torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI)):
+        with monkeypatch.context() as m:
+            m.setattr(where, name, other)
+            assert not _build._binding_up_to_date()
+    assert _build._binding_up_to_date()
+
+
 def test_builds_side_by_side_have_files_of_their_own(monkeypatch, tmp_path):
     made = []
 
@@ -93,11 +102,10 @@ def test_builds_side_by_side_have_files_of_their_own(monkeypatch, tmp_path):
             return 1 if len(made) > 2 else 0
 
     monkeypatch.setattr(_build, "BUILD_DIR", str(tmp_path))
-    monkeypatch.setattr(_build, "BINDING_PATH", str(tmp_path / "tks_binding.so"))
     monkeypatch.setattr(_build.subprocess, "Popen", Compiler)
     a, b = _build.start_binding(force=True), _build.start_binding(force=True)
     assert made[0] != made[1]
-    assert _build.finish_binding(a) == _build.finish_binding(b) and os.listdir(tmp_path) == ["tks_binding.so"]
+    assert _build.finish_binding(a) == _build.finish_binding(b) and os.listdir(tmp_path) == [os.path.basename(_build.binding_path())]
     with pytest.raises(_build.subprocess.CalledProcessError):  # a build that fails leaves nothing behind
         _build.finish_binding(_build.start_binding(force=True))
     assert len(os.listdir(tmp_path)) == 1

@@ -23,7 +23,8 @@
  * of its own stream.)
  * The caller owns every buffer, which must stay valid until the work completes.
  *
- * Results do not depend on timing: the same call gives the same bits.  Waits
+ * Results do not depend on timing: the same call gives the same bits (but for
+ * tokens that are written to one slot, see tks_cache_write).  Waits
  * inside the attention kernels are bounded by TKS_OPT_SPIN_LIMIT_NS; one that
  * runs out is reported as TKS_E_TIMEOUT, and the outputs of that call are then
  * undefined.  (TKS_OPT_TEST_SKIP_ARRIVE makes one run out where a call has more
@@ -77,7 +78,9 @@ typedef struct {
  *            of each (strides for k and v apart; multiples of 16 bytes)
  *   slots    device pointer, int32 [n].  A negative slot skips its token; one
  *            at or beyond pages * page_size is skipped and reported as
- *            TKS_E_INDEX.  Of tokens with the same slot, any may win.
+ *            TKS_E_INDEX.  Slots are to differ: what two tokens with the same
+ *            slot leave there is undefined (it may be a mixture of both, codes
+ *            of one under the scale of the other, and differ from run to run)
  *
  * A cache in bfloat16 takes each value rounded to nearest even.  A cache in 8
  * bits takes, for a row x of one token and head,

@@ -99,8 +99,9 @@ def cache_write(k, v, k_cache, v_cache, slots, scales=None, stream=None):
     """Puts the keys and values of n tokens into a paged cache.
 
     ``k``, ``v``: bfloat16 or float32 CUDA tensors [n, kv_heads, head_dim] (views of a fused
-    projection are read in place).  ``slots``: int32 CUDA tensor [n], where each goes; a
-    negative slot skips its token.  An int8 cache takes each row as codes with a scale of
+    projection are read in place).  ``slots``: int32 CUDA tensor [n], where each goes, all
+    different (what two tokens with one slot leave there is undefined); a negative slot skips
+    its token.  An int8 cache takes each row as codes with a scale of
     max|x| / 127, written to ``scales``; a bfloat16 cache takes the values rounded.
     """
     (_binding or _native()).write(k, v, k_cache, v_cache, slots, scales, _handle(stream))

@@ -126,7 +126,7 @@ typedef struct {
     const int32_t *page_table;  /* int32 [batch][table_pages], row stride table_stride */
     int64_t table_stride;
     int32_t table_pages;
-    float softmax_scale;        /* finite */
+    float softmax_scale;        /* finite, and times log2(e), too: at most 2.3e38 */
 } tks_queries;
 
 /*

@@ -244,10 +244,13 @@ int log2_of(int32_t n) {
   return s;
 }
 
+// What scores are scaled with, as powers of two.
+float scale_log2(const tks_queries* q) { return (float)((double)q->softmax_scale * 1.4426950408889634); }
+
 int check_queries(const tks_cache* c, const tks_queries* q) {
   if (q == nullptr) return TKS_E_INVAL;
   if (q->batch < 0 || q->tokens < 0 || q->q_heads < 1 || q->q_heads % c->kv_heads) return TKS_E_INVAL;
-  if (!std::isfinite(q->softmax_scale)) return TKS_E_INVAL;
+  if (!std::isfinite(scale_log2(q))) return TKS_E_INVAL;
   if (q->table_pages < 0 || q->table_stride < 0) return TKS_E_INVAL;
   if (q->batch == 0 || q->tokens == 0) return TKS_OK;
   if ((int64_t)q->batch * q->tokens > INT32_MAX / q->q_heads) return TKS_E_INVAL;
@@ -284,7 +287,7 @@ Params params_of(const tks_cache* c, const tks_queries* q) {
   p.table = q->page_table;
   p.table_stride = q->table_stride;
   p.table_pages = q->table_pages;
-  p.scale_log2 = (float)((double)q->softmax_scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2(q);
   return p;
 }
 

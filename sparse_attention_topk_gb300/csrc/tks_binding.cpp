@@ -236,7 +236,7 @@ PyObject* attend(const Paged& c, const Tensor& q, const Tensor& table, PyObject*
   want(batch <= INT32_MAX && tokens <= INT32_MAX && heads <= INT32_MAX && table.size(1) <= INT32_MAX, "too many queries");
   const double s = scale == Py_None ? 1.0 / std::sqrt((double)dim) : PyFloat_AsDouble(scale);
   if (PyErr_Occurred()) throw Raised();
-  want(std::isfinite((float)s), "softmax_scale must be finite");
+  want(std::isfinite((float)((double)(float)s * 1.4426950408889634)), "softmax_scale must be finite, times log2(e) too");
   Place place(stream, c.device);
   Tensor out, lse;
   if (out_given == Py_None) {

@@ -12,6 +12,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import sparse_attention_topk_gb300 as tks  # noqa: E402
+from tests.attention_cancelling import cancelling  # noqa: E402
 from tests.attention_plain import PagedCache, check_rows  # noqa: E402
 from tests.test_attention_gpu import HELD, ancestors, gen, rand_rows, random_parents  # noqa: E402
 
@@ -192,3 +193,20 @@ def test_infinite_values_in_a_later_piece(heads):
     assert (out[..., 3] == math.inf).all()
     assert (out[:, 2:, :, 5] == -math.inf).all() and out[:, :2, :, 5].isfinite().all()
     assert out[:, 3, :, 6].isnan().all() and out[:, :3, :, 6].isfinite().all()
+
+
+@pytest.mark.parametrize("q_heads", [4, 16, 40, 130])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_weights_over_a_bfloat16_cache_are_held_to_sixteen_bits(dim, q_heads):
+    """Values that cancel, but for what the weights are off by."""
+    case = cancelling(dim, device="cuda")
+    n = case["k"].shape[0]
+    cache = PagedCache(-(-n // 16) + 1, 16, 1, dim, "bf16")
+    table, kh, vh = cache.fill(case["k"][:, None], case["v"][:, None])
+    q = case["q"].expand(1, 1, q_heads, dim).contiguous()
+    out, lse = tks.tree_attention(q, cache.k, cache.v, table[None], ints(n - 1), softmax_scale=case["scale"], return_lse=True)
+    err = (out[0, 0].double() - case["want"]).abs()
+    assert (err / case["bound"]).max().item() <= 1.0
+    sel, _ = tks.selected_attention(q, cache.k, cache.v, table[None], torch.randperm(n, device="cuda").to(torch.int32).view(1, 1, -1),
+                                    softmax_scale=case["scale"], return_lse=True)
+    assert ((sel[0, 0].double() - case["want"]).abs() / case["bound"]).max().item() <= 1.0

@@ -14,7 +14,9 @@
  * calls are asynchronous on `stream`, argument errors return TKS_E_INVAL and
  * launch nothing, and errors found on the device are read with
  * tks_device_status(stream) (which reports one at a time: first those of the
- * selection, then, at its next call, those of the calls below).  The library
+ * selection, then, at its next call, those of the calls below; of several kinds
+ * of these, TKS_E_TIMEOUT before TKS_E_INDEX before TKS_E_ROW_LEN, and all are
+ * cleared).  The library
  * allocates one workspace for each (device, stream) on the first of these calls
  * on it (make that call before any CUDA-graph capture); later calls allocate
  * nothing and never synchronise, and tks_release frees it with the others.

@@ -163,7 +163,8 @@ def tree_mask(parents):
     ``parents``: an integer tensor [batch, tokens]; the parent of draft i is an earlier draft
     of the same sequence, or -1 for one that follows the context directly.  A draft attends to
     itself, its parent, its parent's parent and so on.  Returns int32 [batch, tokens,
-    ceil(tokens / 32)] on the parents' device.
+    ceil(tokens / 32)] on the parents' device.  The bits are made on the host (parents on a
+    GPU are waited for), so keep them where the tree stays the same from step to step.
     """
     import torch
 

@@ -21,7 +21,9 @@ constexpr int kMaxPositions = 0x7fff0000;
 // accumulator whose small ones, below 2^-24 of it, are dropped: of a flat tail of weights behind a
 // dominant one, n * 2^-24 at most. A longer run of a unit's keys is summed in pieces, joined as the
 // partials of blocks are; at 32,768 the dropped part is 2^-9 at most, half a step of the bfloat16 output,
-// and a piece's begin and end (some 6 us) come once in 0.2 to 0.4 ms.
+// and the pieces cost 0.3 to 2.4 % (304 sequences of 65,536 positions of int8 and one token of 4 heads
+// 846 us, in one go 843; 152 of 131,072 and 32 rows 1351 and 1325; 152 of 65,536 and 128 rows 802 and
+// 784).
 constexpr int kPieceKeys = 32768;
 
 // Arguments of the cache kernels.

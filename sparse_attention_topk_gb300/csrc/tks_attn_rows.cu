@@ -11,7 +11,9 @@
 // so the codes go into the matrix products as they are, exact in half
 // precision, one multiply-add applies both scales to a score, and a weight is
 // rounded to 11 bits of itself (a small one in steps of 2^-31 of the largest,
-// which is the largest contribution to the output: kWeightLog2).
+// which is the largest contribution to the output: kWeightLog2). That is an
+// eighth of what the output's own rounding to bfloat16 may be; a second part of
+// it would cost as many products of values again.
 // Queries are bfloat16; they enter as halves, each row shifted by a power of
 // two of its own that brings its largest element to [2^14, 2^15): exactly, but
 // for elements more than 2^31 below that one.  (One shift for all 16 rows let a
@@ -23,8 +25,10 @@
 // works on 16 rows, so up to 16 rows of a head cost the same; 16 keys of int8
 // (4 KB) take 32 of them, a third of their rate at the memory's pace.
 // Measured: one token over 1,048,576 positions of int8 (4 heads of 128, 1.11 GB)
-// 184-194 us, 5.7-6.0 TB/s; one over 4096 (8 heads, 8.7 MB) 11.6 us, bound by
-// the chain of lookups, copies and joins that a lone call cannot hide.
+// 179-195 us, 5.7-6.2 TB/s, of bfloat16 354 us, 6.1 TB/s; 8 ragged trees of 4
+// drafts over up to 65,536 positions of int8 (16 rows a head, 0.6 GB) 122 us, 4.9
+// TB/s; one token over 4096 (8 heads, 8.7 MB) 11.6 us, bound by the chain of
+// lookups, copies and joins that a lone call cannot hide.
 //
 // Layout.  A block is four warps; each takes every fourth chunk of the block's
 // segment (32 keys of int8, 16 of bfloat16: 8 KB), keeps its own maximum, sum and

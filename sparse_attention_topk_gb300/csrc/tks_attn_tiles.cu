@@ -5,9 +5,11 @@
 // Mathematics: that of tks_attn_rows.cu (running maximum and sum; codes of an
 // 8-bit cache exact in half precision, both scales folded into one
 // multiply-add per score, weights relative to the largest contribution).
-// Each row's queries get their own power of two. What weights are relative to
-// follows only when a row's maximum has grown by more than 2^8, so the output in
-// tensor memory is rarely rescaled.
+// What weights are relative to follows only when a row's maximum has grown by
+// more than 2^8, so the output in tensor memory is rarely rescaled. Over 8 bits
+// each row's queries get their own power of two: a row whose largest element is
+// in [2^-7, 2^14) goes as it is, another is brought to [1, 2). Elements more than
+// 2^10 (2^17) below the largest may be off, by 2^-18 (2^-25) of it at most.
 //
 // Layout.  A block is one SM: 128 query rows (a lane of tensor memory each)
 // against tiles of 128 keys. Warps 0-7 keep the rows: they take scores into
@@ -21,16 +23,19 @@
 // bfloat16 cache goes there by cp.async. Rows are gathered one by one, so
 // pages, lists and the order of positions do not matter.
 //
-// What bounds it: up to 128 rows the cache's bytes (32 KB of int8 a tile, 1400
-// cycles at the memory's rate, against 1024 of tensor work for a full 128
-// rows); beyond, the eight warps that make weights and the eight that widen
-// rows, which share an SM's issue slots and take about as long as each other.
-// Measured: 8 ragged trees of 8 drafts over up to 65,536 positions of bfloat16
-// (32 rows a head, 1.16 GB) 195 us, 5.9 TB/s; two trees of 64 drafts over 32,768
-// positions of int8 (512 rows a head, 137 Gflop) 196 us, 700 Tflop/s, a tile in
+// What bounds it: over bfloat16 and few rows the cache's bytes (64 KB a tile,
+// 2800 cycles at the memory's rate, against 1536 of tensor work for a full 128
+// rows). Over int8, whose tile memory delivers in 1400 cycles, and with many
+// rows: the eight warps that make weights and the eight that widen rows, which
+// share an SM's issue slots and take about as long as each other.
+// Measured: 8 ragged trees of 8 drafts over up to 65,536 positions (32 rows a
+// head) of bfloat16 (1.16 GB) 193-195 us, 5.9-6.0 TB/s, of int8 (0.6 GB) 181 us,
+// 3.3 TB/s, a tile in some 3100 cycles; two trees of 64 drafts over 32,768
+// positions (512 rows a head, 137 Gflop) of int8 196 us, 700 Tflop/s, a tile in
 // some 3500 cycles (161 us without making weights, 178 without loading rows, 103
-// without both); 512 queries of 64 heads over 2048 selected positions each 103 us,
-// of which a block's four changes of segment take some 6 us each.
+// without both), of bfloat16 230 us; 512 queries of 64 heads over 2048 selected
+// positions each 103 us of int8, of which a block's four changes of segment take
+// some 6 us each, and 114 us of bfloat16.
 //
 // Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
 // warp's role, which makes the waits on that warp run out; when all roles have

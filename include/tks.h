@@ -49,7 +49,8 @@ typedef enum {
     TKS_E_INTERNAL = 5,    /* a device-side consistency check failed */
     TKS_E_ROW_LEN = 6,     /* a device row length was < 0 or > row_stride (clamped) */
     TKS_E_TOO_LARGE = 7,   /* more rows than tks_topk_indices_noalloc's fixed scratch holds */
-    TKS_E_INDEX = 8        /* a slot, page or position lay outside the cache (skipped; tks_attention.h) */
+    TKS_E_INDEX = 8,       /* a slot, page or position lay outside the cache (skipped; tks_attention.h) */
+    TKS_E_NO_PAGE = 9      /* no free page was left for a sequence (tks_blocks.h) */
 } tks_status;
 
 /* Largest k accepted. */

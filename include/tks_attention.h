@@ -15,7 +15,8 @@
  * launch nothing, and errors found on the device are read with
  * tks_device_status(stream) (which reports one at a time: first those of the
  * selection, then, at its next call, those of the calls below; of several kinds
- * of these, TKS_E_TIMEOUT before TKS_E_INDEX before TKS_E_ROW_LEN, and all are
+ * of these, TKS_E_TIMEOUT before TKS_E_NO_PAGE (of tks_blocks.h) before
+ * TKS_E_INDEX before TKS_E_ROW_LEN, and all are
  * cleared).  The library
  * allocates one workspace for each (device, stream) on the first of these calls
  * on it (make that call before any CUDA-graph capture); later calls allocate

@@ -9,7 +9,8 @@ missing or the device is unsupported.
     idx = tks.topk_indices(logits, k=2048)            # logits: cuda fp32/bf16 [batch, n]
     idx = tks.topk_indices(logits, 2048, row_len=lens)  # ragged rows (int32 cuda tensor)
 
-The paged cache that the indices point into, and the attention over it, are in ``attention.py``.
+The paged cache that the indices point into, and the attention over it, are in ``attention.py``;
+sparse attention by blocks of it, and what is done with its pages between steps, in ``blocks.py``.
 """
 
 from __future__ import annotations
@@ -19,9 +20,12 @@ import os
 import threading
 
 from . import attention as _attention
+from . import blocks as _blocks
 from ._build import LIB_PATH, build, up_to_date
 from .attention import (TKS_DRAFTS_MAX, TKS_E_INDEX, TKS_I8, Cache, Queries, cache_read, cache_write,
                         selected_attention, tree_attention, tree_mask)
+from .blocks import (TKS_E_NO_PAGE, Bounds, block_attention, block_scores, cache_bounds, cache_compact, cache_copy,
+                     cache_fork)
 
 TKS_F32 = 0
 TKS_BF16 = 1
@@ -46,7 +50,8 @@ TKS_OPT_TEST_SKIP_ARRIVE = 4
 TKS_OPT_FORCE_THREADS = 5
 TKS_OPT_CLUSTER = 6
 
-# Every entry point include/tks.h and include/tks_attention.h declare, with its ctypes signature.
+# Every entry point include/tks.h, include/tks_attention.h and include/tks_blocks.h declare, with its
+# ctypes signature.
 _I32, _I64, _VP = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
 SIGNATURES = {
     "tks_topk_indices": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
@@ -60,6 +65,7 @@ SIGNATURES = {
     "tks_topk_indices_sorted": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
     "tks_topk_indices_host": (ctypes.c_int, [_VP, _VP, _I32, _I64, _I32, _I32, _VP, _VP]),
     **_attention.SIGNATURES,
+    **_blocks.SIGNATURES,
 }
 
 _lock = threading.Lock()
@@ -278,4 +284,5 @@ __all__ = [
     "TKS_OPT_SPIN_LIMIT_NS", "TKS_OPT_MIN_PER_BLOCK", "TKS_OPT_TEST_SKIP_ARRIVE", "TKS_OPT_FORCE_THREADS", "TKS_OPT_CLUSTER",
     "cache_write", "cache_read", "tree_attention", "selected_attention", "tree_mask", "Cache", "Queries",
     "TKS_I8", "TKS_E_INDEX", "TKS_DRAFTS_MAX",
+    "cache_bounds", "block_scores", "block_attention", "cache_fork", "cache_compact", "cache_copy", "Bounds", "TKS_E_NO_PAGE",
 ]

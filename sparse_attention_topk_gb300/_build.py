@@ -1,5 +1,5 @@
 """Builds libtks.so (the CUDA library) in-tree with nvcc, for sm_103a, and the C++ binding
-of the cache and attention calls with the host compiler."""
+of the cache, attention, block and page calls with the host compiler."""
 
 from __future__ import annotations
 
@@ -17,11 +17,13 @@ LIB_PATH = os.path.join(BUILD_DIR, "libtks.so")
 SOURCES = [os.path.join(CSRC, "tks_select.cu"), os.path.join(CSRC, "tks_select512.cu"),
            os.path.join(CSRC, "tks_order.cu"), os.path.join(CSRC, "tks_cache.cu"),
            os.path.join(CSRC, "tks_attn.cu"), os.path.join(CSRC, "tks_attn_rows.cu"),
-           os.path.join(CSRC, "tks_attn_tiles.cu"), os.path.join(CSRC, "tks_attn_tiles_bf16.cu")]
+           os.path.join(CSRC, "tks_attn_tiles.cu"), os.path.join(CSRC, "tks_attn_tiles_bf16.cu"),
+           os.path.join(CSRC, "tks_blocks.cu"), os.path.join(CSRC, "tks_pages.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "tks_device.cuh"), os.path.join(CSRC, "tks_kernel.cuh"),
                      os.path.join(CSRC, "tks_internal.h"), os.path.join(CSRC, "tks_attn.cuh"),
-                     os.path.join(CSRC, "tks_attn_internal.h"), os.path.join(INCLUDE, "tks.h"),
-                     os.path.join(INCLUDE, "tks_attention.h")]
+                     os.path.join(CSRC, "tks_attn_internal.h"), os.path.join(CSRC, "tks_attn_host.h"),
+                     os.path.join(INCLUDE, "tks.h"), os.path.join(INCLUDE, "tks_attention.h"),
+                     os.path.join(INCLUDE, "tks_blocks.h")]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_103a,code=sm_103a",
@@ -85,7 +87,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, out: str = LIB_PATH,
     return out
 
 
-# The C++ step between Python and the cache and attention calls: an extension
+# The C++ step between Python and the cache, attention, block and page calls: an extension
 # module built by the host compiler against torch's headers.
 BINDING_SOURCE = os.path.join(CSRC, "tks_binding.cpp")
 
@@ -106,7 +108,8 @@ def _binding_up_to_date() -> bool:
         return False
     t = os.path.getmtime(path)
     return all(os.path.getmtime(s) <= t for s in (BINDING_SOURCE, os.path.join(INCLUDE, "tks.h"),
-                                                  os.path.join(INCLUDE, "tks_attention.h")))
+                                                  os.path.join(INCLUDE, "tks_attention.h"),
+                                                  os.path.join(INCLUDE, "tks_blocks.h")))
 
 
 def start_binding(force: bool = False):

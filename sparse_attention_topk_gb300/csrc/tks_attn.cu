@@ -1,5 +1,6 @@
-// Host side of the cache and attention calls (include/tks_attention.h), and
-// the kernel that joins partial results.
+// Host side of the cache and attention calls (include/tks_attention.h, and
+// tks_block_attention of include/tks_blocks.h), and the kernel that joins
+// partial results.
 
 #include <algorithm>
 #include <atomic>
@@ -10,11 +11,69 @@
 #include <mutex>
 #include <tuple>
 
-#include "tks_attention.h"
 #include "tks_attn.cuh"
+#include "tks_attn_host.h"
 
 namespace tks {
 namespace attn {
+
+// ---------------------------------------------------------------------------
+// Argument checks (nothing is touched on the device)
+// ---------------------------------------------------------------------------
+// Strides in elements of `size` bytes (with the extents they step over): none is
+// negative, all are whole 16-byte pieces, and every offset in bytes fits 60 bits.
+bool strides_ok(int64_t size, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2) {
+  const int64_t unit = 16 / size;
+  if (s0 < 0 || s1 < 0 || s2 < 0 || s0 % unit || s1 % unit || s2 % unit) return false;
+  const __int128 span = (__int128)n0 * s0 + (__int128)n1 * s1 + (__int128)n2 * s2;
+  return span * size < ((__int128)1 << 60);
+}
+
+int check_cache(const tks_cache* c) {
+  if (c == nullptr) return TKS_E_INVAL;
+  if (c->held != TKS_BF16 && c->held != TKS_I8) return TKS_E_INVAL;
+  if (c->head_dim != 64 && c->head_dim != 128) return TKS_E_INVAL;
+  if (c->kv_heads < 1 || c->pages < 1 || c->page_size < 1 || (c->page_size & (c->page_size - 1)))
+    return TKS_E_INVAL;
+  if ((int64_t)c->pages * c->page_size > INT32_MAX) return TKS_E_INVAL;
+  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return TKS_E_INVAL;
+  const int64_t size = c->held == TKS_I8 ? 1 : 2;
+  if (!strides_ok(size, c->pages, c->page_stride, c->page_size, c->token_stride, c->kv_heads, c->head_stride))
+    return TKS_E_INVAL;
+  if (c->held == TKS_I8 && (!c->scales || !aligned(c->scales, 8))) return TKS_E_INVAL;
+  return TKS_OK;
+}
+
+int log2_of(int32_t n) {
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
+}
+
+// What scores are scaled with, as powers of two.
+static float scale_log2(const tks_queries* q) { return (float)((double)q->softmax_scale * 1.4426950408889634); }
+
+int check_q(int32_t kv_heads, const tks_queries* q) {
+  if (q == nullptr) return TKS_E_INVAL;
+  if (q->batch < 0 || q->tokens < 0 || q->q_heads < 1 || q->q_heads % kv_heads) return TKS_E_INVAL;
+  if (q->table_pages < 0 || q->table_stride < 0) return TKS_E_INVAL;
+  if (q->batch == 0 || q->tokens == 0) return TKS_OK;
+  if ((int64_t)q->batch * q->tokens > INT32_MAX / q->q_heads) return TKS_E_INVAL;
+  if (!q->q || !aligned(q->q, 16)) return TKS_E_INVAL;
+  if (!strides_ok(2, q->batch, q->q_batch_stride, q->tokens, q->q_token_stride, q->q_heads, q->q_head_stride))
+    return TKS_E_INVAL;
+  if (q->table_stride > ((int64_t)1 << 56) / (q->batch > 0 ? q->batch : 1)) return TKS_E_INVAL;
+  if (q->table_pages > 0 && (!q->page_table || !aligned(q->page_table, 4))) return TKS_E_INVAL;
+  return TKS_OK;
+}
+
+int check_queries(const tks_cache* c, const tks_queries* q) {
+  if (q == nullptr || check_q(c->kv_heads, q) != TKS_OK) return TKS_E_INVAL;
+  if (!std::isfinite(scale_log2(q))) return TKS_E_INVAL;
+  if (q->batch == 0 || q->tokens == 0) return TKS_OK;
+  return q->out && aligned(q->out, 16) && aligned(q->lse, 4) ? TKS_OK : TKS_E_INVAL;
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -210,58 +269,6 @@ int prepare(void* stream, Device* dev, Workspace* ws) try {
   return TKS_E_CUDA;
 }
 
-// ---------------------------------------------------------------------------
-// Argument checks (nothing is touched on the device)
-// ---------------------------------------------------------------------------
-bool aligned(const void* p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
-// Strides in elements of `size` bytes (with the extents they step over): none is
-// negative, all are whole 16-byte pieces, and every offset in bytes fits 60 bits.
-bool strides_ok(int64_t size, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2 = 0, int64_t s2 = 0) {
-  const int64_t unit = 16 / size;
-  if (s0 < 0 || s1 < 0 || s2 < 0 || s0 % unit || s1 % unit || s2 % unit) return false;
-  const __int128 span = (__int128)n0 * s0 + (__int128)n1 * s1 + (__int128)n2 * s2;
-  return span * size < ((__int128)1 << 60);
-}
-
-int check_cache(const tks_cache* c) {
-  if (c == nullptr) return TKS_E_INVAL;
-  if (c->held != TKS_BF16 && c->held != TKS_I8) return TKS_E_INVAL;
-  if (c->head_dim != 64 && c->head_dim != 128) return TKS_E_INVAL;
-  if (c->kv_heads < 1 || c->pages < 1 || c->page_size < 1 || (c->page_size & (c->page_size - 1)))
-    return TKS_E_INVAL;
-  if ((int64_t)c->pages * c->page_size > INT32_MAX) return TKS_E_INVAL;
-  if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return TKS_E_INVAL;
-  const int64_t size = c->held == TKS_I8 ? 1 : 2;
-  if (!strides_ok(size, c->pages, c->page_stride, c->page_size, c->token_stride, c->kv_heads, c->head_stride))
-    return TKS_E_INVAL;
-  if (c->held == TKS_I8 && (!c->scales || !aligned(c->scales, 8))) return TKS_E_INVAL;
-  return TKS_OK;
-}
-
-int log2_of(int32_t n) {
-  int s = 0;
-  while ((1 << s) < n) ++s;
-  return s;
-}
-
-// What scores are scaled with, as powers of two.
-float scale_log2(const tks_queries* q) { return (float)((double)q->softmax_scale * 1.4426950408889634); }
-
-int check_queries(const tks_cache* c, const tks_queries* q) {
-  if (q == nullptr) return TKS_E_INVAL;
-  if (q->batch < 0 || q->tokens < 0 || q->q_heads < 1 || q->q_heads % c->kv_heads) return TKS_E_INVAL;
-  if (!std::isfinite(scale_log2(q))) return TKS_E_INVAL;
-  if (q->table_pages < 0 || q->table_stride < 0) return TKS_E_INVAL;
-  if (q->batch == 0 || q->tokens == 0) return TKS_OK;
-  if ((int64_t)q->batch * q->tokens > INT32_MAX / q->q_heads) return TKS_E_INVAL;
-  if (!q->q || !q->out || !aligned(q->q, 16) || !aligned(q->out, 16) || !aligned(q->lse, 4)) return TKS_E_INVAL;
-  if (!strides_ok(2, q->batch, q->q_batch_stride, q->tokens, q->q_token_stride, q->q_heads, q->q_head_stride))
-    return TKS_E_INVAL;
-  if (q->table_stride > ((int64_t)1 << 56) / (q->batch > 0 ? q->batch : 1)) return TKS_E_INVAL;
-  if (q->table_pages > 0 && (!q->page_table || !aligned(q->page_table, 4))) return TKS_E_INVAL;
-  return TKS_OK;
-}
-
 Params params_of(const tks_cache* c, const tks_queries* q) {
   Params p{};
   const long long size = c->held == TKS_I8 ? 1 : 2;
@@ -377,6 +384,18 @@ CacheParams cache_params(const tks_cache* c, const int32_t* slots, int32_t n, un
 }
 
 }  // namespace
+
+int place_of(void* stream, Place* place) {
+  Device d;
+  Workspace ws;
+  const int rc = prepare(stream, &d, &ws);
+  if (rc != TKS_OK) return rc;
+  place->sms = d.sms;
+  place->status = reinterpret_cast<unsigned*>(ws.ptr);
+  place->order = ws.order;
+  return TKS_OK;
+}
+
 }  // namespace attn
 
 int attn_status(int dev, void* stream) {
@@ -405,6 +424,7 @@ int attn_status(int dev, void* stream) {
     return TKS_E_CUDA;
   }
   if (st & kStatTimeoutBit) return TKS_E_TIMEOUT;
+  if (st & kStatNoPageBit) return TKS_E_NO_PAGE;
   return st & kStatIndexBit ? TKS_E_INDEX : TKS_E_ROW_LEN;
 }
 
@@ -506,8 +526,28 @@ extern "C" int tks_selected_attention(const tks_cache* cache, const tks_queries*
   if ((k > 0 && !indices) || !aligned(indices, 4) || !aligned(kv_len, 4)) return TKS_E_INVAL;
   Params p = params_of(cache, queries);
   p.indices = indices;
+  p.list_seq = k;
   p.k_sel = k;
   p.kv_len = kv_len;
+  p.seqs = queries->batch * queries->tokens;
+  p.rows = p.group;
+  return launch(p, cache, true, stream);
+}
+
+extern "C" int tks_block_attention(const tks_cache* cache, const tks_queries* queries, const int32_t* blocks,
+                                   int32_t n, int32_t block, const int32_t* kv_len, void* stream) {
+  if (check_cache(cache) != TKS_OK || check_queries(cache, queries) != TKS_OK) return TKS_E_INVAL;
+  if (n < 0 || block < 1 || (block & (block - 1)) || (int64_t)n * block > TKS_K_MAX) return TKS_E_INVAL;
+  if (queries->batch == 0 || queries->tokens == 0) return TKS_OK;
+  if ((n > 0 && !blocks) || !aligned(blocks, 4) || !aligned(kv_len, 4)) return TKS_E_INVAL;
+  Params p = params_of(cache, queries);
+  p.indices = blocks;
+  p.list_seq = (long long)cache->kv_heads * n;
+  p.list_head = n;
+  p.block_shift = log2_of(block);
+  p.k_sel = n * block;
+  p.kv_len = kv_len;
+  p.kv_tokens = queries->tokens;
   p.seqs = queries->batch * queries->tokens;
   p.rows = p.group;
   return launch(p, cache, true, stream);

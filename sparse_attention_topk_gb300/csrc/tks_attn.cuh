@@ -144,8 +144,27 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int s, bool* bad = nullpt
   return q;
 }
 
-// The number of positions that a list's entries may name; `given`: kv_len[b], or INT_MAX.
-__device__ __forceinline__ int kv_given(const Params& p, int b) { return p.kv_len ? __ldg(p.kv_len + b) : 0x7fffffff; }
+// The list of a token (seq) and head.
+__device__ __forceinline__ const int32_t* list_of(const Params& p, int seq, int head) {
+  return p.indices + seq * p.list_seq + (long long)head * p.list_head;
+}
+// The position of key j of a list, given its entry (that of key j's block), or -1.
+__device__ __forceinline__ int list_position(const Params& p, int entry, int j, int limit, bool& bad) {
+  if (entry < 0) return -1;
+  if (p.block_shift == 0) {
+    bad |= entry >= limit;
+    return entry >= limit ? -1 : entry;
+  }
+  if (entry > (0x7fffffff >> p.block_shift) || entry << p.block_shift >= limit) {
+    bad = true;
+    return -1;
+  }
+  const int pos = entry << p.block_shift | (j & ((1 << p.block_shift) - 1));
+  return pos >= limit ? -1 : pos;  // (a block may reach beyond the length)
+}
+
+// The number of positions that a list's entries may name; `given`: kv_len of the sequence or token, or INT_MAX.
+__device__ __forceinline__ int kv_given(const Params& p, int b, int seq) { return p.kv_len ? __ldg(p.kv_len + (p.kv_tokens ? seq : b)) : 0x7fffffff; }
 __device__ __forceinline__ int kv_limit(const Params& p, int given) {
   const int r = min(max(given, 0), capacity(p));
   if (r != given && p.kv_len) report(p.status, kStatRowLenBit);

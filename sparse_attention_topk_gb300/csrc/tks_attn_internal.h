@@ -13,6 +13,7 @@ namespace attn {
 constexpr unsigned kStatTimeoutBit = 1u << 0;
 constexpr unsigned kStatRowLenBit = 1u << 1;
 constexpr unsigned kStatIndexBit = 1u << 3;
+constexpr unsigned kStatNoPageBit = 1u << 4;
 
 // Most positions of a sequence: indices of keys stay below 2^31 with a tile to spare.
 constexpr int kMaxPositions = 0x7fff0000;
@@ -93,8 +94,12 @@ struct Params {
   int table_pages;
   const int32_t *ctx_len, *draft_len, *tree;  // tree attention
   int tree_words;
-  const int32_t *indices, *kv_len;  // selected attention
-  int k_sel;
+  const int32_t *indices, *kv_len;  // selected attention: lists, and the lengths that their entries keep to,
+  long long list_seq;               // a list's stride in entries, from token to token
+  int list_head;                    // and from head to head (0: one list for all)
+  int block_shift;                  // log2 of the keys that an entry stands for
+  int kv_tokens;                    // tokens of a sequence that have a length of their own (0: one for all)
+  int k_sel;                        // keys of a list
   float scale_log2;  // softmax_scale * log2(e)
   int seqs;          // tree: batch; selected: batch * tokens
   int rows;          // query rows of one (sequence, head)

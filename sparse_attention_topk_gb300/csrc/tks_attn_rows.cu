@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     const int k_beg = t0 * kRowsKeys;  // tiles * kRowsKeys stays below 2^31: len does, rounded up once
     const int k_end = (int)min((long long)len.len, (long long)t1 * kRowsKeys);
     const int32_t* table = p.table + b * p.table_stride;
-    const int32_t* list = SEL ? p.indices + (long long)seq * p.k_sel : nullptr;
-    const int given = SEL ? kv_given(p, b) : 0;
+    const int32_t* list = SEL ? list_of(p, seq, head) : nullptr;
+    const int given = SEL ? kv_given(p, b, seq) : 0;
     const unsigned char* kb = p.k + head * p.head_b;
     const unsigned char* vb = p.v + head * p.head_b;
 
@@ -293,14 +293,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int j = beg + threadIdx.x + i * kThreads;
-        pos[i] = j >= end ? -1 : SEL ? __ldg(list + j) : j;
+        pos[i] = j >= end ? -1 : SEL ? __ldg(list + (j >> p.block_shift)) : j;
       }
       bool bad = false;
       const int limit = SEL ? kv_limit(p, given) : 0;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        bad |= SEL && pos[i] >= limit;
-        if (SEL && pos[i] >= limit) pos[i] = -1;
+        if (SEL) pos[i] = list_position(p, pos[i], beg + threadIdx.x + i * kThreads, limit, bad);
         pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
       __syncthreads();  // the previous keys' copies have started

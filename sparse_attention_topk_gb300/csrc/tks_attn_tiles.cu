@@ -310,13 +310,13 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
   bool bad = false;
   while (uniform((int)it.next(p, s))) {
     const int32_t* table = p.table + s.b * p.table_stride;
-    const int32_t* list = SEL ? p.indices + (long long)s.seq * p.k_sel : nullptr;
-    const int limit = SEL ? kv_limit(p, kv_given(p, s.b)) : 0;
+    const int32_t* list = SEL ? list_of(p, s.seq, s.head) : nullptr;
+    const int limit = SEL ? kv_limit(p, kv_given(p, s.b, s.seq)) : 0;
     const int end = (int)min((long long)s.len.len, (long long)s.t1 * kKeys);
     auto entry = [&](int t, int i) -> int {  // key i of tile t: its list entry, or its position
       const int j = t * kKeys + i;
       if (t >= s.t1 || j >= end) return -1;
-      return SEL ? __ldg(list + j) : j;
+      return SEL ? __ldg(list + (j >> p.block_shift)) : j;
     };
     int t = uniform(s.t0 + (int)((who + 3u - g % 3u) % 3u));
     const int t1 = uniform(s.t1);
@@ -327,9 +327,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
       int pos[4], pg[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        pos[i] = e[i];
-        bad |= SEL && pos[i] >= limit;
-        if (SEL && pos[i] >= limit) pos[i] = -1;
+        pos[i] = SEL ? list_position(p, e[i], t * kKeys + lane + 32 * i, limit, bad) : e[i];
         pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
 #pragma unroll

@@ -1,6 +1,6 @@
-// The Python side of the cache and attention calls: checks of the tensors, the
-// outputs' allocation and the call of the C entry point (include/tks_attention.h),
-// in one C++ step.  A decode step makes these calls for every layer, and the
+// The Python side of the cache, attention, block and page calls: checks of the
+// tensors, the outputs' allocation and the call of the C entry point
+// (include/tks_attention.h, include/tks_blocks.h), in one C++ step.  A decode step makes these calls for every layer, and the
 // same work in Python took longer than the kernels of a short context (33 us
 // of host time a call, 6 so, where the kernels take 9).
 //
@@ -22,6 +22,7 @@
 #include <string>
 
 #include "tks_attention.h"
+#include "tks_blocks.h"
 
 namespace {
 
@@ -31,6 +32,12 @@ decltype(&tks_cache_write) f_write = nullptr;
 decltype(&tks_cache_read) f_read = nullptr;
 decltype(&tks_tree_attention) f_tree = nullptr;
 decltype(&tks_selected_attention) f_selected = nullptr;
+decltype(&tks_cache_bounds) f_bounds = nullptr;
+decltype(&tks_block_scores) f_scores = nullptr;
+decltype(&tks_block_attention) f_block = nullptr;
+decltype(&tks_cache_fork) f_fork = nullptr;
+decltype(&tks_cache_compact) f_compact = nullptr;
+decltype(&tks_cache_copy) f_copy = nullptr;
 PyObject* tks_error = nullptr;  // the package's TksError
 
 struct Refused : std::exception {
@@ -160,11 +167,13 @@ PyObject* guarded(F&& f) {
   return nullptr;
 }
 
-bool arity(Py_ssize_t n, Py_ssize_t wanted) {
-  if (n == wanted && f_write) return true;
-  PyErr_SetString(PyExc_TypeError, f_write ? "wrong number of arguments" : "the library is not set");
+bool arity(Py_ssize_t n, Py_ssize_t wanted, bool set) {
+  if (n == wanted && set) return true;
+  PyErr_SetString(PyExc_TypeError, set ? "wrong number of arguments" : "the library is not set");
   return false;
 }
+bool arity(Py_ssize_t n, Py_ssize_t wanted) { return arity(n, wanted, f_write != nullptr); }
+bool arity_blocks(Py_ssize_t n, Py_ssize_t wanted) { return arity(n, wanted, f_bounds != nullptr); }
 
 int dtype_of(at::ScalarType t, const char* what) {
   want(t == at::kBFloat16 || t == at::kFloat, what);
@@ -224,15 +233,34 @@ PyObject* py_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// What both attention calls share: the queries, the page table, the outputs.
+// The queries and the page table, as the C entry points take them; x: q as the kernels can read it.
+tks_queries queries_of(const Tensor& x, const Tensor& table) {
+  tks_queries r{};
+  r.q = x.data_ptr();
+  r.q_batch_stride = step(x, 0);
+  r.q_token_stride = step(x, 1);
+  r.q_head_stride = step(x, 2);
+  r.batch = (int32_t)x.size(0);
+  r.tokens = (int32_t)x.size(1);
+  r.q_heads = (int32_t)x.size(2);
+  r.page_table = static_cast<const int32_t*>(table.data_ptr());
+  r.table_stride = step(table, 0);
+  r.table_pages = (int32_t)table.size(1);
+  return r;
+}
+void check_table(const Tensor& table, int64_t rows, const at::Device& device, const char* what) {
+  want(table.dim() == 2 && (rows < 0 || table.size(0) == rows) && table.scalar_type() == at::kInt && table.device() == device && table.is_cuda() &&
+           (table.size(1) <= 1 || table.stride(1) == 1),
+       what);
+}
+
+// What the attention calls share: the queries, the page table, the outputs.
 template <typename F>
 PyObject* attend(const Paged& c, const Tensor& q, const Tensor& table, PyObject* scale, PyObject* out_given, bool with_lse, PyObject* stream,
                  const char* what, F&& call) {
   const int64_t batch = q.size(0), tokens = q.size(1), heads = q.size(2), dim = q.size(3);
   want(heads >= 1 && heads % c.c.kv_heads == 0, "q_heads must be a multiple of kv_heads");
-  want(table.dim() == 2 && table.size(0) == batch && table.scalar_type() == at::kInt && table.device() == c.device &&
-           (table.size(1) <= 1 || table.stride(1) == 1),
-       "page_table must be an int32 CUDA tensor [batch, pages of a sequence] with contiguous rows");
+  check_table(table, batch, c.device, "page_table must be an int32 CUDA tensor [batch, pages of a sequence] with contiguous rows");
   want(batch <= INT32_MAX && tokens <= INT32_MAX && heads <= INT32_MAX && table.size(1) <= INT32_MAX, "too many queries");
   const double s = scale == Py_None ? 1.0 / std::sqrt((double)dim) : PyFloat_AsDouble(scale);
   if (PyErr_Occurred()) throw Raised();
@@ -248,19 +276,9 @@ PyObject* attend(const Paged& c, const Tensor& q, const Tensor& table, PyObject*
   }
   if (with_lse) lse = at::empty({batch, tokens, heads}, at::TensorOptions().dtype(at::kFloat).device(c.device));
   const Tensor x = readable(q);
-  tks_queries r{};
-  r.q = x.data_ptr();
-  r.q_batch_stride = step(x, 0);
-  r.q_token_stride = step(x, 1);
-  r.q_head_stride = step(x, 2);
+  tks_queries r = queries_of(x, table);
   r.out = out.data_ptr();
   r.lse = with_lse ? static_cast<float*>(lse.data_ptr()) : nullptr;
-  r.batch = (int32_t)batch;
-  r.tokens = (int32_t)tokens;
-  r.q_heads = (int32_t)heads;
-  r.page_table = static_cast<const int32_t*>(table.data_ptr());
-  r.table_stride = step(table, 0);
-  r.table_pages = (int32_t)table.size(1);
   r.softmax_scale = (float)s;
   check(call(&c.c, &r, place.stream), what);
   if (!with_lse) return THPVariable_Wrap(out);
@@ -330,12 +348,257 @@ PyObject* py_set(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// The bounds of a cache's blocks, and their device. page_size: the cache's, or 0: made of `block`.
+struct Bounds {
+  tks_bounds b;
+  at::Device device;
+};
+Bounds bounds_of(const Tensor& t, int64_t page_size, int64_t block) {
+  want(t.dim() == 5 && t.is_cuda() && t.scalar_type() == at::kBFloat16 && t.size(3) == 2 && t.is_contiguous() && aligned16(t.data_ptr()),
+       "bounds must be a contiguous, 16-byte aligned bfloat16 CUDA tensor [pages, blocks of a page, kv_heads, 2, head_dim]");
+  const int64_t pages = t.size(0), of_page = t.size(1), heads = t.size(2), dim = t.size(4);
+  want(dim == 64 || dim == 128, "head_dim must be 64 or 128");
+  want(pages >= 1 && heads >= 1 && of_page >= 1 && (of_page & (of_page - 1)) == 0, "a page's blocks are a power of two");
+  if (page_size) {
+    want(of_page <= page_size, "a page has at most as many blocks as tokens");
+    block = page_size / of_page;
+  }
+  want(block >= 1 && (block & (block - 1)) == 0 && block <= INT32_MAX / of_page, "block must be a power of two");
+  want(pages <= INT32_MAX && heads <= INT32_MAX, "too many pages or heads");
+  Bounds r{tks_bounds{}, t.device()};
+  r.b.bounds = t.data_ptr();
+  r.b.block = (int32_t)block;
+  r.b.pages = (int32_t)pages;
+  r.b.page_size = (int32_t)(block * of_page);
+  r.b.kv_heads = (int32_t)heads;
+  r.b.head_dim = (int32_t)dim;
+  return r;
+}
+Bounds bounds_of(const Tensor& t, const Paged& c) {
+  Bounds r = bounds_of(t, c.c.page_size, 0);
+  want(r.device == c.device && r.b.pages == c.c.pages && r.b.kv_heads == c.c.kv_heads && r.b.head_dim == c.c.head_dim,
+       "bounds must have the cache's pages, heads, head_dim and device");
+  return r;
+}
+
+int64_t number(PyObject* o, const char* what) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised();
+  if (v < 0 || v > INT32_MAX) throw Refused(std::string(what) + " must be in [0, 2^31)");
+  return v;
+}
+
+// bounds(k_cache, page_table, end, bounds, start, scales, stream)
+PyObject* py_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor k = tensor(a[0], "k_cache"), table = tensor(a[1], "page_table"), end = tensor(a[2], "end"), bounds = tensor(a[3], "bounds");
+    const std::optional<Tensor> start = maybe(a[4], "start");
+    const Paged c = cache_of(k, k, maybe(a[5], "scales"));
+    const Bounds b = bounds_of(bounds, c);
+    check_table(table, -1, c.device, "page_table must be an int32 CUDA tensor [batch, pages of a sequence] with contiguous rows, on the cache's device");
+    const int64_t batch = table.size(0);
+    want(batch <= INT32_MAX && table.size(1) <= INT32_MAX, "too many sequences");
+    const int32_t* p_end = ints(end, {batch}, c.device, "end");
+    const int32_t* p_start = start ? ints(*start, {batch}, c.device, "start") : nullptr;
+    Place place(a[6], c.device);
+    check(f_bounds(&c.c, &b.b, static_cast<const int32_t*>(table.data_ptr()), step(table, 0), (int32_t)table.size(1), (int32_t)batch, p_start, p_end,
+                   place.stream),
+          "tks_cache_bounds");
+    Py_RETURN_NONE;
+  });
+}
+
+// scores(q, bounds, page_table, kv_len, block, first, last, n, out, stream) -> (scores, row_len)
+PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 10)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor q = tensor(a[0], "q"), table = tensor(a[2], "page_table");
+    const std::optional<Tensor> lens = maybe(a[3], "kv_len");
+    const Bounds b = bounds_of(tensor(a[1], "bounds"), 0, number(a[4], "block"));
+    want(q.dim() == 4 && q.scalar_type() == at::kBFloat16 && q.device() == b.device && q.size(3) == b.b.head_dim,
+         "q must be a bfloat16 CUDA tensor [batch, tokens, q_heads, head_dim] on the bounds' device");
+    const int64_t batch = q.size(0), tokens = q.size(1), heads = q.size(2);
+    want(heads >= 1 && heads % b.b.kv_heads == 0, "q_heads must be a multiple of kv_heads");
+    check_table(table, batch, b.device, "page_table must be an int32 CUDA tensor [batch, pages of a sequence] with contiguous rows");
+    want(batch <= INT32_MAX && tokens <= INT32_MAX && heads <= INT32_MAX && table.size(1) <= INT32_MAX, "too many queries");
+    const int32_t* p_lens = lens ? ints(*lens, {batch, tokens}, b.device, "kv_len") : nullptr;
+    const int64_t most = table.size(1) * (b.b.page_size / b.b.block), columns = a[7] == Py_None ? most : number(a[7], "n");
+    want(columns <= most && columns <= INT32_MAX, "n must not exceed the blocks of a page table's row");
+    const int64_t first = number(a[5], "first"), last = number(a[6], "last");
+    Place place(a[9], b.device);
+    const int64_t shape[4] = {batch, tokens, b.b.kv_heads, columns};
+    Tensor out;
+    if (a[8] == Py_None) {
+      out = at::empty(shape, at::TensorOptions().dtype(at::kFloat).device(b.device));
+    } else {
+      out = tensor(a[8], "out");
+      want(out.sizes() == at::IntArrayRef(shape) && out.scalar_type() == at::kFloat && out.device() == b.device && out.is_contiguous(),
+           "out must be a contiguous float32 CUDA tensor [batch, tokens, kv_heads, n]");
+    }
+    Tensor row_len = at::empty({batch, tokens, b.b.kv_heads}, at::TensorOptions().dtype(at::kInt).device(b.device));
+    const Tensor x = readable(q);
+    const tks_queries r = queries_of(x, table);
+    check(f_scores(&b.b, &r, p_lens, (int32_t)first, (int32_t)last, static_cast<float*>(out.data_ptr()), (int32_t)columns,
+                   static_cast<int32_t*>(row_len.data_ptr()), place.stream),
+          "tks_block_scores");
+    return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(row_len));
+  });
+}
+
+// block(q, k_cache, v_cache, page_table, blocks, block, kv_len, scales, softmax_scale, out, return_lse, stream)
+PyObject* py_block(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 12)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor q = tensor(a[0], "q"), table = tensor(a[3], "page_table"), blocks = tensor(a[4], "blocks");
+    const int64_t block = number(a[5], "block");
+    const std::optional<Tensor> lens = maybe(a[6], "kv_len");
+    const Paged c = cache_of(tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), maybe(a[7], "scales"));
+    check_q(q, c);
+    const int64_t batch = q.size(0), tokens = q.size(1);
+    want(blocks.dim() == 4, "blocks must be an int32 CUDA tensor [batch, tokens, kv_heads, n]");
+    const int64_t count = blocks.size(3);
+    const int32_t* p_blocks = ints(blocks, {batch, tokens, c.c.kv_heads, count}, c.device, "blocks");
+    const int32_t* p_lens = lens ? ints(*lens, {batch, tokens}, c.device, "kv_len") : nullptr;
+    want(block >= 1 && (block & (block - 1)) == 0, "block must be a power of two");
+    want(count <= TKS_K_MAX && count * block <= TKS_K_MAX, "too many positions in a list (TKS_K_MAX)");
+    return attend(c, q, table, a[8], a[9], a[10] == Py_True, a[11], "tks_block_attention", [&](const tks_cache* pc, const tks_queries* pq, void* s) {
+      return f_block(pc, pq, p_blocks, (int32_t)count, (int32_t)block, p_lens, s);
+    });
+  });
+}
+
+// What fork and compact share.
+struct Plan {
+  Tensor table, lens;
+  std::optional<Tensor> keep;
+  int64_t rows, width, pages, page;
+  const uint8_t* p_keep;
+  at::Device device;
+};
+Plan plan_of(PyObject* table, PyObject* lens, PyObject* pages, PyObject* page_size, PyObject* keep) {
+  Plan r{tensor(table, "page_table"), tensor(lens, "lens"), maybe(keep, "keep"), 0, 0, number(pages, "pages"), number(page_size, "page_size"), nullptr,
+         at::Device(at::kCPU)};
+  r.device = r.table.device();
+  check_table(r.table, -1, r.device, "page_table must be an int32 CUDA tensor [sequences, pages of a sequence] with contiguous rows");
+  r.rows = r.table.size(0);
+  r.width = r.table.size(1);
+  want(r.rows <= INT32_MAX && r.width <= INT32_MAX, "too many sequences");
+  ints(r.lens, {r.rows}, r.device, "lens");
+  want(r.pages >= 1 && r.page >= 1 && (r.page & (r.page - 1)) == 0 && r.pages * r.page <= INT32_MAX,
+       "a cache has at least one page, of a power of two of tokens, and fewer than 2^31 in all");
+  if (r.keep) {
+    want((r.keep->scalar_type() == at::kByte || r.keep->scalar_type() == at::kBool) && r.keep->dim() == 1 && r.keep->size(0) == r.pages &&
+             r.keep->device() == r.device && r.keep->is_contiguous(),
+         "keep must be a contiguous bool or uint8 CUDA tensor [pages] on the page table's device");
+    r.p_keep = static_cast<const uint8_t*>(r.keep->data_ptr());
+  }
+  return r;
+}
+Tensor new_ints(at::IntArrayRef shape, const at::Device& device) { return at::empty(shape, at::TensorOptions().dtype(at::kInt).device(device)); }
+Tensor table_out(PyObject* given, int64_t rows, int64_t width, const at::Device& device) {
+  const int64_t shape[2] = {rows, width};
+  if (given == Py_None) return new_ints(shape, device);
+  Tensor t = tensor(given, "out");
+  ints(t, shape, device, "out");
+  return t;
+}
+int32_t* words(const Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); }
+
+// fork(page_table, lens, parents, new_lens, pages, page_size, keep, out, stream) -> (table, src, dst)
+PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 9)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Plan p = plan_of(a[0], a[1], a[4], a[5], a[6]);
+    const Tensor parents = tensor(a[2], "parents"), new_lens = tensor(a[3], "new_lens");
+    const int64_t children = parents.numel();
+    want(children <= INT32_MAX, "too many children");
+    const int32_t* p_parents = ints(parents, {children}, p.device, "parents");
+    const int32_t* p_lens = ints(new_lens, {children}, p.device, "new_lens");
+    Place place(a[8], p.device);
+    Tensor out = table_out(a[7], children, p.width, p.device), src = new_ints({children}, p.device), dst = new_ints({children}, p.device);
+    const Tensor scratch = new_ints({TKS_PAGES_SCRATCH(p.pages, children)}, p.device);
+    check(f_fork(words(p.table), step(p.table, 0), (int32_t)p.width, (int32_t)p.rows, words(p.lens), p_parents, p_lens, (int32_t)children, p.p_keep,
+                 (int32_t)p.pages, (int32_t)p.page, words(out), words(src), words(dst), words(scratch), place.stream),
+          "tks_cache_fork");
+    return Py_BuildValue("NNN", THPVariable_Wrap(out), THPVariable_Wrap(src), THPVariable_Wrap(dst));
+  });
+}
+
+// compact(page_table, lens, pages, page_size, keep, out, stream) -> (table, src, dst, count)
+PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 7)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Plan p = plan_of(a[0], a[1], a[2], a[3], a[4]);
+    Place place(a[6], p.device);
+    Tensor out = table_out(a[5], p.rows, p.width, p.device), src = new_ints({p.pages / 2}, p.device), dst = new_ints({p.pages / 2}, p.device);
+    Tensor count = new_ints({2}, p.device);
+    const Tensor scratch = new_ints({TKS_PAGES_SCRATCH(p.pages, p.rows)}, p.device);
+    check(f_compact(words(p.table), step(p.table, 0), (int32_t)p.width, (int32_t)p.rows, words(p.lens), p.p_keep, (int32_t)p.pages, (int32_t)p.page,
+                    words(out), words(src), words(dst), words(count), words(scratch), place.stream),
+          "tks_cache_compact");
+    return Py_BuildValue("NNNN", THPVariable_Wrap(out), THPVariable_Wrap(src), THPVariable_Wrap(dst), THPVariable_Wrap(count));
+  });
+}
+
+// copy(src, dst, k_cache, v_cache, scales, bounds, count, stream)
+PyObject* py_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!arity_blocks(n, 8)) return nullptr;
+  return guarded([&]() -> PyObject* {
+    const Tensor src = tensor(a[0], "src"), dst = tensor(a[1], "dst");
+    const Paged c = cache_of(tensor(a[2], "k_cache"), tensor(a[3], "v_cache"), maybe(a[4], "scales"));
+    const std::optional<Tensor> bounds = maybe(a[5], "bounds"), count = maybe(a[6], "count");
+    std::optional<Bounds> b;
+    if (bounds) b = bounds_of(*bounds, c);
+    const int64_t pairs = src.numel();
+    want(pairs <= INT32_MAX, "too many pages");
+    const int32_t* p_src = ints(src, {pairs}, c.device, "src");
+    const int32_t* p_dst = ints(dst, {pairs}, c.device, "dst");
+    if (count)
+      want(count->scalar_type() == at::kInt && count->numel() >= 1 && count->is_contiguous() && count->device() == c.device,
+           "count must be a contiguous int32 CUDA tensor on the cache's device, whose first element counts");
+    Place place(a[7], c.device);
+    check(f_copy(&c.c, b ? &b->b : nullptr, p_src, p_dst, (int32_t)pairs, count ? words(*count) : nullptr, place.stream), "tks_cache_copy");
+    Py_RETURN_NONE;
+  });
+}
+
+// set_blocks(TksError, bounds, scores, block attention, fork, compact, copy): the entry points' addresses
+PyObject* py_set_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) {
+    PyErr_SetString(PyExc_TypeError, "set_blocks takes TksError and six addresses");
+    return nullptr;
+  }
+  void* f[6];
+  for (int i = 0; i < 6; ++i) {
+    f[i] = PyLong_AsVoidPtr(a[1 + i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  Py_INCREF(a[0]);
+  Py_XDECREF(tks_error);
+  tks_error = a[0];
+  f_bounds = reinterpret_cast<decltype(f_bounds)>(f[0]);
+  f_scores = reinterpret_cast<decltype(f_scores)>(f[1]);
+  f_block = reinterpret_cast<decltype(f_block)>(f[2]);
+  f_fork = reinterpret_cast<decltype(f_fork)>(f[3]);
+  f_compact = reinterpret_cast<decltype(f_compact)>(f[4]);
+  f_copy = reinterpret_cast<decltype(f_copy)>(f[5]);
+  Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {
     {"set_library", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_set)), METH_FASTCALL, nullptr},
     {"write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_write)), METH_FASTCALL, nullptr},
     {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_read)), METH_FASTCALL, nullptr},
     {"tree", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_tree)), METH_FASTCALL, nullptr},
     {"selected", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_selected)), METH_FASTCALL, nullptr},
+    {"set_blocks", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_set_blocks)), METH_FASTCALL, nullptr},
+    {"bounds", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_bounds)), METH_FASTCALL, nullptr},
+    {"scores", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_scores)), METH_FASTCALL, nullptr},
+    {"block", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_block)), METH_FASTCALL, nullptr},
+    {"fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_fork)), METH_FASTCALL, nullptr},
+    {"compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_compact)), METH_FASTCALL, nullptr},
+    {"copy", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(py_copy)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "tks_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,547 @@
+// Page tables of a step's new sequences, moving pages in use together, and
+// copying pages.
+//
+// The two calls that make tables are a few passes over the tables and over one
+// word for each page, with nothing between them but that all of one is done
+// before the next begins: one thread-block cluster makes them, in one launch,
+// its barrier between the passes. What the passes leave for each other lies in the
+// caller's scratch buffer, so that nothing is shared between calls.
+
+#include <algorithm>
+
+#include "tks_attn.cuh"
+#include "tks_attn_host.h"
+
+namespace tks {
+namespace attn {
+namespace {
+
+constexpr int kBlocks = 8, kThreads = 1024, kWarps = kThreads / 32, kAllWarps = kBlocks * kWarps;
+constexpr int kFree = 0x7fffffff, kShared = -1;  // a page that nobody holds; one that is held and not to be written to
+
+struct PlanParams {
+  const int32_t* table;
+  long long table_stride;
+  int table_pages, sequences;
+  const int32_t *lens, *parents, *new_lens;
+  int children;
+  const uint8_t* keep;
+  int pages, page_shift;
+  int32_t *out, *src, *dst, *count;
+  int32_t *owner, *list, *base;  // scratch: a word a page, the free pages in order, a word a child
+  int32_t* sums;                 // and what the warps have counted
+  unsigned* status;
+};
+
+// The cluster's threads; its barrier also orders their accesses to global memory.
+struct Team {
+  int rank, warp, lane, thread;  // of the cluster, warps and threads of all its blocks
+  __device__ __forceinline__ Team() {
+    rank = blockIdx.x;
+    warp = rank * kWarps + (threadIdx.x >> 5);
+    lane = threadIdx.x & 31;
+    thread = rank * kThreads + threadIdx.x;
+  }
+  __device__ __forceinline__ void meet() const {
+    __syncwarp();
+    cluster_sync();
+  }
+};
+
+// Of two numbers that each warp of the cluster has counted, the sums over the warps before this one, and over all.
+// `sums`: global memory, 2 * kAllWarps words.
+struct Before {
+  int a, b, all_a, all_b;
+};
+__device__ __forceinline__ Before sums_before(const Team& me, int32_t* sums, int a, int b) {
+  if (me.lane == 0) {
+    sums[me.warp] = a;
+    sums[kAllWarps + me.warp] = b;
+  }
+  me.meet();
+  Before r = {0, 0, 0, 0};
+  for (int i = me.lane; i < kAllWarps; i += 32) {
+    const int x = __ldcg(sums + i), y = __ldcg(sums + kAllWarps + i);
+    r.all_a += x;
+    r.all_b += y;
+    if (i < me.warp) {
+      r.a += x;
+      r.b += y;
+    }
+  }
+  r.a = __reduce_add_sync(0xffffffffu, r.a);
+  r.b = __reduce_add_sync(0xffffffffu, r.b);
+  r.all_a = __reduce_add_sync(0xffffffffu, r.all_a);
+  r.all_b = __reduce_add_sync(0xffffffffu, r.all_b);
+  return r;
+}
+// A warp's run of n things, in order: [begin, end), begin a multiple of 32.
+__device__ __forceinline__ void share(const Team& me, int n, int& begin, int& end) {
+  const long long each = (((long long)n + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;
+  begin = (int)min((long long)n, each * me.warp);
+  end = (int)min((long long)n, each * (me.warp + 1));
+}
+
+__device__ __forceinline__ int pages_of(const PlanParams& p, int len) { return (int)(((long long)len + (1 << p.page_shift) - 1) >> p.page_shift); }
+__device__ __forceinline__ int held_len(const PlanParams& p, int len, bool& bad) {
+  const long long room = (long long)p.table_pages << p.page_shift;
+  const int r = len < 0 ? 0 : len > room ? (int)room : len;
+  bad |= r != len;
+  return r;
+}
+
+// A child: its parent's row, how many of its entries it keeps, how many it needs, and whether it writes to the last.
+struct Child {
+  const int32_t* row;
+  int have, need;
+  bool writes;
+};
+__device__ __forceinline__ Child child_of(const PlanParams& p, int i, unsigned* bad) {
+  Child c;
+  const int parent = __ldg(p.parents + i);
+  bool len_bad = false;
+  const int wanted = held_len(p, __ldg(p.new_lens + i), len_bad);
+  int had = 0;
+  c.row = p.table;
+  if (parent >= 0 && parent < p.sequences) {
+    had = held_len(p, __ldg(p.lens + parent), len_bad);
+    c.row = p.table + parent * p.table_stride;
+  } else if (parent >= 0 && bad) {
+    *bad |= kStatIndexBit;
+  }
+  if (len_bad && bad) *bad |= kStatRowLenBit;
+  const int kept = min(had, wanted);
+  c.have = pages_of(p, kept);
+  c.need = pages_of(p, wanted);
+  c.writes = (kept & ((1 << p.page_shift) - 1)) != 0 && wanted > kept;
+  return c;
+}
+
+// What a warp does at once: kSpan entries of one row, 32 at a time.
+constexpr int kSpan = 256;
+
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant__ PlanParams p) {
+  const Team me;
+  unsigned bad = 0;
+  grid_wait();
+  grid_launch_dependents();
+  // who holds a page
+  for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = p.keep && p.keep[i] ? kShared : kFree;
+  me.meet();
+  const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
+  const long long units = (long long)p.children * spans;
+  for (long long u = me.warp; u < units; u += kAllWarps) {
+    const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
+    const Child c = child_of(p, i, j0 == 0 ? &bad : nullptr);
+    int e[kSpan / 32];
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      e[k] = j < c.have ? __ldg(c.row + j) : -1;
+      if (j < c.have && (unsigned)e[k] >= (unsigned)p.pages) bad |= kStatIndexBit;
+    }
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      if ((unsigned)e[k] >= (unsigned)p.pages) continue;
+      // (a held page's word only ever falls: to kShared, or to the lowest of those who write to it)
+      if (c.writes && j0 + 32 * k + me.lane == c.have - 1) atomicMin(p.owner + e[k], i);
+      else p.owner[e[k]] = kShared;
+    }
+  }
+  me.meet();
+  // how many pages each child wants, and how many are free
+  auto wants = [&](int i, bool& copied) -> int {
+    const Child c = child_of(p, i, nullptr);
+    copied = false;
+    if (c.writes) {
+      const int tail = __ldg(c.row + c.have - 1);
+      copied = (unsigned)tail < (unsigned)p.pages && __ldcg(p.owner + tail) != i;
+    }
+    return c.need - c.have + (copied ? 1 : 0);
+  };
+  int page0, page1, child0, child1;
+  share(me, p.pages, page0, page1);
+  share(me, p.children, child0, child1);
+  int free = 0, wanted = 0;
+  for (int i = page0 + me.lane; i < page1; i += 32) free += __ldcg(p.owner + i) == kFree;
+  bool copied;
+  for (int i = child0 + me.lane; i < child1; i += 32) wanted += wants(i, copied);
+  const Before before = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, free), __reduce_add_sync(0xffffffffu, wanted));
+  // the free pages that are wanted, in order; where each child's begin
+  int at = before.a;
+  const int most = min(before.all_a, before.all_b);
+  for (int i = page0; i < page1 && at < most; i += 32) {
+    const bool is = i + me.lane < page1 && __ldcg(p.owner + i + me.lane) == kFree;
+    const unsigned m = __ballot_sync(0xffffffffu, is);
+    const int rank = at + __popc(m & ((1u << me.lane) - 1u));
+    if (is && rank < most) p.list[rank] = i + me.lane;
+    at += __popc(m);
+  }
+  at = before.b;
+  for (int i = child0; i < child1; i += 32) {
+    const int n = i + me.lane < child1 ? wants(i + me.lane, copied) : 0;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (me.lane >= o) end += y;
+    }
+    if (i + me.lane < child1) p.base[i + me.lane] = at + end - n;
+    at += __shfl_sync(0xffffffffu, end, 31);
+  }
+  me.meet();
+  if (before.all_b > before.all_a) bad |= kStatNoPageBit;
+  for (long long u = me.warp; u < units; u += kAllWarps) {
+    const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
+    const Child c = child_of(p, i, nullptr);
+    const int base = __ldcg(p.base + i);
+    bool copy;
+    const int n = wants(i, copy);
+    const int extra = n - (c.need - c.have);
+    int32_t* to = p.out + (long long)i * p.table_pages;
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      if (j >= p.table_pages) continue;
+      int e = -1;
+      if (j < c.have) e = __ldg(c.row + j);
+      if ((copy && j == c.have - 1) || (j >= c.have && j < c.need)) {
+        const int rank = base + (j < c.have ? 0 : extra + j - c.have);
+        const int got = rank < most ? __ldcg(p.list + rank) : -1;
+        if (j < c.have) {
+          p.src[i] = got < 0 ? -1 : e;
+          p.dst[i] = got;
+        }
+        e = got;
+      }
+      to[j] = e;
+    }
+    if (!copy && j0 == 0 && me.lane == 0) p.src[i] = p.dst[i] = -1;
+  }
+  if (bad) report(p.status, bad);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_constant__ PlanParams p) {
+  const Team me;
+  unsigned bad = 0;
+  grid_wait();
+  grid_launch_dependents();
+  auto pinned = [&](int i) { return p.keep && p.keep[i] != 0; };
+  for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = pinned(i) ? kShared : kFree;
+  for (int i = me.thread; i < p.pages / 2; i += kBlocks * kThreads) p.src[i] = p.dst[i] = -1;
+  me.meet();
+  const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
+  const long long units = (long long)p.sequences * spans;
+  auto pages_held = [&](int s, bool tell) {
+    bool len_bad = false;
+    const int n = pages_of(p, held_len(p, __ldg(p.lens + s), len_bad));
+    if (len_bad && tell) bad |= kStatRowLenBit;
+    return n;
+  };
+  for (long long u = me.warp; u < units; u += kAllWarps) {
+    const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
+    const int have = pages_held(s, j0 == 0);
+    const int32_t* row = p.table + s * p.table_stride;
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      if (j >= have) continue;
+      const int e = __ldg(row + j);
+      if ((unsigned)e >= (unsigned)p.pages) bad |= kStatIndexBit;
+      else p.owner[e] = kShared;
+    }
+  }
+  me.meet();
+  int page0, page1;
+  share(me, p.pages, page0, page1);
+  int held = 0;
+  for (int i = page0 + me.lane; i < page1; i += 32) held += __ldcg(p.owner + i) != kFree;
+  const int used = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, held), 0).all_a;
+  // pages that move, and places for them
+  auto moves = [&](int i) { return i >= used && i < page1 && __ldcg(p.owner + i) != kFree && !pinned(i); };
+  auto place = [&](int i) { return i < used && i < page1 && __ldcg(p.owner + i) == kFree; };
+  int from = 0, to = 0;
+  for (int i = page0 + me.lane; i < page1; i += 32) {
+    from += moves(i);
+    to += place(i);
+  }
+  const Before before = sums_before(me, p.sums + 2 * kAllWarps, __reduce_add_sync(0xffffffffu, from), __reduce_add_sync(0xffffffffu, to));
+  const int count = before.all_a;
+  int a = before.a, b = before.b;
+  for (int i0 = page0; i0 < page1; i0 += 32) {
+    const int i = i0 + me.lane;
+    const bool is_from = moves(i), is_to = place(i);
+    const unsigned mf = __ballot_sync(0xffffffffu, is_from), mt = __ballot_sync(0xffffffffu, is_to), low = (1u << me.lane) - 1u;
+    if (is_from) {
+      const int rank = a + __popc(mf & low);
+      p.src[rank] = i;
+      p.list[i] = rank;
+    } else if (i < page1) {
+      p.list[i] = -1;
+    }
+    if (is_to) {
+      const int rank = b + __popc(mt & low);
+      if (rank < count) p.dst[rank] = i;
+    }
+    a += __popc(mf);
+    b += __popc(mt);
+  }
+  me.meet();
+  if (me.thread == 0) {
+    p.count[0] = count;
+    p.count[1] = used;
+  }
+  for (long long u = me.warp; u < units; u += kAllWarps) {
+    const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
+    const int have = pages_held(s, false);
+    const int32_t* row = p.table + s * p.table_stride;
+    int32_t* out = p.out + (long long)s * p.table_pages;
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      if (j >= p.table_pages) continue;
+      int e = -1;
+      if (j < have) {
+        e = row[j];  // (out may be the table itself)
+        const int rank = (unsigned)e < (unsigned)p.pages ? __ldcg(p.list + e) : -1;
+        if (rank >= 0) e = __ldcg(p.dst + rank);
+      }
+      out[j] = e;
+    }
+  }
+  if (bad) report(p.status, bad);
+}
+
+template <typename K>
+cudaError_t launch_plan(K kernel, const PlanParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kBlocks);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute a[2] = {};
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, kBlocks);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// ---------------------------------------------------------------------------
+// Copies.
+// ---------------------------------------------------------------------------
+struct CopyParams {
+  unsigned char* base[4];  // keys, values, scales, bounds
+  int planes;              // (2 for keys and values without scales and bounds)
+  long long page_b, token_b, head_b;
+  int pages, tokens, heads, run;       // run: contiguous 16-byte pieces; of which a page has tokens * heads
+  long long page_words[2];             // scales and bounds: words of 8 bytes of a page
+  int chunks[4];                       // of a page, and of the plane
+  int all_chunks;
+  const int32_t *src, *dst, *count;
+  int n;
+  unsigned* status;
+};
+
+constexpr int kCopyThreads = 256, kPer = 4, kChunk = kCopyThreads * kPer;  // pieces (words) of a chunk
+
+// A thread block takes one chunk of one plane of one pair after the other.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+  grid_wait();
+  grid_launch_dependents();
+  const int n = p.count ? min(p.n, max(0, __ldg(p.count))) : p.n;
+  const long long items = (long long)n * p.all_chunks;
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    const int i = (int)(w / p.all_chunks);
+    int chunk = (int)(w - (long long)i * p.all_chunks);
+    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    if (src < 0 || dst < 0) continue;
+    if (src >= p.pages || dst >= p.pages) {
+      if (threadIdx.x == 0) report(p.status, kStatIndexBit);
+      continue;
+    }
+    int plane = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (plane == k && chunk >= p.chunks[k]) {
+        chunk -= p.chunks[k];
+        ++plane;
+      }
+    if (plane < 2) {
+      unsigned char* base = plane ? p.base[1] : p.base[0];
+      const int pieces = p.tokens * p.heads * p.run;
+      uint4 x[kPer];
+      long long at[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int v = chunk * kChunk + k * kCopyThreads + threadIdx.x;
+        at[k] = -1;
+        if (v < pieces) {
+          const int row = v / p.run, token = row / p.heads;
+          at[k] = token * p.token_b + (row - token * p.heads) * p.head_b + (v - row * p.run) * 16LL;
+          x[k] = __ldg(reinterpret_cast<const uint4*>(base + src * p.page_b + at[k]));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (at[k] >= 0) *reinterpret_cast<uint4*>(base + dst * p.page_b + at[k]) = x[k];
+    } else {
+      uint2* base = reinterpret_cast<uint2*>(plane == 2 ? p.base[2] : p.base[3]);
+      const long long words = plane == 2 ? p.page_words[0] : p.page_words[1];
+      uint2 x[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const long long v = (long long)chunk * kChunk + k * kCopyThreads + threadIdx.x;
+        if (v < words) x[k] = __ldg(base + src * words + v);
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const long long v = (long long)chunk * kChunk + k * kCopyThreads + threadIdx.x;
+        if (v < words) base[dst * words + v] = x[k];
+      }
+    }
+  }
+}
+
+bool overlap(const int32_t* a, long long na, const int32_t* b, long long nb) { return a < b + nb && b < a + na; }
+
+int check_plan(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens, int32_t pages,
+               int32_t page_size) {
+  if (pages < 1 || page_size < 1 || (page_size & (page_size - 1)) || (int64_t)pages * page_size > INT32_MAX) return TKS_E_INVAL;
+  if (sequences < 0 || table_pages < 0 || table_stride < 0 || table_stride > ((int64_t)1 << 56) / (sequences > 0 ? sequences : 1)) return TKS_E_INVAL;
+  if (!aligned(page_table, 4) || !aligned(lens, 4)) return TKS_E_INVAL;
+  if (sequences > 0 && (!lens || (table_pages > 0 && !page_table))) return TKS_E_INVAL;
+  return TKS_OK;
+}
+
+PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens,
+                       const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch) {
+  PlanParams p{};
+  p.table = page_table;
+  p.table_stride = table_stride;
+  p.table_pages = table_pages;
+  p.sequences = sequences;
+  p.lens = lens;
+  p.keep = keep;
+  p.pages = pages;
+  p.page_shift = log2_of(page_size);
+  p.out = table;
+  p.src = src;
+  p.dst = dst;
+  p.sums = scratch;
+  p.owner = scratch + 1024;
+  p.list = p.owner + pages;
+  p.base = p.list + pages;
+  return p;
+}
+static_assert(4 * kAllWarps <= 1024, "the warps' sums fit their place in the scratch buffer");
+
+}  // namespace
+}  // namespace attn
+}  // namespace tks
+
+using namespace tks;
+using namespace tks::attn;
+
+extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens,
+                              const int32_t* parents, const int32_t* new_lens, int32_t children, const uint8_t* keep, int32_t pages,
+                              int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch, void* stream) {
+  if (check_plan(page_table, table_stride, table_pages, sequences, lens, pages, page_size) != TKS_OK || children < 0) return TKS_E_INVAL;
+  if ((int64_t)children * table_pages + children > INT32_MAX) return TKS_E_TOO_LARGE;
+  if (children == 0) return TKS_OK;
+  if (!parents || !new_lens || !src || !dst || !scratch || (table_pages > 0 && !table)) return TKS_E_INVAL;
+  if (!aligned(parents, 4) || !aligned(new_lens, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(scratch, 4) || !aligned(table, 4))
+    return TKS_E_INVAL;
+  const long long held = sequences > 0 ? (sequences - 1) * table_stride + table_pages : 0;
+  if (table_pages > 0 && overlap(page_table, held, table, (long long)children * table_pages)) return TKS_E_INVAL;
+  Place place;
+  const int rc = place_of(stream, &place);
+  if (rc != TKS_OK) return rc;
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch);
+  p.parents = parents;
+  p.new_lens = new_lens;
+  p.children = children;
+  p.status = place.status;
+  std::lock_guard<std::mutex> lock(*place.order);
+  if (launch_plan(fork_kernel, p, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}
+
+extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens,
+                                 const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst,
+                                 int32_t* count, int32_t* scratch, void* stream) {
+  if (check_plan(page_table, table_stride, table_pages, sequences, lens, pages, page_size) != TKS_OK) return TKS_E_INVAL;
+  if ((int64_t)sequences * table_pages > INT32_MAX) return TKS_E_TOO_LARGE;
+  if (!count || !scratch || (pages > 1 && (!src || !dst)) || (sequences > 0 && table_pages > 0 && !table)) return TKS_E_INVAL;
+  if (!aligned(count, 4) || !aligned(scratch, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(table, 4)) return TKS_E_INVAL;
+  const long long held = sequences > 0 ? (sequences - 1) * table_stride + table_pages : 0;
+  const bool in_place = table == page_table && (sequences <= 1 || table_stride == table_pages);
+  if (held > 0 && table_pages > 0 && !in_place && overlap(page_table, held, table, (long long)sequences * table_pages)) return TKS_E_INVAL;
+  Place place;
+  const int rc = place_of(stream, &place);
+  if (rc != TKS_OK) return rc;
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch);
+  p.count = count;
+  p.status = place.status;
+  std::lock_guard<std::mutex> lock(*place.order);
+  if (launch_plan(compact_kernel, p, (cudaStream_t)stream) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}
+
+extern "C" int tks_cache_copy(const tks_cache* cache, const tks_bounds* bounds, const int32_t* src, const int32_t* dst, int32_t n,
+                              const int32_t* count, void* stream) {
+  if (check_cache(cache) != TKS_OK || n < 0) return TKS_E_INVAL;
+  if (bounds && (check_bounds(bounds) != TKS_OK || !bounds_of(bounds, cache))) return TKS_E_INVAL;
+  if (n == 0) return TKS_OK;
+  if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4)) return TKS_E_INVAL;
+  CopyParams p{};
+  const long long size = cache->held == TKS_I8 ? 1 : 2, row = cache->head_dim * size;
+  p.base[0] = static_cast<unsigned char*>(cache->k);
+  p.base[1] = static_cast<unsigned char*>(cache->v);
+  p.base[2] = reinterpret_cast<unsigned char*>(cache->scales);
+  p.base[3] = bounds ? static_cast<unsigned char*>(bounds->bounds) : nullptr;
+  p.page_b = cache->page_stride * size;
+  p.token_b = cache->token_stride * size;
+  p.head_b = cache->head_stride * size;
+  p.pages = cache->pages;
+  const __int128 pieces = (__int128)cache->page_size * cache->kv_heads * (row / 16);
+  if (pieces > INT32_MAX / 2) return TKS_E_TOO_LARGE;
+  p.tokens = cache->page_size;
+  p.heads = cache->kv_heads;
+  p.run = (int)(row / 16);
+  // rows that follow each other without a gap are one
+  if ((p.heads == 1 || p.head_b == row) && (p.tokens == 1 || p.token_b == row * p.heads)) {
+    p.run = (int)pieces;
+    p.tokens = p.heads = 1;
+  }
+  p.page_words[0] = cache->held == TKS_I8 ? (long long)cache->page_size * cache->kv_heads : 0;
+  p.page_words[1] = bounds ? (long long)(bounds->page_size / bounds->block) * bounds->kv_heads * bounds->head_dim / 2 : 0;
+  p.chunks[0] = p.chunks[1] = (int)((pieces + kChunk - 1) / kChunk);
+  for (int i = 0; i < 2; ++i) p.chunks[2 + i] = (int)((p.page_words[i] + kChunk - 1) / kChunk);
+  const long long all = 2LL * p.chunks[0] + p.chunks[2] + p.chunks[3];
+  p.all_chunks = (int)all;
+  p.src = src;
+  p.dst = dst;
+  p.count = count;
+  p.n = n;
+  Place place;
+  const int rc = place_of(stream, &place);
+  if (rc != TKS_OK) return rc;
+  p.status = place.status;
+  std::lock_guard<std::mutex> lock(*place.order);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(n * all, place.sms * 8LL));
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute a[1] = {};
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, 0);
+  if (cudaLaunchKernelEx(&cfg, copy_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TKS_E_CUDA;
+  }
+  return TKS_OK;
+}

@@ -475,6 +475,7 @@ extern "C" const char* tks_status_string(int status) {
     case TKS_E_ROW_LEN: return "a row length was outside [0, row_stride] and was clamped";
     case TKS_E_TOO_LARGE: return "more rows than the allocation-free entry point's fixed scratch holds";
     case TKS_E_INDEX: return "a slot, page or position lay outside the cache and was skipped";
+    case TKS_E_NO_PAGE: return "no free page was left for a sequence";
     default: return "unknown status";
   }
 }

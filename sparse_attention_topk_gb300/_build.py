@@ -18,10 +18,12 @@ SOURCES = [os.path.join(CSRC, "tks_select.cu"), os.path.join(CSRC, "tks_select51
            os.path.join(CSRC, "tks_order.cu"), os.path.join(CSRC, "tks_cache.cu"),
            os.path.join(CSRC, "tks_attn.cu"), os.path.join(CSRC, "tks_attn_rows.cu"),
            os.path.join(CSRC, "tks_attn_tiles.cu"), os.path.join(CSRC, "tks_attn_tiles_bf16.cu"),
-           os.path.join(CSRC, "tks_blocks.cu"), os.path.join(CSRC, "tks_pages.cu")]
+           os.path.join(CSRC, "tks_blocks.cu"), os.path.join(CSRC, "tks_scores_tiles.cu"),
+           os.path.join(CSRC, "tks_pages.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, "tks_device.cuh"), os.path.join(CSRC, "tks_kernel.cuh"),
                      os.path.join(CSRC, "tks_internal.h"), os.path.join(CSRC, "tks_attn.cuh"),
                      os.path.join(CSRC, "tks_attn_internal.h"), os.path.join(CSRC, "tks_attn_host.h"),
+                     os.path.join(CSRC, "tks_tensor.cuh"), os.path.join(CSRC, "tks_scores.cuh"),
                      os.path.join(INCLUDE, "tks.h"), os.path.join(INCLUDE, "tks_attention.h"),
                      os.path.join(INCLUDE, "tks_blocks.h")]
 

@@ -11,6 +11,7 @@
 
 #include "tks_attn.cuh"
 #include "tks_attn_host.h"
+#include "tks_scores.cuh"
 
 namespace tks {
 namespace attn {
@@ -33,16 +34,6 @@ struct BoundsParams {
   unsigned* status;
 };
 
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float finite_bf16(float x) { return x > kBf16Max ? kBf16Max : x < -kBf16Max ? -kBf16Max : x; }
 
 // The least and largest of a lane's 16-byte piece of the rows it has seen.
@@ -203,91 +194,43 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 // Scores.
 // ---------------------------------------------------------------------------
-struct ScoreParams {
-  const __nv_bfloat16* bounds;
-  int pages, block_shift, of_page_shift, kv_heads;  // of_page_shift: log2 of the blocks of a page
-  const __nv_bfloat16* q;
-  long long q_batch, q_token, q_head;
-  int batch, tokens, group;
-  const int32_t* table;
-  long long table_stride;
-  const int32_t* kv_len;
-  int first, last;
-  float* out;
-  int n;
-  int32_t* row_len;
-  unsigned* status;
-  int tile_tokens, token_tiles, chunks;
-};
-
-// The blocks that a token sees, of n.
-__device__ __forceinline__ int blocks_seen(const ScoreParams& p, int b, int t, bool& bad) {
-  if (!p.kv_len) return p.n;
-  const int given = __ldg(p.kv_len + (long long)b * p.tokens + t);
-  const long long most = (long long)p.n << p.block_shift;
-  const int len = given < 0 ? 0 : given > most ? (int)most : given;
-  bad |= len != given;
-  return (int)(((long long)len + (1 << p.block_shift) - 1) >> p.block_shift);
-}
-__device__ __forceinline__ float final_score(const ScoreParams& p, float x, int j, int seen) {
-  if (j >= seen) return -INFINITY;
-  return !(x == x) || j < p.first || j >= seen - p.last ? INFINITY : x;
-}
-
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
-// Two bfloat16's positive parts, or their negative ones. (A NaN stays one in either.)
-__device__ __forceinline__ uint32_t part_of_pair(uint32_t w, bool positive) {
-  const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&w), zero = __floats2bfloat162_rn(0.f, 0.f);
-  const __nv_bfloat162 y = positive ? __hmax2_nan(x, zero) : __hmin2_nan(x, zero);
-  return *reinterpret_cast<const uint32_t*>(&y);
-}
-
 constexpr int kScoreWarps = 4, kScoreThreads = kScoreWarps * 32;
 constexpr int kScoreCols = 32;  // blocks that a warp scores at once
-// Bytes of sixteen query rows: a fragment (16 bytes a lane) for each 16 of the 2 * dim summed elements.
-__host__ __device__ constexpr int score_rows_bytes(int dim) { return 2 * dim / 16 * 32 * 16; }
-constexpr int kScoreSmem = 200 * 1024;
 
-// A thread block takes one (sequence, head, tile of tokens) and a run of blocks. Its query rows, in sixteens, lie in shared
-// memory as matrix fragments: of product step s, elements kept apart as in the loads of bounds, lane 4n + c takes
-// 16-byte pieces c, c + 4, ... of column n's 4 * D bytes.
+// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and a run of
+// blocks; its query rows lie in shared memory as matrix fragments: of product step s, lane 4n + c takes the elements that
+// it has of column n's 4 * D bytes: 16-byte pieces c, c + 4, ...
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoreParams p) {
   constexpr int kPieces = 2 * D * 2 / 16 / 4;  // of a lane
   constexpr int kSteps = 2 * kPieces;
-  static_assert(kSteps * 32 * sizeof(uint4) == score_rows_bytes(D), "the launch's shared memory");
-  extern __shared__ __align__(16) unsigned char smem[];
-  uint4* qs = reinterpret_cast<uint4*>(smem);  // [pass][step][lane]
+  __shared__ uint4 qs[kSteps * 32];
   __shared__ float tile_s[kScoreWarps][16][kScoreCols + 1];
-  __shared__ float top_s[kScoreWarps][16][kScoreCols];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-  unsigned unit = blockIdx.x / p.chunks;
+  const unsigned unit = blockIdx.x / p.chunks;
   const int chunk = blockIdx.x - unit * p.chunks;
-  const int tile = unit % p.token_tiles;
-  unit /= p.token_tiles;
-  const int head = unit % p.kv_heads, b = unit / p.kv_heads;
-  const int t0 = tile * p.tile_tokens, tokens = min(p.tile_tokens, p.tokens - t0), rows = tokens * p.group, passes = (rows + 15) / 16;
+  const int head = unit % p.kv_heads, b = unit / p.kv_heads, rows = p.tokens * p.group;
   grid_wait();
   grid_launch_dependents();
 
-  for (int x = threadIdx.x; x < passes * kSteps * 32; x += kScoreThreads) {
-    const int l = x & 31, s = (x >> 5) % kSteps, r = (x >> 5) / kSteps * 16 + (l >> 2);
+  for (int x = threadIdx.x; x < kSteps * 32; x += kScoreThreads) {
+    const int l = x & 31, s = x >> 5, r = l >> 2;
     // elements of the doubled index: the first D are the least's, with the queries' negative parts
     const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    auto row = [&](int i) { return p.q + b * p.q_batch + (t0 + i / p.group) * p.q_token + ((long long)head * p.group + i % p.group) * p.q_head + d % D; };
     if (r < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(row(r)));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
       w.x = part_of_pair(y.x, d >= D);
       w.z = part_of_pair(y.y, d >= D);
     }
     if (r + 8 < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(row(r + 8)));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
       w.y = part_of_pair(y.x, d >= D);
       w.w = part_of_pair(y.y, d >= D);
     }
@@ -295,11 +238,11 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   }
   // the tokens' lengths, a lane each (16 at most)
   bool bad = false;
-  const int mine = lane < tokens ? blocks_seen(p, b, t0 + lane, bad) : 0;
+  const int mine = lane < p.tokens ? blocks_seen(p, b, lane, bad) : 0;
   const int most = __reduce_max_sync(0xffffffffu, mine);
   if (warp == 0 && chunk == 0) {
     if (bad) report(p.status, kStatRowLenBit);
-    if (p.row_len && lane < tokens) p.row_len[((long long)b * p.tokens + t0 + lane) * p.kv_heads + head] = mine;
+    if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = mine;
   }
   __syncthreads();
 
@@ -312,39 +255,33 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
       ok = (unsigned)page < (unsigned)p.pages;
       if (!ok) report(p.status, kStatIndexBit);
       const long long at = ok && col < most ? (((long long)page << p.of_page_shift) + (col & ((1 << p.of_page_shift) - 1))) * p.kv_heads + head : -1;
-      for (int pass = 0; pass < passes; ++pass) {
-        float acc[4][4];
+      float acc[4][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const long long of = __shfl_sync(0xffffffffu, at, 8 * t + n);
-          const uint4* from = reinterpret_cast<const uint4*>(p.bounds + of * (2 * D)) + c;
-          uint4 w[kPieces];
+      for (int t = 0; t < 4; ++t) {
+        const long long of = __shfl_sync(0xffffffffu, at, 8 * t + n);
+        const uint4* from = reinterpret_cast<const uint4*>(p.bounds + of * (2 * D)) + c;
+        uint4 w[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) w[i] = of >= 0 ? __ldg(from + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
-          acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+        for (int i = 0; i < kPieces; ++i) w[i] = of >= 0 ? __ldg(from + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
+        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) {
-            mma_bf16(acc[t], qs[(pass * kSteps + 2 * i) * 32 + lane], w[i].x, w[i].y);
-            mma_bf16(acc[t], qs[(pass * kSteps + 2 * i + 1) * 32 + lane], w[i].z, w[i].w);
-          }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) tile_s[warp][n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
-        __syncwarp();
-        for (int t = 0; t < tokens; ++t) {
-          float x = pass ? top_s[warp][t][lane] : -INFINITY;
-          for (int r = max(0, t * p.group - pass * 16); r < min(16, (t + 1) * p.group - pass * 16); ++r) x = max_nan(x, tile_s[warp][r][lane]);
-          top_s[warp][t][lane] = x;
+        for (int i = 0; i < kPieces; ++i) {
+          mma_bf16(acc[t], qs[2 * i * 32 + lane], w[i].x, w[i].y);
+          mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w[i].z, w[i].w);
         }
       }
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile_s[warp][n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
+      __syncwarp();
     }
-    for (int t = 0; t < tokens; ++t) {
+    for (int t = 0; t < p.tokens; ++t) {
       const int seen = __shfl_sync(0xffffffffu, mine, t);
-      if (col < p.n)
-        p.out[(((long long)b * p.tokens + t0 + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, top_s[warp][t][lane], col, seen);
+      float x = -INFINITY;
+      if (j0 < most)
+        for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile_s[warp][r][lane]);
+      if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, seen);
     }
     __syncwarp();
   }
@@ -374,12 +311,9 @@ cudaError_t launch_scores(const ScoreParams& p, int grid, cudaStream_t stream) {
   cudaLaunchAttribute a[1] = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kScoreThreads);
-  const int rows = std::min(p.tile_tokens, p.tokens) * p.group;
-  cfg.dynamicSmemBytes = (size_t)((rows + 15) / 16) * score_rows_bytes(D);
   cfg.stream = stream;
   with_pdl(cfg, a);
-  const cudaError_t e = cudaFuncSetAttribute(scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, scores_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, scores_kernel<D>, p);
 }
 
 }  // namespace
@@ -469,7 +403,7 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
   p.q_head = queries->q_head_stride;
   p.batch = queries->batch;
   p.tokens = queries->tokens;
-  p.group = queries->q_heads / bounds->kv_heads;
+  p.group = p.group_all = queries->q_heads / bounds->kv_heads;
   p.table = queries->page_table;
   p.table_stride = queries->table_stride;
   p.kv_len = kv_len;
@@ -479,16 +413,31 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
   p.n = n;
   p.row_len = row_len;
   p.status = place.status;
-  p.tile_tokens = std::max(1, 16 / p.group);
-  p.token_tiles = (p.tokens + p.tile_tokens - 1) / p.tile_tokens;
-  if ((int64_t)((p.group + 15) / 16) * score_rows_bytes(bounds->head_dim) > kScoreSmem) return TKS_E_TOO_LARGE;
-  const int64_t units = (int64_t)p.batch * p.kv_heads * p.token_tiles;
-  const int64_t most = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads);
-  p.chunks = (int)std::min<int64_t>(most, std::max<int64_t>(1, place.sms * 16 / units));
-  if (units * p.chunks > INT32_MAX) return TKS_E_TOO_LARGE;
+  p.spin_limit_ns = spin_limit_ns();
+  p.test_skip_arrive = test_skip_arrive();
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
   std::lock_guard<std::mutex> lock(*place.order);
-  const cudaError_t e = bounds->head_dim == 64 ? launch_scores<64>(p, (int)(units * p.chunks), (cudaStream_t)stream)
-                                                : launch_scores<128>(p, (int)(units * p.chunks), (cudaStream_t)stream);
+  if ((int64_t)p.tokens * p.group <= 16) {
+    const int64_t units = (int64_t)p.batch * p.kv_heads;
+    const int64_t most = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads);
+    p.chunks = (int)std::min<int64_t>(most, std::max<int64_t>(1, place.sms * 16 / units));
+    if (units * p.chunks > INT32_MAX) return TKS_E_TOO_LARGE;
+    e = bounds->head_dim == 64 ? launch_scores<64>(p, (int)(units * p.chunks), s) : launch_scores<128>(p, (int)(units * p.chunks), s);
+  } else {
+    // a token's rows lie in one half of a tile: larger groups are scored in parts
+    constexpr int half = kScoreTileRows / 2;
+    const int parts = (p.group_all + half - 1) / half, each = (p.group_all + parts - 1) / parts;
+    for (p.first_of_group = 0; p.first_of_group < p.group_all && e == cudaSuccess; p.first_of_group += each) {
+      p.group = std::min(each, p.group_all - p.first_of_group);
+      p.half_tokens = half / p.group;
+      p.tile_tokens = 2 * p.half_tokens;
+      p.token_tiles = (p.tokens - 1) / p.tile_tokens + 1;
+      e = launch_score_tiles(p, bounds->head_dim, place.sms, s);
+      p.join = true;
+      p.row_len = nullptr;
+    }
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

@@ -1,0 +1,497 @@
+// Scores of a cache's blocks for many query rows of each key/value head: chunks of
+// prompts, drafted tokens, wide head groups, on the tcgen05 tensor cores.
+//
+// Mathematics: that of tks_blocks.cu, a product of blocks' bounds (128 a tile,
+// 2 * dim elements each) with queries' negative and positive parts (256 rows a
+// tile). The blocks are the product's rows and the queries its columns, so that a
+// lane of tensor memory is a block, a token's query heads are neighbouring columns
+// of it, their maximum is taken within a thread, and a warp's stores are whole
+// 128-byte pieces of a row of scores.
+//
+// Layout.  One thread block an SM. Its query tile (128 KB at dim = 128) stays in
+// shared memory while tiles of bounds pass through a ring of K blocks (64 of the
+// summed elements, 16 KB, of 128 blocks), four producer warps' cp.async; one warp
+// issues the products into one of two accumulators of 256 columns; eight warps take
+// the other's maxima and store them. Four more bring the query tile.
+//
+// Work is the axis of all (sequence, tile of tokens)s' heads' tiles of blocks that any of their
+// tokens sees, of which every thread block takes an equal run.
+//
+// Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
+// warp's role, which makes the waits on that warp run out; when all roles have
+// ended the thread block frees its tensor memory and returns.
+
+#include <algorithm>
+
+#include "tks_scores.cuh"
+#include "tks_tensor.cuh"
+
+namespace tks {
+namespace attn {
+namespace {
+
+constexpr int kRows = kScoreTileRows, kBlocks = kScoreTileBlocks;
+constexpr int kMaxWarps = 8, kProducer0 = 8, kQuery0 = 12, kMulWarp = 16, kThreads = 17 * 32;
+constexpr int kUnits = 256;  // tiles of tokens whose lengths are looked at before the work is split
+
+template <int D>
+struct Shape {
+  static constexpr int kSteps = 2 * D / 64;             // K blocks
+  static constexpr int kStage = kBlocks * 128;          // of bounds
+  static constexpr int kQueries = kRows * 128;          // of queries
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kRing = kSteps * kQueries;       // where the ring begins
+  static constexpr int kSmem = kRing + kStages * kStage + 1024;  // and room to align the base
+};
+
+enum Bar { kFull = 0, kEmpty = kFull + 8, kSumFull = kEmpty + 8, kSumEmpty = kSumFull + 2, kQFull = kSumEmpty + 2, kQEmpty = kQFull + 1,
+           kFinal = kQEmpty + 1, kBars = kFinal + 1 };
+
+struct Shared {
+  unsigned long long bars[kBars];
+  uint32_t tmem;
+  int upto[kUnits + 1];             // tiles of blocks of the tiles of tokens before this one, each counted for one head
+  int seen[kMaxWarps][kRows / 2];   // the blocks that a half's tokens see (a copy for each warp)
+};
+
+struct Block {
+  uint32_t bars, queries, ring;
+  unsigned char* smem;
+  unsigned* status;
+  long long limit;
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
+  template <bool NAP = false>
+  __device__ __forceinline__ bool wait(int i, uint32_t parity) const { return bar_wait<NAP>(bar(i), parity, limit, status); }
+};
+
+// A run of tiles of blocks of one (sequence, tile of tokens, head).
+struct Item {
+  int b, t0, tokens, head;  // tokens: of this tile
+  int j0, j1;               // tiles of blocks
+};
+// A thread block's items, in order.
+struct Items {
+  long long at, end;
+  int unit, upto0, upto1;  // the tile of tokens that `at` lies in, and the tiles of blocks before it and up to its end
+  __device__ __forceinline__ int all(const ScoreParams& p) const { return (p.n + kBlocks - 1) / kBlocks; }
+  __device__ __forceinline__ void begin(const ScoreParams& p, const Shared& s) {
+    const int units = p.batch * p.token_tiles;
+    const bool counted = units <= kUnits;
+    const long long work = (counted ? (long long)s.upto[units] : (long long)units * all(p)) * p.kv_heads;
+    at = work / gridDim.x * blockIdx.x + min((long long)blockIdx.x, work % gridDim.x);
+    end = at + work / gridDim.x + (blockIdx.x < work % gridDim.x ? 1 : 0);
+    if (at >= end) return;
+    if (!counted) {
+      const long long one = (long long)all(p) * p.kv_heads;
+      unit = (int)(at / one);
+      upto0 = 0;  // (counted from the unit's begin on)
+      upto1 = all(p);
+      at -= unit * one;
+      end -= unit * one;
+    } else {
+      unit = 0;
+      while ((long long)s.upto[unit + 1] * p.kv_heads <= at) ++unit;
+      upto0 = s.upto[unit];
+      upto1 = s.upto[unit + 1];
+    }
+  }
+  __device__ __forceinline__ bool next(const ScoreParams& p, const Shared& s, Item& it) {
+    if (at >= end) return false;
+    const int tiles = upto1 - upto0;
+    const long long in = at - (long long)upto0 * p.kv_heads;
+    it.b = unit / p.token_tiles;
+    it.t0 = (unit - it.b * p.token_tiles) * p.tile_tokens;
+    it.tokens = min(p.tile_tokens, p.tokens - it.t0);
+    it.head = (int)(in / tiles);
+    it.j0 = (int)(in - (long long)it.head * tiles);
+    it.j1 = (int)min((long long)tiles, it.j0 + end - at);
+    at += it.j1 - it.j0;
+    if (at == (long long)upto1 * p.kv_heads && at < end) {
+      if (p.batch * p.token_tiles > kUnits) {
+        at = 0;
+        end -= (long long)upto1 * p.kv_heads;
+        ++unit;
+      } else {
+        do {
+          ++unit;
+          upto0 = upto1;
+          upto1 = s.upto[unit + 1];
+        } while (upto1 == upto0);
+      }
+    }
+    return true;
+  }
+};
+
+// Where a block's bounds lie, in elements, or -1 where its page is outside the cache.
+__device__ __forceinline__ long long bounds_at(const ScoreParams& p, int page, int j, int head, int dim) {
+  if ((unsigned)page >= (unsigned)p.pages) return -1;
+  return ((((long long)page << p.of_page_shift) + (j & ((1 << p.of_page_shift) - 1))) * p.kv_heads + head) * (2 * dim);
+}
+
+// Warps 8-11: bounds into the ring. A warp brings 32 blocks of every tile: lane l looks block l up, a tile ahead, and takes
+// piece l % 8 of every fourth block of a K block.
+template <int D>
+__device__ __forceinline__ void bring_bounds(const ScoreParams& p, const Block& k, const Shared& s) {
+  using S = Shape<D>;
+  const int lane = threadIdx.x & 31, mine = (threadIdx.x >> 5) - kProducer0, piece = lane & 7, row0 = 32 * mine + (lane >> 3);
+  Items ahead;
+  ahead.begin(p, s);
+  Item a;
+  bool more = ahead.next(p, s, a);
+  auto look_up = [&]() -> int {  // the page of this lane's block of the tile ahead (its first block's, behind the row's end)
+    const int j = a.j0 * kBlocks + 32 * mine + lane;
+    return j < p.n ? __ldg(p.table + a.b * p.table_stride + (j >> p.of_page_shift)) : -1;
+  };
+  int page = more ? look_up() : 0;
+  Ring<S::kStages> st;
+  unsigned g = 0;  // stages filled
+  while (uniform((int)more)) {
+    const long long at = bounds_at(p, page, a.j0 * kBlocks + 32 * mine + lane, a.head, D);
+    long long from[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) from[i] = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
+    if (++a.j0 == a.j1) more = ahead.next(p, s, a);
+    if (more) page = look_up();
+#pragma unroll 1
+    for (int step = 0; step < S::kSteps; ++step, ++g) {
+      if (g >= S::kStages && !k.wait<true>(kEmpty + st.i, st.parity ^ 1)) {
+        cp_wait<0>();
+        return;
+      }
+      const uint32_t to = k.ring + st.i * S::kStage + row0 * 128;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = row0 + 4 * i;
+        const __nv_bfloat16* src = p.bounds + (from[i] < 0 ? 0 : from[i] + step * 64 + piece * 8);
+        cp16(to + i * 512 + ((piece ^ (r & 7)) << 4), src, from[i] < 0 ? 0 : 16);
+      }
+      cp_commit();
+      // a stage is announced when the next two's copies are under way
+      if (g >= 2) {
+        cp_wait<2>();
+        __syncwarp();
+        bar_arrive(k.bar(kFull + (st.i + S::kStages - 2) % S::kStages));
+      }
+      st.next();
+    }
+  }
+  cp_wait<0>();
+  __syncwarp();
+  for (unsigned i = g < 2 ? 0 : g - 2; i < g; ++i) bar_arrive(k.bar(kFull + i % S::kStages));
+}
+
+// Warps 12-15: an item's query rows. Row 128 * h + i is row i of the h-th half of the tile's tokens.
+template <int D>
+__device__ __forceinline__ void bring_queries(const ScoreParams& p, const Block& k, const Shared& s) {
+  using S = Shape<D>;
+  constexpr int kPieces = D / 8, kPer = 128 / kPieces;  // pieces of a row; rows that 128 threads cover
+  const int t = threadIdx.x - kQuery0 * 32, piece = t % kPieces;
+  Items items;
+  items.begin(p, s);
+  Item it;
+  for (unsigned n = 0; uniform((int)items.next(p, s, it)); ++n) {
+    if (n > 0 && !k.wait<true>(kQEmpty, (n - 1) & 1)) return;
+#pragma unroll 1
+    for (int r0 = t / kPieces; r0 < kRows; r0 += 8 * kPer) {
+      uint4 w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * kPer, in = r & 127, tl = in / p.group, token = (r >> 7) * p.half_tokens + tl;
+        w[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < kRows && tl < p.half_tokens && token < it.tokens)
+          w[i] = __ldg(reinterpret_cast<const uint4*>(score_query(p, it.b, it.t0 + token, it.head, in - tl * p.group) + piece * 8));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * kPer;
+        if (r >= kRows) continue;
+        unsigned char* to = k.smem + (piece >> 3) * S::kQueries + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
+        *reinterpret_cast<uint4*>(to + S::kSteps / 2 * S::kQueries) =
+            make_uint4(part_of_pair(w[i].x, true), part_of_pair(w[i].y, true), part_of_pair(w[i].z, true), part_of_pair(w[i].w, true));
+      }
+    }
+    __syncwarp();
+    bar_arrive(k.bar(kQFull));
+  }
+}
+
+// One K block's product: 64 elements, sixteen an instruction, and an arrival when it is done.
+__device__ __forceinline__ void multiply_step(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b64 x, y;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"((unsigned)add), "r"(bar)
+      : "memory");
+}
+
+// Warp 16: the products.
+template <int D>
+__device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, const Shared& s, uint32_t tmem) {
+  using S = Shape<D>;
+  Items items;
+  items.begin(p, s);
+  Item it;
+  Ring<S::kStages> st;
+  const uint64_t ring = operand(k.ring, 16), queries = operand(k.queries, 16);
+  uint32_t g = 0;  // tiles
+  bool ok = true;
+  for (unsigned n = 0; ok && uniform((int)items.next(p, s, it)); ++n) {
+    if (!k.wait(kQFull, n & 1)) break;
+    // columns in use, in sixteens
+    const int rows = it.tokens > p.half_tokens ? 128 + (it.tokens - p.half_tokens) * p.group : it.tokens * p.group;
+    const uint32_t idesc = uniform(instr(false, false, (rows + 15) / 16 * 16));
+    const int tiles = uniform(it.j1 - it.j0);
+#pragma unroll 1
+    for (int i = 0; i < tiles && ok; ++i, ++g) {
+      if (g >= 2 && !k.wait(kSumEmpty + (g & 1), (g >> 1 & 1) ^ 1)) { ok = false; break; }
+#pragma unroll 1
+      for (int step = 0; step < S::kSteps; ++step) {
+        if (!k.wait(kFull + st.i, st.parity)) { ok = false; break; }
+        proxy_fence();
+        tc_fence_after();
+        multiply_step(tmem + (g & 1) * kRows, ring + (uint32_t)(st.i * (S::kStage >> 4)), queries + (uint32_t)(step * (S::kQueries >> 4)), idesc, step > 0,
+                      k.bar(kEmpty + st.i));
+        st.next();
+      }
+      if (ok) tc_commit(k.bar(kSumFull + (g & 1)));
+    }
+    if (ok) tc_commit(k.bar(kQEmpty));
+  }
+  // nothing may be under way when tensor memory is freed
+  tc_commit(k.bar(kFinal));
+  k.wait(kFinal, 0);
+}
+
+// Warps 0-7: maxima over a token's heads, and the stores. Warps w and w + 4 have the lanes (blocks) 32w .. 32w + 31, and each
+// one half's columns. GROUP: heads of a token, or 0: any.
+template <int GROUP>
+__device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k, Shared& s, uint32_t tmem) {
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
+  const int group = GROUP ? GROUP : p.group;
+  const bool plain = p.first == 0 && p.last == 0 && !p.join;
+  Items items;
+  items.begin(p, s);
+  Item it;
+  int* seen_s = s.seen[warp];
+  uint32_t g = 0;
+  while (uniform((int)items.next(p, s, it))) {
+    const int tokens = uniform(min(p.half_tokens, it.tokens - half * p.half_tokens)), first = it.t0 + half * p.half_tokens;
+    __syncwarp();
+    for (int t = lane; t < tokens; t += 32) {
+      bool bad = false;
+      seen_s[t] = blocks_seen(p, it.b, first + t, bad);
+    }
+    __syncwarp();
+    const long long stride = (long long)p.kv_heads * p.n;
+    for (int i = it.j0; i < it.j1; ++i, ++g) {
+      const int j = i * kBlocks + 32 * quarter + lane;
+      const int page = j < p.n ? __ldg(p.table + it.b * p.table_stride + (j >> p.of_page_shift)) : 0;
+      if (!k.wait(kSumFull + (g & 1), g >> 1 & 1)) return;
+      tc_fence_after();
+      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (g & 1) * kRows + half * 128;
+      float* to = p.out + (((long long)it.b * p.tokens + first) * p.kv_heads + it.head) * p.n + j;
+      const bool there = (unsigned)page < (unsigned)p.pages;
+      float top = -INFINITY;  // GROUP = 0: of the token's columns so far
+      int in = 0, t = 0;
+      bool missing = false;
+      auto put = [&](float x, int t) {
+        const int seen = seen_s[t];
+        if (plain) x = j >= seen ? -INFINITY : x == x ? x : INFINITY;
+        else x = final_score(p, x, j, seen);
+        if (!there) {
+          missing |= j < seen;
+          x = -INFINITY;
+        }
+        if (j < p.n) {
+          if (p.join) x = fmaxf(x, *to);
+          *to = x;
+        }
+        to += stride;
+      };
+#pragma unroll 1
+      for (int c = 0; c < 4 && c * 32 < tokens * group; ++c) {
+        uint32_t x[32];
+        __syncwarp();
+        tc_ld32(x, from + 32 * c);
+        tc_wait_ld();
+        if (GROUP) {
+          constexpr int kG = GROUP ? GROUP : 1;
+#pragma unroll
+          for (int u = 0; u < 32 / kG; ++u) {
+            float m = __uint_as_float(x[u * kG]);
+#pragma unroll
+            for (int e = 1; e < kG; ++e) m = max_nan(m, __uint_as_float(x[u * kG + e]));
+            const int tl = c * (32 / kG) + u;
+            if (tl < tokens) put(m, tl);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            top = max_nan(top, __uint_as_float(x[e]));
+            if (++in == group) {
+              if (t < tokens) put(top, t);
+              ++t;
+              in = 0;
+              top = -INFINITY;
+            }
+          }
+        }
+      }
+      if (missing && j < p.n) report(p.status, kStatIndexBit);
+      tc_fence_before();
+      __syncwarp();
+      if (!(p.test_skip_arrive && g == 0)) bar_arrive(k.bar(kSumEmpty + (g & 1)));
+    }
+  }
+}
+
+template <int D, int GROUP>
+__global__ void __launch_bounds__(kThreads, 1) score_tiles_kernel(const __grid_constant__ ScoreParams p) {
+  using S = Shape<D>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared s;
+  unsigned char* smem = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  Block k;
+  k.smem = smem;
+  k.queries = smem_addr(smem);
+  k.ring = k.queries + S::kRing;
+  k.bars = smem_addr(s.bars);
+  k.status = p.status;
+  k.limit = p.spin_limit_ns;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (warp == kMulWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::kStages; ++i) {
+      bar_init(k.bar(kFull + i), 4);
+      bar_init(k.bar(kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(k.bar(kSumFull + i), 1);
+      bar_init(k.bar(kSumEmpty + i), kMaxWarps);
+    }
+    bar_init(k.bar(kQFull), 4);
+    bar_init(k.bar(kQEmpty), 1);
+    bar_init(k.bar(kFinal), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  grid_wait();
+  grid_launch_dependents();
+
+  // how many tiles of blocks the tiles of tokens see
+  const int units = p.batch * p.token_tiles, all = (p.n + kBlocks - 1) / kBlocks;
+  if (units <= kUnits) {
+    for (int u = warp; u < units; u += kThreads / 32) {
+      const int b = u / p.token_tiles, t0 = (u - b * p.token_tiles) * p.tile_tokens, tokens = min(p.tile_tokens, p.tokens - t0);
+      int most = 0;
+      bool bad = false;
+      for (int t = lane; t < tokens; t += 32) most = max(most, blocks_seen(p, b, t0 + t, bad));
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) s.upto[u + 1] = (most + kBlocks - 1) / kBlocks;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int sum = 0;
+      if (lane == 0) s.upto[0] = 0;
+      for (int u0 = 0; u0 < units; u0 += 32) {
+        int x = u0 + lane < units ? s.upto[u0 + lane + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (u0 + lane < units) s.upto[u0 + lane + 1] = sum + x;
+        sum += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = uniform(s.tmem);
+
+  if (warp < kMaxWarps) {
+    // the rows' lengths, and the tiles of blocks that no token of a tile sees, a token of a head each warp
+    const long long rows = (long long)p.batch * p.tokens * p.kv_heads;
+    for (long long r = (long long)warp * gridDim.x + blockIdx.x; r < rows; r += (long long)gridDim.x * kMaxWarps) {
+      const int head = (int)(r % p.kv_heads);
+      const long long bt = r / p.kv_heads;
+      const int b = (int)(bt / p.tokens), t = (int)(bt - (long long)b * p.tokens);
+      bool bad = false;
+      const int seen = blocks_seen(p, b, t, bad);
+      if (lane == 0) {
+        if (bad) report(p.status, kStatRowLenBit);
+        if (p.row_len) p.row_len[r] = seen;
+      }
+      const int u = b * p.token_tiles + t / p.tile_tokens;
+      const int from = units <= kUnits ? s.upto[u + 1] - s.upto[u] : all;
+      (void)head;
+      for (long long j = (long long)from * kBlocks + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
+    }
+    take_maxima<GROUP>(p, k, s, tmem);
+  } else if (warp < kQuery0) {
+    bring_bounds<D>(p, k, s);
+  } else if (warp < kMulWarp) {
+    bring_queries<D>(p, k, s);
+  } else {
+    multiply<D>(p, k, s, tmem);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D, int GROUP>
+cudaError_t launch(const ScoreParams& p, int sms, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape<D>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute a[2] = {};
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, 0);
+  return cudaLaunchKernelEx(&cfg, score_tiles_kernel<D, GROUP>, p);
+}
+template <int D>
+cudaError_t launch_dim(const ScoreParams& p, int sms, cudaStream_t stream) {
+  switch (p.group) {
+    case 1: return launch<D, 1>(p, sms, stream);
+    case 2: return launch<D, 2>(p, sms, stream);
+    case 4: return launch<D, 4>(p, sms, stream);
+    case 8: return launch<D, 8>(p, sms, stream);
+    case 16: return launch<D, 16>(p, sms, stream);
+    default: return launch<D, 0>(p, sms, stream);
+  }
+}
+template <int D>
+cudaError_t opt_in() {
+  cudaError_t e = cudaSuccess;
+  for (auto kernel : {score_tiles_kernel<D, 0>, score_tiles_kernel<D, 1>, score_tiles_kernel<D, 2>, score_tiles_kernel<D, 4>, score_tiles_kernel<D, 8>,
+                      score_tiles_kernel<D, 16>})
+    if (e == cudaSuccess) e = allow(kernel, Shape<D>::kSmem);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t setup_score_tiles() {
+  const cudaError_t e = opt_in<64>();
+  return e != cudaSuccess ? e : opt_in<128>();
+}
+
+cudaError_t launch_score_tiles(const ScoreParams& p, int head_dim, int sms, cudaStream_t stream) {
+  return head_dim == 64 ? launch_dim<64>(p, sms, stream) : launch_dim<128>(p, sms, stream);
+}
+
+}  // namespace attn
+}  // namespace tks

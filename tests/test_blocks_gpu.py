@@ -307,6 +307,49 @@ def test_scores_that_are_no_numbers_are_picked(tokens, q_heads):
     assert (got[0, 0, 0] == math.inf).all() and torch.equal(got[0, 1:, 1], good[0, 1:, 1]) and torch.equal(got[0, 0, 1], good[0, 0, 1])
 
 
+@pytest.mark.parametrize("tokens, q_heads, kv_heads", [(3, 40, 1), (2, 257, 1), (9, 100, 2), (20, 128, 1), (7, 129, 1)])
+def test_scores_of_wide_groups_in_chunks(tokens, q_heads, kv_heads):
+    score_case([300, 20], tokens, q_heads, kv_heads, 64, 32, 16, seed=tokens, first=1)
+
+
+def test_scores_of_many_tiles():
+    """More tiles of tokens than are counted before the work is split, and several tiles of blocks for each."""
+    g = gen(12)
+    bounds = torch.randn(300, 1, 1, 2, 64, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(30, 300, 8, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(300, (30, 200), device="cuda", generator=g).to(torch.int32)
+    lens = torch.randint(0, 1601, (30, 300), device="cuda", generator=g).to(torch.int32)
+    scores, seen = tks.block_scores(q, bounds, table, lens, 8)
+    assert torch.equal(seen[..., 0], (lens + 7) // 8)
+    for b in (0, 13, 29):
+        lo, hi = (bounds[table[b].long(), 0, 0, i].double() for i in (0, 1))
+        x = q[b].double()
+        want = (x.clamp(min=0) @ hi.T + x.clamp(max=0) @ lo.T).amax(1)
+        size = (x.abs() @ torch.maximum(lo.abs(), hi.abs()).T).amax(1)
+        there = torch.arange(200, device="cuda") < seen[b]
+        assert (scores[b, :, 0][~there] == -math.inf).all()
+        assert ((scores[b, :, 0].double() - want).abs() <= 128 * 2.0 ** -23 * size)[there].all()
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """(Of the kernel for many rows: a warp does not say that it has read the first tile.)"""
+    g = gen(13)
+    bounds = torch.randn(50, 1, 1, 2, 64, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(1, 40, 8, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(50, (1, 128 * 1000), device="cuda", generator=g).to(torch.int32)  # six tiles or more a thread block
+    want, _ = tks.block_scores(q, bounds, table, None, 8)
+    assert tks.device_status() == tks.TKS_OK
+    tks.set_option(tks.TKS_OPT_SPIN_LIMIT_NS, 20_000_000)
+    tks.set_option(tks.TKS_OPT_TEST_SKIP_ARRIVE, 1)
+    try:
+        tks.block_scores(q, bounds, table, None, 8)
+        assert tks.device_status() == tks.TKS_E_TIMEOUT
+    finally:
+        tks.set_option(tks.TKS_OPT_TEST_SKIP_ARRIVE, 0)
+        tks.set_option(tks.TKS_OPT_SPIN_LIMIT_NS, 1_000_000_000)
+    assert torch.equal(want, tks.block_scores(q, bounds, table, None, 8)[0])
+
+
 def test_scores_bound_every_product():
     lens = [500, 61]
     cache, table, rows = filled(lens, 32, 2, 64, "bf16")

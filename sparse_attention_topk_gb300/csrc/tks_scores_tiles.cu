@@ -12,7 +12,7 @@
 // shared memory while tiles of bounds pass through a ring of K blocks (64 of the
 // summed elements, 16 KB, of 128 blocks), four producer warps' cp.async; one warp
 // issues the products into one of two accumulators of 256 columns; eight warps take
-// the other's maxima and store them. Four more bring the query tile.
+// the other's maxima and store them. Three more bring the query tile.
 //
 // Work is the axis of all (sequence, tile of tokens)s' heads' tiles of blocks that any of their
 // tokens sees, of which every thread block takes an equal run.
@@ -22,6 +22,7 @@
 // ended the thread block frees its tensor memory and returns.
 
 #include <algorithm>
+#include <climits>
 
 #include "tks_scores.cuh"
 #include "tks_tensor.cuh"
@@ -31,12 +32,14 @@ namespace attn {
 namespace {
 
 constexpr int kRows = kScoreTileRows, kBlocks = kScoreTileBlocks;
-constexpr int kMaxWarps = 8, kProducer0 = 8, kQuery0 = 12, kMulWarp = 16, kThreads = 17 * 32;
+constexpr int kMaxWarps = 8, kProducer0 = 8, kQuery0 = 12, kQueryWarps = 3, kMulWarp = 15, kThreads = 16 * 32;
 constexpr int kUnits = 256;  // tiles of tokens whose lengths are looked at before the work is split
 
 template <int D>
 struct Shape {
-  static constexpr int kSteps = 2 * D / 64;             // K blocks
+  static constexpr int kSteps = 2 * D / 64;             // K blocks, taken in this order: 64 elements' negative parts, their
+  static constexpr int kParts = kSteps / 2;             // positive ones, the next 64 elements'
+  static __device__ __forceinline__ int k_block(int step) { return (step >> 1) + (step & 1) * kParts; }
   static constexpr int kStage = kBlocks * 128;          // of bounds
   static constexpr int kQueries = kRows * 128;          // of queries
   static constexpr int kStages = D == 128 ? 5 : 8;
@@ -44,14 +47,16 @@ struct Shape {
   static constexpr int kSmem = kRing + kStages * kStage + 1024;  // and room to align the base
 };
 
-enum Bar { kFull = 0, kEmpty = kFull + 8, kSumFull = kEmpty + 8, kSumEmpty = kSumFull + 2, kQFull = kSumEmpty + 2, kQEmpty = kQFull + 1,
-           kFinal = kQEmpty + 1, kBars = kFinal + 1 };
+enum Bar { kFull = 0, kEmpty = kFull + 8, kSumFull = kEmpty + 8, kSumEmpty = kSumFull + 2, kQFull = kSumEmpty + 2, kQEmpty = kQFull + 2,
+           kFinal = kQEmpty + 2, kBars = kFinal + 1 };
 
 struct Shared {
   unsigned long long bars[kBars];
   uint32_t tmem;
   int upto[kUnits + 1];             // tiles of blocks of the tiles of tokens before this one, each counted for one head
   int seen[kMaxWarps][kRows / 2];   // the blocks that a half's tokens see (a copy for each warp)
+  long long row[kRows];             // a query row's place behind its tile's first, in elements,
+  int token[kRows];                 // and its token in the tile (one beyond all of them: none)
 };
 
 struct Block {
@@ -155,7 +160,7 @@ __device__ __forceinline__ void bring_bounds(const ScoreParams& p, const Block& 
     if (more) page = look_up();
 #pragma unroll 1
     for (int step = 0; step < S::kSteps; ++step, ++g) {
-      if (g >= S::kStages && !k.wait<true>(kEmpty + st.i, st.parity ^ 1)) {
+      if (g >= S::kStages && !k.wait(kEmpty + st.i, st.parity ^ 1)) {
         cp_wait<0>();
         return;
       }
@@ -163,57 +168,59 @@ __device__ __forceinline__ void bring_bounds(const ScoreParams& p, const Block& 
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = row0 + 4 * i;
-        const __nv_bfloat16* src = p.bounds + (from[i] < 0 ? 0 : from[i] + step * 64 + piece * 8);
+        const __nv_bfloat16* src = p.bounds + (from[i] < 0 ? 0 : from[i] + S::k_block(step) * 64 + piece * 8);
         cp16(to + i * 512 + ((piece ^ (r & 7)) << 4), src, from[i] < 0 ? 0 : 16);
       }
+      // the copies announce themselves, a thread's when they are all there
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(k.bar(kFull + st.i)) : "memory");
       cp_commit();
-      // a stage is announced when the next two's copies are under way
-      if (g >= 2) {
-        cp_wait<2>();
-        __syncwarp();
-        bar_arrive(k.bar(kFull + (st.i + S::kStages - 2) % S::kStages));
-      }
       st.next();
     }
   }
   cp_wait<0>();
-  __syncwarp();
-  for (unsigned i = g < 2 ? 0 : g - 2; i < g; ++i) bar_arrive(k.bar(kFull + i % S::kStages));
 }
 
-// Warps 12-15: an item's query rows. Row 128 * h + i is row i of the h-th half of the tile's tokens.
+// Warps 12-14: an item's query rows, 64 elements of all of them after the other. Row 128 * h + i is row i of the h-th half of
+// the tile's tokens. The item before still needs what is there: meanwhile the first rows are loaded.
 template <int D>
 __device__ __forceinline__ void bring_queries(const ScoreParams& p, const Block& k, const Shared& s) {
   using S = Shape<D>;
-  constexpr int kPieces = D / 8, kPer = 128 / kPieces;  // pieces of a row; rows that 128 threads cover
-  const int t = threadIdx.x - kQuery0 * 32, piece = t % kPieces;
+  constexpr int kPer = kQueryWarps * 32 / 8, kAtOnce = 11;  // rows that the threads cover, eight pieces each; how often at once
+  static_assert(2 * kAtOnce * kPer >= kRows, "two passes bring all rows");
+  const int t = threadIdx.x - kQuery0 * 32, piece = t % 8;
   Items items;
   items.begin(p, s);
   Item it;
   for (unsigned n = 0; uniform((int)items.next(p, s, it)); ++n) {
-    if (n > 0 && !k.wait<true>(kQEmpty, (n - 1) & 1)) return;
+    const __nv_bfloat16* q = score_query(p, it.b, it.t0, it.head, 0) + piece * 8;
 #pragma unroll 1
-    for (int r0 = t / kPieces; r0 < kRows; r0 += 8 * kPer) {
-      uint4 w[8];
+    for (int part = 0; part < S::kParts; ++part) {
+#pragma unroll 1
+      for (int r0 = t / 8; r0 < kRows; r0 += kAtOnce * kPer) {
+        uint4 w[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i * kPer, in = r & 127, tl = in / p.group, token = (r >> 7) * p.half_tokens + tl;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < kRows && tl < p.half_tokens && token < it.tokens)
-          w[i] = __ldg(reinterpret_cast<const uint4*>(score_query(p, it.b, it.t0 + token, it.head, in - tl * p.group) + piece * 8));
-      }
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int r = r0 + i * kPer;
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < kRows && s.token[r] < it.tokens) w[i] = __ldg(reinterpret_cast<const uint4*>(q + s.row[r] + part * 64));
+        }
+        if (r0 < kPer) {
+          __syncwarp();
+          if (n > 0 && !k.wait(kQEmpty + part, (n - 1) & 1)) return;
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i * kPer;
-        if (r >= kRows) continue;
-        unsigned char* to = k.smem + (piece >> 3) * S::kQueries + r * 128 + (((piece & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
-        *reinterpret_cast<uint4*>(to + S::kSteps / 2 * S::kQueries) =
-            make_uint4(part_of_pair(w[i].x, true), part_of_pair(w[i].y, true), part_of_pair(w[i].z, true), part_of_pair(w[i].w, true));
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int r = r0 + i * kPer;
+          if (r >= kRows) continue;
+          unsigned char* to = k.smem + part * S::kQueries + r * 128 + ((piece ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
+          *reinterpret_cast<uint4*>(to + S::kParts * S::kQueries) =
+              make_uint4(part_of_pair(w[i].x, true), part_of_pair(w[i].y, true), part_of_pair(w[i].z, true), part_of_pair(w[i].w, true));
+        }
       }
+      __syncwarp();
+      bar_arrive(k.bar(kQFull + part));
     }
-    __syncwarp();
-    bar_arrive(k.bar(kQFull));
   }
 }
 
@@ -230,7 +237,7 @@ __device__ __forceinline__ void multiply_step(uint32_t d, uint64_t a, uint64_t b
       : "memory");
 }
 
-// Warp 16: the products.
+// Warp 15: the products.
 template <int D>
 __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, const Shared& s, uint32_t tmem) {
   using S = Shape<D>;
@@ -242,7 +249,6 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
   uint32_t g = 0;  // tiles
   bool ok = true;
   for (unsigned n = 0; ok && uniform((int)items.next(p, s, it)); ++n) {
-    if (!k.wait(kQFull, n & 1)) break;
     // columns in use, in sixteens
     const int rows = it.tokens > p.half_tokens ? 128 + (it.tokens - p.half_tokens) * p.group : it.tokens * p.group;
     const uint32_t idesc = uniform(instr(false, false, (rows + 15) / 16 * 16));
@@ -252,16 +258,17 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
       if (g >= 2 && !k.wait(kSumEmpty + (g & 1), (g >> 1 & 1) ^ 1)) { ok = false; break; }
 #pragma unroll 1
       for (int step = 0; step < S::kSteps; ++step) {
+        if (i == 0 && (step & 1) == 0 && !k.wait(kQFull + (step >> 1), n & 1)) { ok = false; break; }
         if (!k.wait(kFull + st.i, st.parity)) { ok = false; break; }
         proxy_fence();
         tc_fence_after();
-        multiply_step(tmem + (g & 1) * kRows, ring + (uint32_t)(st.i * (S::kStage >> 4)), queries + (uint32_t)(step * (S::kQueries >> 4)), idesc, step > 0,
+        multiply_step(tmem + (g & 1) * kRows, ring + (uint32_t)(st.i * (S::kStage >> 4)), queries + (uint32_t)(S::k_block(step) * (S::kQueries >> 4)), idesc, step > 0,
                       k.bar(kEmpty + st.i));
+        if (i == tiles - 1 && (step & 1)) tc_commit(k.bar(kQEmpty + (step >> 1)));
         st.next();
       }
       if (ok) tc_commit(k.bar(kSumFull + (g & 1)));
     }
-    if (ok) tc_commit(k.bar(kQEmpty));
   }
   // nothing may be under way when tensor memory is freed
   tc_commit(k.bar(kFinal));
@@ -269,7 +276,9 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
 }
 
 // Warps 0-7: maxima over a token's heads, and the stores. Warps w and w + 4 have the lanes (blocks) 32w .. 32w + 31, and each
-// one half's columns. GROUP: heads of a token, or 0: any.
+// one half's columns. GROUP: heads of a token, or 0: any. 32 columns are on their way while the 32 before them are joined.
+// Most tiles hold blocks that all their tokens see: what their scores go through is kept short (the whole way for all of them
+// took 101 us instead of XX for 2048 tokens of 32 heads over 2048 blocks).
 template <int GROUP>
 __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k, Shared& s, uint32_t tmem) {
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
@@ -282,28 +291,34 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
   uint32_t g = 0;
   while (uniform((int)items.next(p, s, it))) {
     const int tokens = uniform(min(p.half_tokens, it.tokens - half * p.half_tokens)), first = it.t0 + half * p.half_tokens;
+    const int chunks = tokens <= 0 ? 0 : uniform((tokens * group + 31) / 32);
+    int least = p.n;  // blocks that all of these tokens see
     __syncwarp();
     for (int t = lane; t < tokens; t += 32) {
       bool bad = false;
-      seen_s[t] = blocks_seen(p, it.b, first + t, bad);
+      const int seen = blocks_seen(p, it.b, first + t, bad);
+      seen_s[t] = seen;
+      least = min(least, seen);
     }
+    least = __reduce_min_sync(0xffffffffu, least);
     __syncwarp();
     const long long stride = (long long)p.kv_heads * p.n;
-    for (int i = it.j0; i < it.j1; ++i, ++g) {
-      const int j = i * kBlocks + 32 * quarter + lane;
-      const int page = j < p.n ? __ldg(p.table + it.b * p.table_stride + (j >> p.of_page_shift)) : 0;
+    const int j1 = uniform(it.j1);
+    auto page_of = [&](int j) -> int { return j < p.n ? __ldg(p.table + it.b * p.table_stride + (j >> p.of_page_shift)) : 0; };
+    int next_page = page_of(it.j0 * kBlocks + 32 * quarter + lane);  // (looked up a tile ahead)
+    for (int i = uniform(it.j0); i < j1; ++i, ++g) {
+      const int j = i * kBlocks + 32 * quarter + lane, page = next_page;
+      if (i + 1 < j1) next_page = page_of(j + kBlocks);
       if (!k.wait(kSumFull + (g & 1), g >> 1 & 1)) return;
       tc_fence_after();
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (g & 1) * kRows + half * 128;
       float* to = p.out + (((long long)it.b * p.tokens + first) * p.kv_heads + it.head) * p.n + j;
       const bool there = (unsigned)page < (unsigned)p.pages;
-      float top = -INFINITY;  // GROUP = 0: of the token's columns so far
-      int in = 0, t = 0;
+      const bool simple = plain && i * kBlocks + 32 * quarter + 32 <= least && __all_sync(0xffffffffu, there);
       bool missing = false;
       auto put = [&](float x, int t) {
         const int seen = seen_s[t];
-        if (plain) x = j >= seen ? -INFINITY : x == x ? x : INFINITY;
-        else x = final_score(p, x, j, seen);
+        x = final_score(p, x, j, seen);
         if (!there) {
           missing |= j < seen;
           x = -INFINITY;
@@ -314,21 +329,29 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
         }
         to += stride;
       };
-#pragma unroll 1
-      for (int c = 0; c < 4 && c * 32 < tokens * group; ++c) {
-        uint32_t x[32];
-        __syncwarp();
-        tc_ld32(x, from + 32 * c);
-        tc_wait_ld();
+      float top = -INFINITY;  // GROUP = 0: of the token's columns so far
+      int in = 0, t = 0;
+      auto join = [&](const uint32_t (&x)[32], int c) {
         if (GROUP) {
           constexpr int kG = GROUP ? GROUP : 1;
+          float m[32 / kG];
 #pragma unroll
           for (int u = 0; u < 32 / kG; ++u) {
-            float m = __uint_as_float(x[u * kG]);
+            m[u] = __uint_as_float(x[u * kG]);
 #pragma unroll
-            for (int e = 1; e < kG; ++e) m = max_nan(m, __uint_as_float(x[u * kG + e]));
-            const int tl = c * (32 / kG) + u;
-            if (tl < tokens) put(m, tl);
+            for (int e = 1; e < kG; ++e) m[u] = max_nan(m[u], __uint_as_float(x[u * kG + e]));
+          }
+          const int t0 = c * (32 / kG);
+          if (simple && t0 + 32 / kG <= tokens) {
+#pragma unroll
+            for (int u = 0; u < 32 / kG; ++u) {
+              *to = m[u] == m[u] ? m[u] : INFINITY;
+              to += stride;
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32 / kG; ++u)
+              if (t0 + u < tokens) put(m[u], t0 + u);
           }
         } else {
 #pragma unroll
@@ -340,6 +363,24 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
               in = 0;
               top = -INFINITY;
             }
+          }
+        }
+      };
+      if (chunks > 0) {
+        uint32_t x[32], y[32];
+        __syncwarp();
+        tc_ld32(x, from);
+#pragma unroll 1
+        for (int c = 0; c < chunks; c += 2) {
+          tc_wait_ld();
+          __syncwarp();
+          if (c + 1 < chunks) tc_ld32(y, from + 32 * (c + 1));
+          join(x, c);
+          if (c + 1 < chunks) {
+            tc_wait_ld();
+            __syncwarp();
+            if (c + 2 < chunks) tc_ld32(x, from + 32 * (c + 2));
+            join(y, c + 1);
           }
         }
       }
@@ -371,21 +412,28 @@ __global__ void __launch_bounds__(kThreads, 1) score_tiles_kernel(const __grid_c
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kStages; ++i) {
-      bar_init(k.bar(kFull + i), 4);
+      bar_init(k.bar(kFull + i), 4 * 32);
       bar_init(k.bar(kEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(k.bar(kSumFull + i), 1);
       bar_init(k.bar(kSumEmpty + i), kMaxWarps);
     }
-    bar_init(k.bar(kQFull), 4);
-    bar_init(k.bar(kQEmpty), 1);
+    for (int i = 0; i < 2; ++i) {
+      bar_init(k.bar(kQFull + i), kQueryWarps);
+      bar_init(k.bar(kQEmpty + i), 1);
+    }
     bar_init(k.bar(kFinal), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   grid_wait();
   grid_launch_dependents();
 
+  if (threadIdx.x < kRows) {
+    const int r = threadIdx.x, in = r & 127, tl = in / p.group, token = (r >> 7) * p.half_tokens + tl;
+    s.token[r] = tl < p.half_tokens ? token : INT_MAX;
+    s.row[r] = token * p.q_token + (in - tl * p.group) * p.q_head;
+  }
   // how many tiles of blocks the tiles of tokens see
   const int units = p.batch * p.token_tiles, all = (p.n + kBlocks - 1) / kBlocks;
   if (units <= kUnits) {
@@ -419,23 +467,21 @@ __global__ void __launch_bounds__(kThreads, 1) score_tiles_kernel(const __grid_c
   const uint32_t tmem = uniform(s.tmem);
 
   if (warp < kMaxWarps) {
-    // the rows' lengths, and the tiles of blocks that no token of a tile sees, a token of a head each warp
-    const long long rows = (long long)p.batch * p.tokens * p.kv_heads;
-    for (long long r = (long long)warp * gridDim.x + blockIdx.x; r < rows; r += (long long)gridDim.x * kMaxWarps) {
-      const int head = (int)(r % p.kv_heads);
-      const long long bt = r / p.kv_heads;
-      const int b = (int)(bt / p.tokens), t = (int)(bt - (long long)b * p.tokens);
+    // the rows' lengths, a lane each
+    const int rows = p.batch * p.tokens * p.kv_heads, warps = gridDim.x * kMaxWarps, mine = warp * gridDim.x + blockIdx.x;
+    for (long long r = mine * 32LL + lane; r < rows; r += warps * 32LL) {
+      const int bt = (int)r / p.kv_heads, b = bt / p.tokens;
       bool bad = false;
-      const int seen = blocks_seen(p, b, t, bad);
-      if (lane == 0) {
-        if (bad) report(p.status, kStatRowLenBit);
-        if (p.row_len) p.row_len[r] = seen;
-      }
-      const int u = b * p.token_tiles + t / p.tile_tokens;
-      const int from = units <= kUnits ? s.upto[u + 1] - s.upto[u] : all;
-      (void)head;
-      for (long long j = (long long)from * kBlocks + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
+      const int seen = blocks_seen(p, b, bt - b * p.tokens, bad);
+      if (bad) report(p.status, kStatRowLenBit);
+      if (p.row_len) p.row_len[r] = seen;
     }
+    // the tiles of blocks that no token of a tile sees, a row each warp
+    if (units <= kUnits && s.upto[units] < units * (long long)all)
+      for (long long r = mine; r < rows; r += warps) {
+        const int bt = (int)r / p.kv_heads, b = bt / p.tokens, u = b * p.token_tiles + (bt - b * p.tokens) / p.tile_tokens;
+        for (long long j = (long long)(s.upto[u + 1] - s.upto[u]) * kBlocks + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
+      }
     take_maxima<GROUP>(p, k, s, tmem);
   } else if (warp < kQuery0) {
     bring_bounds<D>(p, k, s);

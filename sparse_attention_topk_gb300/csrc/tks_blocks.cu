@@ -425,6 +425,8 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
     if (units * p.chunks > INT32_MAX) return TKS_E_TOO_LARGE;
     e = bounds->head_dim == 64 ? launch_scores<64>(p, (int)(units * p.chunks), s) : launch_scores<128>(p, (int)(units * p.chunks), s);
   } else {
+    // (134 MB of scores, stored as what is not read again soon: 58 us, 63 without; fewer stay for the selector)
+    p.stream_out = (int64_t)p.batch * p.tokens * p.kv_heads * n > (64 << 20) / 4;
     // a token's rows lie in one half of a tile: larger groups are scored in parts
     constexpr int half = kScoreTileRows / 2;
     const int parts = (p.group_all + half - 1) / half, each = (p.group_all + parts - 1) / parts;

@@ -21,6 +21,7 @@ struct ScoreParams {
   int n;
   int32_t* row_len;
   unsigned* status;
+  bool stream_out;                     // scores are more than stay in L2
   bool join;                           // the largest of this launch's heads and of what is there
   int tile_tokens, token_tiles;        // tokens of a tile of query rows, and how many tiles a sequence has
   int chunks;                          // few rows: thread blocks of a unit

@@ -345,7 +345,9 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
           if (simple && t0 + 32 / kG <= tokens) {
 #pragma unroll
             for (int u = 0; u < 32 / kG; ++u) {
-              *to = m[u] == m[u] ? m[u] : INFINITY;
+              const float x = m[u] == m[u] ? m[u] : INFINITY;
+              if (p.stream_out) __stcs(to, x);
+              else *to = x;
               to += stride;
             }
           } else {

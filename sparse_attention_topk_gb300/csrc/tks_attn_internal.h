@@ -121,6 +121,12 @@ constexpr int kClusterMax = 8;
 constexpr int kRowsTile = 16;  // query rows of a block
 constexpr int kRowsKeys = 64;  // keys of a tile
 constexpr int kRowsBlocksPerSm = 2;
+constexpr int kRowsBlocksPerSmOfBlocks = 3;  // lists of blocks
+// Whether a list's blocks, and the pages, are at least as long as the chunks (32 keys of int8, 16 of bfloat16) that warps take.
+inline bool blocks_by_chunks(const Params& p, bool i8) {
+  const int chunk = i8 ? 5 : 4;
+  return p.block_shift >= chunk && p.page_shift >= chunk;
+}
 cudaError_t setup_rows();
 cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,
                         cudaStream_t stream);

@@ -53,7 +53,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
-template <int D, bool I8>
+template <int D, bool I8, bool BLOCKS = false>
 struct Shape {
   static constexpr int kElem = I8 ? 1 : 2;
   static constexpr int kRow = D * kElem;               // bytes of a row
@@ -66,12 +66,13 @@ struct Shape {
   static constexpr int kOps = 2 * kChunk * kRow;       // keys, then values
   static constexpr int kScales = I8 ? kChunk * 8 : 0;
   static constexpr int kStage = kOps + kScales + 16;   // and the mask of valid keys
-  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kStages = BLOCKS ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 5;
   static constexpr int kQs = D / 16 * 32 * 16;         // query fragments, behind the rings
   static constexpr int kConst = I8 ? kWarps * 32 * 16 : 0;  // and each warp's scales as they are used
   static constexpr int kRings = kWarps * kStages * kStage;
-  static constexpr int kSlots = 1024 * 4;              // and where keys lie
+  static constexpr int kSlots = BLOCKS ? 256 * 4 : 1024 * 4;  // and where keys lie (of a list of blocks: where chunks begin)
   static constexpr int kSmem = kRings + kQs + kConst + kSlots;
+  static constexpr int kPerSm = BLOCKS ? kRowsBlocksPerSmOfBlocks : kRowsBlocksPerSm;
   static_assert(kRings >= (kWarps + 1) * (16 * D * 4 + 16 * 8), "the merge fits the ring");
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
@@ -113,10 +114,11 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
   return lo || hi;
 }
 
-// PAGED: every chunk lies in one page (positions in order, pages of at least a chunk).
+// PAGED: every chunk lies in one page (positions in order, or lists of blocks; pages, and blocks, of at least a chunk).
 template <int D, bool I8, bool SEL, bool PAGED>
-__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant__ Params p) {
-  using S = Shape<D, I8>;
+__global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED>::kPerSm) rows_kernel(const __grid_constant__ Params p) {
+  constexpr bool BLOCKS = SEL && PAGED;
+  using S = Shape<D, I8, BLOCKS>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Start start;
   __shared__ float2 ml_s[kWarps + 1][16];  // maxima and sums: the warps', and those of a run's pieces before
@@ -181,16 +183,26 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     }
 
     // The page of the warp's chunk that starts at key j.
-    auto page = [&](int j) -> int { return PAGED && j < k_end ? table[j >> p.page_shift] : -1; };
+    auto page = [&](int j) -> int { return PAGED && !BLOCKS && j < k_end ? table[j >> p.page_shift] : -1; };
     // Starts the copies of the chunk at key j into stage `st`; pg: its page; beg: the key of slots[0].
     auto issue = [&](int j, int st, int pg, int beg, int end) {
       if (j < end) {
         const uint32_t to = st * S::kStage;
-        unsigned valid;
+        unsigned valid = 0;
         if (PAGED) {
+          int in_page;
+          // (a list's chunk: the slot that it begins at, and in the bits below a chunk, how many keys it has less one; or -1)
+          if (BLOCKS) {
+            const int at = slots[(j - beg) / kChunk];
+            pg = at < 0 ? -1 : at >> p.page_shift;
+            valid = at & (kChunk - 1);
+            in_page = at & ((1 << p.page_shift) - kChunk);
+          } else {
+            in_page = j & ((1 << p.page_shift) - 1);
+          }
           const bool ok = (unsigned)pg < (unsigned)p.pages;
-          if (!ok) report(p.status, kStatIndexBit);
-          const int n_valid = ok ? min(kChunk, end - j) : 0, in_page = j & ((1 << p.page_shift) - 1);
+          if (!BLOCKS && !ok) report(p.status, kStatIndexBit);
+          const int n_valid = !ok ? 0 : BLOCKS ? (int)valid + 1 : min(kChunk, end - j);
           const long long off = ok ? pg * p.page_b + in_page * p.token_b : 0;
           const unsigned char* ks = kb + off + row0 * p.token_b + piece * 16;
           const unsigned char* vs = vb + off + row0 * p.token_b + piece * 16;
@@ -284,8 +296,36 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     bool poisoned = false;  // a draft's value held an infinity or NaN (bfloat16)
 
     // ---- the warp's chunks: of the whole segment, or of the keys looked up at once ----
-    for (int beg = k_beg; beg < k_end; beg += PAGED ? k_end - k_beg : kSlots) {
-    const int end = PAGED ? k_end : (int)min((long long)k_end, (long long)beg + kSlots);
+    constexpr int kLookUp = BLOCKS ? kSlots * kChunk : kSlots;  // keys
+    for (int beg = k_beg; beg < k_end; beg += PAGED && !BLOCKS ? k_end - k_beg : kLookUp) {
+    const int end = PAGED && !BLOCKS ? k_end : (int)min((long long)k_end, (long long)beg + kLookUp);
+    if (BLOCKS) {
+      // all list entries, then all pages, a chunk each
+      constexpr int kMine = kSlots / kThreads;
+      int pos[kMine], pg[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int j = beg + (threadIdx.x + i * kThreads) * kChunk;
+        pos[i] = j >= end ? -1 : __ldg(list + (j >> p.block_shift));
+      }
+      bool bad = false;
+      const int limit = kv_limit(p, given);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        pos[i] = list_position(p, pos[i], beg + (threadIdx.x + i * kThreads) * kChunk, limit, bad);
+        pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
+      }
+      __syncthreads();  // the previous chunks' copies have started
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const bool ok = pos[i] >= 0 && (unsigned)pg[i] < (unsigned)p.pages;
+        bad |= pos[i] >= 0 && !ok;
+        slots[threadIdx.x + i * kThreads] =
+            ok ? (int)(((unsigned)pg[i] << p.page_shift) + (pos[i] & ((1 << p.page_shift) - 1))) + min(kChunk, limit - pos[i]) - 1 : -1;
+      }
+      if (bad) report(p.status, kStatIndexBit);
+      __syncthreads();
+    }
     if (!PAGED) {
       // all list entries, then all pages: two waits, not one for each key
       constexpr int kMine = kSlots / kThreads;
@@ -630,7 +670,7 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<D, I8>::kSmem;
+  cfg.dynamicSmemBytes = Shape<D, I8, SEL && PAGED>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
@@ -639,7 +679,8 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
 }
 template <int D, bool I8>
 cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream) {
-  if (selected) return launch<D, I8, true, false>(p, grid, stream);
+  if (selected)
+    return p.block_shift && blocks_by_chunks(p, I8) ? launch<D, I8, true, true>(p, grid, stream) : launch<D, I8, true, false>(p, grid, stream);
   return (1 << p.page_shift) >= Shape<D, I8>::kChunk ? launch<D, I8, false, true>(p, grid, stream)
                                                      : launch<D, I8, false, false>(p, grid, stream);
 }
@@ -647,6 +688,7 @@ cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream
 template <int D, bool I8>
 cudaError_t opt_in() {
   cudaError_t e = allow(rows_kernel<D, I8, true, false>, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = allow(rows_kernel<D, I8, true, true>, Shape<D, I8, true>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, true>, Shape<D, I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, false>, Shape<D, I8>::kSmem);
   return e;

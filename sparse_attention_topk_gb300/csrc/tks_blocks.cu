@@ -36,42 +36,65 @@ struct BoundsParams {
 
 __device__ __forceinline__ float finite_bf16(float x) { return x > kBf16Max ? kBf16Max : x < -kBf16Max ? -kBf16Max : x; }
 
-// The least and largest of a lane's 16-byte piece of the rows it has seen.
+// The least (or largest) of three; a NaN among them wins.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t bits_of(__nv_bfloat162 x) { return *reinterpret_cast<const uint32_t*>(&x); }
+
+// The least and largest of a lane's 16-byte piece of the rows it has seen, two rows at a time. At the end they are
+// bfloat16 (rounding keeps the order, so the least of rounded values is the rounded least).
 template <bool I8>
 struct Extent;
 template <>
 struct Extent<true> {
+  static constexpr int kPairs = 8;
   float lo[16], hi[16];
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < 16; ++i) lo[i] = INFINITY, hi[i] = -INFINITY;
   }
-  __device__ __forceinline__ void add(const uint4& w, float scale) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  // Four codes' values: codes become halves, exactly, then 32-bit floats.
+  static __device__ __forceinline__ void values(uint32_t codes, float scale, float (&x)[4]) {
+    const uint32_t u = codes ^ 0x80808080u, a = codes_to_half2<0x4140>(u), b = codes_to_half2<0x4342>(u);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a)), g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    x[0] = f.x * scale;
+    x[1] = f.y * scale;
+    x[2] = g.x * scale;
+    x[3] = g.y * scale;
+  }
+  __device__ __forceinline__ void add(const uint4& w, const uint4& v, float ws, float vs) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = (float)(int)(signed char)(u[i >> 2] >> (8 * (i & 3))) * scale;
-      lo[i] = min_nan(lo[i], x);
-      hi[i] = max_nan(hi[i], x);
+    for (int i = 0; i < 4; ++i) {
+      float x[4], y[4];
+      values(a[i], ws, x);
+      values(b[i], vs, y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        lo[4 * i + j] = min3_nan(lo[4 * i + j], x[j], y[j]);
+        hi[4 * i + j] = max3_nan(hi[4 * i + j], x[j], y[j]);
+      }
     }
   }
-  __device__ __forceinline__ void join(int o) {
+  __device__ __forceinline__ void rounded(__nv_bfloat162 (&l)[8], __nv_bfloat162 (&h)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      lo[i] = min_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-      hi[i] = max_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+    for (int i = 0; i < 8; ++i) {
+      l[i] = __floats2bfloat162_rn(finite_bf16(lo[2 * i]), finite_bf16(lo[2 * i + 1]));
+      h[i] = __floats2bfloat162_rn(finite_bf16(hi[2 * i]), finite_bf16(hi[2 * i + 1]));
     }
-  }
-  static __device__ __forceinline__ void put(__nv_bfloat16* to, const float (&x)[16]) {
-    uint32_t u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = pack_bf16(finite_bf16(x[2 * i]), finite_bf16(x[2 * i + 1]));
-    reinterpret_cast<uint4*>(to)[0] = make_uint4(u[0], u[1], u[2], u[3]);
-    reinterpret_cast<uint4*>(to)[1] = make_uint4(u[4], u[5], u[6], u[7]);
   }
 };
 template <>
 struct Extent<false> {
+  static constexpr int kPairs = 4;
   __nv_bfloat162 lo[4], hi[4];
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -80,27 +103,21 @@ struct Extent<false> {
       hi[i] = __floats2bfloat162_rn(-INFINITY, -INFINITY);
     }
   }
-  __device__ __forceinline__ void add(const uint4& w, float) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  __device__ __forceinline__ void add(const uint4& w, const uint4& v, float, float) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w}, b[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&u[i]);
-      lo[i] = __hmin2_nan(lo[i], x);
-      hi[i] = __hmax2_nan(hi[i], x);
+      const __nv_bfloat162 x = *reinterpret_cast<const __nv_bfloat162*>(&a[i]), y = *reinterpret_cast<const __nv_bfloat162*>(&b[i]);
+      lo[i] = __hmin2_nan(lo[i], __hmin2_nan(x, y));
+      hi[i] = __hmax2_nan(hi[i], __hmax2_nan(x, y));
     }
   }
-  __device__ __forceinline__ void join(int o) {
+  __device__ __forceinline__ void rounded(__nv_bfloat162 (&l)[4], __nv_bfloat162 (&h)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-      hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+      l[i] = __floats2bfloat162_rn(finite_bf16(__low2float(lo[i])), finite_bf16(__high2float(lo[i])));
+      h[i] = __floats2bfloat162_rn(finite_bf16(__low2float(hi[i])), finite_bf16(__high2float(hi[i])));
     }
-  }
-  static __device__ __forceinline__ void put(__nv_bfloat16* to, const __nv_bfloat162 (&x)[4]) {
-    uint32_t u[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = pack_bf16(finite_bf16(__low2float(x[i])), finite_bf16(__high2float(x[i])));
-    *reinterpret_cast<uint4*>(to) = make_uint4(u[0], u[1], u[2], u[3]);
   }
 };
 
@@ -109,7 +126,7 @@ constexpr int kBoundsThreads = 256;
 // An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time.
 template <int D, bool I8>
 __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
-  constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 4;
+  constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 8;
   __shared__ long long upto[kBoundsThreads];  // blocks of the sequences up to and with this one
   __shared__ int first_s[kBoundsThreads], end_s[kBoundsThreads];
   __shared__ long long warps_s[kBoundsThreads / 32];
@@ -174,16 +191,27 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
           sc[i] = I8 ? __ldg(scales + 2LL * r * p.kv_heads) : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) x.add(w[i], sc[i]);
+        for (int i = 0; i < kAhead; i += 2) x.add(w[i], w[i + 1], sc[i], sc[i + 1]);
       }
       __syncwarp();
+      constexpr int kPairs = Extent<I8>::kPairs;
+      __nv_bfloat162 lo[kPairs], hi[kPairs];
+      x.rounded(lo, hi);
 #pragma unroll
-      for (int o = kPieces; o < 32; o <<= 1) x.join(o);
+      for (int o = kPieces; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+          hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        }
       const int of_page = 1 << (p.page_shift - p.block_shift);
-      __nv_bfloat16* to = p.bounds + (((long long)page * of_page + (in_page >> p.block_shift)) * p.kv_heads + head) * (2 * D) + piece * kE;
+      uint4* to = reinterpret_cast<uint4*>(p.bounds + (((long long)page * of_page + (in_page >> p.block_shift)) * p.kv_heads + head) * (2 * D) + piece * kE);
       if (sub == 0) {
-        Extent<I8>::put(to, x.lo);
-        Extent<I8>::put(to + D, x.hi);
+#pragma unroll
+        for (int i = 0; i < kPairs; i += 4) {
+          to[i / 4] = make_uint4(bits_of(lo[i]), bits_of(lo[i + 1]), bits_of(lo[i + 2]), bits_of(lo[i + 3]));
+          to[D / 8 + i / 4] = make_uint4(bits_of(hi[i]), bits_of(hi[i + 1]), bits_of(hi[i + 2]), bits_of(hi[i + 3]));
+        }
       }
     }
     next -= items;
@@ -203,85 +231,127 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const uint4& a, uint32_t
 constexpr int kScoreWarps = 4, kScoreThreads = kScoreWarps * 32;
 constexpr int kScoreCols = 32;  // blocks that a warp scores at once
 
-// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and a run of
-// blocks; its query rows lie in shared memory as matrix fragments: of product step s, lane 4n + c takes the elements that
-// it has of column n's 4 * D bytes: 16-byte pieces c, c + 4, ...
+template <int D>
+struct ScoreShape {
+  static constexpr int kRow = 4 * D;            // bytes of a block's bounds
+  static constexpr int kWarp = kScoreCols * kRow;
+  static constexpr int kPieces = kRow / 16;     // 16-byte pieces
+  static constexpr int kSteps = 2 * D / 16;     // products of 16 of the summed elements
+  static constexpr int kQs = kSteps * 32 * 16;  // the query rows' fragments
+  static constexpr int kSmem = kScoreWarps * kWarp + kQs;
+  static_assert(16 * (kScoreCols + 1) * 4 <= kWarp, "a warp's scores fit where its bounds were");
+};
+
+// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and 128 blocks at
+// a time, a warp 32 of them, whose copies to shared memory are all under way at once, and start before the queries and
+// lengths are there. The query rows lie in shared memory as matrix fragments: of product step s, lane 4n + c takes the
+// elements that it has of column n's bytes: pieces c, c + 4, ... (XOR-swizzled, so that eight lanes' reads do not meet).
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_constant__ ScoreParams p) {
-  constexpr int kPieces = 2 * D * 2 / 16 / 4;  // of a lane
-  constexpr int kSteps = 2 * kPieces;
-  __shared__ uint4 qs[kSteps * 32];
-  __shared__ float tile_s[kScoreWarps][16][kScoreCols + 1];
+  using S = ScoreShape<D>;
+  extern __shared__ __align__(16) unsigned char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+  unsigned char* mine = smem + warp * S::kWarp;
+  float(*tile)[kScoreCols + 1] = reinterpret_cast<float(*)[kScoreCols + 1]>(mine);
+  uint4* qs = reinterpret_cast<uint4*>(smem + kScoreWarps * S::kWarp);
   const unsigned unit = blockIdx.x / p.chunks;
   const int chunk = blockIdx.x - unit * p.chunks;
   const int head = unit % p.kv_heads, b = unit / p.kv_heads, rows = p.tokens * p.group;
+  const int32_t* table = p.table + b * p.table_stride;
+  // the lane's pieces of a row, and its first row, in the copies
+  constexpr int kPer = 32 / S::kPieces > 0 ? 32 / S::kPieces : 1;  // rows that 32 lanes cover
+  const int piece = lane % S::kPieces, row0 = lane / S::kPieces;
   grid_wait();
   grid_launch_dependents();
 
-  for (int x = threadIdx.x; x < kSteps * 32; x += kScoreThreads) {
-    const int l = x & 31, s = x >> 5, r = l >> 2;
-    // elements of the doubled index: the first D are the least's, with the queries' negative parts
-    const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
-      w.x = part_of_pair(y.x, d >= D);
-      w.z = part_of_pair(y.y, d >= D);
-    }
-    if (r + 8 < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
-      w.y = part_of_pair(y.x, d >= D);
-      w.w = part_of_pair(y.y, d >= D);
-    }
-    qs[x] = w;
-  }
-  // the tokens' lengths, a lane each (16 at most)
-  bool bad = false;
-  const int mine = lane < p.tokens ? blocks_seen(p, b, lane, bad) : 0;
-  const int most = __reduce_max_sync(0xffffffffu, mine);
-  if (warp == 0 && chunk == 0) {
-    if (bad) report(p.status, kStatRowLenBit);
-    if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = mine;
-  }
-  __syncthreads();
-
-  const int32_t* table = p.table + b * p.table_stride;
-  for (long long j0 = ((long long)chunk * kScoreWarps + warp) * kScoreCols; j0 < p.n; j0 += (long long)p.chunks * kScoreThreads) {
+  bool bad = false, ready = false;
+  int seen = 0, most = 0;
+  for (long long j0 = ((long long)chunk * kScoreWarps + warp) * kScoreCols;; j0 += (long long)p.chunks * kScoreThreads) {
+    const bool any = j0 < p.n;
     const int col = (int)j0 + lane;
-    bool ok = true;
-    if (j0 < most) {
-      const int page = col < most ? __ldg(table + (col >> p.of_page_shift)) : 0;
-      ok = (unsigned)page < (unsigned)p.pages;
-      if (!ok) report(p.status, kStatIndexBit);
+    const int page = any && col < p.n ? __ldg(table + (col >> p.of_page_shift)) : -1;
+    if (!ready) {
+      // the tokens' lengths, a lane each (16 at most), and the query rows
+      if (lane < p.tokens) seen = blocks_seen(p, b, lane, bad);
+      for (int x = threadIdx.x; x < S::kSteps * 32; x += kScoreThreads) {
+        const int l = x & 31, s = x >> 5, r = l >> 2;
+        // elements of the doubled index: the first D are the least's, with the queries' negative parts
+        const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
+          w.x = part_of_pair(y.x, d >= D);
+          w.z = part_of_pair(y.y, d >= D);
+        }
+        if (r + 8 < rows) {
+          const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
+          w.y = part_of_pair(y.x, d >= D);
+          w.w = part_of_pair(y.y, d >= D);
+        }
+        qs[x] = w;
+      }
+      most = __reduce_max_sync(0xffffffffu, seen);
+    }
+    const bool ok = (unsigned)page < (unsigned)p.pages;
+    if (any && j0 < most) {
+      if (!ok && col < most) report(p.status, kStatIndexBit);
       const long long at = ok && col < most ? (((long long)page << p.of_page_shift) + (col & ((1 << p.of_page_shift) - 1))) * p.kv_heads + head : -1;
-      float acc[4][4];
+      const uint32_t to = smem_addr(mine) + row0 * S::kRow;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const long long of = __shfl_sync(0xffffffffu, at, 8 * t + n);
-        const uint4* from = reinterpret_cast<const uint4*>(p.bounds + of * (2 * D)) + c;
-        uint4 w[kPieces];
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) w[i] = of >= 0 ? __ldg(from + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
-        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) {
-          mma_bf16(acc[t], qs[2 * i * 32 + lane], w[i].x, w[i].y);
-          mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w[i].z, w[i].w);
+        for (int i = 0; i < 8 / kPer; ++i) {
+          const int r = 8 * t + i * kPer + row0;  // the column; its pieces lie swizzled
+          const long long of = __shfl_sync(0xffffffffu, at, r);
+          cp16(to + (8 * t + i * kPer) * S::kRow + ((piece ^ ((r & 1) << 2)) << 4), reinterpret_cast<const unsigned char*>(p.bounds) + (of < 0 ? 0 : of * S::kRow) + piece * 16,
+               of < 0 ? 0 : 16);
         }
+        cp_commit();
       }
+    }
+    if (!ready) {
+      if (warp == 0 && chunk == 0) {
+        if (bad) report(p.status, kStatRowLenBit);
+        if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = seen;
+      }
+      __syncthreads();
+      ready = true;
+    }
+    if (!any) break;  // (every warp has come to the barrier)
+    if (j0 < most) {
+      float acc[4][4];
+      auto columns = [&](int t) {
+        __syncwarp();
+        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+        const unsigned char* row = mine + (8 * t + n) * S::kRow;
+#pragma unroll
+        for (int i = 0; i < S::kPieces / 4; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + 4 * i) ^ ((n & 1) << 2)) << 4));
+          mma_bf16(acc[t], qs[2 * i * 32 + lane], w.x, w.y);
+          mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w.z, w.w);
+        }
+      };
+      cp_wait<3>();
+      columns(0);
+      cp_wait<2>();
+      columns(1);
+      cp_wait<1>();
+      columns(2);
+      cp_wait<0>();
+      columns(3);
+      __syncwarp();  // (scores go where the bounds were)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) tile_s[warp][n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
+        for (int e = 0; e < 4; ++e) tile[n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
       __syncwarp();
     }
     for (int t = 0; t < p.tokens; ++t) {
-      const int seen = __shfl_sync(0xffffffffu, mine, t);
+      const int blocks = __shfl_sync(0xffffffffu, seen, t);
       float x = -INFINITY;
       if (j0 < most)
-        for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile_s[warp][r][lane]);
-      if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, seen);
+        for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile[r][lane]);
+      if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, blocks);
     }
     __syncwarp();
   }
@@ -311,12 +381,18 @@ cudaError_t launch_scores(const ScoreParams& p, int grid, cudaStream_t stream) {
   cudaLaunchAttribute a[1] = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kScoreThreads);
+  cfg.dynamicSmemBytes = ScoreShape<D>::kSmem;
   cfg.stream = stream;
   with_pdl(cfg, a);
   return cudaLaunchKernelEx(&cfg, scores_kernel<D>, p);
 }
 
 }  // namespace
+
+cudaError_t setup_scores() {
+  const cudaError_t e = allow(scores_kernel<64>, ScoreShape<64>::kSmem);
+  return e != cudaSuccess ? e : allow(scores_kernel<128>, ScoreShape<128>::kSmem);
+}
 
 int check_bounds(const tks_bounds* b) {
   if (b == nullptr || !b->bounds || !aligned(b->bounds, 16)) return TKS_E_INVAL;

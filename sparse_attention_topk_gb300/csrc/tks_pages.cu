@@ -119,20 +119,52 @@ __device__ __forceinline__ Child child_of(const PlanParams& p, int i, unsigned* 
 
 // What a warp does at once: kSpan entries of one row, 32 at a time.
 constexpr int kSpan = 256;
+// Children that each thread block keeps in shared memory, looked up once (each look goes through three loads that wait for
+// each other: parent, length, entry).
+constexpr int kHeldChildren = 2048;
 
+// HELD: all children fit there.
+template <bool HELD>
 __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant__ PlanParams p) {
+  __shared__ struct {
+    int parent[kHeldChildren], have[kHeldChildren], need[kHeldChildren], tail[kHeldChildren], base[kHeldChildren];
+    int warps[kWarps];
+  } held;  // (tail: the entry that is going to be written to, or -1; later, the one that is copied)
   const Team me;
   unsigned bad = 0;
   grid_wait();
   grid_launch_dependents();
-  // who holds a page
+  // the entry that child c writes to, or -1
+  auto tail_of = [&](const Child& c) -> int {
+    const int e = c.writes ? __ldg(c.row + c.have - 1) : -1;
+    return (unsigned)e < (unsigned)p.pages ? e : -1;
+  };
+  // who holds a page: nobody yet
   for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = p.keep && p.keep[i] ? kShared : kFree;
+  if (HELD)
+    for (int i = threadIdx.x; i < p.children; i += kThreads) {
+      const Child c = child_of(p, i, me.rank == 0 ? &bad : nullptr);
+      held.parent[i] = c.have > 0 ? __ldg(p.parents + i) : 0;
+      held.have[i] = c.have;
+      held.need[i] = c.need;
+      held.tail[i] = tail_of(c);
+    }
+  auto child = [&](int i, int& tail, unsigned* bad) -> Child {
+    if (!HELD) {
+      const Child c = child_of(p, i, bad);
+      tail = tail_of(c);
+      return c;
+    }
+    tail = held.tail[i];
+    return Child{p.table + held.parent[i] * p.table_stride, held.have[i], held.need[i], tail >= 0};
+  };
   me.meet();
   const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
   const long long units = (long long)p.children * spans;
   for (long long u = me.warp; u < units; u += kAllWarps) {
     const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
-    const Child c = child_of(p, i, j0 == 0 ? &bad : nullptr);
+    int tail;
+    const Child c = child(i, tail, j0 == 0 ? &bad : nullptr);
     int e[kSpan / 32];
 #pragma unroll
     for (int k = 0; k < kSpan / 32; ++k) {
@@ -144,29 +176,60 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     for (int k = 0; k < kSpan / 32; ++k) {
       if ((unsigned)e[k] >= (unsigned)p.pages) continue;
       // (a held page's word only ever falls: to kShared, or to the lowest of those who write to it)
-      if (c.writes && j0 + 32 * k + me.lane == c.have - 1) atomicMin(p.owner + e[k], i);
+      if (tail >= 0 && j0 + 32 * k + me.lane == c.have - 1) atomicMin(p.owner + e[k], i);
       else p.owner[e[k]] = kShared;
     }
   }
   me.meet();
   // how many pages each child wants, and how many are free
   auto wants = [&](int i, bool& copied) -> int {
-    const Child c = child_of(p, i, nullptr);
-    copied = false;
-    if (c.writes) {
-      const int tail = __ldg(c.row + c.have - 1);
-      copied = (unsigned)tail < (unsigned)p.pages && __ldcg(p.owner + tail) != i;
-    }
+    int tail;
+    const Child c = child(i, tail, nullptr);
+    copied = tail >= 0 && __ldcg(p.owner + tail) != i;
     return c.need - c.have + (copied ? 1 : 0);
   };
-  int page0, page1, child0, child1;
+  int page0, page1, child0 = 0, child1 = 0;
   share(me, p.pages, page0, page1);
-  share(me, p.children, child0, child1);
   int free = 0, wanted = 0;
   for (int i = page0 + me.lane; i < page1; i += 32) free += __ldcg(p.owner + i) == kFree;
   bool copied;
-  for (int i = child0 + me.lane; i < child1; i += 32) wanted += wants(i, copied);
-  const Before before = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, free), __reduce_add_sync(0xffffffffu, wanted));
+  if (HELD) {
+    // every thread block for itself: the children's wishes before each child
+    int n[kHeldChildren / kThreads], sum = 0;
+#pragma unroll
+    for (int k = 0; k < kHeldChildren / kThreads; ++k) {
+      const int i = threadIdx.x * (kHeldChildren / kThreads) + k;
+      n[k] = 0;
+      if (i < p.children) {
+        n[k] = wants(i, copied);
+        if (!copied) held.tail[i] = -1;
+      }
+      sum += n[k];
+    }
+    int end = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (me.lane >= o) end += y;
+    }
+    if (me.lane == 31) held.warps[threadIdx.x >> 5] = end;
+    __syncthreads();
+    const int w = held.warps[me.lane], before = __reduce_add_sync(0xffffffffu, me.lane < (int)(threadIdx.x >> 5) ? w : 0);
+    wanted = __reduce_add_sync(0xffffffffu, w);
+    int at = before + end - sum;
+#pragma unroll
+    for (int k = 0; k < kHeldChildren / kThreads; ++k) {
+      const int i = threadIdx.x * (kHeldChildren / kThreads) + k;
+      if (i < p.children) held.base[i] = at;
+      at += n[k];
+    }
+  } else {
+    share(me, p.children, child0, child1);
+    for (int i = child0 + me.lane; i < child1; i += 32) wanted += wants(i, copied);
+    wanted = __reduce_add_sync(0xffffffffu, wanted);
+  }
+  Before before = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, free), wanted);
+  if (HELD) before.all_b = wanted;
   // the free pages that are wanted, in order; where each child's begin
   int at = before.a;
   const int most = min(before.all_a, before.all_b);
@@ -177,44 +240,49 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     if (is && rank < most) p.list[rank] = i + me.lane;
     at += __popc(m);
   }
-  at = before.b;
-  for (int i = child0; i < child1; i += 32) {
-    const int n = i + me.lane < child1 ? wants(i + me.lane, copied) : 0;
-    int end = n;
+  if (!HELD) {
+    at = before.b;
+    for (int i = child0; i < child1; i += 32) {
+      const int n = i + me.lane < child1 ? wants(i + me.lane, copied) : 0;
+      int end = n;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, end, o);
-      if (me.lane >= o) end += y;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, end, o);
+        if (me.lane >= o) end += y;
+      }
+      if (i + me.lane < child1) p.base[i + me.lane] = at + end - n;
+      at += __shfl_sync(0xffffffffu, end, 31);
     }
-    if (i + me.lane < child1) p.base[i + me.lane] = at + end - n;
-    at += __shfl_sync(0xffffffffu, end, 31);
   }
   me.meet();
   if (before.all_b > before.all_a) bad |= kStatNoPageBit;
   for (long long u = me.warp; u < units; u += kAllWarps) {
     const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
-    const Child c = child_of(p, i, nullptr);
-    const int base = __ldcg(p.base + i);
-    bool copy;
-    const int n = wants(i, copy);
-    const int extra = n - (c.need - c.have);
+    int tail;
+    const Child c = child(i, tail, nullptr);
+    const int base = HELD ? held.base[i] : __ldcg(p.base + i);
+    const bool copy = HELD ? tail >= 0 : tail >= 0 && __ldcg(p.owner + tail) != i;
     int32_t* to = p.out + (long long)i * p.table_pages;
+    int e[kSpan / 32];
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      e[k] = j < c.have ? __ldg(c.row + j) : -1;
+    }
 #pragma unroll
     for (int k = 0; k < kSpan / 32; ++k) {
       const int j = j0 + 32 * k + me.lane;
       if (j >= p.table_pages) continue;
-      int e = -1;
-      if (j < c.have) e = __ldg(c.row + j);
       if ((copy && j == c.have - 1) || (j >= c.have && j < c.need)) {
-        const int rank = base + (j < c.have ? 0 : extra + j - c.have);
+        const int rank = base + (j < c.have ? 0 : (copy ? 1 : 0) + j - c.have);
         const int got = rank < most ? __ldcg(p.list + rank) : -1;
         if (j < c.have) {
-          p.src[i] = got < 0 ? -1 : e;
+          p.src[i] = got < 0 ? -1 : e[k];
           p.dst[i] = got;
         }
-        e = got;
+        e[k] = got;
       }
-      to[j] = e;
+      to[j] = e[k];
     }
     if (!copy && j0 == 0 && me.lane == 0) p.src[i] = p.dst[i] = -1;
   }
@@ -460,7 +528,8 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
   p.children = children;
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
-  if (launch_plan(fork_kernel, p, (cudaStream_t)stream) != cudaSuccess) {
+  const bool fit = children <= kHeldChildren;
+  if ((fit ? launch_plan(fork_kernel<true>, p, (cudaStream_t)stream) : launch_plan(fork_kernel<false>, p, (cudaStream_t)stream)) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
   }

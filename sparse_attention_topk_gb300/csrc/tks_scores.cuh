@@ -64,6 +64,8 @@ __device__ __forceinline__ const __nv_bfloat16* score_query(const ScoreParams& p
   return p.q + b * p.q_batch + t * p.q_token + ((long long)head * p.group_all + p.first_of_group + g) * p.q_head;
 }
 
+cudaError_t setup_scores();  // the kernel for few query rows (tks_blocks.cu)
+
 // The kernel for many query rows (tks_scores_tiles.cu).
 constexpr int kScoreTileRows = 256;  // query rows of a tile, in two halves
 constexpr int kScoreTileBlocks = 128;

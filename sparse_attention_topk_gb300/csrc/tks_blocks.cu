@@ -121,11 +121,11 @@ struct Extent<false> {
   }
 };
 
-constexpr int kBoundsThreads = 256;
+constexpr int kBoundsThreads = 128, kBoundsPerSm = 7;
 
 // An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time.
 template <int D, bool I8>
-__global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_constant__ BoundsParams p) {
+__global__ void __launch_bounds__(kBoundsThreads, kBoundsPerSm) bounds_kernel(const __grid_constant__ BoundsParams p) {
   constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 8;
   __shared__ long long upto[kBoundsThreads];  // blocks of the sequences up to and with this one
   __shared__ int first_s[kBoundsThreads], end_s[kBoundsThreads];
@@ -242,8 +242,8 @@ struct ScoreShape {
   static_assert(16 * (kScoreCols + 1) * 4 <= kWarp, "a warp's scores fit where its bounds were");
 };
 
-// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and 128 blocks at
-// a time, a warp 32 of them, whose copies to shared memory are all under way at once, and start before the queries and
+// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and 128 blocks,
+// a warp 32 of them, whose copies to shared memory are all under way at once, and start before the queries and
 // lengths are there. The query rows lie in shared memory as matrix fragments: of product step s, lane 4n + c takes the
 // elements that it has of column n's bytes: pieces c, c + 4, ... (XOR-swizzled, so that eight lanes' reads do not meet).
 template <int D>
@@ -264,97 +264,325 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   grid_wait();
   grid_launch_dependents();
 
-  bool bad = false, ready = false;
-  int seen = 0, most = 0;
-  for (long long j0 = ((long long)chunk * kScoreWarps + warp) * kScoreCols;; j0 += (long long)p.chunks * kScoreThreads) {
-    const bool any = j0 < p.n;
-    const int col = (int)j0 + lane;
-    const int page = any && col < p.n ? __ldg(table + (col >> p.of_page_shift)) : -1;
-    if (!ready) {
-      // the tokens' lengths, a lane each (16 at most), and the query rows
-      if (lane < p.tokens) seen = blocks_seen(p, b, lane, bad);
-      for (int x = threadIdx.x; x < S::kSteps * 32; x += kScoreThreads) {
-        const int l = x & 31, s = x >> 5, r = l >> 2;
-        // elements of the doubled index: the first D are the least's, with the queries' negative parts
-        const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) {
-          const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
-          w.x = part_of_pair(y.x, d >= D);
-          w.z = part_of_pair(y.y, d >= D);
-        }
-        if (r + 8 < rows) {
-          const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
-          w.y = part_of_pair(y.x, d >= D);
-          w.w = part_of_pair(y.y, d >= D);
-        }
-        qs[x] = w;
-      }
-      most = __reduce_max_sync(0xffffffffu, seen);
+  const long long j0 = ((long long)chunk * kScoreWarps + warp) * kScoreCols;
+  const int col = (int)j0 + lane;
+  const int page = j0 < p.n && col < p.n ? __ldg(table + (col >> p.of_page_shift)) : -1;
+  // the tokens' lengths, a lane each (16 at most), and the query rows
+  bool bad = false;
+  const int seen = lane < p.tokens ? blocks_seen(p, b, lane, bad) : 0;
+  for (int x = threadIdx.x; x < S::kSteps * 32; x += kScoreThreads) {
+    const int l = x & 31, s = x >> 5, r = l >> 2;
+    // elements of the doubled index: the first D are the least's, with the queries' negative parts
+    const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
+      w.x = part_of_pair(y.x, d >= D);
+      w.z = part_of_pair(y.y, d >= D);
     }
-    const bool ok = (unsigned)page < (unsigned)p.pages;
-    if (any && j0 < most) {
-      if (!ok && col < most) report(p.status, kStatIndexBit);
-      const long long at = ok && col < most ? (((long long)page << p.of_page_shift) + (col & ((1 << p.of_page_shift) - 1))) * p.kv_heads + head : -1;
-      const uint32_t to = smem_addr(mine) + row0 * S::kRow;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-#pragma unroll
-        for (int i = 0; i < 8 / kPer; ++i) {
-          const int r = 8 * t + i * kPer + row0;  // the column; its pieces lie swizzled
-          const long long of = __shfl_sync(0xffffffffu, at, r);
-          cp16(to + (8 * t + i * kPer) * S::kRow + ((piece ^ ((r & 1) << 2)) << 4), reinterpret_cast<const unsigned char*>(p.bounds) + (of < 0 ? 0 : of * S::kRow) + piece * 16,
-               of < 0 ? 0 : 16);
-        }
-        cp_commit();
-      }
+    if (r + 8 < rows) {
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
+      w.y = part_of_pair(y.x, d >= D);
+      w.w = part_of_pair(y.y, d >= D);
     }
-    if (!ready) {
-      if (warp == 0 && chunk == 0) {
-        if (bad) report(p.status, kStatRowLenBit);
-        if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = seen;
+    qs[x] = w;
+  }
+  const int most = __reduce_max_sync(0xffffffffu, seen);
+  const bool ok = (unsigned)page < (unsigned)p.pages;
+  if (j0 < most) {
+    if (!ok && col < most) report(p.status, kStatIndexBit);
+    const long long at = ok && col < most ? (((long long)page << p.of_page_shift) + (col & ((1 << p.of_page_shift) - 1))) * p.kv_heads + head : -1;
+    const uint32_t to = smem_addr(mine) + row0 * S::kRow;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8 / kPer; ++i) {
+        const int r = 8 * t + i * kPer + row0;  // the column; its pieces lie swizzled
+        const long long of = __shfl_sync(0xffffffffu, at, r);
+        cp16(to + (8 * t + i * kPer) * S::kRow + ((piece ^ ((r & 1) << 2)) << 4),
+             reinterpret_cast<const unsigned char*>(p.bounds) + (of < 0 ? 0 : of * S::kRow) + piece * 16, of < 0 ? 0 : 16);
       }
-      __syncthreads();
-      ready = true;
+      cp_commit();
     }
-    if (!any) break;  // (every warp has come to the barrier)
-    if (j0 < most) {
-      float acc[4][4];
-      auto columns = [&](int t) {
-        __syncwarp();
-        acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
-        const unsigned char* row = mine + (8 * t + n) * S::kRow;
-#pragma unroll
-        for (int i = 0; i < S::kPieces / 4; ++i) {
-          const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + 4 * i) ^ ((n & 1) << 2)) << 4));
-          mma_bf16(acc[t], qs[2 * i * 32 + lane], w.x, w.y);
-          mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w.z, w.w);
-        }
-      };
-      cp_wait<3>();
-      columns(0);
-      cp_wait<2>();
-      columns(1);
-      cp_wait<1>();
-      columns(2);
-      cp_wait<0>();
-      columns(3);
-      __syncwarp();  // (scores go where the bounds were)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tile[n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
+  }
+  if (warp == 0 && chunk == 0) {
+    if (bad) report(p.status, kStatRowLenBit);
+    if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = seen;
+  }
+  __syncthreads();
+  if (j0 < most) {
+    float acc[4][4];
+    auto columns = [&](int t) {
       __syncwarp();
-    }
-    for (int t = 0; t < p.tokens; ++t) {
-      const int blocks = __shfl_sync(0xffffffffu, seen, t);
-      float x = -INFINITY;
-      if (j0 < most)
-        for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile[r][lane]);
-      if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, blocks);
-    }
+      acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
+      const unsigned char* row = mine + (8 * t + n) * S::kRow;
+#pragma unroll
+      for (int i = 0; i < S::kPieces / 4; ++i) {
+        const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + 4 * i) ^ ((n & 1) << 2)) << 4));
+        mma_bf16(acc[t], qs[2 * i * 32 + lane], w.x, w.y);
+        mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w.z, w.w);
+      }
+    };
+    cp_wait<3>();
+    columns(0);
+    cp_wait<2>();
+    columns(1);
+    cp_wait<1>();
+    columns(2);
+    cp_wait<0>();
+    columns(3);
+    __syncwarp();  // (scores go where the bounds were)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[n + 8 * (e >> 1)][8 * t + 2 * c + (e & 1)] = acc[t][e];
     __syncwarp();
   }
+  if (j0 >= p.n) return;
+  for (int t = 0; t < p.tokens; ++t) {
+    const int blocks = __shfl_sync(0xffffffffu, seen, t);
+    float x = -INFINITY;
+    if (j0 < most)
+      for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile[r][lane]);
+    if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, blocks);
+  }
+}
+
+// The same for more blocks than the device scores at once: every warp takes an equal run of the axis of all (sequence,
+// head)s' groups of eight blocks that any token sees, brings them through a ring of its own, and keeps the query rows of the
+// (sequence, head) that it is at in registers, so that warps wait for nobody.
+constexpr int kStreamWarps = 16, kStreamThreads = kStreamWarps * 32, kStreamCounted = 1024;
+template <int D>
+struct StreamShape {
+  static constexpr int kRow = 4 * D, kGroup = 8 * kRow, kPieces = kRow / 16, kSteps = 2 * D / 16;
+  static constexpr int kDepth = D == 128 ? 3 : 6;
+  static constexpr int kRing = kDepth * kGroup, kTile = 16 * 9 * 4;
+  static constexpr int kSmem = kStreamWarps * (kRing + kTile);
+};
+
+// A warp's run, piece by piece: groups g0 .. g1 - 1 of a (sequence, head).
+struct Piece {
+  int b, head, g0, g1;
+};
+struct Pieces {
+  long long at, end;
+  int b;
+  __device__ __forceinline__ bool next(const ScoreParams& p, const int* upto, Piece& x) {
+    if (at >= end) return false;
+    const bool counted = p.batch <= kStreamCounted;
+    const int all = (p.n + 7) / 8;
+    if (!counted) {
+      b = (int)(at / ((long long)all * p.kv_heads));
+    } else {
+      while ((long long)upto[b + 1] * p.kv_heads <= at) ++b;
+    }
+    const long long before = counted ? upto[b] : (long long)all * b;
+    const int mine = counted ? upto[b + 1] - upto[b] : all;
+    const long long in = at - before * p.kv_heads;
+    x.b = b;
+    x.head = (int)(in / mine);
+    x.g0 = (int)(in - (long long)x.head * mine);
+    x.g1 = (int)min((long long)mine, x.g0 + end - at);
+    at += x.g1 - x.g0;
+    return true;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kStreamThreads, 1) scores_stream_kernel(const __grid_constant__ ScoreParams p) {
+  using S = StreamShape<D>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int upto[kStreamCounted + 1];  // groups of the sequences before this one, each counted for one head
+  __shared__ int warps_s[kStreamWarps];
+  __shared__ unsigned there_s[kStreamWarps][S::kDepth];  // which of a group's blocks lie in a page of the cache
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+  unsigned char* ring = smem + warp * S::kRing;
+  float(*tile)[9] = reinterpret_cast<float(*)[9]>(smem + kStreamWarps * S::kRing + warp * S::kTile);
+  constexpr int kPer = 32 / S::kPieces > 0 ? 32 / S::kPieces : 1;
+  const int piece = lane % S::kPieces, row0 = lane / S::kPieces, rows = p.tokens * p.group, all = (p.n + 7) / 8;
+  const bool counted = p.batch <= kStreamCounted;
+  grid_wait();
+  grid_launch_dependents();
+
+  if (counted) {
+    int sum = 0, mine[kStreamCounted / kStreamThreads];
+#pragma unroll
+    for (int i = 0; i < kStreamCounted / kStreamThreads; ++i) {
+      const int b = threadIdx.x * (kStreamCounted / kStreamThreads) + i;
+      int most = 0;
+      bool bad = false;
+      if (b < p.batch)
+        for (int t = 0; t < p.tokens; ++t) most = max(most, blocks_seen(p, b, t, bad));
+      mine[i] = (most + 7) / 8;
+      sum += mine[i];
+    }
+    int end = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += y;
+    }
+    if (lane == 31) warps_s[warp] = end;
+    __syncthreads();
+    int at = end - sum;
+    for (int i = 0; i < warp; ++i) at += warps_s[i];
+    if (threadIdx.x == 0) upto[0] = 0;
+#pragma unroll
+    for (int i = 0; i < kStreamCounted / kStreamThreads; ++i) {
+      at += mine[i];
+      upto[threadIdx.x * (kStreamCounted / kStreamThreads) + i + 1] = at;
+    }
+    __syncthreads();
+  }
+
+  const long long work = (counted ? (long long)upto[kStreamCounted] : (long long)all * p.batch) * p.kv_heads;
+  const int warps = gridDim.x * kStreamWarps, me = warp * gridDim.x + blockIdx.x;
+  Pieces copies;
+  copies.at = work / warps * me + min((long long)me, work % warps);
+  copies.end = copies.at + work / warps + (me < work % warps ? 1 : 0);
+  copies.b = 0;
+  if (counted && copies.at < copies.end) {  // the first one's sequence: the last with upto * heads <= at
+    int low = 0;
+#pragma unroll
+    for (int step = kStreamCounted / 2; step; step >>= 1)
+      if ((long long)upto[low + step] * p.kv_heads <= copies.at) low += step;
+    copies.b = low;
+  }
+  Pieces scored = copies;
+  int groups = (int)(copies.end - copies.at);
+
+  // ---- copies, a group at a time; blocks are looked up 32 at once, and their pages 32 ahead
+  Piece from{0, 0, 0, 0};
+  const int32_t* table = nullptr;
+  int base = 0, page = -1, most = 0, slot = 0;
+  long long place = -1;
+  bool more = true;
+  auto page_of = [&](int col) -> int { return col < most ? __ldg(table + (col >> p.of_page_shift)) : -1; };
+  auto issue = [&] {
+    if (more && from.g0 == from.g1) {
+      more = copies.next(p, upto, from);
+      if (more) {
+        table = p.table + from.b * p.table_stride;
+        // (the columns of the piece's groups: those that no token sees are masked when they are written)
+        most = (int)min((long long)p.n, 8LL * from.g1);
+        base = 8 * from.g0 - 32;
+        page = page_of(base + 32 + lane);
+      }
+    }
+    if (more) {
+      if (8 * from.g0 == base + 32) {
+        base += 32;
+        const int col = base + lane;
+        place = (unsigned)page < (unsigned)p.pages
+                    ? (((long long)page << p.of_page_shift) + (col & ((1 << p.of_page_shift) - 1))) * p.kv_heads + from.head : -1;
+        page = page_of(col + 32);
+      }
+      const int in = 8 * from.g0 - base;
+      const uint32_t to = smem_addr(ring) + slot * S::kGroup + row0 * S::kRow;
+#pragma unroll
+      for (int i = 0; i < 8 / kPer; ++i) {
+        const int r = i * kPer + row0;
+        const long long of = __shfl_sync(0xffffffffu, place, in + r);
+        cp16(to + i * kPer * S::kRow + ((piece ^ ((r & 1) << 2)) << 4), reinterpret_cast<const unsigned char*>(p.bounds) + (of < 0 ? 0 : of * S::kRow) + piece * 16,
+             of < 0 ? 0 : 16);
+      }
+      const unsigned there = __ballot_sync(0xffffffffu, place >= 0) >> in & 0xffu;
+      if (lane == 0) there_s[warp][slot] = there;
+      ++from.g0;
+      slot = slot + 1 == S::kDepth ? 0 : slot + 1;
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < S::kDepth - 1; ++i) issue();
+
+  // ---- scores
+  Piece at{0, 0, 0, 0};
+  uint4 a[S::kSteps];
+  int seen = 0, stage = 0;
+  float* out = nullptr;
+  for (; groups > 0; --groups) {
+    if (at.g0 == at.g1) {
+      scored.next(p, upto, at);
+      bool bad = false;
+      seen = lane < p.tokens ? blocks_seen(p, at.b, lane, bad) : 0;
+      auto row = [&](int r) { return score_query(p, at.b, r / p.group, at.head, r % p.group); };
+      const __nv_bfloat16 *q0 = row(n < rows ? n : 0), *q1 = row(n + 8 < rows ? n + 8 : 0);
+#pragma unroll
+      for (int s = 0; s < S::kSteps / 2; ++s) {  // the same elements of the least's and of the largest's half
+        const int d = 8 * (c + 4 * (s >> 1)) + 4 * (s & 1);
+        const uint2 x = n < rows ? __ldg(reinterpret_cast<const uint2*>(q0 + d)) : make_uint2(0u, 0u);
+        const uint2 y = n + 8 < rows ? __ldg(reinterpret_cast<const uint2*>(q1 + d)) : make_uint2(0u, 0u);
+        a[s] = make_uint4(part_of_pair(x.x, false), part_of_pair(y.x, false), part_of_pair(x.y, false), part_of_pair(y.y, false));
+        a[s + S::kSteps / 2] = make_uint4(part_of_pair(x.x, true), part_of_pair(y.x, true), part_of_pair(x.y, true), part_of_pair(y.y, true));
+      }
+      out = p.out + ((long long)at.b * p.tokens * p.kv_heads + at.head) * p.n;
+    }
+    cp_wait<S::kDepth - 2>();
+    __syncwarp();
+    issue();  // (where the group before was)
+    float acc[2][4] = {};
+    const unsigned char* row = ring + stage * S::kGroup + n * S::kRow;
+#pragma unroll
+    for (int i = 0; i < S::kPieces / 4; ++i) {
+      const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + 4 * i) ^ ((n & 1) << 2)) << 4));
+      mma_bf16(acc[0], a[2 * i], w.x, w.y);
+      mma_bf16(acc[1], a[2 * i + 1], w.z, w.w);
+    }
+    const unsigned there = there_s[warp][stage];
+    stage = stage + 1 == S::kDepth ? 0 : stage + 1;
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = acc[0][e] + acc[1][e];
+    const int col0 = 8 * at.g0++;
+    if (p.tokens == 1) {
+      float v[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        v[e] = n < rows ? x[e] : -INFINITY;
+        if (n + 8 < rows) v[e] = max_nan(v[e], x[2 + e]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) v[e] = max_nan(v[e], __shfl_xor_sync(0xffffffffu, v[e], o));
+      }
+      const float v0 = __shfl_sync(0xffffffffu, v[0], lane >> 1), v1 = __shfl_sync(0xffffffffu, v[1], lane >> 1);
+      const int blocks = __shfl_sync(0xffffffffu, seen, 0), col = col0 + lane;
+      if (lane < 8 && col < p.n) {
+        const bool ok = there >> lane & 1u;
+        if (!ok && col < blocks) report(p.status, kStatIndexBit);
+        out[col] = ok ? final_score(p, lane & 1 ? v1 : v0, col, blocks) : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile[n + 8 * (e >> 1)][2 * c + (e & 1)] = x[e];
+      __syncwarp();
+      for (int i = lane; i < (p.tokens * 8 + 31) / 32 * 32; i += 32) {
+        const int t = i >> 3, col = col0 + (i & 7);
+        const int blocks = __shfl_sync(0xffffffffu, seen, t & 31);
+        if (t < p.tokens && col < p.n) {
+          float y = -INFINITY;
+          for (int r = t * p.group; r < (t + 1) * p.group; ++r) y = max_nan(y, tile[r][i & 7]);
+          const bool ok = there >> (i & 7) & 1u;
+          if (!ok && col < blocks) report(p.status, kStatIndexBit);
+          out[(long long)t * p.kv_heads * p.n + col] = ok ? final_score(p, y, col, blocks) : -INFINITY;
+        }
+      }
+    }
+  }
+  cp_wait<0>();
+
+  // ---- the rows' lengths, a lane each, and the groups that no token of a sequence sees, a row each warp
+  const int out_rows = p.batch * p.tokens * p.kv_heads;
+  for (long long r = me * 32LL + lane; r < out_rows; r += warps * 32LL) {
+    const int bt = (int)r / p.kv_heads, b = bt / p.tokens;
+    bool bad = false;
+    const int blocks = blocks_seen(p, b, bt - b * p.tokens, bad);
+    if (bad) report(p.status, kStatRowLenBit);
+    if (p.row_len) p.row_len[r] = blocks;
+  }
+  if (counted && upto[kStreamCounted] < (long long)all * p.batch)
+    for (long long r = me; r < out_rows; r += warps) {
+      const int b = (int)r / p.kv_heads / p.tokens;
+      for (long long j = 8LL * (upto[b + 1] - upto[b]) + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
+    }
 }
 
 void with_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a) {
@@ -387,11 +615,25 @@ cudaError_t launch_scores(const ScoreParams& p, int grid, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, scores_kernel<D>, p);
 }
 
+template <int D>
+cudaError_t launch_scores_stream(const ScoreParams& p, int grid, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute a[1] = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kStreamThreads);
+  cfg.dynamicSmemBytes = StreamShape<D>::kSmem;
+  cfg.stream = stream;
+  with_pdl(cfg, a);
+  return cudaLaunchKernelEx(&cfg, scores_stream_kernel<D>, p);
+}
+
 }  // namespace
 
 cudaError_t setup_scores() {
-  const cudaError_t e = allow(scores_kernel<64>, ScoreShape<64>::kSmem);
-  return e != cudaSuccess ? e : allow(scores_kernel<128>, ScoreShape<128>::kSmem);
+  cudaError_t e = allow(scores_kernel<64>, ScoreShape<64>::kSmem);
+  if (e == cudaSuccess) e = allow(scores_kernel<128>, ScoreShape<128>::kSmem);
+  if (e == cudaSuccess) e = allow(scores_stream_kernel<64>, StreamShape<64>::kSmem);
+  return e != cudaSuccess ? e : allow(scores_stream_kernel<128>, StreamShape<128>::kSmem);
 }
 
 int check_bounds(const tks_bounds* b) {
@@ -446,7 +688,7 @@ extern "C" int tks_cache_bounds(const tks_cache* cache, const tks_bounds* bounds
   p.status = place.status;
   // as many blocks as there may be items for, and no more than the device holds at once
   const __int128 items = (__int128)batch * std::max(1, table_pages) * (bounds->page_size / bounds->block) * cache->kv_heads;
-  const int grid = (int)std::min<__int128>(items, place.sms * 4);
+  const int grid = (int)std::min<__int128>(items, place.sms * kBoundsPerSm);
   std::lock_guard<std::mutex> lock(*place.order);
   const cudaError_t e = cache->head_dim == 64 ? launch_bounds<64>(p, i8, grid, (cudaStream_t)stream) : launch_bounds<128>(p, i8, grid, (cudaStream_t)stream);
   if (e != cudaSuccess) {
@@ -463,7 +705,7 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
   if (first < 0 || last < 0 || n < 0 || n > (int64_t)queries->table_pages * of_page) return TKS_E_INVAL;
   if (queries->batch == 0 || queries->tokens == 0) return TKS_OK;
   if (!aligned(kv_len, 4) || !aligned(row_len, 4) || !aligned(scores, 4) || (n > 0 && !scores)) return TKS_E_INVAL;
-  if ((int64_t)queries->batch * queries->tokens * bounds->kv_heads > INT32_MAX) return TKS_E_TOO_LARGE;
+  if ((int64_t)queries->batch * queries->tokens * bounds->kv_heads > INT32_MAX || (int64_t)queries->batch * (n / 8 + 1) > INT32_MAX) return TKS_E_TOO_LARGE;
   Place place;
   const int rc = place_of(stream, &place);
   if (rc != TKS_OK) return rc;
@@ -495,11 +737,14 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
   cudaError_t e = cudaSuccess;
   std::lock_guard<std::mutex> lock(*place.order);
   if ((int64_t)p.tokens * p.group <= 16) {
-    const int64_t units = (int64_t)p.batch * p.kv_heads;
-    const int64_t most = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads);
-    p.chunks = (int)std::min<int64_t>(most, std::max<int64_t>(1, place.sms * 16 / units));
-    if (units * p.chunks > INT32_MAX) return TKS_E_TOO_LARGE;
-    e = bounds->head_dim == 64 ? launch_scores<64>(p, (int)(units * p.chunks), s) : launch_scores<128>(p, (int)(units * p.chunks), s);
+    const int64_t units = (int64_t)p.batch * p.kv_heads, tiles = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads);
+    const bool wide = bounds->head_dim == 128;
+    if (units * tiles <= place.sms * 3) {
+      p.chunks = (int)tiles;
+      e = wide ? launch_scores<128>(p, (int)(units * tiles), s) : launch_scores<64>(p, (int)(units * tiles), s);
+    } else {
+      e = wide ? launch_scores_stream<128>(p, place.sms, s) : launch_scores_stream<64>(p, place.sms, s);
+    }
   } else {
     // (134 MB of scores, stored as what is not read again soon: 58 us, 63 without; fewer stay for the selector)
     p.stream_out = (int64_t)p.batch * p.tokens * p.kv_heads * n > (64 << 20) / 4;

@@ -629,3 +629,82 @@ def test_refusals():
     for bad in (dict(block="8"), dict(first=1.5), dict(n=2.0)):
         with pytest.raises(TypeError):
             tks.block_scores(**{**good_s, **bad})
+
+
+# ---------------------------------------------------------------------------
+# More blocks than the device scores at once (decode steps of batches)
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("tokens, q_heads, kv_heads", [(1, 8, 1), (1, 32, 2), (1, 17, 1), (3, 10, 2), (16, 2, 2), (2, 16, 2)])
+def test_scores_of_ragged_batches(tokens, q_heads, kv_heads, dim):
+    g = gen(tokens + dim)
+    batch, of_page, width = 70, 4, 300
+    bounds = torch.randn(500, of_page, kv_heads, 2, dim, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(batch, tokens, q_heads, dim, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(500, (batch, width), device="cuda", generator=g).to(torch.int32)
+    lens = torch.randint(0, width * of_page * 8 + 1, (batch, tokens), device="cuda", generator=g)
+    lens[3], lens[4], lens[5], lens[-1] = 0, 1, width * of_page * 8, 64
+    lens = lens.to(torch.int32)
+    for first, last, n in ((0, 0, None), (2, 1, 1001)):
+        cut = lens if n is None else lens.clamp(max=8 * n)
+        scores, seen = tks.block_scores(q, bounds, table, cut, 8, first=first, last=last, n=n)
+        columns = width * of_page if n is None else n
+        count = (cut + 7) // 8
+        assert torch.equal(seen, count.unsqueeze(-1).expand(-1, -1, kv_heads))
+        group = q_heads // kv_heads
+        j = torch.arange(columns, device="cuda")
+        for b in (0, 3, 4, 5, 33, 69):
+            mine = bounds[table[b][j // of_page].long(), j % of_page].double()
+            for h in range(kv_heads):
+                x = q[b, :, h * group : (h + 1) * group].double()
+                lo, hi = mine[:, h, 0], mine[:, h, 1]
+                want = (x.clamp(min=0) @ hi.T + x.clamp(max=0) @ lo.T).amax(1)
+                size = (x.abs() @ torch.maximum(lo.abs(), hi.abs()).T).amax(1)
+                vis = j < count[b].unsqueeze(1)
+                forced = vis & ((j < first) | (j >= count[b].unsqueeze(1) - last))
+                got = scores[b, :, h]
+                assert (got[~vis] == -math.inf).all() and (got[forced] == math.inf).all()
+                plain = vis & ~forced
+                assert ((got.double() - want).abs() <= 2 * dim * 2.0 ** -23 * size)[plain].all()
+
+
+def test_scores_of_more_sequences_than_are_counted():
+    g = gen(21)
+    bounds = torch.randn(90, 2, 1, 2, 64, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(1500, 1, 4, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(90, (1500, 60), device="cuda", generator=g).to(torch.int32)
+    lens = torch.randint(0, 961, (1500, 1), device="cuda", generator=g).to(torch.int32)
+    many, seen = tks.block_scores(q, bounds, table, lens, 8)
+    for at in range(0, 1500, 20):  # a few at a time, by the other kernel
+        few, n = tks.block_scores(q[at : at + 20], bounds, table[at : at + 20], lens[at : at + 20], 8)
+        assert torch.equal(seen[at : at + 20], n)
+        a, b = many[at : at + 20], few
+        assert torch.equal(a == -math.inf, b == -math.inf) and ((a - b).abs() <= 1e-4)[a != -math.inf].all()
+
+
+def test_wrong_pages_and_numbers_among_many():
+    g = gen(22)
+    bounds = torch.randn(100, 2, 2, 2, 64, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(40, 1, 8, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(1, 100, (40, 900), device="cuda", generator=g).to(torch.int32)
+    lens = torch.full((40, 1), 14400, dtype=torch.int32, device="cuda")
+    good, _ = tks.block_scores(q, bounds, table, lens, 8)
+    wrong = table.clone()
+    wrong[7, 450], wrong[9, 0], wrong[11, 899] = 100, -1, 2 ** 31 - 1
+    got, _ = tks.block_scores(q, bounds, wrong, lens, 8)
+    assert tks.device_status() == tks.TKS_E_INDEX
+    bad = torch.zeros(40, 900, dtype=torch.bool, device="cuda")
+    bad[7, 450] = bad[9, 0] = bad[11, 899] = True
+    bad = bad.repeat_interleave(2, 1)[:, None, None].expand_as(good)
+    assert (got[bad] == -math.inf).all() and torch.equal(got[~bad], good[~bad])
+    bounds[0, 1, 1, 0, 5] = math.nan
+    wrong[7, 450] = 0
+    wrong[9, 0], wrong[11, 899] = table[9, 0], table[11, 899]
+    got, _ = tks.block_scores(q, bounds, wrong, lens, 8)
+    assert got[7, 0, 1, 901] == math.inf and got.isinf().sum() == 1
+    many = lens.clone()
+    many[3] = 14401
+    got, seen = tks.block_scores(q, bounds, table, many, 8)
+    assert tks.device_status() == tks.TKS_E_ROW_LEN and torch.equal(got, good) and (seen == 1800).all()

@@ -113,9 +113,10 @@ int tks_block_scores(const tks_bounds *bounds, const tks_queries *queries, const
 int tks_block_attention(const tks_cache *cache, const tks_queries *queries, const int32_t *blocks,
                         int32_t n, int32_t block, const int32_t *kv_len, void *stream);
 
-/* Elements of the scratch buffer of a page call (int32, device; what it holds
- * before the call does not matter; calls that may run at the same time need one each). */
-#define TKS_PAGES_SCRATCH(pages, rows) (2 * (int64_t)(pages) + (int64_t)(rows) + 1024)
+/* Elements of the scratch buffer of a page call (int32, device, 16-byte aligned; what
+ * it holds before the call does not matter; calls that may run at the same time need
+ * one each). */
+#define TKS_PAGES_SCRATCH(pages, rows) (2 * (int64_t)(pages) + (int64_t)(rows) + 1056)
 
 /*
  * tks_cache_fork - the page tables of the next step's sequences, each a

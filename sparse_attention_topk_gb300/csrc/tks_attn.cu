@@ -222,7 +222,7 @@ Key key_of(int dev, void* stream) {
 std::map<Key, Workspace> g_ws;
 
 size_t part_bytes(const Device& d) {
-  const size_t few = (size_t)d.sms * std::max(kRowsBlocksPerSm, kRowsBlocksPerSmOfBlocks) * 2 * kPartFloats<kRowsTile, 128>;
+  const size_t few = (size_t)d.sms * std::max(kRowsBlocksPerSm, kRowsManyPerSm) * 2 * kPartFloats<kRowsTile, 128>;
   const size_t many = (size_t)d.sms * 2 * kPartFloats<kTilesRows, 128>;
   return (few > many ? few : many) * sizeof(float);
 }
@@ -339,7 +339,7 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   if ((keys / tile_keys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
   const long long units = (long long)p.seqs * p.kv_heads * p.row_tiles;
   if (units > INT32_MAX) return TKS_E_TOO_LARGE;
-  int grid = !few ? d.sms : d.sms * (selected && p.block_shift && blocks_by_chunks(p, i8) ? kRowsBlocksPerSmOfBlocks : kRowsBlocksPerSm);
+  int grid = !few ? d.sms : d.sms * (selected && rows_many(p, i8) ? kRowsManyPerSm : kRowsBlocksPerSm);
   p.plan = reinterpret_cast<Split*>(ws.ptr + kPlanOffset);
   if (selected) {
     const long long tiles = std::max(1, (p.k_sel + tile_keys - 1) / tile_keys);

@@ -121,11 +121,18 @@ constexpr int kClusterMax = 8;
 constexpr int kRowsTile = 16;  // query rows of a block
 constexpr int kRowsKeys = 64;  // keys of a tile
 constexpr int kRowsBlocksPerSm = 2;
-constexpr int kRowsBlocksPerSmOfBlocks = 3;  // lists of blocks
 // Whether a list's blocks, and the pages, are at least as long as the chunks (32 keys of int8, 16 of bfloat16) that warps take.
 inline bool blocks_by_chunks(const Params& p, bool i8) {
   const int chunk = i8 ? 5 : 4;
   return p.block_shift >= chunk && p.page_shift >= chunk;
+}
+// Lists of bfloat16 blocks that together are longer than the sequence come from L2, which answers sooner than memory: more
+// warps with less under way each (512 tokens of 64 heads on 4 over 32 blocks of 64: 233 us so, 260 otherwise). Of memory, or
+// in 8 bits, they do not help (64 tokens over 64 blocks of int8 of 8 heads: 156 us so, 125 otherwise; the former in int8 212
+// and 215).
+constexpr int kRowsManyPerSm = 3;
+inline bool rows_many(const Params& p, bool i8) {
+  return !i8 && blocks_by_chunks(p, i8) && (long long)p.tokens * p.k_sel >= (long long)p.table_pages << p.page_shift;
 }
 cudaError_t setup_rows();
 cudaError_t launch_rows(const Params& p, int head_dim, bool i8, bool selected, int grid,

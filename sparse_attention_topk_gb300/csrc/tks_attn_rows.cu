@@ -53,7 +53,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 
-template <int D, bool I8, bool BLOCKS = false>
+// BLOCKS: lists of blocks. MANY: and three thread blocks an SM, of two stages, instead of two of three.
+template <int D, bool I8, bool BLOCKS = false, bool MANY = false>
 struct Shape {
   static constexpr int kElem = I8 ? 1 : 2;
   static constexpr int kRow = D * kElem;               // bytes of a row
@@ -66,13 +67,13 @@ struct Shape {
   static constexpr int kOps = 2 * kChunk * kRow;       // keys, then values
   static constexpr int kScales = I8 ? kChunk * 8 : 0;
   static constexpr int kStage = kOps + kScales + 16;   // and the mask of valid keys
-  static constexpr int kStages = BLOCKS ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 5;
+  static constexpr int kStages = MANY ? (D == 128 ? 2 : 4) : D == 128 ? 3 : 5;
   static constexpr int kQs = D / 16 * 32 * 16;         // query fragments, behind the rings
   static constexpr int kConst = I8 ? kWarps * 32 * 16 : 0;  // and each warp's scales as they are used
   static constexpr int kRings = kWarps * kStages * kStage;
   static constexpr int kSlots = BLOCKS ? 256 * 4 : 1024 * 4;  // and where keys lie (of a list of blocks: where chunks begin)
   static constexpr int kSmem = kRings + kQs + kConst + kSlots;
-  static constexpr int kPerSm = BLOCKS ? kRowsBlocksPerSmOfBlocks : kRowsBlocksPerSm;
+  static constexpr int kPerSm = MANY ? kRowsManyPerSm : kRowsBlocksPerSm;
   static_assert(kRings >= (kWarps + 1) * (16 * D * 4 + 16 * 8), "the merge fits the ring");
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
@@ -115,10 +116,10 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
 }
 
 // PAGED: every chunk lies in one page (positions in order, or lists of blocks; pages, and blocks, of at least a chunk).
-template <int D, bool I8, bool SEL, bool PAGED>
-__global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED>::kPerSm) rows_kernel(const __grid_constant__ Params p) {
+template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false>
+__global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kPerSm) rows_kernel(const __grid_constant__ Params p) {
   constexpr bool BLOCKS = SEL && PAGED;
-  using S = Shape<D, I8, BLOCKS>;
+  using S = Shape<D, I8, BLOCKS, MANY>;
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Start start;
   __shared__ float2 ml_s[kWarps + 1][16];  // maxima and sums: the warps', and those of a run's pieces before
@@ -665,22 +666,24 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED>::kPerSm) 
   }
 }
 
-template <int D, bool I8, bool SEL, bool PAGED>
+template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<D, I8, SEL && PAGED>::kSmem;
+  cfg.dynamicSmemBytes = Shape<D, I8, SEL && PAGED, MANY>::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
   cfg.numAttrs = launch_attributes(a, p.cluster);
-  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED>, p);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED, MANY>, p);
 }
 template <int D, bool I8>
 cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream) {
-  if (selected)
-    return p.block_shift && blocks_by_chunks(p, I8) ? launch<D, I8, true, true>(p, grid, stream) : launch<D, I8, true, false>(p, grid, stream);
+  if (selected) {
+    if (!I8 && rows_many(p, I8)) return launch<D, I8, true, true, !I8>(p, grid, stream);
+    return blocks_by_chunks(p, I8) ? launch<D, I8, true, true>(p, grid, stream) : launch<D, I8, true, false>(p, grid, stream);
+  }
   return (1 << p.page_shift) >= Shape<D, I8>::kChunk ? launch<D, I8, false, true>(p, grid, stream)
                                                      : launch<D, I8, false, false>(p, grid, stream);
 }
@@ -689,6 +692,7 @@ template <int D, bool I8>
 cudaError_t opt_in() {
   cudaError_t e = allow(rows_kernel<D, I8, true, false>, Shape<D, I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, true, true>, Shape<D, I8, true>::kSmem);
+  if (e == cudaSuccess && !I8) e = allow(rows_kernel<D, I8, true, true, !I8>, Shape<D, I8, true, !I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, true>, Shape<D, I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, false>, Shape<D, I8>::kSmem);
   return e;

@@ -4,8 +4,12 @@
 // The two calls that make tables are a few passes over the tables and over one
 // word for each page, with nothing between them but that all of one is done
 // before the next begins: one thread-block cluster makes them, in one launch,
-// its barrier between the passes. What the passes leave for each other lies in the
-// caller's scratch buffer, so that nothing is shared between calls.
+// its barrier between the passes. A pass is as long as the loads in it that wait
+// for each other, so there are three: who holds which page; how many pages of
+// each kind lie before each 32 (and their bits); and the tables, where the r-th
+// free page, or the number of moving pages before one, is looked up in those. What
+// the passes leave for each other lies in the caller's scratch buffer, so that
+// nothing is shared between calls.
 
 #include <algorithm>
 
@@ -19,6 +23,13 @@ namespace {
 constexpr int kBlocks = 8, kThreads = 1024, kWarps = kThreads / 32, kAllWarps = kBlocks * kWarps;
 constexpr int kFree = 0x7fffffff, kShared = -1;  // a page that nobody holds; one that is held and not to be written to
 
+// Of 32 pages: those that are free (fork), or held (compact), those that move (compact), and how many of either lie before
+// them in the warp's run of pages.
+struct __align__(16) Tally {
+  uint32_t a, b;
+  int before_a, before_b;
+};
+
 struct PlanParams {
   const int32_t* table;
   long long table_stride;
@@ -28,8 +39,10 @@ struct PlanParams {
   const uint8_t* keep;
   int pages, page_shift;
   int32_t *out, *src, *dst, *count;
-  int32_t *owner, *list, *base;  // scratch: a word a page, the free pages in order, a word a child
-  int32_t* sums;                 // and what the warps have counted
+  // scratch: what the warps have counted, 32 pages' tallies, a word a page, a word a child
+  int32_t* sums;
+  Tally* tallies;
+  int32_t *owner, *base;
   unsigned* status;
 };
 
@@ -48,38 +61,86 @@ struct Team {
   }
 };
 
-// Of two numbers that each warp of the cluster has counted, the sums over the warps before this one, and over all.
-// `sums`: global memory, 2 * kAllWarps words.
-struct Before {
-  int a, b, all_a, all_b;
+// Of two numbers that each warp of the cluster has counted: the sums over the warps before each one, in shared memory.
+struct Sums {
+  int a[kAllWarps + 1], b[kAllWarps + 1], warps[2][kAllWarps / 32];
 };
-__device__ __forceinline__ Before sums_before(const Team& me, int32_t* sums, int a, int b) {
+__device__ __forceinline__ void sum_up(const Team& me, const PlanParams& p, Sums& s, int a, int b) {
   if (me.lane == 0) {
-    sums[me.warp] = a;
-    sums[kAllWarps + me.warp] = b;
+    p.sums[me.warp] = a;
+    p.sums[kAllWarps + me.warp] = b;
   }
   me.meet();
-  Before r = {0, 0, 0, 0};
-  for (int i = me.lane; i < kAllWarps; i += 32) {
-    const int x = __ldcg(sums + i), y = __ldcg(sums + kAllWarps + i);
-    r.all_a += x;
-    r.all_b += y;
-    if (i < me.warp) {
-      r.a += x;
-      r.b += y;
+  const int t = threadIdx.x, w = t >> 5;
+  int x = 0, y = 0;
+  if (t < kAllWarps) {
+    x = __ldcg(p.sums + t);
+    y = __ldcg(p.sums + kAllWarps + t);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (me.lane >= o) {
+        x += u;
+        y += v;
+      }
+    }
+    if (me.lane == 31) {
+      s.warps[0][w] = x;
+      s.warps[1][w] = y;
     }
   }
-  r.a = __reduce_add_sync(0xffffffffu, r.a);
-  r.b = __reduce_add_sync(0xffffffffu, r.b);
-  r.all_a = __reduce_add_sync(0xffffffffu, r.all_a);
-  r.all_b = __reduce_add_sync(0xffffffffu, r.all_b);
-  return r;
+  __syncthreads();
+  if (t < kAllWarps) {
+    for (int i = 0; i < w; ++i) {
+      x += s.warps[0][i];
+      y += s.warps[1][i];
+    }
+    s.a[t + 1] = x;
+    s.b[t + 1] = y;
+    if (t == 0) s.a[0] = s.b[0] = 0;
+  }
+  __syncthreads();
 }
 // A warp's run of n things, in order: [begin, end), begin a multiple of 32.
+__device__ __forceinline__ int share(int n) { return (int)((((long long)n + kAllWarps - 1) / kAllWarps + 31) / 32 * 32); }
 __device__ __forceinline__ void share(const Team& me, int n, int& begin, int& end) {
-  const long long each = (((long long)n + kAllWarps - 1) / kAllWarps + 31) / 32 * 32;
+  const long long each = share(n);
   begin = (int)min((long long)n, each * me.warp);
   end = (int)min((long long)n, each * (me.warp + 1));
+}
+// The place of the n-th set bit (n < the bits' number).
+__device__ __forceinline__ int nth_bit(uint32_t bits, int n) {
+  int at = 0;
+#pragma unroll
+  for (int w = 16; w; w >>= 1) {
+    const int low = __popc(bits & ((1u << w) - 1u));
+    if (n >= low) {
+      n -= low;
+      bits >>= w;
+      at += w;
+    }
+  }
+  return at;
+}
+// The free page of this rank (FORK: of the tallies' a; else, a being held ones, of those without a bit there, below page `end`).
+template <bool FORK>
+__device__ __forceinline__ int free_page(const PlanParams& p, const Sums& s, int rank) {
+  const int each = share(p.pages);
+  int run = 0;
+#pragma unroll
+  for (int step = kAllWarps / 2; step; step >>= 1)
+    if ((FORK ? s.a[run + step] : (int)min((long long)p.pages, (long long)each * (run + step)) - s.a[run + step]) <= rank) run += step;
+  rank -= FORK ? s.a[run] : (int)min((long long)p.pages, (long long)each * run) - s.a[run];
+  const int first = run * (each / 32);
+  int low = 0, high = min(each / 32, (p.pages + 31) / 32 - first);
+  while (high - low > 1) {  // (the last 32 with no more before them than the rank)
+    const int mid = (low + high) / 2, before = __ldcg(&p.tallies[first + mid].before_a);
+    if ((FORK ? before : 32 * mid - before) <= rank) low = mid;
+    else high = mid;
+  }
+  const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p.tallies + first + low));
+  rank -= FORK ? (int)t.z : 32 * low - (int)t.z;
+  return (first + low) * 32 + nth_bit(FORK ? t.x : ~t.x, rank);
 }
 
 __device__ __forceinline__ int pages_of(const PlanParams& p, int len) { return (int)(((long long)len + (1 << p.page_shift) - 1) >> p.page_shift); }
@@ -130,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     int parent[kHeldChildren], have[kHeldChildren], need[kHeldChildren], tail[kHeldChildren], base[kHeldChildren];
     int warps[kWarps];
   } held;  // (tail: the entry that is going to be written to, or -1; later, the one that is copied)
+  __shared__ Sums sums;
   const Team me;
   unsigned bad = 0;
   grid_wait();
@@ -191,7 +253,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   int page0, page1, child0 = 0, child1 = 0;
   share(me, p.pages, page0, page1);
   int free = 0, wanted = 0;
-  for (int i = page0 + me.lane; i < page1; i += 32) free += __ldcg(p.owner + i) == kFree;
+#pragma unroll 4
+  for (int i = page0; i < page1; i += 32) {
+    const uint32_t m = __ballot_sync(0xffffffffu, i + me.lane < page1 && __ldcg(p.owner + i + me.lane) == kFree);
+    if (me.lane == 0) p.tallies[i / 32] = Tally{m, 0, free, 0};
+    free += __popc(m);
+  }
   bool copied;
   if (HELD) {
     // every thread block for itself: the children's wishes before each child
@@ -223,25 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
       if (i < p.children) held.base[i] = at;
       at += n[k];
     }
+    sum_up(me, p, sums, free, 0);
   } else {
     share(me, p.children, child0, child1);
     for (int i = child0 + me.lane; i < child1; i += 32) wanted += wants(i, copied);
-    wanted = __reduce_add_sync(0xffffffffu, wanted);
-  }
-  Before before = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, free), wanted);
-  if (HELD) before.all_b = wanted;
-  // the free pages that are wanted, in order; where each child's begin
-  int at = before.a;
-  const int most = min(before.all_a, before.all_b);
-  for (int i = page0; i < page1 && at < most; i += 32) {
-    const bool is = i + me.lane < page1 && __ldcg(p.owner + i + me.lane) == kFree;
-    const unsigned m = __ballot_sync(0xffffffffu, is);
-    const int rank = at + __popc(m & ((1u << me.lane) - 1u));
-    if (is && rank < most) p.list[rank] = i + me.lane;
-    at += __popc(m);
-  }
-  if (!HELD) {
-    at = before.b;
+    sum_up(me, p, sums, free, __reduce_add_sync(0xffffffffu, wanted));
+    int at = sums.b[me.warp];
     for (int i = child0; i < child1; i += 32) {
       const int n = i + me.lane < child1 ? wants(i + me.lane, copied) : 0;
       int end = n;
@@ -253,9 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
       if (i + me.lane < child1) p.base[i + me.lane] = at + end - n;
       at += __shfl_sync(0xffffffffu, end, 31);
     }
+    wanted = sums.b[kAllWarps];
+    me.meet();
   }
-  me.meet();
-  if (before.all_b > before.all_a) bad |= kStatNoPageBit;
+  const int most = sums.a[kAllWarps];  // pages to hand out
+  if (wanted > most) bad |= kStatNoPageBit;
   for (long long u = me.warp; u < units; u += kAllWarps) {
     const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
     int tail;
@@ -275,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
       if (j >= p.table_pages) continue;
       if ((copy && j == c.have - 1) || (j >= c.have && j < c.need)) {
         const int rank = base + (j < c.have ? 0 : (copy ? 1 : 0) + j - c.have);
-        const int got = rank < most ? __ldcg(p.list + rank) : -1;
+        const int got = rank < most ? free_page<true>(p, sums, rank) : -1;
         if (j < c.have) {
           p.src[i] = got < 0 ? -1 : e[k];
           p.dst[i] = got;
@@ -290,13 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
 }
 
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_constant__ PlanParams p) {
+  __shared__ Sums sums;
   const Team me;
   unsigned bad = 0;
   grid_wait();
   grid_launch_dependents();
   auto pinned = [&](int i) { return p.keep && p.keep[i] != 0; };
   for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = pinned(i) ? kShared : kFree;
-  for (int i = me.thread; i < p.pages / 2; i += kBlocks * kThreads) p.src[i] = p.dst[i] = -1;
   me.meet();
   const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
   const long long units = (long long)p.sequences * spans;
@@ -310,71 +366,69 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
     const int have = pages_held(s, j0 == 0);
     const int32_t* row = p.table + s * p.table_stride;
+    int e[kSpan / 32];
 #pragma unroll
     for (int k = 0; k < kSpan / 32; ++k) {
       const int j = j0 + 32 * k + me.lane;
-      if (j >= have) continue;
-      const int e = __ldg(row + j);
-      if ((unsigned)e >= (unsigned)p.pages) bad |= kStatIndexBit;
-      else p.owner[e] = kShared;
+      e[k] = j < have ? row[j] : -1;
+      if (j < have && (unsigned)e[k] >= (unsigned)p.pages) bad |= kStatIndexBit;
     }
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k)
+      if ((unsigned)e[k] < (unsigned)p.pages) p.owner[e[k]] = kShared;
   }
   me.meet();
-  int page0, page1;
+  int page0, page1, held = 0, movable = 0;
   share(me, p.pages, page0, page1);
-  int held = 0;
-  for (int i = page0 + me.lane; i < page1; i += 32) held += __ldcg(p.owner + i) != kFree;
-  const int used = sums_before(me, p.sums, __reduce_add_sync(0xffffffffu, held), 0).all_a;
-  // pages that move, and places for them
-  auto moves = [&](int i) { return i >= used && i < page1 && __ldcg(p.owner + i) != kFree && !pinned(i); };
-  auto place = [&](int i) { return i < used && i < page1 && __ldcg(p.owner + i) == kFree; };
-  int from = 0, to = 0;
-  for (int i = page0 + me.lane; i < page1; i += 32) {
-    from += moves(i);
-    to += place(i);
-  }
-  const Before before = sums_before(me, p.sums + 2 * kAllWarps, __reduce_add_sync(0xffffffffu, from), __reduce_add_sync(0xffffffffu, to));
-  const int count = before.all_a;
-  int a = before.a, b = before.b;
+#pragma unroll 4
   for (int i0 = page0; i0 < page1; i0 += 32) {
     const int i = i0 + me.lane;
-    const bool is_from = moves(i), is_to = place(i);
-    const unsigned mf = __ballot_sync(0xffffffffu, is_from), mt = __ballot_sync(0xffffffffu, is_to), low = (1u << me.lane) - 1u;
-    if (is_from) {
-      const int rank = a + __popc(mf & low);
-      p.src[rank] = i;
-      p.list[i] = rank;
-    } else if (i < page1) {
-      p.list[i] = -1;
-    }
-    if (is_to) {
-      const int rank = b + __popc(mt & low);
-      if (rank < count) p.dst[rank] = i;
-    }
-    a += __popc(mf);
-    b += __popc(mt);
+    const bool is = i < page1 && __ldcg(p.owner + i) != kFree;
+    const uint32_t a = __ballot_sync(0xffffffffu, is), b = __ballot_sync(0xffffffffu, is && !pinned(i));
+    if (me.lane == 0) p.tallies[i0 / 32] = Tally{a, b, held, movable};
+    held += __popc(a);
+    movable += __popc(b);
   }
-  me.meet();
+  sum_up(me, p, sums, held, movable);
+  const int used = sums.a[kAllWarps], each = share(p.pages);
+  // movable pages before page i
+  auto before = [&](int i, const uint4& t) { return sums.b[i / each] + (int)t.w + __popc(t.y & ((1u << (i & 31)) - 1u)); };
+  auto tally = [&](int i) { return __ldcg(reinterpret_cast<const uint4*>(p.tallies + i / 32)); };
+  const int below = used < p.pages ? before(used, tally(used)) : sums.b[kAllWarps];
+  const int count = sums.b[kAllWarps] - below;
+  // where page i goes
+  auto place = [&](int i) -> int {
+    if (i < used) return i;
+    const uint4 t = tally(i);
+    return t.y >> (i & 31) & 1u ? free_page<false>(p, sums, before(i, t) - below) : i;
+  };
   if (me.thread == 0) {
     p.count[0] = count;
     p.count[1] = used;
+  }
+  for (int i = count + me.thread; i < p.pages / 2; i += kBlocks * kThreads) p.src[i] = p.dst[i] = -1;
+  for (int i = used + me.thread; i < p.pages; i += kBlocks * kThreads) {
+    const uint4 t = tally(i);
+    if (!(t.y >> (i & 31) & 1u)) continue;
+    const int rank = before(i, t) - below;
+    p.src[rank] = i;
+    p.dst[rank] = free_page<false>(p, sums, rank);
   }
   for (long long u = me.warp; u < units; u += kAllWarps) {
     const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
     const int have = pages_held(s, false);
     const int32_t* row = p.table + s * p.table_stride;
     int32_t* out = p.out + (long long)s * p.table_pages;
+    int e[kSpan / 32];
 #pragma unroll
     for (int k = 0; k < kSpan / 32; ++k) {
       const int j = j0 + 32 * k + me.lane;
-      if (j >= p.table_pages) continue;
-      int e = -1;
-      if (j < have) {
-        e = row[j];  // (out may be the table itself)
-        const int rank = (unsigned)e < (unsigned)p.pages ? __ldcg(p.list + e) : -1;
-        if (rank >= 0) e = __ldcg(p.dst + rank);
-      }
-      out[j] = e;
+      e[k] = j < have ? row[j] : -1;  // (out may be the table itself)
+    }
+#pragma unroll
+    for (int k = 0; k < kSpan / 32; ++k) {
+      const int j = j0 + 32 * k + me.lane;
+      if (j < p.table_pages) out[j] = (unsigned)e[k] < (unsigned)p.pages ? place(e[k]) : e[k];
     }
   }
   if (bad) report(p.status, bad);
@@ -494,12 +548,12 @@ PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t 
   p.src = src;
   p.dst = dst;
   p.sums = scratch;
-  p.owner = scratch + 1024;
-  p.list = p.owner + pages;
-  p.base = p.list + pages;
+  p.tallies = reinterpret_cast<Tally*>(scratch + 1024);
+  p.owner = scratch + 1024 + (pages + 31) / 32 * 4;
+  p.base = p.owner + pages;
   return p;
 }
-static_assert(4 * kAllWarps <= 1024, "the warps' sums fit their place in the scratch buffer");
+static_assert(2 * kAllWarps <= 1024 && sizeof(Tally) == 16, "the scratch buffer's layout");
 
 }  // namespace
 }  // namespace attn
@@ -515,7 +569,7 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
   if ((int64_t)children * table_pages + children > INT32_MAX) return TKS_E_TOO_LARGE;
   if (children == 0) return TKS_OK;
   if (!parents || !new_lens || !src || !dst || !scratch || (table_pages > 0 && !table)) return TKS_E_INVAL;
-  if (!aligned(parents, 4) || !aligned(new_lens, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(scratch, 4) || !aligned(table, 4))
+  if (!aligned(parents, 4) || !aligned(new_lens, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(scratch, 16) || !aligned(table, 4))
     return TKS_E_INVAL;
   const long long held = sequences > 0 ? (sequences - 1) * table_stride + table_pages : 0;
   if (table_pages > 0 && overlap(page_table, held, table, (long long)children * table_pages)) return TKS_E_INVAL;
@@ -542,7 +596,7 @@ extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride
   if (check_plan(page_table, table_stride, table_pages, sequences, lens, pages, page_size) != TKS_OK) return TKS_E_INVAL;
   if ((int64_t)sequences * table_pages > INT32_MAX) return TKS_E_TOO_LARGE;
   if (!count || !scratch || (pages > 1 && (!src || !dst)) || (sequences > 0 && table_pages > 0 && !table)) return TKS_E_INVAL;
-  if (!aligned(count, 4) || !aligned(scratch, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(table, 4)) return TKS_E_INVAL;
+  if (!aligned(count, 4) || !aligned(scratch, 16) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(table, 4)) return TKS_E_INVAL;
   const long long held = sequences > 0 ? (sequences - 1) * table_stride + table_pages : 0;
   const bool in_place = table == page_table && (sequences <= 1 || table_stride == table_pages);
   if (held > 0 && table_pages > 0 && !in_place && overlap(page_table, held, table, (long long)sequences * table_pages)) return TKS_E_INVAL;

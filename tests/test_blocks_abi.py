@@ -85,14 +85,14 @@ def test_bad_block_attention(bad):
 @pytest.mark.parametrize("bad", [dict(table=None), dict(table=66), dict(stride=-1), dict(width=-1), dict(sequences=-1), dict(lens=None), dict(lens=66),
                                  dict(parents=None), dict(parents=66), dict(new_lens=None), dict(new_lens=66), dict(children=-1), dict(pages=0), dict(page=12),
                                  dict(page=0), dict(pages=1 << 30), dict(out=None), dict(out=66), dict(src=None), dict(dst=None), dict(scratch=None),
-                                 dict(src=66), dict(dst=66), dict(scratch=66), dict(out=1 << 20), dict(out=(1 << 20) + 28), dict(out=(1 << 20) - 28)], ids=str)
+                                 dict(src=66), dict(dst=66), dict(scratch=68), dict(out=1 << 20), dict(out=(1 << 20) + 28), dict(out=(1 << 20) - 28)], ids=str)
 def test_bad_forks(bad):
     assert call_fork(**bad) == INVAL
 
 
 @pytest.mark.parametrize("bad", [dict(table=None), dict(table=66), dict(stride=-1), dict(width=-1), dict(sequences=-1), dict(lens=None), dict(lens=66),
                                  dict(pages=0), dict(page=12), dict(pages=1 << 30), dict(out=None), dict(out=66), dict(src=None), dict(dst=None),
-                                 dict(count=None), dict(scratch=None), dict(count=66), dict(scratch=66), dict(out=(1 << 20) + 4),
+                                 dict(count=None), dict(scratch=None), dict(count=66), dict(scratch=68), dict(out=(1 << 20) + 4),
                                  dict(out=1 << 20, stride=5)], ids=str)
 def test_bad_compactions(bad):
     assert call_compact(**bad) == INVAL

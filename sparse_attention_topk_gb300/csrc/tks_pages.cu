@@ -5,9 +5,9 @@
 // word for each page, with nothing between them but that all of one is done
 // before the next begins: one thread-block cluster makes them, in one launch,
 // its barrier between the passes. A pass is as long as the loads in it that wait
-// for each other, so there are three: who holds which page; how many pages of
-// each kind lie before each 32 (and their bits); and the tables, where the r-th
-// free page, or the number of moving pages before one, is looked up in those. What
+// for each other, so there are few: who holds which page; how many pages of each
+// kind lie before each 32 (and their bits); and the tables, for which the r-th free
+// page, or the number of moving pages before one, is looked up in those. What
 // the passes leave for each other lies in the caller's scratch buffer, so that
 // nothing is shared between calls.
 
@@ -39,6 +39,7 @@ struct PlanParams {
   const uint8_t* keep;
   int pages, page_shift;
   int32_t *out, *src, *dst, *count;
+  int lanes, spans;  // how rows are cut up (kLanes)
   // scratch: what the warps have counted, 32 pages' tallies, a word a page, a word a child
   int32_t* sums;
   Tally* tallies;
@@ -178,8 +179,8 @@ __device__ __forceinline__ Child child_of(const PlanParams& p, int i, unsigned* 
   return c;
 }
 
-// What a warp does at once: kSpan entries of one row, 32 at a time.
-constexpr int kSpan = 256;
+// What a warp does at once: a span of one row, kLanes entries a lane; where that left warps without a span (compact), fewer.
+constexpr int kLanes = 8;
 // Children that each thread block keeps in shared memory, looked up once (each look goes through three loads that wait for
 // each other: parent, length, entry).
 constexpr int kHeldChildren = 2048;
@@ -221,21 +222,21 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     return Child{p.table + held.parent[i] * p.table_stride, held.have[i], held.need[i], tail >= 0};
   };
   me.meet();
-  const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
-  const long long units = (long long)p.children * spans;
-  for (long long u = me.warp; u < units; u += kAllWarps) {
-    const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
+  constexpr int span = 32 * kLanes;
+  const int spans = p.spans, units = p.children * spans;
+  for (int u = me.warp; u < units; u += kAllWarps) {
+    const int i = u / spans, j0 = (u - i * spans) * span;
     int tail;
     const Child c = child(i, tail, j0 == 0 ? &bad : nullptr);
-    int e[kSpan / 32];
+    int e[kLanes];
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
       e[k] = j < c.have ? __ldg(c.row + j) : -1;
       if (j < c.have && (unsigned)e[k] >= (unsigned)p.pages) bad |= kStatIndexBit;
     }
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       if ((unsigned)e[k] >= (unsigned)p.pages) continue;
       // (a held page's word only ever falls: to kShared, or to the lowest of those who write to it)
       if (tail >= 0 && j0 + 32 * k + me.lane == c.have - 1) atomicMin(p.owner + e[k], i);
@@ -312,21 +313,21 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   }
   const int most = sums.a[kAllWarps];  // pages to hand out
   if (wanted > most) bad |= kStatNoPageBit;
-  for (long long u = me.warp; u < units; u += kAllWarps) {
-    const int i = (int)(u / spans), j0 = (int)(u - (long long)i * spans) * kSpan;
+  for (int u = me.warp; u < units; u += kAllWarps) {
+    const int i = u / spans, j0 = (u - i * spans) * span;
     int tail;
     const Child c = child(i, tail, nullptr);
     const int base = HELD ? held.base[i] : __ldcg(p.base + i);
     const bool copy = HELD ? tail >= 0 : tail >= 0 && __ldcg(p.owner + tail) != i;
     int32_t* to = p.out + (long long)i * p.table_pages;
-    int e[kSpan / 32];
+    int e[kLanes];
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
       e[k] = j < c.have ? __ldg(c.row + j) : -1;
     }
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
       if (j >= p.table_pages) continue;
       if ((copy && j == c.have - 1) || (j >= c.have && j < c.need)) {
@@ -354,27 +355,26 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
   auto pinned = [&](int i) { return p.keep && p.keep[i] != 0; };
   for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = pinned(i) ? kShared : kFree;
   me.meet();
-  const int spans = max(1, (p.table_pages + kSpan - 1) / kSpan);
-  const long long units = (long long)p.sequences * spans;
+  const int lanes = p.lanes, span = 32 * lanes, spans = p.spans, units = p.sequences * spans;
   auto pages_held = [&](int s, bool tell) {
     bool len_bad = false;
     const int n = pages_of(p, held_len(p, __ldg(p.lens + s), len_bad));
     if (len_bad && tell) bad |= kStatRowLenBit;
     return n;
   };
-  for (long long u = me.warp; u < units; u += kAllWarps) {
-    const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
+  for (int u = me.warp; u < units; u += kAllWarps) {
+    const int s = u / spans, j0 = (u - s * spans) * span;
     const int have = pages_held(s, j0 == 0);
     const int32_t* row = p.table + s * p.table_stride;
-    int e[kSpan / 32];
+    int e[kLanes];
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
-      e[k] = j < have ? row[j] : -1;
-      if (j < have && (unsigned)e[k] >= (unsigned)p.pages) bad |= kStatIndexBit;
+      e[k] = k < lanes && j < have ? row[j] : -1;
+      if (k < lanes && j < have && (unsigned)e[k] >= (unsigned)p.pages) bad |= kStatIndexBit;
     }
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k)
+    for (int k = 0; k < kLanes; ++k)
       if ((unsigned)e[k] < (unsigned)p.pages) p.owner[e[k]] = kShared;
   }
   me.meet();
@@ -396,12 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
   auto tally = [&](int i) { return __ldcg(reinterpret_cast<const uint4*>(p.tallies + i / 32)); };
   const int below = used < p.pages ? before(used, tally(used)) : sums.b[kAllWarps];
   const int count = sums.b[kAllWarps] - below;
-  // where page i goes
-  auto place = [&](int i) -> int {
-    if (i < used) return i;
-    const uint4 t = tally(i);
-    return t.y >> (i & 31) & 1u ? free_page<false>(p, sums, before(i, t) - below) : i;
-  };
   if (me.thread == 0) {
     p.count[0] = count;
     p.count[1] = used;
@@ -414,21 +408,33 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     p.src[rank] = i;
     p.dst[rank] = free_page<false>(p, sums, rank);
   }
-  for (long long u = me.warp; u < units; u += kAllWarps) {
-    const int s = (int)(u / spans), j0 = (int)(u - (long long)s * spans) * kSpan;
+  me.meet();
+  for (int u = me.warp; u < units; u += kAllWarps) {
+    const int s = u / spans, j0 = (u - s * spans) * span;
     const int have = pages_held(s, false);
     const int32_t* row = p.table + s * p.table_stride;
     int32_t* out = p.out + (long long)s * p.table_pages;
-    int e[kSpan / 32];
+    int e[kLanes], to[kLanes];
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
-      e[k] = j < have ? row[j] : -1;  // (out may be the table itself)
+      e[k] = k < lanes && j < have ? row[j] : -1;  // (out may be the table itself)
     }
 #pragma unroll
-    for (int k = 0; k < kSpan / 32; ++k) {
+    for (int k = 0; k < kLanes; ++k) {  // which of the moves, or none
+      to[k] = -1;
+      if (e[k] >= used && e[k] < p.pages) {
+        const uint4 t = tally(e[k]);
+        if (t.y >> (e[k] & 31) & 1u) to[k] = before(e[k], t) - below;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k)
+      if (to[k] >= 0) e[k] = __ldcg(p.dst + to[k]);
+#pragma unroll
+    for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
-      if (j < p.table_pages) out[j] = (unsigned)e[k] < (unsigned)p.pages ? place(e[k]) : e[k];
+      if (k < lanes && j < p.table_pages) out[j] = e[k];
     }
   }
   if (bad) report(p.status, bad);
@@ -470,10 +476,18 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
   grid_launch_dependents();
   const int n = p.count ? min(p.n, max(0, __ldg(p.count))) : p.n;
   const long long items = (long long)n * p.all_chunks;
-  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+  int next_src = -1, next_dst = -1;  // of the next item: looked up while this one's pieces are on their way
+  auto look_up = [&](long long w) {
+    if (w >= items) return;
     const int i = (int)(w / p.all_chunks);
-    int chunk = (int)(w - (long long)i * p.all_chunks);
-    const int src = __ldg(p.src + i), dst = __ldg(p.dst + i);
+    next_src = __ldg(p.src + i);
+    next_dst = __ldg(p.dst + i);
+  };
+  look_up(blockIdx.x);
+  for (long long w = blockIdx.x; w < items; w += gridDim.x) {
+    int chunk = (int)(w % p.all_chunks);
+    const int src = next_src, dst = next_dst;
+    look_up(w + gridDim.x);
     if (src < 0 || dst < 0) continue;
     if (src >= p.pages || dst >= p.pages) {
       if (threadIdx.x == 0) report(p.status, kStatIndexBit);
@@ -534,7 +548,7 @@ int check_plan(const int32_t* page_table, int64_t table_stride, int32_t table_pa
 }
 
 PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens,
-                       const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch) {
+                       const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch, int rows, bool few) {
   PlanParams p{};
   p.table = page_table;
   p.table_stride = table_stride;
@@ -547,6 +561,9 @@ PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t 
   p.out = table;
   p.src = src;
   p.dst = dst;
+  p.lanes = kLanes;
+  while (few && p.lanes > 1 && (long long)rows * (((long long)table_pages + 32 * p.lanes - 1) / (32 * p.lanes)) < kAllWarps) p.lanes /= 2;
+  p.spans = std::max(1, (int)(((long long)table_pages + 32 * p.lanes - 1) / (32 * p.lanes)));
   p.sums = scratch;
   p.tallies = reinterpret_cast<Tally*>(scratch + 1024);
   p.owner = scratch + 1024 + (pages + 31) / 32 * 4;
@@ -566,7 +583,7 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
                               const int32_t* parents, const int32_t* new_lens, int32_t children, const uint8_t* keep, int32_t pages,
                               int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch, void* stream) {
   if (check_plan(page_table, table_stride, table_pages, sequences, lens, pages, page_size) != TKS_OK || children < 0) return TKS_E_INVAL;
-  if ((int64_t)children * table_pages + children > INT32_MAX) return TKS_E_TOO_LARGE;
+  if ((int64_t)children * table_pages + children > INT32_MAX - (1 << 16)) return TKS_E_TOO_LARGE;
   if (children == 0) return TKS_OK;
   if (!parents || !new_lens || !src || !dst || !scratch || (table_pages > 0 && !table)) return TKS_E_INVAL;
   if (!aligned(parents, 4) || !aligned(new_lens, 4) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(scratch, 16) || !aligned(table, 4))
@@ -576,7 +593,7 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
   Place place;
   const int rc = place_of(stream, &place);
   if (rc != TKS_OK) return rc;
-  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch);
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, children, false);
   p.parents = parents;
   p.new_lens = new_lens;
   p.children = children;
@@ -594,7 +611,7 @@ extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride
                                  const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst,
                                  int32_t* count, int32_t* scratch, void* stream) {
   if (check_plan(page_table, table_stride, table_pages, sequences, lens, pages, page_size) != TKS_OK) return TKS_E_INVAL;
-  if ((int64_t)sequences * table_pages > INT32_MAX) return TKS_E_TOO_LARGE;
+  if ((int64_t)sequences * table_pages + sequences > INT32_MAX - (1 << 16)) return TKS_E_TOO_LARGE;
   if (!count || !scratch || (pages > 1 && (!src || !dst)) || (sequences > 0 && table_pages > 0 && !table)) return TKS_E_INVAL;
   if (!aligned(count, 4) || !aligned(scratch, 16) || !aligned(src, 4) || !aligned(dst, 4) || !aligned(table, 4)) return TKS_E_INVAL;
   const long long held = sequences > 0 ? (sequences - 1) * table_stride + table_pages : 0;
@@ -603,7 +620,7 @@ extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride
   Place place;
   const int rc = place_of(stream, &place);
   if (rc != TKS_OK) return rc;
-  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch);
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, sequences, true);
   p.count = count;
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
@@ -656,7 +673,7 @@ extern "C" int tks_cache_copy(const tks_cache* cache, const tks_bounds* bounds, 
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(n * all, place.sms * 8LL));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(n * all, place.sms * 5LL));
   cfg.blockDim = dim3(kCopyThreads);
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute a[1] = {};

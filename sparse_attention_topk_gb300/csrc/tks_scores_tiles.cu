@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kRows = kScoreTileRows, kBlocks = kScoreTileBlocks;
 constexpr int kMaxWarps = 8, kProducer0 = 8, kQuery0 = 12, kQueryWarps = 3, kMulWarp = 15, kThreads = 16 * 32;
-constexpr int kUnits = 256;  // tiles of tokens whose lengths are looked at before the work is split
+constexpr int kUnits = 1024;  // tiles of tokens whose lengths are looked at before the work is split
 
 template <int D>
 struct Shape {
@@ -94,8 +94,12 @@ struct Items {
       at -= unit * one;
       end -= unit * one;
     } else {
-      unit = 0;
-      while ((long long)s.upto[unit + 1] * p.kv_heads <= at) ++unit;
+      unit = 0;  // the last with no more before it
+      for (int high = units; high - unit > 1;) {
+        const int mid = (unit + high) / 2;
+        if ((long long)s.upto[mid] * p.kv_heads <= at) unit = mid;
+        else high = mid;
+      }
       upto0 = s.upto[unit];
       upto1 = s.upto[unit + 1];
     }
@@ -278,7 +282,7 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
 // Warps 0-7: maxima over a token's heads, and the stores. Warps w and w + 4 have the lanes (blocks) 32w .. 32w + 31, and each
 // one half's columns. GROUP: heads of a token, or 0: any. 32 columns are on their way while the 32 before them are joined.
 // Most tiles hold blocks that all their tokens see: what their scores go through is kept short (the whole way for all of them
-// took 101 us instead of XX for 2048 tokens of 32 heads over 2048 blocks).
+// took 101 us for 2048 tokens of 32 heads over 2048 blocks, and 69 so).
 template <int GROUP>
 __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k, Shared& s, uint32_t tmem) {
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
@@ -439,13 +443,20 @@ __global__ void __launch_bounds__(kThreads, 1) score_tiles_kernel(const __grid_c
   // how many tiles of blocks the tiles of tokens see
   const int units = p.batch * p.token_tiles, all = (p.n + kBlocks - 1) / kBlocks;
   if (units <= kUnits) {
-    for (int u = warp; u < units; u += kThreads / 32) {
-      const int b = u / p.token_tiles, t0 = (u - b * p.token_tiles) * p.tile_tokens, tokens = min(p.tile_tokens, p.tokens - t0);
-      int most = 0;
+    for (int u = threadIdx.x; u <= units; u += kThreads) s.upto[u] = 0;
+    __syncthreads();
+    const int tokens = p.batch * p.tokens;  // (no more than units * tokens of a tile)
+#pragma unroll 4
+    for (int i = threadIdx.x; i < (tokens + 31) / 32 * 32; i += kThreads) {
+      const int b = min(i, tokens - 1) / p.tokens, t = min(i, tokens - 1) - b * p.tokens, u = b * p.token_tiles + t / p.tile_tokens;
       bool bad = false;
-      for (int t = lane; t < tokens; t += 32) most = max(most, blocks_seen(p, b, t0 + t, bad));
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (lane == 0) s.upto[u + 1] = (most + kBlocks - 1) / kBlocks;
+      const int tiles = (blocks_seen(p, b, t, bad) + kBlocks - 1) / kBlocks;
+      const int most = __reduce_max_sync(0xffffffffu, tiles);
+      if (__shfl_sync(0xffffffffu, u, 0) == __shfl_sync(0xffffffffu, u, 31)) {
+        if (lane == 0) atomicMax(&s.upto[u + 1], most);
+      } else {
+        atomicMax(&s.upto[u + 1], tiles);
+      }
     }
     __syncthreads();
     if (warp == 0) {

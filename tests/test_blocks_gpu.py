@@ -708,3 +708,15 @@ def test_wrong_pages_and_numbers_among_many():
     many[3] = 14401
     got, seen = tks.block_scores(q, bounds, table, many, 8)
     assert tks.device_status() == tks.TKS_E_ROW_LEN and torch.equal(got, good) and (seen == 1800).all()
+
+
+def test_scores_of_more_tiles_than_are_counted():
+    g = gen(31)
+    bounds = torch.randn(60, 1, 1, 2, 64, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(110, 330, 8, 64, device="cuda", generator=g).to(torch.bfloat16)
+    table = torch.randint(60, (110, 150), device="cuda", generator=g).to(torch.int32)
+    lens = torch.randint(0, 1201, (110, 330), device="cuda", generator=g).to(torch.int32)
+    many, seen = tks.block_scores(q, bounds, table, lens, 8, first=1)
+    for at in (0, 37, 100):
+        few, n = tks.block_scores(q[at : at + 10], bounds, table[at : at + 10], lens[at : at + 10], 8, first=1)
+        assert torch.equal(seen[at : at + 10], n) and torch.equal(many[at : at + 10], few)

@@ -528,7 +528,6 @@ extern "C" int tks_selected_attention(const tks_cache* cache, const tks_queries*
   if ((k > 0 && !indices) || !aligned(indices, 4) || !aligned(kv_len, 4)) return TKS_E_INVAL;
   Params p = params_of(cache, queries);
   p.indices = indices;
-  p.list_seq = k;
   p.k_sel = k;
   p.kv_len = kv_len;
   p.seqs = queries->batch * queries->tokens;
@@ -543,13 +542,13 @@ extern "C" int tks_block_attention(const tks_cache* cache, const tks_queries* qu
   if (queries->batch == 0 || queries->tokens == 0) return TKS_OK;
   if ((n > 0 && !blocks) || !aligned(blocks, 4) || !aligned(kv_len, 4)) return TKS_E_INVAL;
   Params p = params_of(cache, queries);
+  p.blocks = true;
   p.indices = blocks;
   p.list_seq = (long long)cache->kv_heads * n;
   p.list_head = n;
   p.block_shift = log2_of(block);
   p.k_sel = n * block;
   p.kv_len = kv_len;
-  p.kv_tokens = queries->tokens;
   p.seqs = queries->batch * queries->tokens;
   p.rows = p.group;
   return launch(p, cache, true, stream);

@@ -144,17 +144,24 @@ __device__ __forceinline__ Seq seq_of(const Params& p, int s, bool* bad = nullpt
   return q;
 }
 
+// Lists of positions, or (BLK) of blocks. (Lists of positions as blocks of one: one token over 2048 of them takes 9.65 us
+// instead of 9.2, 512 of 64 heads 103.8 instead of 101.6.)
 // The list of a token (seq) and head.
+template <bool BLK>
 __device__ __forceinline__ const int32_t* list_of(const Params& p, int seq, int head) {
-  return p.indices + seq * p.list_seq + (long long)head * p.list_head;
+  return BLK ? p.indices + seq * p.list_seq + (long long)head * p.list_head : p.indices + (long long)seq * p.k_sel;
 }
-// The position of key j of a list, given its entry (that of key j's block), or -1.
+// The place of key j's entry in a list.
+template <bool BLK>
+__device__ __forceinline__ int list_entry(const Params& p, int j) { return BLK ? j >> p.block_shift : j; }
+// The position of key j of a list, given its entry, or -1.
+template <bool BLK>
 __device__ __forceinline__ int list_position(const Params& p, int entry, int j, int limit, bool& bad) {
-  if (entry < 0) return -1;
-  if (p.block_shift == 0) {
+  if (!BLK) {
     bad |= entry >= limit;
     return entry >= limit ? -1 : entry;
   }
+  if (entry < 0) return -1;
   if (entry > (0x7fffffff >> p.block_shift) || entry << p.block_shift >= limit) {
     bad = true;
     return -1;
@@ -163,8 +170,9 @@ __device__ __forceinline__ int list_position(const Params& p, int entry, int j, 
   return pos >= limit ? -1 : pos;  // (a block may reach beyond the length)
 }
 
-// The number of positions that a list's entries may name; `given`: kv_len of the sequence or token, or INT_MAX.
-__device__ __forceinline__ int kv_given(const Params& p, int b, int seq) { return p.kv_len ? __ldg(p.kv_len + (p.kv_tokens ? seq : b)) : 0x7fffffff; }
+// The number of positions that a list's entries may name; `given`: kv_len of the sequence (or token), or INT_MAX.
+template <bool BLK>
+__device__ __forceinline__ int kv_given(const Params& p, int b, int seq) { return p.kv_len ? __ldg(p.kv_len + (BLK ? seq : b)) : 0x7fffffff; }
 __device__ __forceinline__ int kv_limit(const Params& p, int given) {
   const int r = min(max(given, 0), capacity(p));
   if (r != given && p.kv_len) report(p.status, kStatRowLenBit);

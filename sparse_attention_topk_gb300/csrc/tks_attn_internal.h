@@ -95,11 +95,11 @@ struct Params {
   const int32_t *ctx_len, *draft_len, *tree;  // tree attention
   int tree_words;
   const int32_t *indices, *kv_len;  // selected attention: lists, and the lengths that their entries keep to,
+  int k_sel;                        // and the keys of a list
+  bool blocks;                      // attention over blocks: lists of blocks, one for each head, and lengths of tokens
+  int block_shift;                  // log2 of a block's keys
   long long list_seq;               // a list's stride in entries, from token to token
-  int list_head;                    // and from head to head (0: one list for all)
-  int block_shift;                  // log2 of the keys that an entry stands for
-  int kv_tokens;                    // tokens of a sequence that have a length of their own (0: one for all)
-  int k_sel;                        // keys of a list
+  int list_head;                    // and from head to head
   float scale_log2;  // softmax_scale * log2(e)
   int seqs;          // tree: batch; selected: batch * tokens
   int rows;          // query rows of one (sequence, head)
@@ -124,7 +124,7 @@ constexpr int kRowsBlocksPerSm = 2;
 // Whether a list's blocks, and the pages, are at least as long as the chunks (32 keys of int8, 16 of bfloat16) that warps take.
 inline bool blocks_by_chunks(const Params& p, bool i8) {
   const int chunk = i8 ? 5 : 4;
-  return p.block_shift >= chunk && p.page_shift >= chunk;
+  return p.blocks && p.block_shift >= chunk && p.page_shift >= chunk;
 }
 // Lists of bfloat16 blocks that together are longer than the sequence come from L2, which answers sooner than memory: more
 // warps with less under way each (512 tokens of 64 heads on 4 over 32 blocks of 64: 233 us so, 260 otherwise). Of memory, or

@@ -116,7 +116,8 @@ __device__ __forceinline__ bool clear_nonfinite(uint32_t& w) {
 }
 
 // PAGED: every chunk lies in one page (positions in order, or lists of blocks; pages, and blocks, of at least a chunk).
-template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false>
+// BLK: lists of blocks.
+template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false, bool BLK = SEL && PAGED>
 __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kPerSm) rows_kernel(const __grid_constant__ Params p) {
   constexpr bool BLOCKS = SEL && PAGED;
   using S = Shape<D, I8, BLOCKS, MANY>;
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
     const int k_beg = t0 * kRowsKeys;  // tiles * kRowsKeys stays below 2^31: len does, rounded up once
     const int k_end = (int)min((long long)len.len, (long long)t1 * kRowsKeys);
     const int32_t* table = p.table + b * p.table_stride;
-    const int32_t* list = SEL ? list_of(p, seq, head) : nullptr;
-    const int given = SEL ? kv_given(p, b, seq) : 0;
+    const int32_t* list = SEL ? list_of<BLK>(p, seq, head) : nullptr;
+    const int given = SEL ? kv_given<BLK>(p, b, seq) : 0;
     const unsigned char* kb = p.k + head * p.head_b;
     const unsigned char* vb = p.v + head * p.head_b;
 
@@ -189,21 +190,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
     auto issue = [&](int j, int st, int pg, int beg, int end) {
       if (j < end) {
         const uint32_t to = st * S::kStage;
-        unsigned valid = 0;
+        unsigned valid;
         if (PAGED) {
-          int in_page;
           // (a list's chunk: the slot that it begins at, and in the bits below a chunk, how many keys it has less one; or -1)
-          if (BLOCKS) {
-            const int at = slots[(j - beg) / kChunk];
-            pg = at < 0 ? -1 : at >> p.page_shift;
-            valid = at & (kChunk - 1);
-            in_page = at & ((1 << p.page_shift) - kChunk);
-          } else {
-            in_page = j & ((1 << p.page_shift) - 1);
-          }
+          const int at = BLOCKS ? slots[(j - beg) / kChunk] : 0;
+          if (BLOCKS) pg = at < 0 ? -1 : at >> p.page_shift;
           const bool ok = (unsigned)pg < (unsigned)p.pages;
           if (!BLOCKS && !ok) report(p.status, kStatIndexBit);
-          const int n_valid = !ok ? 0 : BLOCKS ? (int)valid + 1 : min(kChunk, end - j);
+          const int n_valid = ok ? (BLOCKS ? (at & (kChunk - 1)) + 1 : min(kChunk, end - j)) : 0;
+          const int in_page = BLOCKS ? at & ((1 << p.page_shift) - kChunk) : j & ((1 << p.page_shift) - 1);
           const long long off = ok ? pg * p.page_b + in_page * p.token_b : 0;
           const unsigned char* ks = kb + off + row0 * p.token_b + piece * 16;
           const unsigned char* vs = vb + off + row0 * p.token_b + piece * 16;
@@ -307,13 +302,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int j = beg + (threadIdx.x + i * kThreads) * kChunk;
-        pos[i] = j >= end ? -1 : __ldg(list + (j >> p.block_shift));
+        pos[i] = j >= end ? -1 : __ldg(list + list_entry<true>(p, j));
       }
       bool bad = false;
       const int limit = kv_limit(p, given);
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        pos[i] = list_position(p, pos[i], beg + (threadIdx.x + i * kThreads) * kChunk, limit, bad);
+        pos[i] = list_position<true>(p, pos[i], beg + (threadIdx.x + i * kThreads) * kChunk, limit, bad);
         pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
       __syncthreads();  // the previous chunks' copies have started
@@ -334,13 +329,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int j = beg + threadIdx.x + i * kThreads;
-        pos[i] = j >= end ? -1 : SEL ? __ldg(list + (j >> p.block_shift)) : j;
+        pos[i] = j >= end ? -1 : SEL ? __ldg(list + list_entry<BLK>(p, j)) : j;
       }
       bool bad = false;
       const int limit = SEL ? kv_limit(p, given) : 0;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        if (SEL) pos[i] = list_position(p, pos[i], beg + threadIdx.x + i * kThreads, limit, bad);
+        if (SEL) pos[i] = list_position<BLK>(p, pos[i], beg + threadIdx.x + i * kThreads, limit, bad);
         pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
       __syncthreads();  // the previous keys' copies have started
@@ -666,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
   }
 }
 
-template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false>
+template <int D, bool I8, bool SEL, bool PAGED, bool MANY = false, bool BLK = SEL && PAGED>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -676,13 +671,14 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
   cfg.numAttrs = launch_attributes(a, p.cluster);
-  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED, MANY>, p);
+  return cudaLaunchKernelEx(&cfg, rows_kernel<D, I8, SEL, PAGED, MANY, BLK>, p);
 }
 template <int D, bool I8>
 cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream) {
   if (selected) {
     if (!I8 && rows_many(p, I8)) return launch<D, I8, true, true, !I8>(p, grid, stream);
-    return blocks_by_chunks(p, I8) ? launch<D, I8, true, true>(p, grid, stream) : launch<D, I8, true, false>(p, grid, stream);
+    if (blocks_by_chunks(p, I8)) return launch<D, I8, true, true>(p, grid, stream);
+    return p.blocks ? launch<D, I8, true, false, false, true>(p, grid, stream) : launch<D, I8, true, false>(p, grid, stream);
   }
   return (1 << p.page_shift) >= Shape<D, I8>::kChunk ? launch<D, I8, false, true>(p, grid, stream)
                                                      : launch<D, I8, false, false>(p, grid, stream);
@@ -691,6 +687,7 @@ cudaError_t launch(const Params& p, bool selected, int grid, cudaStream_t stream
 template <int D, bool I8>
 cudaError_t opt_in() {
   cudaError_t e = allow(rows_kernel<D, I8, true, false>, Shape<D, I8>::kSmem);
+  if (e == cudaSuccess) e = allow(rows_kernel<D, I8, true, false, false, true>, Shape<D, I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, true, true>, Shape<D, I8, true>::kSmem);
   if (e == cudaSuccess && !I8) e = allow(rows_kernel<D, I8, true, true, !I8>, Shape<D, I8, true, !I8>::kSmem);
   if (e == cudaSuccess) e = allow(rows_kernel<D, I8, false, true>, Shape<D, I8>::kSmem);

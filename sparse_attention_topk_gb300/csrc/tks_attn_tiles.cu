@@ -204,7 +204,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // ---------------------------------------------------------------------------
 
 // Warps 9-11: the lookups of every third tile.
-template <int D, bool I8, bool SEL>
+template <int D, bool I8, bool SEL, bool BLK>
 __device__ __forceinline__ void look_up(const Params& p, const Block& k, const Start& start, int who) {
   const int lane = threadIdx.x & 31;
   Segments<SEL, kKeys> it;
@@ -214,13 +214,13 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
   bool bad = false;
   while (uniform((int)it.next(p, s))) {
     const int32_t* table = p.table + s.b * p.table_stride;
-    const int32_t* list = SEL ? list_of(p, s.seq, s.head) : nullptr;
-    const int limit = SEL ? kv_limit(p, kv_given(p, s.b, s.seq)) : 0;
+    const int32_t* list = SEL ? list_of<BLK>(p, s.seq, s.head) : nullptr;
+    const int limit = SEL ? kv_limit(p, kv_given<BLK>(p, s.b, s.seq)) : 0;
     const int end = (int)min((long long)s.len.len, (long long)s.t1 * kKeys);
     auto entry = [&](int t, int i) -> int {  // key i of tile t: its list entry, or its position
       const int j = t * kKeys + i;
       if (t >= s.t1 || j >= end) return -1;
-      return SEL ? __ldg(list + (j >> p.block_shift)) : j;
+      return SEL ? __ldg(list + list_entry<BLK>(p, j)) : j;
     };
     int t = uniform(s.t0 + (int)((who + 3u - g % 3u) % 3u));
     const int t1 = uniform(s.t1);
@@ -231,7 +231,7 @@ __device__ __forceinline__ void look_up(const Params& p, const Block& k, const S
       int pos[4], pg[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        pos[i] = SEL ? list_position(p, e[i], t * kKeys + lane + 32 * i, limit, bad) : e[i];
+        pos[i] = SEL ? list_position<BLK>(p, e[i], t * kKeys + lane + 32 * i, limit, bad) : e[i];
         pg[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
       }
 #pragma unroll
@@ -872,7 +872,7 @@ __device__ __forceinline__ void rows(const Params& p, const Block& k, const Star
   }
 }
 
-template <int D, bool I8, bool SEL, int STEPS>
+template <int D, bool I8, bool SEL, int STEPS, bool BLK>
 __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, I8>;
   extern __shared__ unsigned char raw[];
@@ -944,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     if (warp == kMulWarp) {
       multiply<D, I8, SEL>(p, k, start, tmem);
     } else {
-      look_up<D, I8, SEL>(p, k, start, warp - kMetaWarp0);
+      look_up<D, I8, SEL, BLK>(p, k, start, warp - kMetaWarp0);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(I8 ? 80 : 64));
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   if (warp == kMulWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-template <int D, bool I8, bool SEL, int STEPS>
+template <int D, bool I8, bool SEL, int STEPS, bool BLK = false>
 cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
@@ -971,13 +971,17 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t stream) {
   cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
   cfg.numAttrs = launch_attributes(a, p.cluster);
-  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL, STEPS>, p);
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, I8, SEL, STEPS, BLK>, p);
 }
 template <bool I8>
 cudaError_t launch_held(const Params& p, int head_dim, bool selected, int grid, cudaStream_t stream) {
   // Up to 64 rows lie in the first 16 lanes of each quarter, one step of 16 rows a warp instead of two
   // (8 ragged trees of 32 rows a head: 195 us so, 230 in two steps).
   const bool one = p.rows <= 64;
+  if (p.blocks) {
+    if (head_dim == 64) return one ? launch<64, I8, true, 1, true>(p, grid, stream) : launch<64, I8, true, 2, true>(p, grid, stream);
+    return one ? launch<128, I8, true, 1, true>(p, grid, stream) : launch<128, I8, true, 2, true>(p, grid, stream);
+  }
   if (head_dim == 64) {
     if (selected) return one ? launch<64, I8, true, 1>(p, grid, stream) : launch<64, I8, true, 2>(p, grid, stream);
     return one ? launch<64, I8, false, 1>(p, grid, stream) : launch<64, I8, false, 2>(p, grid, stream);
@@ -986,10 +990,10 @@ cudaError_t launch_held(const Params& p, int head_dim, bool selected, int grid, 
   return one ? launch<128, I8, false, 1>(p, grid, stream) : launch<128, I8, false, 2>(p, grid, stream);
 }
 
-template <int D, bool I8, bool SEL>
+template <int D, bool I8, bool SEL, bool BLK = false>
 cudaError_t opt_in() {
-  const cudaError_t e = allow(tiles_kernel<D, I8, SEL, 1>, Shape<D, I8>::kSmem);
-  return e != cudaSuccess ? e : allow(tiles_kernel<D, I8, SEL, 2>, Shape<D, I8>::kSmem);
+  const cudaError_t e = allow(tiles_kernel<D, I8, SEL, 1, BLK>, Shape<D, I8>::kSmem);
+  return e != cudaSuccess ? e : allow(tiles_kernel<D, I8, SEL, 2, BLK>, Shape<D, I8>::kSmem);
 }
 template <bool I8>
 cudaError_t setup_held() {
@@ -997,6 +1001,8 @@ cudaError_t setup_held() {
   if (e == cudaSuccess) e = opt_in<64, I8, true>();
   if (e == cudaSuccess) e = opt_in<128, I8, false>();
   if (e == cudaSuccess) e = opt_in<128, I8, true>();
+  if (e == cudaSuccess) e = opt_in<64, I8, true, true>();
+  if (e == cudaSuccess) e = opt_in<128, I8, true, true>();
   return e;
 }
 

@@ -312,16 +312,19 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   __syncthreads();
   if (j0 < most) {
     float acc[4][4];
-    auto columns = [&](int t) {
+    auto columns = [&](int t) {  // (in two sums, which neither wait for each other nor round at one size)
       __syncwarp();
+      float odd[4] = {0.f, 0.f, 0.f, 0.f};
       acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.f;
       const unsigned char* row = mine + (8 * t + n) * S::kRow;
 #pragma unroll
       for (int i = 0; i < S::kPieces / 4; ++i) {
         const uint4 w = *reinterpret_cast<const uint4*>(row + (((c + 4 * i) ^ ((n & 1) << 2)) << 4));
         mma_bf16(acc[t], qs[2 * i * 32 + lane], w.x, w.y);
-        mma_bf16(acc[t], qs[(2 * i + 1) * 32 + lane], w.z, w.w);
+        mma_bf16(odd, qs[(2 * i + 1) * 32 + lane], w.z, w.w);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[t][e] += odd[e];
     };
     cp_wait<3>();
     columns(0);

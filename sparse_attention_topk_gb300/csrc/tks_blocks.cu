@@ -121,12 +121,12 @@ struct Extent<false> {
   }
 };
 
-constexpr int kBoundsThreads = 128, kBoundsPerSm = 7;
+constexpr int kBoundsThreads = 128, kBoundsPerSm = 4;
 
 // An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time.
 template <int D, bool I8>
 __global__ void __launch_bounds__(kBoundsThreads, kBoundsPerSm) bounds_kernel(const __grid_constant__ BoundsParams p) {
-  constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 8;
+  constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 16;
   __shared__ long long upto[kBoundsThreads];  // blocks of the sequences up to and with this one
   __shared__ int first_s[kBoundsThreads], end_s[kBoundsThreads];
   __shared__ long long warps_s[kBoundsThreads / 32];
@@ -498,6 +498,21 @@ __global__ void __launch_bounds__(kStreamThreads, 1) scores_stream_kernel(const 
   };
   for (int i = 0; i < S::kDepth - 1; ++i) issue();
 
+  // ---- while these are under way: the rows' lengths, a lane each, and the groups that no token of a sequence sees, a row each warp
+  const int out_rows = p.batch * p.tokens * p.kv_heads;
+  for (long long r = me * 32LL + lane; r < out_rows; r += warps * 32LL) {
+    const int bt = (int)r / p.kv_heads, b = bt / p.tokens;
+    bool bad = false;
+    const int blocks = blocks_seen(p, b, bt - b * p.tokens, bad);
+    if (bad) report(p.status, kStatRowLenBit);
+    if (p.row_len) p.row_len[r] = blocks;
+  }
+  if (counted && upto[kStreamCounted] < (long long)all * p.batch)
+    for (long long r = me; r < out_rows; r += warps) {
+      const int b = (int)r / p.kv_heads / p.tokens;
+      for (long long j = 8LL * (upto[b + 1] - upto[b]) + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
+    }
+
   // ---- scores
   Piece at{0, 0, 0, 0};
   uint4 a[S::kSteps];
@@ -572,20 +587,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) scores_stream_kernel(const 
   }
   cp_wait<0>();
 
-  // ---- the rows' lengths, a lane each, and the groups that no token of a sequence sees, a row each warp
-  const int out_rows = p.batch * p.tokens * p.kv_heads;
-  for (long long r = me * 32LL + lane; r < out_rows; r += warps * 32LL) {
-    const int bt = (int)r / p.kv_heads, b = bt / p.tokens;
-    bool bad = false;
-    const int blocks = blocks_seen(p, b, bt - b * p.tokens, bad);
-    if (bad) report(p.status, kStatRowLenBit);
-    if (p.row_len) p.row_len[r] = blocks;
-  }
-  if (counted && upto[kStreamCounted] < (long long)all * p.batch)
-    for (long long r = me; r < out_rows; r += warps) {
-      const int b = (int)r / p.kv_heads / p.tokens;
-      for (long long j = 8LL * (upto[b + 1] - upto[b]) + lane; j < p.n; j += 32) p.out[r * p.n + j] = -INFINITY;
-    }
 }
 
 void with_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a) {

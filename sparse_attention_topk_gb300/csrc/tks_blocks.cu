@@ -5,7 +5,20 @@
 //     q . k_i <= sum_d max(q_d lo_d, q_d hi_d) = sum_d max(q_d, 0) hi_d + min(q_d, 0) lo_d,
 // so a block's score is a product with a summed index of twice the head's size:
 // the queries' positive and negative parts against the largest and the least
-// values. Both parts are exact in bfloat16, as the products are in 32 bits.
+// values. Both parts are exact in bfloat16, as the products are in 32 bits; their
+// sum is in 32 bits.  Bounds are rounded to bfloat16, to nearest: a score is off by
+// at most 2^-8 of the sum of its terms' magnitudes for that.
+//
+// What bounds it: bytes, or the way to them.  Bounds read each key once, and
+// write 1/16 as much (blocks of 64 in 8 bits); scores read those, and write 4 bytes a block
+// and head. A decode step's calls are short: they are chains of lookups (lengths,
+// page, rows) that a lone call cannot hide, so what a chain does not need is loaded
+// beside it.
+// Measured: bounds of a prompt of 32,768 tokens of 8 int8 heads of 128 (37 MB) 10.2
+// us, 3.6 TB/s, 12.7 from memory; of 64 decode steps 3.7 us.  Scores of one token
+// of 32 heads on 8 over 2048 blocks (8.5 MB) 4.7 us; of 64 ragged sequences of 16
+// heads on 2 over up to 2048 blocks (71 MB) 14.8 us, 4.8 TB/s, 18.8 from memory (with a
+// thread block for every 128 blocks, as for one token, 20.7).
 
 #include <algorithm>
 
@@ -121,6 +134,7 @@ struct Extent<false> {
   }
 };
 
+// (Sixteen pieces a lane under way in four thread blocks an SM: 64 decode steps take 3.7 us, with eight in seven 5.1.)
 constexpr int kBoundsThreads = 128, kBoundsPerSm = 4;
 
 // An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time.
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   }
 }
 
-// The same for more blocks than the device scores at once: every warp takes an equal run of the axis of all (sequence,
+// The same for more blocks than the device holds at once, 128 to a thread block: every warp takes an equal run of the axis of all (sequence,
 // head)s' groups of eight blocks that any token sees, brings them through a ring of its own, and keeps the query rows of the
 // (sequence, head) that it is at in registers, so that warps wait for nobody.
 constexpr int kStreamWarps = 16, kStreamThreads = kStreamWarps * 32, kStreamCounted = 1024;

@@ -31,8 +31,8 @@
 // lookups, copies and joins that a lone call cannot hide.
 //
 // Lists of blocks (each head its own) are looked up by the chunk, not by the key: 512
-// tokens of 64 heads on 4 over 32 blocks of 64 int8 keys each (2048 lists a head, 1.1 GB out
-// of L2) 215 us, 266 by the key; one token over 32 blocks of 8 heads 8.5 us, 9.5 by
+// tokens of 64 heads on 4 over 32 blocks of 64 int8 keys each (2048 lists of 2048 keys, 1.1 GB
+// out of L2) 215 us, 266 by the key; one token over 32 blocks of 8 heads 8.5 us, 9.5 by
 // the key; 64 ragged tokens over 64 blocks of 32 bfloat16 keys of 2 heads 28.5 us.
 //
 // Layout.  A block is four warps; each takes every fourth chunk of the block's

@@ -16,7 +16,7 @@
 // of 16 prompts over up to 65,536 positions in pages of 64: 12.4 us (launch 0.9, children
 // looked up 0.8, marks 4, counts 2.8, tables 4); a pool of 8192 pages compacted 11.7 us; a
 // few short beams 7.4 us. Copies: 2048 pages of 135 KB 92 us, 6.0 TB/s; more under way
-// (5 thread blocks an SM 95, pieces of 32 KB in 4 of them 113) is slower.
+// (five or six thread blocks an SM instead of four) 95.
 
 #include <algorithm>
 

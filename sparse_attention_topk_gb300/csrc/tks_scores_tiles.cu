@@ -21,9 +21,9 @@
 // 128 cycles of the tensor cores and reads 12 KB of operands, 96 of the 128 bytes a
 // cycle; the ring's copies write 32 more, and the scores' stores go the same way.
 // Measured: 2048 tokens of 32 heads on 8 over 131,072 positions in blocks of 64 (68
-// Gflop, 134 MB of scores) 58 us, 1.17 PFLOP/s, 64 from memory; without the stores
-// 50, without maxima and stores 48, without the copies either some 45. (A pair of SMs on one
-// product would halve the reads of queries: not tried.)
+// Gflop, 134 MB of scores) 58 us, 1.17 PFLOP/s, 64 from memory; without most of the
+// stores 50, without maxima and stores 48. (A pair of SMs on one product would halve the
+// reads of queries: not tried.)
 //
 // Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
 // warp's role, which makes the waits on that warp run out; when all roles have

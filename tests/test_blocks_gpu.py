@@ -720,3 +720,43 @@ def test_scores_of_more_tiles_than_are_counted():
     for at in (0, 37, 100):
         few, n = tks.block_scores(q[at : at + 10], bounds, table[at : at + 10], lens[at : at + 10], 8, first=1)
         assert torch.equal(seen[at : at + 10], n) and torch.equal(many[at : at + 10], few)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages at the far end of a cache, and of bounds, of more than 2^31 elements."""
+    pages, page, heads, dim, block = 20_000, 64, 16, 128, 4
+    k, v = (torch.empty((pages, page, heads, dim), dtype=torch.int8, device="cuda") for _ in range(2))
+    scales = torch.empty((pages, page, heads, 2), device="cuda")
+    bounds = torch.empty((pages, page // block, heads, 2, dim), dtype=torch.bfloat16, device="cuda")
+    assert k.numel() > 2 ** 31 and bounds.numel() > 2 ** 30 and bounds.numel() * 2 > 2 ** 31
+    g = gen(41)
+    far = [pages - 1, pages - 2, pages - 3]
+    for pg in far[:2] + [0, 1]:
+        for c in (k, v):
+            c[pg] = torch.randint(-127, 128, c.shape[1:], dtype=torch.int8, device="cuda", generator=g)
+        scales[pg] = torch.rand(scales.shape[1:], device="cuda", generator=g) + 0.01
+    table, lens = ints([far[:2], [0, 1]]), ints([100, 128])
+    tks.cache_bounds(k, table, lens, bounds, scales=scales)
+    values = lambda c, plane, pgs: c[pgs].flatten(0, 1).float() * scales[pgs].flatten(0, 1)[..., plane, None]  # noqa: E731
+    for b, pgs in enumerate((far[:2], [0, 1])):
+        n = int(lens[b])
+        got = bounds[pgs].flatten(0, 1)[: n // block]
+        assert torch.equal(got, bounds_of(values(k, 0, pgs)[:n], block))
+    for tokens in (1, 20):  # few rows, and many
+        q = torch.randn(2, tokens, 32, dim, device="cuda", generator=g).to(torch.bfloat16)
+        kv = lens.unsqueeze(1).expand(2, tokens).contiguous()
+        scores, seen = tks.block_scores(q, bounds, table, kv, block)
+        picked = tks.topk_indices(scores.flatten(0, 2), 9, row_len=seen.flatten()).view(*seen.shape, 9)
+        out, lse = tks.block_attention(q, k, v, table, picked, block, kv_len=kv, scales=scales, return_lse=True)
+        for b, pgs in enumerate((far[:2], [0, 1])):
+            for h in (0, 15):
+                mine = bounds[pgs].flatten(0, 1)[: int(lens[b]) // block, h]
+                want, size = scores_of(q[b, 0, 2 * h : 2 * h + 2], mine)
+                assert ((scores[b, 0, h, : len(want)].double() - want).abs() <= 2 * dim * 2.0 ** -23 * size).all()
+                pos = (picked[b, 0, h].long().unsqueeze(1) * block + torch.arange(block, device="cuda")).flatten()
+                kk, vv = (values(c, plane, pgs)[pos, h].double() for c, plane in ((k, 0), (v, 1)))
+                check_rows(out[b, 0, 2 * h : 2 * h + 2], lse[b, 0, 2 * h : 2 * h + 2], q[b, 0, 2 * h : 2 * h + 2].double(), kk, vv,
+                           torch.ones(2, len(pos), dtype=torch.bool, device="cuda"), dim ** -0.5, "int8")
+    tks.cache_copy(ints([far[0], 1]), ints([2, far[2]]), k, v, scales=scales, bounds=bounds)
+    for c in (k, v, scales, bounds):
+        assert torch.equal(c[2], c[far[0]]) and torch.equal(c[far[2]], c[1])

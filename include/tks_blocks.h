@@ -90,7 +90,9 @@ int tks_cache_bounds(const tks_cache *cache, const tks_bounds *bounds, const int
  * kv_len is held to [0, n * block] and reported as TKS_E_ROW_LEN.  A block
  * whose page is outside [0, pages) scores -inf and is reported as TKS_E_INDEX.  A
  * score that is not a number becomes +inf, so that a key that is none is
- * attended to, as it would be without a selection.  Sizes that cannot be
+ * attended to, as it would be without a selection.  Where tokens * q_heads /
+ * kv_heads is more than 16, waits inside the kernel are bounded, as those of the
+ * attention calls are (TKS_E_TIMEOUT; scores are then undefined).  Sizes that cannot be
  * counted in 32 bits (batch * tokens * kv_heads, or batch * n / 8) return
  * TKS_E_TOO_LARGE.
  */

@@ -771,9 +771,16 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
     const int parts = (p.group_all + half - 1) / half, each = (p.group_all + parts - 1) / parts;
     for (p.first_of_group = 0; p.first_of_group < p.group_all && e == cudaSuccess; p.first_of_group += each) {
       p.group = std::min(each, p.group_all - p.first_of_group);
-      p.half_tokens = half / p.group;
-      p.tile_tokens = 2 * p.half_tokens;
-      p.token_tiles = (p.tokens - 1) / p.tile_tokens + 1;
+      p.group_room = 1 << log2_of(p.group);
+      // Whole tiles, or smaller ones where these leave SMs without work (2 * 300 tokens of 4 heads over 938 blocks: 17.5 us,
+      // 25 in whole ones).
+      for (p.half_rows = half;; p.half_rows /= 2) {
+        p.half_tokens = p.half_rows / p.group_room;
+        p.tile_tokens = 2 * p.half_tokens;
+        p.token_tiles = (p.tokens - 1) / p.tile_tokens + 1;
+        const int64_t tiles = (int64_t)p.batch * p.token_tiles * p.kv_heads * (((int64_t)n + kScoreTileBlocks - 1) / kScoreTileBlocks);
+        if (tiles >= place.sms || p.half_rows <= std::max(32, p.group_room)) break;
+      }
       e = launch_score_tiles(p, bounds->head_dim, place.sms, s);
       p.join = true;
       p.row_len = nullptr;

@@ -25,7 +25,8 @@ struct ScoreParams {
   bool join;                           // the largest of this launch's heads and of what is there
   int tile_tokens, token_tiles;        // tokens of a tile of query rows, and how many tiles a sequence has
   int chunks;                          // few rows: thread blocks of a unit
-  int half_tokens;                     // many rows: tokens of half a tile
+  int group_room;                      // many rows: columns of a token, a power of two,
+  int half_rows, half_tokens;          // columns of half a tile, and tokens
   long long spin_limit_ns;
   int test_skip_arrive;
 };

@@ -140,6 +140,11 @@ struct Items {
   }
 };
 
+// The rows of an item's query tile that are in use, up to the last one.
+__device__ __forceinline__ int used_rows(const ScoreParams& p, const Item& it) {
+  return it.tokens > p.half_tokens ? p.half_rows + (it.tokens - p.half_tokens) * p.group_room : it.tokens * p.group_room;
+}
+
 // Where a block's bounds lie, in elements, or -1 where its page is outside the cache.
 __device__ __forceinline__ long long bounds_at(const ScoreParams& p, int page, int j, int head, int dim) {
   if ((unsigned)page >= (unsigned)p.pages) return -1;
@@ -192,8 +197,8 @@ __device__ __forceinline__ void bring_bounds(const ScoreParams& p, const Block& 
   cp_wait<0>();
 }
 
-// Warps 12-14: an item's query rows, 64 elements of all of them after the other. Row 128 * h + i is row i of the h-th half of
-// the tile's tokens. The item before still needs what is there: meanwhile the first rows are loaded.
+// Warps 12-14: an item's query rows, 64 elements of all of them after the other. Row half_rows * h + i is row i of the h-th half
+// of the tile's tokens. The item before still needs what is there: meanwhile the first rows are loaded.
 template <int D>
 __device__ __forceinline__ void bring_queries(const ScoreParams& p, const Block& k, const Shared& s) {
   using S = Shape<D>;
@@ -205,25 +210,28 @@ __device__ __forceinline__ void bring_queries(const ScoreParams& p, const Block&
   Item it;
   for (unsigned n = 0; uniform((int)items.next(p, s, it)); ++n) {
     const __nv_bfloat16* q = score_query(p, it.b, it.t0, it.head, 0) + piece * 8;
+    const int rows = used_rows(p, it);
 #pragma unroll 1
     for (int part = 0; part < S::kParts; ++part) {
+      bool ready = n == 0;
 #pragma unroll 1
-      for (int r0 = t / 8; r0 < kRows; r0 += kAtOnce * kPer) {
+      for (int first = 0; first < rows; first += kAtOnce * kPer) {
         uint4 w[kAtOnce];
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-          const int r = r0 + i * kPer;
+          const int r = first + t / 8 + i * kPer;
           w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < kRows && s.token[r] < it.tokens) w[i] = __ldg(reinterpret_cast<const uint4*>(q + s.row[r] + part * 64));
+          if (r < rows && s.token[r] < it.tokens) w[i] = __ldg(reinterpret_cast<const uint4*>(q + s.row[r] + part * 64));
         }
-        if (r0 < kPer) {
+        if (!ready) {
           __syncwarp();
-          if (n > 0 && !k.wait(kQEmpty + part, (n - 1) & 1)) return;
+          if (!k.wait(kQEmpty + part, (n - 1) & 1)) return;
+          ready = true;
         }
 #pragma unroll
         for (int i = 0; i < kAtOnce; ++i) {
-          const int r = r0 + i * kPer;
-          if (r >= kRows) continue;
+          const int r = first + t / 8 + i * kPer;
+          if (r >= rows) continue;
           unsigned char* to = k.smem + part * S::kQueries + r * 128 + ((piece ^ (r & 7)) << 4);
           *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
           *reinterpret_cast<uint4*>(to + S::kParts * S::kQueries) =
@@ -261,9 +269,7 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
   uint32_t g = 0;  // tiles
   bool ok = true;
   for (unsigned n = 0; ok && uniform((int)items.next(p, s, it)); ++n) {
-    // columns in use, in sixteens
-    const int rows = it.tokens > p.half_tokens ? 128 + (it.tokens - p.half_tokens) * p.group : it.tokens * p.group;
-    const uint32_t idesc = uniform(instr(false, false, (rows + 15) / 16 * 16));
+    const uint32_t idesc = uniform(instr(false, false, (used_rows(p, it) + 15) / 16 * 16));
     const int tiles = uniform(it.j1 - it.j0);
 #pragma unroll 1
     for (int i = 0; i < tiles && ok; ++i, ++g) {
@@ -288,13 +294,14 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
 }
 
 // Warps 0-7: maxima over a token's heads, and the stores. Warps w and w + 4 have the lanes (blocks) 32w .. 32w + 31, and each
-// one half's columns. GROUP: heads of a token, or 0: any. 32 columns are on their way while the 32 before them are joined.
-// Most tiles hold blocks that all their tokens see: what their scores go through is kept short (the whole way for all of them
-// took 101 us for 2048 tokens of 32 heads over 2048 blocks, and 69 so).
+// one half's columns. GROUP: columns of a token, a power of two; 32: or some thirty-twos. (Heads that are not a power of two
+// are filled up with the last one again, which changes no maximum: of 7 heads and 4 * 200 tokens of size 64 over up to 1250
+// blocks 17 us, 49 where columns were counted.) 32 columns are on their way while the 32 before them are joined. Most tiles hold
+// blocks that all their tokens see: what their scores go through is kept short (the whole way for all of them took 101 us for
+// 2048 tokens of 32 heads over 2048 blocks, and 69 so).
 template <int GROUP>
 __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k, Shared& s, uint32_t tmem) {
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
-  const int group = GROUP ? GROUP : p.group;
   const bool plain = p.first == 0 && p.last == 0 && !p.join;
   Items items;
   items.begin(p, s);
@@ -303,7 +310,7 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
   uint32_t g = 0;
   while (uniform((int)items.next(p, s, it))) {
     const int tokens = uniform(min(p.half_tokens, it.tokens - half * p.half_tokens)), first = it.t0 + half * p.half_tokens;
-    const int chunks = tokens <= 0 ? 0 : uniform((tokens * group + 31) / 32);
+    const int chunks = tokens <= 0 ? 0 : uniform((tokens * p.group_room + 31) / 32), each = GROUP < 32 ? 1 : p.group_room / 32;
     int least = p.n;  // blocks that all of these tokens see
     __syncwarp();
     for (int t = lane; t < tokens; t += 32) {
@@ -323,7 +330,7 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
       if (i + 1 < j1) next_page = page_of(j + kBlocks);
       if (!k.wait(kSumFull + (g & 1), g >> 1 & 1)) return;
       tc_fence_after();
-      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (g & 1) * kRows + half * 128;
+      const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (g & 1) * kRows + half * p.half_rows;
       float* to = p.out + (((long long)it.b * p.tokens + first) * p.kv_heads + it.head) * p.n + j;
       const bool there = (unsigned)page < (unsigned)p.pages;
       const bool simple = plain && i * kBlocks + 32 * quarter + 32 <= least && __all_sync(0xffffffffu, there);
@@ -341,43 +348,37 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
         }
         to += stride;
       };
-      float top = -INFINITY;  // GROUP = 0: of the token's columns so far
-      int in = 0, t = 0;
+      float top = -INFINITY;  // of the token's columns so far
+      int in = 0;             // and how many thirty-twos
       auto join = [&](const uint32_t (&x)[32], int c) {
-        if (GROUP) {
-          constexpr int kG = GROUP ? GROUP : 1;
-          float m[32 / kG];
+        float m[32 / GROUP];
 #pragma unroll
-          for (int u = 0; u < 32 / kG; ++u) {
-            m[u] = __uint_as_float(x[u * kG]);
+        for (int u = 0; u < 32 / GROUP; ++u) {
+          m[u] = __uint_as_float(x[u * GROUP]);
 #pragma unroll
-            for (int e = 1; e < kG; ++e) m[u] = max_nan(m[u], __uint_as_float(x[u * kG + e]));
-          }
-          const int t0 = c * (32 / kG);
-          if (simple && t0 + 32 / kG <= tokens) {
+          for (int e = 1; e < GROUP; ++e) m[u] = max_nan(m[u], __uint_as_float(x[u * GROUP + e]));
+        }
+        int t0 = c * (32 / GROUP);
+        if (GROUP == 32) {
+          m[0] = max_nan(m[0], top);
+          top = m[0];
+          if (++in < each) return;
+          in = 0;
+          top = -INFINITY;
+          t0 = c / each;
+        }
+        if (simple && t0 + 32 / GROUP <= tokens) {
 #pragma unroll
-            for (int u = 0; u < 32 / kG; ++u) {
-              const float x = m[u] == m[u] ? m[u] : INFINITY;
-              if (p.stream_out) __stcs(to, x);
-              else *to = x;
-              to += stride;
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32 / kG; ++u)
-              if (t0 + u < tokens) put(m[u], t0 + u);
+          for (int u = 0; u < 32 / GROUP; ++u) {
+            const float x = m[u] == m[u] ? m[u] : INFINITY;
+            if (p.stream_out) __stcs(to, x);
+            else *to = x;
+            to += stride;
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            top = max_nan(top, __uint_as_float(x[e]));
-            if (++in == group) {
-              if (t < tokens) put(top, t);
-              ++t;
-              in = 0;
-              top = -INFINITY;
-            }
-          }
+          for (int u = 0; u < 32 / GROUP; ++u)
+            if (t0 + u < tokens) put(m[u], t0 + u);
         }
       };
       if (chunks > 0) {
@@ -444,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1) score_tiles_kernel(const __grid_c
   grid_launch_dependents();
 
   if (threadIdx.x < kRows) {
-    const int r = threadIdx.x, in = r & 127, tl = in / p.group, token = (r >> 7) * p.half_tokens + tl;
-    s.token[r] = tl < p.half_tokens ? token : INT_MAX;
-    s.row[r] = token * p.q_token + (in - tl * p.group) * p.q_head;
+    const int r = threadIdx.x, half = r / p.half_rows, in = r - half * p.half_rows, tl = in / p.group_room, token = half * p.half_tokens + tl;
+    s.token[r] = half < 2 ? token : INT_MAX;
+    s.row[r] = token * p.q_token + min(in - tl * p.group_room, p.group - 1) * p.q_head;
   }
   // how many tiles of blocks the tiles of tokens see
   const int units = p.batch * p.token_tiles, all = (p.n + kBlocks - 1) / kBlocks;
@@ -531,20 +532,20 @@ cudaError_t launch(const ScoreParams& p, int sms, cudaStream_t stream) {
 }
 template <int D>
 cudaError_t launch_dim(const ScoreParams& p, int sms, cudaStream_t stream) {
-  switch (p.group) {
+  switch (p.group_room) {
     case 1: return launch<D, 1>(p, sms, stream);
     case 2: return launch<D, 2>(p, sms, stream);
     case 4: return launch<D, 4>(p, sms, stream);
     case 8: return launch<D, 8>(p, sms, stream);
     case 16: return launch<D, 16>(p, sms, stream);
-    default: return launch<D, 0>(p, sms, stream);
+    default: return launch<D, 32>(p, sms, stream);
   }
 }
 template <int D>
 cudaError_t opt_in() {
   cudaError_t e = cudaSuccess;
-  for (auto kernel : {score_tiles_kernel<D, 0>, score_tiles_kernel<D, 1>, score_tiles_kernel<D, 2>, score_tiles_kernel<D, 4>, score_tiles_kernel<D, 8>,
-                      score_tiles_kernel<D, 16>})
+  for (auto kernel : {score_tiles_kernel<D, 1>, score_tiles_kernel<D, 2>, score_tiles_kernel<D, 4>, score_tiles_kernel<D, 8>, score_tiles_kernel<D, 16>,
+                      score_tiles_kernel<D, 32>})
     if (e == cudaSuccess) e = allow(kernel, Shape<D>::kSmem);
   return e;
 }

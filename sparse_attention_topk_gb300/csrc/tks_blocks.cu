@@ -21,6 +21,7 @@
 // thread block for every 128 blocks, as for one token, 20.7).
 
 #include <algorithm>
+#include <cmath>
 
 #include "tks_attn.cuh"
 #include "tks_attn_host.h"
@@ -256,7 +257,7 @@ struct ScoreShape {
   static_assert(16 * (kScoreCols + 1) * 4 <= kWarp, "a warp's scores fit where its bounds were");
 };
 
-// Up to 16 query rows of a key/value head (all tokens' together). A thread block takes one (sequence, head) and 128 blocks,
+// Up to 16 query rows of a key/value head: a tile of tokens. A thread block takes one (sequence, tile, head) and 128 blocks,
 // a warp 32 of them, whose copies to shared memory are all under way at once, and start before the queries and
 // lengths are there. The query rows lie in shared memory as matrix fragments: of product step s, lane 4n + c takes the
 // elements that it has of column n's bytes: pieces c, c + 4, ... (XOR-swizzled, so that eight lanes' reads do not meet).
@@ -270,7 +271,8 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   uint4* qs = reinterpret_cast<uint4*>(smem + kScoreWarps * S::kWarp);
   const unsigned unit = blockIdx.x / p.chunks;
   const int chunk = blockIdx.x - unit * p.chunks;
-  const int head = unit % p.kv_heads, b = unit / p.kv_heads, rows = p.tokens * p.group;
+  const int head = unit % p.kv_heads, bt = unit / p.kv_heads, b = bt / p.token_tiles, t0 = (bt - b * p.token_tiles) * p.tile_tokens;
+  const int tokens = min(p.tile_tokens, p.tokens - t0), rows = tokens * p.group;
   const int32_t* table = p.table + b * p.table_stride;
   // the lane's pieces of a row, and its first row, in the copies
   constexpr int kPer = 32 / S::kPieces > 0 ? 32 / S::kPieces : 1;  // rows that 32 lanes cover
@@ -283,19 +285,19 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   const int page = j0 < p.n && col < p.n ? __ldg(table + (col >> p.of_page_shift)) : -1;
   // the tokens' lengths, a lane each (16 at most), and the query rows
   bool bad = false;
-  const int seen = lane < p.tokens ? blocks_seen(p, b, lane, bad) : 0;
+  const int seen = lane < tokens ? blocks_seen(p, b, t0 + lane, bad) : 0;
   for (int x = threadIdx.x; x < S::kSteps * 32; x += kScoreThreads) {
     const int l = x & 31, s = x >> 5, r = l >> 2;
     // elements of the doubled index: the first D are the least's, with the queries' negative parts
     const int d = 8 * ((l & 3) + 4 * (s >> 1)) + 4 * (s & 1);
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     if (r < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, r / p.group, head, r % p.group) + d % D));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, t0 + r / p.group, head, r % p.group) + d % D));
       w.x = part_of_pair(y.x, d >= D);
       w.z = part_of_pair(y.y, d >= D);
     }
     if (r + 8 < rows) {
-      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(score_query(p, b, t0 + (r + 8) / p.group, head, (r + 8) % p.group) + d % D));
       w.y = part_of_pair(y.x, d >= D);
       w.w = part_of_pair(y.y, d >= D);
     }
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
   }
   if (warp == 0 && chunk == 0) {
     if (bad) report(p.status, kStatRowLenBit);
-    if (p.row_len && lane < p.tokens) p.row_len[((long long)b * p.tokens + lane) * p.kv_heads + head] = seen;
+    if (p.row_len && lane < tokens) p.row_len[((long long)b * p.tokens + t0 + lane) * p.kv_heads + head] = seen;
   }
   __syncthreads();
   if (j0 < most) {
@@ -356,12 +358,12 @@ __global__ void __launch_bounds__(kScoreThreads) scores_kernel(const __grid_cons
     __syncwarp();
   }
   if (j0 >= p.n) return;
-  for (int t = 0; t < p.tokens; ++t) {
+  for (int t = 0; t < tokens; ++t) {
     const int blocks = __shfl_sync(0xffffffffu, seen, t);
     float x = -INFINITY;
     if (j0 < most)
       for (int r = t * p.group; r < (t + 1) * p.group; ++r) x = max_nan(x, tile[r][lane]);
-    if (col < p.n) p.out[(((long long)b * p.tokens + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, blocks);
+    if (col < p.n) p.out[(((long long)b * p.tokens + t0 + t) * p.kv_heads + head) * p.n + col] = !ok ? -INFINITY : final_score(p, x, col, blocks);
   }
 }
 
@@ -754,15 +756,21 @@ extern "C" int tks_block_scores(const tks_bounds* bounds, const tks_queries* que
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e = cudaSuccess;
   std::lock_guard<std::mutex> lock(*place.order);
-  if ((int64_t)p.tokens * p.group <= 16) {
-    const int64_t units = (int64_t)p.batch * p.kv_heads, tiles = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads);
-    const bool wide = bounds->head_dim == 128;
-    if (units * tiles <= place.sms * 3) {
-      p.chunks = (int)tiles;
-      e = wide ? launch_scores<128>(p, (int)(units * tiles), s) : launch_scores<64>(p, (int)(units * tiles), s);
-    } else {
-      e = wide ? launch_scores_stream<128>(p, place.sms, s) : launch_scores_stream<64>(p, place.sms, s);
-    }
+  // Three ways: at once (a thread block for each 16 rows and 128 blocks, three an SM, some 6.5 us each); as streams, where all
+  // of a head's rows are 16 at most and there is more than one wave of these; as tiles on the tensor cores, whose start takes
+  // some 8 us, a tile of queries 3.5 and one of blocks 1.1. What is likely to take longer is left (8 * 8 drafts of 32 heads
+  // on 8 over up to 1024 blocks: 17 us at once, 10.3 as tiles; 62 * 18 tokens of 8 heads over one block 19.5 and 22).
+  const bool wide = bounds->head_dim == 128, few = (int64_t)p.tokens * p.group <= 16;
+  const int64_t chunks = std::max<int64_t>(1, ((int64_t)n + kScoreThreads - 1) / kScoreThreads), heads = (int64_t)p.batch * p.kv_heads;
+  p.tile_tokens = std::min(p.tokens, std::max(1, 16 / p.group));
+  p.token_tiles = (p.tokens - 1) / p.tile_tokens + 1;
+  p.chunks = (int)chunks;
+  const double at_once = (double)heads * p.token_tiles * chunks, of_tile = std::max(1, 2 * (kScoreTileRows / 2 / p.group)),
+               as_tiles = 8 + heads * std::ceil(p.tokens / of_tile) * (3.5 + 1.1 * chunks) / place.sms;
+  if (p.group <= 16 && (few ? at_once <= 3 * place.sms : at_once < 65536 && 2 + 2.2 * at_once / place.sms < as_tiles)) {
+    e = wide ? launch_scores<128>(p, (int)at_once, s) : launch_scores<64>(p, (int)at_once, s);
+  } else if (few) {
+    e = wide ? launch_scores_stream<128>(p, place.sms, s) : launch_scores_stream<64>(p, place.sms, s);
   } else {
     // (134 MB of scores, stored as what is not read again soon: 58 us, 63 without; fewer stay for the selector)
     p.stream_out = (int64_t)p.batch * p.tokens * p.kv_heads * n > (64 << 20) / 4;

@@ -482,6 +482,7 @@ struct CopyParams {
   int pages, tokens, heads, run;       // run: contiguous 16-byte pieces; of which a page has tokens * heads
   long long page_words[2];             // scales and bounds: words of 8 bytes of a page
   int chunks[4];                       // of a page, and of the plane
+  int scale_pieces, all_pieces;        // flat: of a page's scales, and of all
   int all_chunks;
   const int32_t *src, *dst, *count;
   int n;
@@ -490,8 +491,8 @@ struct CopyParams {
 
 constexpr int kCopyThreads = 256, kPer = 4, kChunk = kCopyThreads * kPer;  // pieces (words) of a chunk
 
-// A thread block takes one chunk of one plane of one pair after the other. FLAT: a page's keys are one run (and its values):
-// the place of a piece needs no divisions.
+// A thread block takes one chunk of one plane of one pair after the other. FLAT: a page's keys are one run, and its values, and its
+// scales and bounds are whole 16-byte pieces: the pieces of all planes are one axis, and their places need no divisions.
 template <bool FLAT>
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
   grid_wait();
@@ -515,6 +516,38 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       if (threadIdx.x == 0) report(p.status, kStatIndexBit);
       continue;
     }
+    if (FLAT) {
+      uint4 x[kPer];
+      uint4* to[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        int v = chunk * kChunk + k * kCopyThreads + threadIdx.x;
+        to[k] = nullptr;
+        if (v >= p.all_pieces) continue;
+        unsigned char* base = p.base[0];
+        long long page = p.page_b;
+        if (v >= p.run) {
+          v -= p.run;
+          base = p.base[1];
+          if (v >= p.run) {
+            v -= p.run;
+            base = p.base[2];
+            page = p.page_words[0] * 8;
+            if (v >= p.scale_pieces) {
+              v -= p.scale_pieces;
+              base = p.base[3];
+              page = p.page_words[1] * 8;
+            }
+          }
+        }
+        x[k] = __ldg(reinterpret_cast<const uint4*>(base + src * page) + v);
+        to[k] = reinterpret_cast<uint4*>(base + dst * page) + v;
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k)
+        if (to[k]) *to[k] = x[k];
+      continue;
+    }
     int plane = 0;
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -524,7 +557,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       }
     if (plane < 2) {
       unsigned char* base = plane ? p.base[1] : p.base[0];
-      const int pieces = FLAT ? p.run : p.tokens * p.heads * p.run;
+      const int pieces = p.tokens * p.heads * p.run;
       uint4 x[kPer];
       long long at[kPer];
 #pragma unroll
@@ -532,12 +565,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
         const int v = chunk * kChunk + k * kCopyThreads + threadIdx.x;
         at[k] = -1;
         if (v < pieces) {
-          if (FLAT) {
-            at[k] = v * 16LL;
-          } else {
-            const int row = v / p.run, token = row / p.heads;
-            at[k] = token * p.token_b + (row - token * p.heads) * p.head_b + (v - row * p.run) * 16LL;
-          }
+          const int row = v / p.run, token = row / p.heads;
+          at[k] = token * p.token_b + (row - token * p.heads) * p.head_b + (v - row * p.run) * 16LL;
           x[k] = __ldg(reinterpret_cast<const uint4*>(base + src * p.page_b + at[k]));
         }
       }
@@ -687,7 +716,14 @@ extern "C" int tks_cache_copy(const tks_cache* cache, const tks_bounds* bounds, 
   p.page_words[1] = bounds ? (long long)(bounds->page_size / bounds->block) * bounds->kv_heads * bounds->head_dim / 2 : 0;
   p.chunks[0] = p.chunks[1] = (int)((pieces + kChunk - 1) / kChunk);
   for (int i = 0; i < 2; ++i) p.chunks[2 + i] = (int)((p.page_words[i] + kChunk - 1) / kChunk);
-  const long long all = 2LL * p.chunks[0] + p.chunks[2] + p.chunks[3];
+  long long all = 2LL * p.chunks[0] + p.chunks[2] + p.chunks[3];
+  const long long all_pieces = 2 * (long long)pieces + (p.page_words[0] + p.page_words[1]) / 2;
+  const bool flat = p.tokens == 1 && p.heads == 1 && p.page_words[0] % 2 == 0 && aligned(p.base[2], 16) && all_pieces < INT32_MAX - kChunk;
+  if (flat) {
+    p.scale_pieces = (int)(p.page_words[0] / 2);
+    p.all_pieces = (int)all_pieces;
+    all = (all_pieces + kChunk - 1) / kChunk;
+  }
   p.all_chunks = (int)all;
   p.src = src;
   p.dst = dst;
@@ -705,7 +741,6 @@ extern "C" int tks_cache_copy(const tks_cache* cache, const tks_bounds* bounds, 
   cudaLaunchAttribute a[1] = {};
   cfg.attrs = a;
   cfg.numAttrs = launch_attributes(a, 0);
-  const bool flat = p.tokens == 1 && p.heads == 1;
   if ((flat ? cudaLaunchKernelEx(&cfg, copy_kernel<true>, p) : cudaLaunchKernelEx(&cfg, copy_kernel<false>, p)) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

@@ -197,47 +197,53 @@ __device__ __forceinline__ void bring_bounds(const ScoreParams& p, const Block& 
   cp_wait<0>();
 }
 
+// 64 elements of the first N * kQueryPer query rows at most, of `rows` in use, and what is waited for before they are stored.
+constexpr int kQueryPer = kQueryWarps * 32 / 8;  // rows that the threads cover, eight pieces each
+template <int D, int N, typename F>
+__device__ __forceinline__ bool bring_rows(const Block& k, const Shared& s, const __nv_bfloat16* q, int rows, int tokens, int part, F&& wait) {
+  using S = Shape<D>;
+  const int t = threadIdx.x - kQuery0 * 32, piece = t % 8;
+  uint4 w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = t / 8 + i * kQueryPer;
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows && s.token[r] < tokens) w[i] = __ldg(reinterpret_cast<const uint4*>(q + s.row[r] + part * 64 + piece * 8));
+  }
+  __syncwarp();
+  if (!wait()) return false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = t / 8 + i * kQueryPer;
+    if (r >= rows) continue;
+    unsigned char* to = k.smem + part * S::kQueries + r * 128 + ((piece ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
+    *reinterpret_cast<uint4*>(to + S::kParts * S::kQueries) =
+        make_uint4(part_of_pair(w[i].x, true), part_of_pair(w[i].y, true), part_of_pair(w[i].z, true), part_of_pair(w[i].w, true));
+  }
+  return true;
+}
+
 // Warps 12-14: an item's query rows, 64 elements of all of them after the other. Row half_rows * h + i is row i of the h-th half
 // of the tile's tokens. The item before still needs what is there: meanwhile the first rows are loaded.
 template <int D>
 __device__ __forceinline__ void bring_queries(const ScoreParams& p, const Block& k, const Shared& s) {
   using S = Shape<D>;
-  constexpr int kPer = kQueryWarps * 32 / 8, kAtOnce = 11;  // rows that the threads cover, eight pieces each; how often at once
-  static_assert(2 * kAtOnce * kPer >= kRows, "two passes bring all rows");
-  const int t = threadIdx.x - kQuery0 * 32, piece = t % 8;
+  constexpr int kSome = 4;
+  static_assert(22 * kQueryPer >= kRows, "all rows at once");
   Items items;
   items.begin(p, s);
   Item it;
   for (unsigned n = 0; uniform((int)items.next(p, s, it)); ++n) {
-    const __nv_bfloat16* q = score_query(p, it.b, it.t0, it.head, 0) + piece * 8;
-    const int rows = used_rows(p, it);
+    const __nv_bfloat16* q = score_query(p, it.b, it.t0, it.head, 0);
+    const int rows = uniform(used_rows(p, it));
 #pragma unroll 1
     for (int part = 0; part < S::kParts; ++part) {
-      bool ready = n == 0;
-#pragma unroll 1
-      for (int first = 0; first < rows; first += kAtOnce * kPer) {
-        uint4 w[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int r = first + t / 8 + i * kPer;
-          w[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows && s.token[r] < it.tokens) w[i] = __ldg(reinterpret_cast<const uint4*>(q + s.row[r] + part * 64));
-        }
-        if (!ready) {
-          __syncwarp();
-          if (!k.wait(kQEmpty + part, (n - 1) & 1)) return;
-          ready = true;
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-          const int r = first + t / 8 + i * kPer;
-          if (r >= rows) continue;
-          unsigned char* to = k.smem + part * S::kQueries + r * 128 + ((piece ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(to) = make_uint4(part_of_pair(w[i].x, false), part_of_pair(w[i].y, false), part_of_pair(w[i].z, false), part_of_pair(w[i].w, false));
-          *reinterpret_cast<uint4*>(to + S::kParts * S::kQueries) =
-              make_uint4(part_of_pair(w[i].x, true), part_of_pair(w[i].y, true), part_of_pair(w[i].z, true), part_of_pair(w[i].w, true));
-        }
-      }
+      auto wait = [&] { return n == 0 || k.wait(kQEmpty + part, (n - 1) & 1); };
+      if (!(rows <= kSome * kQueryPer ? bring_rows<D, kSome>(k, s, q, rows, it.tokens, part, wait)
+            : rows <= 11 * kQueryPer  ? bring_rows<D, 11>(k, s, q, rows, it.tokens, part, wait)
+                                      : bring_rows<D, 22>(k, s, q, rows, it.tokens, part, wait)))
+        return;
       __syncwarp();
       bar_arrive(k.bar(kQFull + part));
     }

@@ -339,13 +339,24 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   if ((keys / tile_keys + 1) * p.kv_heads * p.row_tiles > INT32_MAX) return TKS_E_TOO_LARGE;
   const long long units = (long long)p.seqs * p.kv_heads * p.row_tiles;
   if (units > INT32_MAX) return TKS_E_TOO_LARGE;
+  bool whole = false;  // no unit is split
   int grid = !few ? d.sms : d.sms * (selected && rows_many(p, i8) ? kRowsManyPerSm : kRowsBlocksPerSm);
   p.plan = reinterpret_cast<Split*>(ws.ptr + kPlanOffset);
   if (selected) {
     const long long tiles = std::max(1, (p.k_sel + tile_keys - 1) / tile_keys);
     p.split.set(units * tiles, (unsigned)tiles, units, grid);
+    // Lists of blocks in more units than blocks, few rows each: whole units, where the last round's empty places cost less than
+    // a segment more for each block and the joining kernel (8 and 7 tiles: 6.4 and 5.4 us, a tile 0.78): 512 tokens of 64
+    // heads on 4 over 32 blocks of 64 208 us so, 215 as equal runs; 608 over one block 51 and 56.
+    whole = few && p.blocks && units >= grid && ((units + grid - 1) / grid * grid - units) * (8 + tiles) <= 15LL * grid;
+    if (whole) {
+      p.split.q = (unsigned)(units / grid);
+      p.split.r = (unsigned)(units % grid);
+      p.split.step = (unsigned)tiles;
+      p.split.share = 0;
+    }
   }
-  const int cluster = selected && !few ? 0 : cluster_of(units, (keys + tile_keys - 1) / tile_keys, tile_keys, grid);
+  const int cluster = whole || (selected && !few) ? 0 : cluster_of(units, (keys + tile_keys - 1) / tile_keys, tile_keys, grid);
   if (cluster > 0) {
     p.cluster = cluster;
     p.split.share = (unsigned)cluster;
@@ -354,7 +365,7 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
   std::lock_guard<std::mutex> lock(*ws.order);
   if (few) {
     e = launch_rows(p, c->head_dim, i8, selected, grid, s);
-    if (e == cudaSuccess && !cluster) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
+    if (e == cudaSuccess && !cluster && !whole) e = launch_combine<kRowsTile, kRowsKeys>(p, c->head_dim, selected, grid, s);
   } else {
     e = launch_tiles(p, c->head_dim, i8, selected, grid, s);
     if (e == cudaSuccess && !cluster) e = launch_combine<kTilesRows, kTilesKeys>(p, c->head_dim, selected, grid, s);

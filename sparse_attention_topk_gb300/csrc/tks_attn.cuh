@@ -267,8 +267,12 @@ __device__ __forceinline__ void find_start(const Params& p, Start* st) {
     }
     return;
   }
-  const long long w = split.start(block);
-  const unsigned left = split.q + ((unsigned)block < split.r ? 1 : 0);
+  long long w = split.start(block);
+  unsigned left = split.q + ((unsigned)block < split.r ? 1 : 0);
+  if (SEL && split.step) {  // (whole units)
+    w *= split.step;
+    left *= split.step;
+  }
   if (SEL) {
     if (lane == 0) {
       const unsigned each = per * (unsigned)tiles_of<TK>(p.k_sel);

@@ -53,6 +53,7 @@ struct Split {
   long long W;
   unsigned share;  // blocks of a unit (even shares), or 0 (one run)
   unsigned q, r;   // one run: tiles of a block, q or, for the first r blocks, q + 1
+  unsigned step;   // (lists of blocks: times this; 0: 1)
 
   __host__ __device__ void set(long long w, unsigned longest, long long units, int G) {
     W = w;

@@ -83,6 +83,11 @@ struct Shape {
   // Piece swizzles: the eight lanes of a phase read pieces c..c+3 of rows n
   // and n+1 (keys), or pieces n, n+1 of rows 0, 2, 4, 6 (values).
   static __device__ __forceinline__ int ksw(int r) { return kPieces >= 8 ? (r & 1) << 2 : 0; }
+  // Where element d (a multiple of four) of row r of a warp's output lies in its row: a warp's stores have one float4 of eight
+  // rows and of four places 2 * kEV apart, which would all lie in the same banks (1800 of a short list's 6000 cycles).
+  static __device__ __forceinline__ int osw(int r, int d) {
+    return d ^ (kEV == 16 ? ((d >> 5 & 3) | (r & 1) << 2) << 2 : ((d >> 5 & 1) | (r & 1) << 1) << 2);
+  }
   static __device__ __forceinline__ int vsw(int r) {
     return kPieces >= 8 ? ((r >> 1) & 3) << 1 : ((r >> 1) & 1) << 1;
   }
@@ -594,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
 #pragma unroll
         for (int j = 0; j < S::kEV; j += 4) {
           const int d = S::kEV * (2 * c + e + 8 * h) + j, i = h * S::kEV + j;
-          *reinterpret_cast<float4*>(om + n * D + d) = make_float4(acc[i][e], acc[i + 1][e], acc[i + 2][e], acc[i + 3][e]);
-          *reinterpret_cast<float4*>(om + (n + 8) * D + d) = make_float4(acc[i][2 + e], acc[i + 1][2 + e], acc[i + 2][2 + e], acc[i + 3][2 + e]);
+          *reinterpret_cast<float4*>(om + n * D + S::osw(n, d)) = make_float4(acc[i][e], acc[i + 1][e], acc[i + 2][e], acc[i + 3][e]);
+          *reinterpret_cast<float4*>(om + (n + 8) * D + S::osw(n, d)) = make_float4(acc[i][2 + e], acc[i + 1][2 + e], acc[i + 2][2 + e], acc[i + 3][2 + e]);
         }
     if (c == 0) {
       ml_s[warp][n] = make_float2(m[0], l[0]);
@@ -624,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, I8, SEL && PAGED, MANY>::kP
       for (int i = 0; i < kWarps; ++i)
         if (active && q[i].y != 0.f) {  // (a warp whose keys are all unseen has a sum of zero)
           const float f = q[i].x == mm ? 1.f : ex2(q[i].x - mm);
-          const float4 a = *reinterpret_cast<const float4*>(om0 + (i * 16 + r) * D + d);
+          const float4 a = *reinterpret_cast<const float4*>(om0 + (i * 16 + r) * D + S::osw(r, d));
           ll += f * q[i].y;
           o.x += f * a.x; o.y += f * a.y; o.z += f * a.z; o.w += f * a.w;
         }

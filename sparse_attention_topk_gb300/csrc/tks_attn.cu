@@ -346,9 +346,10 @@ int launch(Params& p, const tks_cache* c, bool selected, void* stream) {
     const long long tiles = std::max(1, (p.k_sel + tile_keys - 1) / tile_keys);
     p.split.set(units * tiles, (unsigned)tiles, units, grid);
     // Lists of blocks in more units than blocks, few rows each: whole units, where the last round's empty places cost less than
-    // a segment more for each block and the joining kernel (8 and 7 tiles: 6.4 and 5.4 us, a tile 0.78): 512 tokens of 64
-    // heads on 4 over 32 blocks of 64 208 us so, 215 as equal runs; 608 over one block 51 and 56.
-    whole = few && p.blocks && units >= grid && ((units + grid - 1) / grid * grid - units) * (8 + tiles) <= 15LL * grid;
+    // a segment more for each block and the joining kernel (5 and 7 tiles: 3.5 and 5.4 us, a tile 0.78; 512 tokens of 64
+    // heads on 4 over 32 blocks of 64 took 208 us so and 215 as equal runs, 608 over one block 51 and 56, before the joins'
+    // stores were free of bank conflicts).
+    whole = few && p.blocks && units >= grid && ((units + grid - 1) / grid * grid - units) * (5 + tiles) <= 12LL * grid;
     if (whole) {
       p.split.q = (unsigned)(units / grid);
       p.split.r = (unsigned)(units % grid);

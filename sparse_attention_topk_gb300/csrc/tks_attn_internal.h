@@ -128,9 +128,9 @@ inline bool blocks_by_chunks(const Params& p, bool i8) {
   return p.blocks && p.block_shift >= chunk && p.page_shift >= chunk;
 }
 // Lists of bfloat16 blocks that together are longer than the sequence come from L2, which answers sooner than memory: more
-// warps with less under way each (512 tokens of 64 heads on 4 over 32 blocks of 64: 233 us so, 260 otherwise). Of memory, or
-// in 8 bits, they do not help (64 tokens over 64 blocks of int8 of 8 heads: 156 us so, 125 otherwise; the former in int8 212
-// and 215).
+// warps with less under way each (512 tokens of 64 heads on 4 over 32 blocks of 64: 228 us so, some 255 otherwise). Of memory,
+// or in 8 bits, they do not help (64 tokens over 64 blocks of int8 of 8 heads: 156 us so, 125 otherwise; the former in int8
+// 199 and 198).
 constexpr int kRowsManyPerSm = 3;
 inline bool rows_many(const Params& p, bool i8) {
   return !i8 && blocks_by_chunks(p, i8) && (long long)p.tokens * p.k_sel >= (long long)p.table_pages << p.page_shift;

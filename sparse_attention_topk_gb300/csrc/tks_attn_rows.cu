@@ -27,13 +27,14 @@
 // Measured: one token over 1,048,576 positions of int8 (4 heads of 128, 1.11 GB)
 // 179-195 us, 5.7-6.2 TB/s, of bfloat16 354 us, 6.1 TB/s; 8 ragged trees of 4
 // drafts over up to 65,536 positions of int8 (16 rows a head, 0.6 GB) 122 us, 4.9
-// TB/s; one token over 4096 (8 heads, 8.7 MB) 11.6 us, bound by the chain of
+// TB/s; one token over 4096 (8 heads, 8.7 MB) 11.0 us, bound by the chain of
 // lookups, copies and joins that a lone call cannot hide.
 //
-// Lists of blocks (each head its own) are looked up by the chunk, not by the key: 512
-// tokens of 64 heads on 4 over 32 blocks of 64 int8 keys each (2048 lists of 2048 keys, 1.1 GB
-// out of L2) 215 us, 266 by the key; one token over 32 blocks of 8 heads 8.5 us, 9.5 by
-// the key; 64 ragged tokens over 64 blocks of 32 bfloat16 keys of 2 heads 28.5 us.
+// Lists of blocks (each head its own) are looked up by the chunk, not by the key (512
+// tokens of 64 heads on 4 over 32 blocks of 64 int8 keys: a fifth less time): these, 2048
+// lists of 2048 keys, 1.1 GB out of L2, 198 us; one token over 32 blocks of 8 heads 7.8 us; 64
+// ragged tokens over 64 blocks of 32 bfloat16 keys of 2 heads 28.9 us. A list's start and end
+// cost 3.5 us of a block, 64 of its keys 0.78.
 //
 // Layout.  A block is four warps; each takes every fourth chunk of the block's
 // segment (32 keys of int8, 16 of bfloat16: 8 KB), keeps its own maximum, sum and

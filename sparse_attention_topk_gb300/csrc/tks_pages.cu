@@ -9,14 +9,16 @@
 // kind lie before each 32 (and their bits); and the tables, for which the r-th free
 // page, or the number of moving pages before one, is looked up in those. What
 // the passes leave for each other lies in the caller's scratch buffer, so that
-// nothing is shared between calls.
+// nothing is shared between calls. Small tables are made by a single thread block,
+// which keeps it in shared memory.
 //
 // What bounds it: latency, of launch, barriers and loads that wait for each other; and,
 // where rows are long, the scattered stores of who holds a page. Measured: 64 beams
 // of 16 prompts over up to 65,536 positions in pages of 64: 12.4 us (launch 0.9, children
 // looked up 0.8, marks 4, counts 2.8, tables 4); a pool of 8192 pages compacted 11.7 us; a
-// few short beams 7.4 us. Copies: 2048 pages of 135 KB 92 us, 6.0 TB/s; more under way
-// (five or six thread blocks an SM instead of four) 95.
+// few short beams 4.2 us (7.4 by a cluster), a pool of 639 pages compacted 5.5 (9.2).
+// Copies: 2048 pages of 135 KB 92 us, 6.0 TB/s; more under way (five or six thread blocks
+// an SM instead of four) 95.
 
 #include <algorithm>
 
@@ -27,7 +29,7 @@ namespace tks {
 namespace attn {
 namespace {
 
-constexpr int kBlocks = 8, kThreads = 1024, kWarps = kThreads / 32, kAllWarps = kBlocks * kWarps;
+constexpr int kBlocks = 8, kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kFree = 0x7fffffff, kShared = -1;  // a page that nobody holds; one that is held and not to be written to
 
 // Of 32 pages: those that are free (fork), or held (compact), those that move (compact), and how many of either lie before
@@ -54,36 +56,75 @@ struct PlanParams {
   unsigned* status;
 };
 
-// The cluster's threads; its barrier also orders their accesses to global memory.
+// Who makes the tables: a cluster, whose barrier also orders its accesses to global memory, or (ONE) a single thread block, which
+// keeps what the passes leave for each other in shared memory.
+constexpr int kOnePages = 4096, kOneRows = 32;  // at most
+template <bool ONE>
 struct Team {
-  int rank, warp, lane, thread;  // of the cluster, warps and threads of all its blocks
+  static constexpr int kBlocksOf = ONE ? 1 : kBlocks, kAllWarps = kBlocksOf * kWarps, kAllThreads = kBlocksOf * kThreads;
+  int rank, warp, lane, thread;  // warps and threads of all its blocks
   __device__ __forceinline__ Team() {
-    rank = blockIdx.x;
+    rank = ONE ? 0 : blockIdx.x;
     warp = rank * kWarps + (threadIdx.x >> 5);
     lane = threadIdx.x & 31;
     thread = rank * kThreads + threadIdx.x;
   }
   __device__ __forceinline__ void meet() const {
-    __syncwarp();
-    cluster_sync();
+    if (ONE) {
+      __syncthreads();
+    } else {
+      __syncwarp();
+      cluster_sync();
+    }
   }
 };
+template <bool ONE>
+struct Store {
+  int32_t *owner, *dst;
+  Tally* tallies;
+  __device__ __forceinline__ Store(const PlanParams& p) : owner(p.owner), dst(p.dst), tallies(p.tallies) {}
+  template <typename T>
+  __device__ __forceinline__ T read(const T* at) const { return __ldcg(at); }
+};
+template <>
+struct Store<true> {
+  int32_t *owner, *dst;
+  Tally* tallies;
+  __device__ __forceinline__ Store(const PlanParams& p) {
+    __shared__ int32_t words[kOnePages + kOnePages / 2];
+    __shared__ Tally each32[kOnePages / 32];
+    owner = words;
+    dst = words + kOnePages;
+    tallies = each32;
+  }
+  template <typename T>
+  __device__ __forceinline__ T read(const T* at) const { return *at; }
+};
 
-// Of two numbers that each warp of the cluster has counted: the sums over the warps before each one, in shared memory.
+// Of two numbers that each warp has counted: the sums over the warps before each one, in shared memory.
+template <bool ONE>
 struct Sums {
+  static constexpr int kAllWarps = Team<ONE>::kAllWarps;
   int a[kAllWarps + 1], b[kAllWarps + 1], warps[2][kAllWarps / 32];
 };
-__device__ __forceinline__ void sum_up(const Team& me, const PlanParams& p, Sums& s, int a, int b) {
+template <bool ONE>
+__device__ __forceinline__ void sum_up(const Team<ONE>& me, const PlanParams& p, Sums<ONE>& s, int a, int b) {
+  constexpr int kAllWarps = Team<ONE>::kAllWarps;
   if (me.lane == 0) {
-    p.sums[me.warp] = a;
-    p.sums[kAllWarps + me.warp] = b;
+    if (ONE) {
+      s.a[me.warp + 1] = a;
+      s.b[me.warp + 1] = b;
+    } else {
+      p.sums[me.warp] = a;
+      p.sums[kAllWarps + me.warp] = b;
+    }
   }
   me.meet();
   const int t = threadIdx.x, w = t >> 5;
   int x = 0, y = 0;
   if (t < kAllWarps) {
-    x = __ldcg(p.sums + t);
-    y = __ldcg(p.sums + kAllWarps + t);
+    x = ONE ? s.a[t + 1] : __ldcg(p.sums + t);
+    y = ONE ? s.b[t + 1] : __ldcg(p.sums + kAllWarps + t);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
@@ -92,17 +133,18 @@ __device__ __forceinline__ void sum_up(const Team& me, const PlanParams& p, Sums
         y += v;
       }
     }
-    if (me.lane == 31) {
+    if (!ONE && me.lane == 31) {
       s.warps[0][w] = x;
       s.warps[1][w] = y;
     }
   }
-  __syncthreads();
+  if (!ONE) __syncthreads();
   if (t < kAllWarps) {
-    for (int i = 0; i < w; ++i) {
-      x += s.warps[0][i];
-      y += s.warps[1][i];
-    }
+    if (!ONE)
+      for (int i = 0; i < w; ++i) {
+        x += s.warps[0][i];
+        y += s.warps[1][i];
+      }
     s.a[t + 1] = x;
     s.b[t + 1] = y;
     if (t == 0) s.a[0] = s.b[0] = 0;
@@ -110,9 +152,14 @@ __device__ __forceinline__ void sum_up(const Team& me, const PlanParams& p, Sums
   __syncthreads();
 }
 // A warp's run of n things, in order: [begin, end), begin a multiple of 32.
-__device__ __forceinline__ int share(int n) { return (int)((((long long)n + kAllWarps - 1) / kAllWarps + 31) / 32 * 32); }
-__device__ __forceinline__ void share(const Team& me, int n, int& begin, int& end) {
-  const long long each = share(n);
+template <bool ONE>
+__device__ __forceinline__ int share(int n) {
+  constexpr int kAllWarps = Team<ONE>::kAllWarps;
+  return (int)((((long long)n + kAllWarps - 1) / kAllWarps + 31) / 32 * 32);
+}
+template <bool ONE>
+__device__ __forceinline__ void share(const Team<ONE>& me, int n, int& begin, int& end) {
+  const long long each = share<ONE>(n);
   begin = (int)min((long long)n, each * me.warp);
   end = (int)min((long long)n, each * (me.warp + 1));
 }
@@ -131,22 +178,22 @@ __device__ __forceinline__ int nth_bit(uint32_t bits, int n) {
   return at;
 }
 // The free page of this rank (FORK: of the tallies' a; else, a being held ones, of those without a bit there, below page `end`).
-template <bool FORK>
-__device__ __forceinline__ int free_page(const PlanParams& p, const Sums& s, int rank) {
-  const int each = share(p.pages);
+template <bool FORK, bool ONE>
+__device__ __forceinline__ int free_page(const PlanParams& p, const Sums<ONE>& s, const Store<ONE>& store, int rank) {
+  const int each = share<ONE>(p.pages);
   int run = 0;
 #pragma unroll
-  for (int step = kAllWarps / 2; step; step >>= 1)
+  for (int step = Team<ONE>::kAllWarps / 2; step; step >>= 1)
     if ((FORK ? s.a[run + step] : (int)min((long long)p.pages, (long long)each * (run + step)) - s.a[run + step]) <= rank) run += step;
   rank -= FORK ? s.a[run] : (int)min((long long)p.pages, (long long)each * run) - s.a[run];
   const int first = run * (each / 32);
   int low = 0, high = min(each / 32, (p.pages + 31) / 32 - first);
   while (high - low > 1) {  // (the last 32 with no more before them than the rank)
-    const int mid = (low + high) / 2, before = __ldcg(&p.tallies[first + mid].before_a);
+    const int mid = (low + high) / 2, before = store.read(&store.tallies[first + mid].before_a);
     if ((FORK ? before : 32 * mid - before) <= rank) low = mid;
     else high = mid;
   }
-  const uint4 t = __ldcg(reinterpret_cast<const uint4*>(p.tallies + first + low));
+  const uint4 t = store.read(reinterpret_cast<const uint4*>(store.tallies + first + low));
   rank -= FORK ? (int)t.z : 32 * low - (int)t.z;
   return (first + low) * 32 + nth_bit(FORK ? t.x : ~t.x, rank);
 }
@@ -193,14 +240,17 @@ constexpr int kLanes = 8;
 constexpr int kHeldChildren = 2048;
 
 // HELD: all children fit there.
-template <bool HELD>
+template <bool HELD, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant__ PlanParams p) {
+  static_assert(HELD || !ONE, "a single thread block holds all children");
+  constexpr int kHeld = ONE ? kOneRows : kHeldChildren, kMine = (kHeld + kThreads - 1) / kThreads, kAllWarps = Team<ONE>::kAllWarps;
   __shared__ struct {
-    int parent[kHeldChildren], have[kHeldChildren], need[kHeldChildren], tail[kHeldChildren], base[kHeldChildren];
+    int parent[kHeld], have[kHeld], need[kHeld], tail[kHeld], base[kHeld];
     int warps[kWarps];
   } held;  // (tail: the entry that is going to be written to, or -1; later, the one that is copied)
-  __shared__ Sums sums;
-  const Team me;
+  __shared__ Sums<ONE> sums;
+  const Team<ONE> me;
+  const Store<ONE> store(p);
   unsigned bad = 0;
   grid_wait();
   grid_launch_dependents();
@@ -210,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     return (unsigned)e < (unsigned)p.pages ? e : -1;
   };
   // who holds a page: nobody yet
-  for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = p.keep && p.keep[i] ? kShared : kFree;
+  for (int i = me.thread; i < p.pages; i += me.kAllThreads) store.owner[i] = p.keep && p.keep[i] ? kShared : kFree;
   if (HELD)
     for (int i = threadIdx.x; i < p.children; i += kThreads) {
       const Child c = child_of(p, i, me.rank == 0 ? &bad : nullptr);
@@ -259,8 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     for (int k = 0; k < kLanes; ++k) {
       if ((unsigned)e[k] >= (unsigned)p.pages) continue;
       // (a held page's word only ever falls: to kShared, or to the lowest of those who write to it)
-      if (tail >= 0 && j0 + 32 * k + me.lane == c.have - 1) atomicMin(p.owner + e[k], i);
-      else p.owner[e[k]] = kShared;
+      if (tail >= 0 && j0 + 32 * k + me.lane == c.have - 1) atomicMin(store.owner + e[k], i);
+      else store.owner[e[k]] = kShared;
     }
   }
   me.meet();
@@ -268,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   auto wants = [&](int i, bool& copied) -> int {
     int tail;
     const Child c = child(i, tail, nullptr);
-    copied = tail >= 0 && __ldcg(p.owner + tail) != i;
+    copied = tail >= 0 && store.read(store.owner + tail) != i;
     return c.need - c.have + (copied ? 1 : 0);
   };
   int page0, page1, child0 = 0, child1 = 0;
@@ -276,17 +326,17 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   int free = 0, wanted = 0;
 #pragma unroll 4
   for (int i = page0; i < page1; i += 32) {
-    const uint32_t m = __ballot_sync(0xffffffffu, i + me.lane < page1 && __ldcg(p.owner + i + me.lane) == kFree);
-    if (me.lane == 0) p.tallies[i / 32] = Tally{m, 0, free, 0};
+    const uint32_t m = __ballot_sync(0xffffffffu, i + me.lane < page1 && store.read(store.owner + i + me.lane) == kFree);
+    if (me.lane == 0) store.tallies[i / 32] = Tally{m, 0, free, 0};
     free += __popc(m);
   }
   bool copied;
   if (HELD) {
     // every thread block for itself: the children's wishes before each child
-    int n[kHeldChildren / kThreads], sum = 0;
+    int n[kMine], sum = 0;
 #pragma unroll
-    for (int k = 0; k < kHeldChildren / kThreads; ++k) {
-      const int i = threadIdx.x * (kHeldChildren / kThreads) + k;
+    for (int k = 0; k < kMine; ++k) {
+      const int i = threadIdx.x * kMine + k;
       n[k] = 0;
       if (i < p.children) {
         n[k] = wants(i, copied);
@@ -306,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     wanted = __reduce_add_sync(0xffffffffu, w);
     int at = before + end - sum;
 #pragma unroll
-    for (int k = 0; k < kHeldChildren / kThreads; ++k) {
-      const int i = threadIdx.x * (kHeldChildren / kThreads) + k;
+    for (int k = 0; k < kMine; ++k) {
+      const int i = threadIdx.x * kMine + k;
       if (i < p.children) held.base[i] = at;
       at += n[k];
     }
@@ -338,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
     int tail;
     const Child c = child(i, tail, nullptr);
     const int base = HELD ? held.base[i] : __ldcg(p.base + i);
-    const bool copy = HELD ? tail >= 0 : tail >= 0 && __ldcg(p.owner + tail) != i;
+    const bool copy = HELD ? tail >= 0 : tail >= 0 && store.read(store.owner + tail) != i;
     int32_t* to = p.out + (long long)i * p.table_pages;
     int e[kLanes];
 #pragma unroll
@@ -352,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
       if (j >= p.table_pages) continue;
       if ((copy && j == c.have - 1) || (j >= c.have && j < c.need)) {
         const int rank = base + (j < c.have ? 0 : (copy ? 1 : 0) + j - c.have);
-        const int got = rank < most ? free_page<true>(p, sums, rank) : -1;
+        const int got = rank < most ? free_page<true>(p, sums, store, rank) : -1;
         if (j < c.have) {
           p.src[i] = got < 0 ? -1 : e[k];
           p.dst[i] = got;
@@ -366,14 +416,17 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const __grid_constant
   if (bad) report(p.status, bad);
 }
 
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_constant__ PlanParams p) {
-  __shared__ Sums sums;
-  const Team me;
+  __shared__ Sums<ONE> sums;
+  const Team<ONE> me;
+  const Store<ONE> store(p);
   unsigned bad = 0;
   grid_wait();
   grid_launch_dependents();
+  constexpr int kAllWarps = Team<ONE>::kAllWarps;
   auto pinned = [&](int i) { return p.keep && p.keep[i] != 0; };
-  for (int i = me.thread; i < p.pages; i += kBlocks * kThreads) p.owner[i] = pinned(i) ? kShared : kFree;
+  for (int i = me.thread; i < p.pages; i += me.kAllThreads) store.owner[i] = pinned(i) ? kShared : kFree;
   me.meet();
   const int lanes = p.lanes, span = 32 * lanes, spans = p.spans, units = p.sequences * spans;
   auto pages_held = [&](int s, bool tell) {
@@ -395,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     }
 #pragma unroll
     for (int k = 0; k < kLanes; ++k)
-      if ((unsigned)e[k] < (unsigned)p.pages) p.owner[e[k]] = kShared;
+      if ((unsigned)e[k] < (unsigned)p.pages) store.owner[e[k]] = kShared;
   }
   me.meet();
   int page0, page1, held = 0, movable = 0;
@@ -403,30 +456,32 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
 #pragma unroll 4
   for (int i0 = page0; i0 < page1; i0 += 32) {
     const int i = i0 + me.lane;
-    const bool is = i < page1 && __ldcg(p.owner + i) != kFree;
+    const bool is = i < page1 && store.read(store.owner + i) != kFree;
     const uint32_t a = __ballot_sync(0xffffffffu, is), b = __ballot_sync(0xffffffffu, is && !pinned(i));
-    if (me.lane == 0) p.tallies[i0 / 32] = Tally{a, b, held, movable};
+    if (me.lane == 0) store.tallies[i0 / 32] = Tally{a, b, held, movable};
     held += __popc(a);
     movable += __popc(b);
   }
   sum_up(me, p, sums, held, movable);
-  const int used = sums.a[kAllWarps], each = share(p.pages);
+  const int used = sums.a[kAllWarps], each = share<ONE>(p.pages);
   // movable pages before page i
   auto before = [&](int i, const uint4& t) { return sums.b[i / each] + (int)t.w + __popc(t.y & ((1u << (i & 31)) - 1u)); };
-  auto tally = [&](int i) { return __ldcg(reinterpret_cast<const uint4*>(p.tallies + i / 32)); };
+  auto tally = [&](int i) { return store.read(reinterpret_cast<const uint4*>(store.tallies + i / 32)); };
   const int below = used < p.pages ? before(used, tally(used)) : sums.b[kAllWarps];
   const int count = sums.b[kAllWarps] - below;
   if (me.thread == 0) {
     p.count[0] = count;
     p.count[1] = used;
   }
-  for (int i = count + me.thread; i < p.pages / 2; i += kBlocks * kThreads) p.src[i] = p.dst[i] = -1;
-  for (int i = used + me.thread; i < p.pages; i += kBlocks * kThreads) {
+  for (int i = count + me.thread; i < p.pages / 2; i += me.kAllThreads) p.src[i] = p.dst[i] = -1;
+  for (int i = used + me.thread; i < p.pages; i += me.kAllThreads) {
     const uint4 t = tally(i);
     if (!(t.y >> (i & 31) & 1u)) continue;
     const int rank = before(i, t) - below;
     p.src[rank] = i;
-    p.dst[rank] = free_page<false>(p, sums, rank);
+    const int to = free_page<false>(p, sums, store, rank);
+    p.dst[rank] = to;
+    if (ONE) store.dst[rank] = to;
   }
   me.meet();
   for (int u = me.warp; u < units; u += kAllWarps) {
@@ -450,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
     }
 #pragma unroll
     for (int k = 0; k < kLanes; ++k)
-      if (to[k] >= 0) e[k] = __ldcg(p.dst + to[k]);
+      if (to[k] >= 0) e[k] = store.read(store.dst + to[k]);
 #pragma unroll
     for (int k = 0; k < kLanes; ++k) {
       const int j = j0 + 32 * k + me.lane;
@@ -461,14 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
 }
 
 template <typename K>
-cudaError_t launch_plan(K kernel, const PlanParams& p, cudaStream_t stream) {
+cudaError_t launch_plan(K kernel, const PlanParams& p, bool one, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kBlocks);
+  cfg.gridDim = dim3(one ? 1 : kBlocks);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute a[2] = {};
   cfg.attrs = a;
-  cfg.numAttrs = launch_attributes(a, kBlocks);
+  cfg.numAttrs = launch_attributes(a, one ? 0 : kBlocks);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -602,8 +657,15 @@ int check_plan(const int32_t* page_table, int64_t table_stride, int32_t table_pa
   return TKS_OK;
 }
 
+// A single thread block's passes are shorter, as long as no warp has more than one piece of the tables (16 rows of 256 pages, of
+// 4096: forked in 4.9 us so and in 9.5 by a cluster, compacted in 5.8 and 8.9; 64 of 64: 7.6 and 9.0, 8.2 and 9.0; 256 of 16:
+// 18.5 and 8.4, 22.5 and 8.8).
+bool one_block(int32_t pages, int32_t rows, int32_t table_pages) {
+  return pages <= kOnePages && rows * std::max(1LL, (table_pages + 32LL * kLanes - 1) / (32 * kLanes)) <= kOneRows;
+}
+
 PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t table_pages, int32_t sequences, const int32_t* lens,
-                       const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch, int rows, bool few) {
+                       const uint8_t* keep, int32_t pages, int32_t page_size, int32_t* table, int32_t* src, int32_t* dst, int32_t* scratch, int rows, bool few, bool one) {
   PlanParams p{};
   p.table = page_table;
   p.table_stride = table_stride;
@@ -617,7 +679,7 @@ PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t 
   p.src = src;
   p.dst = dst;
   p.lanes = kLanes;
-  while (few && p.lanes > 1 && (long long)rows * (((long long)table_pages + 32 * p.lanes - 1) / (32 * p.lanes)) < kAllWarps) p.lanes /= 2;
+  while (few && p.lanes > 1 && (long long)rows * (((long long)table_pages + 32 * p.lanes - 1) / (32 * p.lanes)) < (one ? Team<true>::kAllWarps : Team<false>::kAllWarps)) p.lanes /= 2;
   p.spans = std::max(1, (int)(((long long)table_pages + 32 * p.lanes - 1) / (32 * p.lanes)));
   p.sums = scratch;
   p.tallies = reinterpret_cast<Tally*>(scratch + 1024);
@@ -625,7 +687,7 @@ PlanParams plan_params(const int32_t* page_table, int64_t table_stride, int32_t 
   p.base = p.owner + pages;
   return p;
 }
-static_assert(2 * kAllWarps <= 1024 && sizeof(Tally) == 16, "the scratch buffer's layout");
+static_assert(2 * Team<false>::kAllWarps <= 1024 && sizeof(Tally) == 16, "the scratch buffer's layout");
 
 }  // namespace
 }  // namespace attn
@@ -648,14 +710,16 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
   Place place;
   const int rc = place_of(stream, &place);
   if (rc != TKS_OK) return rc;
-  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, children, false);
+  const bool one = one_block(pages, children, table_pages);
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, children, false, one);
   p.parents = parents;
   p.new_lens = new_lens;
   p.children = children;
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
   const bool fit = children <= kHeldChildren;
-  if ((fit ? launch_plan(fork_kernel<true>, p, (cudaStream_t)stream) : launch_plan(fork_kernel<false>, p, (cudaStream_t)stream)) != cudaSuccess) {
+  const auto kernel = one ? fork_kernel<true, true> : fit ? fork_kernel<true, false> : fork_kernel<false, false>;
+  if (launch_plan(kernel, p, one, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
   }
@@ -675,11 +739,12 @@ extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride
   Place place;
   const int rc = place_of(stream, &place);
   if (rc != TKS_OK) return rc;
-  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, sequences, true);
+  const bool one = one_block(pages, sequences, table_pages);
+  PlanParams p = plan_params(page_table, table_stride, table_pages, sequences, lens, keep, pages, page_size, table, src, dst, scratch, sequences, true, one);
   p.count = count;
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
-  if (launch_plan(compact_kernel, p, (cudaStream_t)stream) != cudaSuccess) {
+  if (launch_plan(one ? compact_kernel<true> : compact_kernel<false>, p, one, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
   }

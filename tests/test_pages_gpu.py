@@ -209,6 +209,18 @@ def test_a_large_pool():
     check_compact(table, lens, 60_001, 16)
 
 
+@pytest.mark.parametrize("pages", [4095, 4096, 4097])
+@pytest.mark.parametrize("sequences, width", [(1, 8192), (1, 8193), (2, 4096), (31, 256), (32, 256), (33, 256), (32, 257), (16, 512)])
+def test_tables_about_as_large_as_one_thread_block_makes(sequences, width, pages):
+    rng = random.Random(sequences * width)
+    keep = [rng.random() < 0.05 for _ in range(pages)]
+    for share in (0.1, 0.9):
+        table, lens = pool(rng, sequences, width, pages, 2, share=share)
+        check_compact(table, lens, pages, 2, keep)
+        parents = [rng.randrange(-1, sequences) for _ in range(sequences)]
+        check_fork(table, lens, parents, [min(width * 2, max(0, lens[p] + rng.randrange(-4, 6))) for p in parents], pages, 2, keep)
+
+
 # ---------------------------------------------------------------------------
 # Copies
 # ---------------------------------------------------------------------------

@@ -243,7 +243,7 @@ int prepare(void* stream, Device* dev, Workspace* ws) try {
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, id) == cudaSuccess &&
         cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, id) == cudaSuccess)
       d.ok = major == 10 && minor == 3 && setup_rows() == cudaSuccess && setup_tiles() == cudaSuccess && setup_scores() == cudaSuccess &&
-             setup_score_tiles() == cudaSuccess;
+             setup_score_tiles() == cudaSuccess && setup_pages() == cudaSuccess;
     cudaGetLastError();
     di = g_dev.emplace(id, d).first;
   }

@@ -2,6 +2,8 @@
 // arguments, and where a call's status goes.
 #pragma once
 
+#include <cuda_runtime.h>
+
 #include <memory>
 #include <mutex>
 
@@ -26,6 +28,7 @@ struct Place {
   std::shared_ptr<std::mutex> order;  // held while a call is queued
 };
 int place_of(void* stream, Place* place);
+cudaError_t setup_pages();  // (tks_pages.cu)
 
 }  // namespace attn
 }  // namespace tks

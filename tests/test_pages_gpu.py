@@ -209,6 +209,36 @@ def test_a_large_pool():
     check_compact(table, lens, 60_001, 16)
 
 
+@pytest.mark.parametrize("pages", [360_447, 360_448, 360_449, 500_001])
+def test_very_large_pools(pages):
+    rng = random.Random(pages)
+    table, lens = pool(rng, 40, 3000, pages, 2, share=0.3)
+    keep = [rng.random() < 0.1 for _ in range(pages)] if pages % 2 else None
+    check_compact(table, lens, pages, 2, keep)
+    parents = [rng.randrange(-1, 40) for _ in range(60)]
+    check_fork(table, lens, parents, [min(6000, max(0, lens[p] + rng.randrange(-4, 400))) for p in parents], pages, 2, keep)
+
+
+@pytest.mark.parametrize("children", [2047, 2048, 2049])
+def test_about_as_many_children_as_are_held(children):
+    rng = random.Random(children)
+    table, lens = pool(rng, 300, 40, 9001, 4, share=0.5)
+    keep = [rng.random() < 0.1 for _ in range(9001)]
+    parents = [rng.randrange(-1, 300) for _ in range(children)]
+    check_fork(table, lens, parents, [min(160, max(0, lens[p] + rng.randrange(-4, 3))) for p in parents], 9001, 4, keep)
+
+
+@pytest.mark.parametrize("pages", [1023, 1024, 1025, 8191, 8192, 8193])
+@pytest.mark.parametrize("sequences, width", [(1, 2048), (1, 4096), (1, 4097), (8, 512), (8, 513), (16, 129), (32, 64), (32, 65), (32, 128), (33, 16)])
+def test_small_tables_and_pools_of_both_ways(sequences, width, pages):
+    rng = random.Random(sequences * width + pages)
+    keep = [rng.random() < 0.05 for _ in range(pages)] if pages % 2 else None
+    table, lens = pool(rng, sequences, width, pages, 2, share=0.5)
+    check_compact(table, lens, pages, 2, keep)
+    parents = [rng.randrange(-1, sequences) for _ in range(sequences)]
+    check_fork(table, lens, parents, [min(width * 2, max(0, lens[p] + rng.randrange(-4, 6))) for p in parents], pages, 2, keep)
+
+
 @pytest.mark.parametrize("pages", [4095, 4096, 4097])
 @pytest.mark.parametrize("sequences, width", [(1, 8192), (1, 8193), (2, 4096), (31, 256), (32, 256), (33, 256), (32, 257), (16, 512)])
 def test_tables_about_as_large_as_one_thread_block_makes(sequences, width, pages):

@@ -13,7 +13,7 @@
 // buffer instead, and a barrier more; nothing is shared between calls.
 //
 // What bounds it: latency, of launch, barrier and loads that wait for each other.
-// Measured: 64 beams of 16 prompts over up to 65,536 positions in pages of 64 9.2 us
+// Measured: 64 beams of 16 prompts over up to 65,536 positions in pages of 64 8.8 us
 // (12.4 by words: the scattered stores and the counts over them take longest); a pool
 // of 8192 pages compacted 6.9 us (11.5 by words); a few short beams 4.4 us (7.4 by words
 // and cluster), a pool of 639 pages compacted 4.4 (9.2). Many: 2048 rows of 1024 pages
@@ -226,7 +226,7 @@ __device__ __forceinline__ int sum_before(int x, int (&warps)[kWarps], int& all)
 // other: parent, length, entry).
 constexpr int kHeldChildren = 2048;
 template <int N>
-struct __align__(16) Children {
+struct Children {
   int parent[N], have[N], need[N], tail[N], base[N], warps[kWarps];  // (tail: as above; later, the entry that is copied)
   __device__ __forceinline__ void look_up(const PlanParams& p, unsigned* bad) {
     for (int i = threadIdx.x; i < p.children; i += kThreads) {
@@ -241,15 +241,17 @@ struct __align__(16) Children {
     written = tail[i];
     return Child{p.table + parent[i] * p.table_stride, have[i], need[i], written >= 0};
   }
-  // Whether a child before i writes to page e.
-  __device__ __forceinline__ bool written_before(int i, int e) const {
-    bool is = false;
-#pragma unroll 4
-    for (int j = 0; j < i; j += 4) {
-      const int4 x = *reinterpret_cast<const int4*>(tail + j);
-      is |= x.x == e || (x.y == e && j + 1 < i) || (x.z == e && j + 2 < i) || (x.w == e && j + 3 < i);
+  // Into base: whether a child before writes to the same page.
+  __device__ __forceinline__ void look_for_writers(const PlanParams& p) {
+    const int lane = threadIdx.x & 31;
+    for (int i = threadIdx.x >> 5; i < p.children; i += kWarps) {
+      const int e = tail[i];
+      bool is = false;
+      if (e >= 0)
+        for (int j = lane; j < i; j += 32) is |= tail[j] == e;
+      is = __any_sync(0xffffffffu, is);
+      if (lane == 0) base[i] = is;
     }
-    return is;
   }
   // The pages that the children before each one want, and that all do; copied(i): whether child i's tail, which it has, is copied.
   template <typename F>
@@ -485,6 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const __grid_const
 // them: so each knows by itself which pages are free, and how many are before each 32.
 // ---------------------------------------------------------------------------
 constexpr int kBitPages = 352 * 1024;           // (of compact, five arrays of that many bits)
+// That look for others who write to the same page among all before them, instead of by a word for each page (64 beams over up to
+// 65,536 positions 8.8 us so and 9.3 otherwise; 40 short ones 8.3 and 8.5, 100 8.9 and 8.8, 256 10.8 and 9.1).
+constexpr int kFewChildren = 64;
 constexpr int kOnePages = 8192, kOneRows = 32;  // of tables that a single thread block makes, at most (one_block)
 
 __device__ __forceinline__ uint4 ld_peer(uint32_t addr, unsigned rank) {
@@ -564,8 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_bits_kernel(const __grid_con
     for (int w = me.thread; 32 * w < p.pages; w += me.kAllThreads) atomicOr(own + w, kept(p, w));
   for (int i = threadIdx.x; i < p.children; i += kThreads)
     if (held.tail[i] >= 0) set_bit(written, held.tail[i]);
-  if (!ONE && me.rank == 0) {
-    // The lowest of those who write to a page. (Looked for among 64 children, as a single thread block does: 10.2 us in all, 9.3 so.)
+  const bool few = ONE || p.children <= kFewChildren;
+  if (few) {
+    held.look_for_writers(p);
+  } else if (me.rank == 0) {
+    // the lowest of those who write to a page
     for (int i = threadIdx.x; i < p.children; i += kThreads)
       if (held.tail[i] >= 0) p.owner[held.tail[i]] = kFree;
     __syncthreads();
@@ -596,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_bits_kernel(const __grid_con
   const int wanted = held.sum_up(p, [&](int i) {
     const int e = held.tail[i];
     if (free[e >> 5] >> (e & 31) & 1u) return true;
-    return ONE ? held.written_before(i, e) : __ldcg(p.owner + e) != i;
+    return few ? held.base[i] != 0 : __ldcg(p.owner + e) != i;
   });
   const int each = (words / 4 + kThreads - 1) / kThreads, q0 = min(words / 4, (int)threadIdx.x * each), q1 = min(words / 4, q0 + each);
   int sum = 0, most;

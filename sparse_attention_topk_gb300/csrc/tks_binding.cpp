@@ -128,6 +128,14 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device& devic
   return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
 }
 
+// A tensor of 32-bit words over a part of an int32 one, whose storage it shares (an allocation costs the host 0.7 us, this 0.2).
+Tensor part(const Tensor& whole, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
+  Tensor t = at::detail::make_tensor<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), at::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // The device and stream of a call: what is allocated here belongs to the stream that writes it.
 struct Place {
   c10::cuda::OptionalCUDAStreamGuard stream_guard;
@@ -415,6 +423,9 @@ PyObject* py_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// Scores and row lengths of so many words are one allocation: who keeps one of them keeps both.
+constexpr int64_t kSmallWords = 1 << 18;
+
 // scores(q, bounds, page_table, kv_len, block, first, last, n, out, stream) -> (scores, row_len)
 PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity_blocks(n, 10)) return nullptr;
@@ -433,16 +444,20 @@ PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want(columns <= most && columns <= INT32_MAX, "n must not exceed the blocks of a page table's row");
     const int64_t first = number(a[5], "first"), last = number(a[6], "last");
     Place place(a[9], b.device);
-    const int64_t shape[4] = {batch, tokens, b.b.kv_heads, columns};
-    Tensor out;
-    if (a[8] == Py_None) {
+    const int64_t shape[4] = {batch, tokens, b.b.kv_heads, columns}, rows = batch * tokens * b.b.kv_heads;
+    Tensor out, row_len;
+    if (a[8] == Py_None && columns >= 0 && rows <= kSmallWords && rows * (columns + 1) <= kSmallWords) {
+      const Tensor whole = fresh({rows * (columns + 1)}, at::kInt, b.device);
+      out = part(whole, 0, shape, at::kFloat);
+      row_len = part(whole, rows * columns, {batch, tokens, b.b.kv_heads}, at::kInt);
+    } else if (a[8] == Py_None) {
       out = fresh(shape, at::kFloat, b.device);
     } else {
       out = tensor(a[8], "out");
       want(out.sizes() == at::IntArrayRef(shape) && out.scalar_type() == at::kFloat && out.device() == b.device && out.is_contiguous(),
            "out must be a contiguous float32 CUDA tensor [batch, tokens, kv_heads, n]");
     }
-    Tensor row_len = fresh({batch, tokens, b.b.kv_heads}, at::kInt, b.device);
+    if (!row_len.defined()) row_len = fresh({batch, tokens, b.b.kv_heads}, at::kInt, b.device);
     const Tensor x = readable(q);
     const tks_queries r = queries_of(x, table);
     check(f_scores(&b.b, &r, p_lens, (int32_t)first, (int32_t)last, static_cast<float*>(out.data_ptr()), (int32_t)columns,
@@ -502,7 +517,7 @@ Plan plan_of(PyObject* table, PyObject* lens, PyObject* pages, PyObject* page_si
   return r;
 }
 Tensor new_ints(at::IntArrayRef shape, const at::Device& device) { return fresh(shape, at::kInt, device); }
-// int32 tensors of these lengths, one behind the other in one allocation (which costs the host 0.7 us, a tensor over a part 0.2).
+// int32 tensors of these lengths, one behind the other in one allocation.
 template <size_t N>
 std::array<Tensor, N> parts(const int64_t (&lengths)[N], const at::Device& device) {
   int64_t all = 0;
@@ -511,10 +526,7 @@ std::array<Tensor, N> parts(const int64_t (&lengths)[N], const at::Device& devic
   std::array<Tensor, N> out;
   int64_t at = 0;
   for (size_t i = 0; i < N; ++i) {
-    out[i] = at::detail::make_tensor<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
-    at::TensorImpl* impl = out[i].unsafeGetTensorImpl();
-    impl->set_storage_offset(at);
-    impl->set_sizes_contiguous(lengths[i]);
+    out[i] = part(whole, at, {lengths[i]}, at::kInt);
     at += lengths[i];
   }
   return out;

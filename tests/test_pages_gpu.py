@@ -209,6 +209,21 @@ def test_a_large_pool():
     check_compact(table, lens, 60_001, 16)
 
 
+@pytest.mark.parametrize("pages", [100, 9000, 9013])
+@pytest.mark.parametrize("offset", [1, 2, 4, 7])
+def test_kept_pages_at_any_alignment(offset, pages):
+    rng = random.Random(offset)
+    table, lens = pool(rng, 50, 60, pages, 2, share=0.9)
+    keep = torch.tensor([rng.random() < 0.3 for _ in range(pages)], device="cuda")
+    other = torch.ones(pages + 16, dtype=torch.uint8, device="cuda")[offset : offset + pages].copy_(keep.to(torch.uint8) * 128)
+    parents = [rng.randrange(-1, 50) for _ in range(50)]
+    args = (ints(table, (50, 60)), ints(lens, (50,)))
+    more = (ints(parents, (50,)), ints([min(120, lens[p] + 3) for p in parents], (50,)), pages, 2)
+    for call in (lambda k: tks.cache_fork(*args, *more, keep=k), lambda k: tks.cache_compact(*args, pages, 2, keep=k)):
+        assert all(torch.equal(x, y) for x, y in zip(call(keep), call(other)))
+        tks.device_status()
+
+
 @pytest.mark.parametrize("pages", [360_447, 360_448, 360_449, 500_001])
 def test_very_large_pools(pages):
     rng = random.Random(pages)

@@ -60,8 +60,12 @@ typedef struct {
  * range of bfloat16 and, at last, rounded to it; a channel with a NaN has NaN
  * bounds.  start and end are held to [0, table_pages * page_size] and reported
  * as TKS_E_ROW_LEN; a block whose page is outside [0, pages) is skipped and
- * reported as TKS_E_INDEX.  Sequences that share a page and differ in length
- * within a block leave either one's bounds there.
+ * reported as TKS_E_INDEX.  Where sequences of the call hold a page at the same
+ * place of their rows and end differently within a block of it, the block is taken
+ * up to the furthest of their ends, whichever of them has new positions there, so
+ * that its bounds hold for all of them.  (A page at different places of rows, in
+ * blocks that their sequences do not fill alike, has no such order: its bounds
+ * there are undefined.)
  */
 int tks_cache_bounds(const tks_cache *cache, const tks_bounds *bounds, const int32_t *page_table,
                      int64_t table_stride, int32_t table_pages, int32_t batch,

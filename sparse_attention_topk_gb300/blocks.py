@@ -66,7 +66,8 @@ def cache_bounds(k_cache, page_table, end, bounds, start=None, scales=None, stre
     ``bounds``: bfloat16 CUDA tensor [pages, page_size // block, kv_heads, 2, head_dim], the least
     and the largest value of each block's keys in every channel; only the blocks named are written.
     ``page_table``: int32 [batch, n]; ``end``: int32 [batch], the sequences' lengths; ``start``:
-    int32 [batch], the lengths before the last write (None: 0).
+    int32 [batch], the lengths before the last write (None: 0).  A block of a page that several of the
+    sequences hold, at one place of their rows, is taken up to the furthest of their ends.
     """
     _native().bounds(k_cache, page_table, end, bounds, start, scales, _handle(stream))
 

@@ -15,7 +15,7 @@
 // page, rows) that a lone call cannot hide, so what a chain does not need is loaded
 // beside it.
 // Measured: bounds of a prompt of 32,768 tokens of 8 int8 heads of 128 (37 MB) 10.2
-// us, 3.6 TB/s, 12.7 from memory; of 64 decode steps 3.7 us.  Scores of one token
+// us, 3.6 TB/s, 12.7 from memory; of 64 decode steps 4.1 us.  Scores of one token
 // of 32 heads on 8 over 2048 blocks (8.5 MB) 4.7 us; of 64 ragged sequences of 16
 // heads on 2 over up to 2048 blocks (71 MB) 14.8 us, 4.8 TB/s, 18.8 from memory (with a
 // thread block for every 128 blocks, as for one token, 20.7).
@@ -138,8 +138,28 @@ struct Extent<false> {
 // (Sixteen pieces a lane under way in four thread blocks an SM: 64 decode steps take 3.7 us, with eight in seven 5.1.)
 constexpr int kBoundsThreads = 128, kBoundsPerSm = 4;
 
-// An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time.
-template <int D, bool I8>
+// The furthest end (of `end` and on) of the sequences that hold this page at the same place of their rows.
+__device__ __forceinline__ int furthest_end(const BoundsParams& p, int end, int page, int at, int cap) {
+  const int lane = threadIdx.x & 31;
+  int furthest = end;
+  for (int s = lane; s - lane < p.batch; s += 128) {
+    int e[4], held[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = s + 32 * i < p.batch ? min(__ldg(p.end + s + 32 * i), cap) : 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) held[i] = e[i] > end ? __ldg(p.table + (s + 32 * i) * p.table_stride + at) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (held[i] == page) furthest = max(furthest, e[i]);
+  }
+  return __reduce_max_sync(0xffffffffu, furthest);
+}
+
+// An item is (block, head), of all sequences' new blocks in order, head fastest; a warp takes one at a time, or (ALL, many sequences)
+// all heads of a block. Of a block that a sequence does not fill, another may hold more: both take it as far as either does, so that
+// it does not matter who stores last. Looking the others up takes 0.5 of 64 decode steps' 4.1 us, 1.9 of 256
+// steps' 10.5, and, of 4096 steps' 249, which look at 2048 rows each, 105 (434 in all where each head looks for itself).
+template <int D, bool I8, bool ALL>
 __global__ void __launch_bounds__(kBoundsThreads, kBoundsPerSm) bounds_kernel(const __grid_constant__ BoundsParams p) {
   constexpr int kElem = I8 ? 1 : 2, kPieces = D * kElem / 16, kRows = 32 / kPieces, kE = 16 / kElem, kAhead = 16;
   __shared__ long long upto[kBoundsThreads];  // blocks of the sequences up to and with this one
@@ -176,56 +196,62 @@ __global__ void __launch_bounds__(kBoundsThreads, kBoundsPerSm) bounds_kernel(co
     for (int i = 0; i < warp; ++i) sum += warps_s[i];
     upto[threadIdx.x] = sum;
     __syncthreads();
-    const long long items = upto[kBoundsThreads - 1] * p.kv_heads;
+    const int of_block = ALL ? 1 : p.kv_heads;
+    const long long items = upto[kBoundsThreads - 1] * of_block;
     for (; next < items; next += warps) {
-      const long long number = next / p.kv_heads;
-      const int head = (int)(next - number * p.kv_heads);
+      const long long number = next / of_block;
+      const int head0 = ALL ? 0 : (int)(next - number * of_block);
       int at = 0;
 #pragma unroll
       for (int step = kBoundsThreads / 2; step; step >>= 1)
         if (upto[at + step - 1] <= number) at += step;
       const int block = first_s[at] + (int)(number - (at ? upto[at - 1] : 0));
-      const int pos = block << p.block_shift, count = min(1 << p.block_shift, end_s[at] - pos);
-      const int page = __ldg(p.table + (s0 + at) * p.table_stride + (pos >> p.page_shift));
+      const int pos = block << p.block_shift, place = pos >> p.page_shift, end = end_s[at];
+      const int page = __ldg(p.table + (s0 + at) * p.table_stride + place);
       if ((unsigned)page >= (unsigned)p.pages) {
         if (lane == 0) report(p.status, kStatIndexBit);
         continue;
       }
+      int upto_end = end;
+      if (end - pos < 1 << p.block_shift && p.batch > 1) upto_end = furthest_end(p, end, page, place, cap);
+      const int count = min(1 << p.block_shift, upto_end - pos);
       const int in_page = pos & ((1 << p.page_shift) - 1);
-      const unsigned char* base = p.k + page * p.page_b + in_page * p.token_b + head * p.head_b + piece * 16;
-      const float* scales = I8 ? p.scales + 2 * ((((long long)page << p.page_shift) + in_page) * p.kv_heads + head) : nullptr;
-      Extent<I8> x;
-      x.clear();
-      for (int r0 = sub; r0 < count; r0 += kRows * kAhead) {  // (rows past the last are the last again)
-        uint4 w[kAhead];
-        float sc[kAhead];
+      for (int head = head0; head < (ALL ? p.kv_heads : head0 + 1); ++head) {
+        const unsigned char* base = p.k + page * p.page_b + in_page * p.token_b + head * p.head_b + piece * 16;
+        const float* scales = I8 ? p.scales + 2 * ((((long long)page << p.page_shift) + in_page) * p.kv_heads + head) : nullptr;
+        Extent<I8> x;
+        x.clear();
+        for (int r0 = sub; r0 < count; r0 += kRows * kAhead) {  // (rows past the last are the last again)
+          uint4 w[kAhead];
+          float sc[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          const int r = min(r0 + i * kRows, count - 1);
-          w[i] = __ldg(reinterpret_cast<const uint4*>(base + r * p.token_b));
-          sc[i] = I8 ? __ldg(scales + 2LL * r * p.kv_heads) : 0.f;
+          for (int i = 0; i < kAhead; ++i) {
+            const int r = min(r0 + i * kRows, count - 1);
+            w[i] = __ldg(reinterpret_cast<const uint4*>(base + r * p.token_b));
+            sc[i] = I8 ? __ldg(scales + 2LL * r * p.kv_heads) : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; i += 2) x.add(w[i], w[i + 1], sc[i], sc[i + 1]);
         }
+        __syncwarp();
+        constexpr int kPairs = Extent<I8>::kPairs;
+        __nv_bfloat162 lo[kPairs], hi[kPairs];
+        x.rounded(lo, hi);
 #pragma unroll
-        for (int i = 0; i < kAhead; i += 2) x.add(w[i], w[i + 1], sc[i], sc[i + 1]);
-      }
-      __syncwarp();
-      constexpr int kPairs = Extent<I8>::kPairs;
-      __nv_bfloat162 lo[kPairs], hi[kPairs];
-      x.rounded(lo, hi);
+        for (int o = kPieces; o < 32; o <<= 1)
 #pragma unroll
-      for (int o = kPieces; o < 32; o <<= 1)
+          for (int i = 0; i < kPairs; ++i) {
+            lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+            hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+          }
+        const int of_page = 1 << (p.page_shift - p.block_shift);
+        uint4* to = reinterpret_cast<uint4*>(p.bounds + (((long long)page * of_page + (in_page >> p.block_shift)) * p.kv_heads + head) * (2 * D) + piece * kE);
+        if (sub == 0) {
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) {
-          lo[i] = __hmin2_nan(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
-          hi[i] = __hmax2_nan(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
-        }
-      const int of_page = 1 << (p.page_shift - p.block_shift);
-      uint4* to = reinterpret_cast<uint4*>(p.bounds + (((long long)page * of_page + (in_page >> p.block_shift)) * p.kv_heads + head) * (2 * D) + piece * kE);
-      if (sub == 0) {
-#pragma unroll
-        for (int i = 0; i < kPairs; i += 4) {
-          to[i / 4] = make_uint4(bits_of(lo[i]), bits_of(lo[i + 1]), bits_of(lo[i + 2]), bits_of(lo[i + 3]));
-          to[D / 8 + i / 4] = make_uint4(bits_of(hi[i]), bits_of(hi[i + 1]), bits_of(hi[i + 2]), bits_of(hi[i + 3]));
+          for (int i = 0; i < kPairs; i += 4) {
+            to[i / 4] = make_uint4(bits_of(lo[i]), bits_of(lo[i + 1]), bits_of(lo[i + 2]), bits_of(lo[i + 3]));
+            to[D / 8 + i / 4] = make_uint4(bits_of(hi[i]), bits_of(hi[i + 1]), bits_of(hi[i + 2]), bits_of(hi[i + 3]));
+          }
         }
       }
     }
@@ -613,14 +639,15 @@ void with_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a) {
 }
 
 template <int D>
-cudaError_t launch_bounds(const BoundsParams& p, bool i8, int grid, cudaStream_t stream) {
+cudaError_t launch_bounds(const BoundsParams& p, bool i8, bool all, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute a[1] = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kBoundsThreads);
   cfg.stream = stream;
   with_pdl(cfg, a);
-  return i8 ? cudaLaunchKernelEx(&cfg, bounds_kernel<D, true>, p) : cudaLaunchKernelEx(&cfg, bounds_kernel<D, false>, p);
+  if (all) return i8 ? cudaLaunchKernelEx(&cfg, bounds_kernel<D, true, true>, p) : cudaLaunchKernelEx(&cfg, bounds_kernel<D, false, true>, p);
+  return i8 ? cudaLaunchKernelEx(&cfg, bounds_kernel<D, true, false>, p) : cudaLaunchKernelEx(&cfg, bounds_kernel<D, false, false>, p);
 }
 
 template <int D>
@@ -710,7 +737,10 @@ extern "C" int tks_cache_bounds(const tks_cache* cache, const tks_bounds* bounds
   const __int128 items = (__int128)batch * std::max(1, table_pages) * (bounds->page_size / bounds->block) * cache->kv_heads;
   const int grid = (int)std::min<__int128>(items, place.sms * kBoundsPerSm);
   std::lock_guard<std::mutex> lock(*place.order);
-  const cudaError_t e = cache->head_dim == 64 ? launch_bounds<64>(p, i8, grid, (cudaStream_t)stream) : launch_bounds<128>(p, i8, grid, (cudaStream_t)stream);
+  // (where every sequence has a new block, a block each warp and more)
+  const bool all = (int64_t)batch >= (int64_t)place.sms * kBoundsPerSm * (kBoundsThreads / 32) / 4;
+  const cudaError_t e = cache->head_dim == 64 ? launch_bounds<64>(p, i8, all, grid, (cudaStream_t)stream)
+                                              : launch_bounds<128>(p, i8, all, grid, (cudaStream_t)stream);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

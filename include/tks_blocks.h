@@ -6,7 +6,8 @@
  * power of two.  tks_cache_bounds keeps, beside the cache of tks_attention.h,
  * the least and the largest value of each block's keys in every channel;
  * tks_block_scores makes of them, for every query token and key/value head, a
- * score of every block, which no key of the block exceeds; the selector of tks.h
+ * score of every block, which no key of the block exceeds (over 8 bits: but for the
+ * bounds' rounding); the selector of tks.h
  * picks the best (rows of scores, with the row lengths that come with them); and
  * tks_block_attention attends to the blocks picked.
  *
@@ -76,9 +77,11 @@ int tks_cache_bounds(const tks_cache *cache, const tks_bounds *bounds, const int
  * block j that the token sees,
  *     scores[b][t][g][j] = max over the query heads h of g of
  *         sum over the channels d of max(q_h,d * least_j,d, q_h,d * largest_j,d)
- * (as sum of max(q, 0) * largest + min(q, 0) * least, in 32 bits), which is at
- * least the product of any of these heads with any key of the block, but for
- * the rounding of the bounds.
+ * (as sum of max(q, 0) * largest + min(q, 0) * least, in 32 bits), which, but for
+ * the sum's rounding, is at least the product of any of these heads with any finite
+ * key of the block in a bfloat16 cache.  Over 8 bits, bounds are rounded to nearest,
+ * and a key's product can exceed its block's score by up to 2^-8 of
+ * sum |q_d| max(|least_d|, |largest_d|).
  *
  *   queries   out, lse and softmax_scale are not looked at
  *   kv_len    device, int32 [batch][tokens], or NULL (n * block): the token

@@ -79,7 +79,9 @@ def block_scores(q, bounds, page_table, kv_len, block, first=0, last=0, n=None, 
     ``kv_len``: int32 [batch, tokens], the positions that a token sees (None: all).  The score of a
     block, for a token and key/value head, is the largest over the head's query heads of
     ``sum_d max(q_d * least_d, q_d * largest_d)``; a token's ``first`` first and ``last`` last blocks
-    score +inf, blocks that it does not see -inf.
+    score +inf, blocks that it does not see -inf.  No (finite) key of a bfloat16 cache has a larger
+    product than its block's score; of an int8 one, by at most 2^-8 of the terms' magnitudes, as the
+    bounds are rounded to nearest.
 
     Returns (scores, seen): float32 [batch, tokens, kv_heads, n], of the row's first n blocks (None:
     all that the page table has room for), and int32 [batch, tokens, kv_heads], how many of them the

@@ -423,9 +423,6 @@ PyObject* py_bounds(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// Scores and row lengths of so many words are one allocation: who keeps one of them keeps both.
-constexpr int64_t kSmallWords = 1 << 18;
-
 // scores(q, bounds, page_table, kv_len, block, first, last, n, out, stream) -> (scores, row_len)
 PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (!arity_blocks(n, 10)) return nullptr;
@@ -444,20 +441,17 @@ PyObject* py_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want(columns <= most && columns <= INT32_MAX, "n must not exceed the blocks of a page table's row");
     const int64_t first = number(a[5], "first"), last = number(a[6], "last");
     Place place(a[9], b.device);
-    const int64_t shape[4] = {batch, tokens, b.b.kv_heads, columns}, rows = batch * tokens * b.b.kv_heads;
-    Tensor out, row_len;
-    if (a[8] == Py_None && columns >= 0 && rows <= kSmallWords && rows * (columns + 1) <= kSmallWords) {
-      const Tensor whole = fresh({rows * (columns + 1)}, at::kInt, b.device);
-      out = part(whole, 0, shape, at::kFloat);
-      row_len = part(whole, rows * columns, {batch, tokens, b.b.kv_heads}, at::kInt);
-    } else if (a[8] == Py_None) {
+    const int64_t shape[4] = {batch, tokens, b.b.kv_heads, columns};
+    Tensor out;
+    if (a[8] == Py_None) {
       out = fresh(shape, at::kFloat, b.device);
     } else {
       out = tensor(a[8], "out");
       want(out.sizes() == at::IntArrayRef(shape) && out.scalar_type() == at::kFloat && out.device() == b.device && out.is_contiguous(),
            "out must be a contiguous float32 CUDA tensor [batch, tokens, kv_heads, n]");
     }
-    if (!row_len.defined()) row_len = fresh({batch, tokens, b.b.kv_heads}, at::kInt, b.device);
+    // (an allocation of its own: storage that float32 and int32 tensors share cannot be saved)
+    const Tensor row_len = fresh({batch, tokens, b.b.kv_heads}, at::kInt, b.device);
     const Tensor x = readable(q);
     const tks_queries r = queries_of(x, table);
     check(f_scores(&b.b, &r, p_lens, (int32_t)first, (int32_t)last, static_cast<float*>(out.data_ptr()), (int32_t)columns,

@@ -16,7 +16,6 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include <array>
 #include <cmath>
 #include <exception>
 #include <optional>
@@ -126,14 +125,6 @@ int64_t step(const Tensor& t, int64_t i) { return t.size(i) > 1 ? t.stride(i) : 
 // An output (without the dispatcher's way, which takes half a microsecond more).
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const at::Device& device) {
   return Tensor(at::detail::empty_cuda(shape, type, device, std::nullopt));
-}
-
-// A tensor of 32-bit words over a part of an int32 one, whose storage it shares (an allocation costs the host 0.7 us, this 0.2).
-Tensor part(const Tensor& whole, int64_t at, at::IntArrayRef shape, at::ScalarType type) {
-  Tensor t = at::detail::make_tensor<at::TensorImpl>(c10::Storage(whole.storage()), whole.key_set(), at::scalarTypeToTypeMeta(type));
-  t.unsafeGetTensorImpl()->set_storage_offset(at);
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  return t;
 }
 
 // The device and stream of a call: what is allocated here belongs to the stream that writes it.
@@ -510,21 +501,8 @@ Plan plan_of(PyObject* table, PyObject* lens, PyObject* pages, PyObject* page_si
   }
   return r;
 }
+// (An allocation for each output and for the scratch buffer: as parts of one, whoever kept one of them would keep them all.)
 Tensor new_ints(at::IntArrayRef shape, const at::Device& device) { return fresh(shape, at::kInt, device); }
-// int32 tensors of these lengths, one behind the other in one allocation.
-template <size_t N>
-std::array<Tensor, N> parts(const int64_t (&lengths)[N], const at::Device& device) {
-  int64_t all = 0;
-  for (const int64_t n : lengths) all += n;
-  const Tensor whole = new_ints({all}, device);
-  std::array<Tensor, N> out;
-  int64_t at = 0;
-  for (size_t i = 0; i < N; ++i) {
-    out[i] = part(whole, at, {lengths[i]}, at::kInt);
-    at += lengths[i];
-  }
-  return out;
-}
 Tensor table_out(PyObject* given, int64_t rows, int64_t width, const at::Device& device) {
   const int64_t shape[2] = {rows, width};
   if (given == Py_None) return new_ints(shape, device);
@@ -546,7 +524,7 @@ PyObject* py_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* p_lens = ints(new_lens, {children}, p.device, "new_lens");
     Place place(a[8], p.device);
     Tensor out = table_out(a[7], children, p.width, p.device);
-    auto [scratch, src, dst] = parts({TKS_PAGES_SCRATCH(p.pages, children), children, children}, p.device);
+    const Tensor scratch = new_ints({TKS_PAGES_SCRATCH(p.pages, children)}, p.device), src = new_ints({children}, p.device), dst = new_ints({children}, p.device);
     check(f_fork(words(p.table), step(p.table, 0), (int32_t)p.width, (int32_t)p.rows, words(p.lens), p_parents, p_lens, (int32_t)children, p.p_keep,
                  (int32_t)p.pages, (int32_t)p.page, words(out), words(src), words(dst), words(scratch), place.stream),
           "tks_cache_fork");
@@ -561,7 +539,8 @@ PyObject* py_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Plan p = plan_of(a[0], a[1], a[2], a[3], a[4]);
     Place place(a[6], p.device);
     Tensor out = table_out(a[5], p.rows, p.width, p.device);
-    auto [scratch, src, dst, count] = parts({TKS_PAGES_SCRATCH(p.pages, p.rows), p.pages / 2, p.pages / 2, (int64_t)2}, p.device);
+    const Tensor scratch = new_ints({TKS_PAGES_SCRATCH(p.pages, p.rows)}, p.device), src = new_ints({p.pages / 2}, p.device),
+                 dst = new_ints({p.pages / 2}, p.device), count = new_ints({2}, p.device);
     check(f_compact(words(p.table), step(p.table, 0), (int32_t)p.width, (int32_t)p.rows, words(p.lens), p.p_keep, (int32_t)p.pages, (int32_t)p.page,
                     words(out), words(src), words(dst), words(count), words(scratch), place.stream),
           "tks_cache_compact");

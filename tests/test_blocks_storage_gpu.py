@@ -33,3 +33,25 @@ def test_scores_and_row_lengths_are_saved_together(columns):
     assert scores.untyped_storage().data_ptr() != seen.untyped_storage().data_ptr()
     assert scores.untyped_storage().nbytes() == 4 * scores.numel() and seen.untyped_storage().nbytes() == 4 * seen.numel()
     assert tks.device_status() == tks.TKS_OK
+
+
+def owns(*tensors):
+    assert len({t.untyped_storage().data_ptr() for t in tensors}) == len(tensors)
+    for t in tensors:
+        assert t.untyped_storage().nbytes() == 4 * t.numel()
+        a, size = saved(t)
+        assert torch.equal(a, t) and size < 4 * t.numel() + 4096
+
+
+@pytest.mark.parametrize("children", [2, 100])
+@pytest.mark.parametrize("pages", [64, 9000, 400_000])
+def test_what_a_fork_returns_holds_nothing_else(pages, children):
+    table, lens = ints([[5, 7, -1]]), ints([20])
+    owns(*tks.cache_fork(table, lens, ints([0] * children), ints([20] * children), pages, 16))
+    assert tks.device_status() == tks.TKS_OK
+
+
+@pytest.mark.parametrize("pages", [64, 9000, 400_000])
+def test_what_a_compaction_returns_holds_nothing_else(pages):
+    owns(*tks.cache_compact(ints([[5, 7, -1]]), ints([20]), pages, 16))
+    assert tks.device_status() == tks.TKS_OK

@@ -631,13 +631,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1) scores_stream_kernel(const 
 
 }
 
-void with_pdl(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* a) {
-  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = a;
-  cfg.numAttrs = 1;
-}
-
 template <int D>
 cudaError_t launch_bounds(const BoundsParams& p, bool i8, bool all, int grid, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
@@ -645,7 +638,8 @@ cudaError_t launch_bounds(const BoundsParams& p, bool i8, bool all, int grid, cu
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kBoundsThreads);
   cfg.stream = stream;
-  with_pdl(cfg, a);
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, 0);
   if (all) return i8 ? cudaLaunchKernelEx(&cfg, bounds_kernel<D, true, true>, p) : cudaLaunchKernelEx(&cfg, bounds_kernel<D, false, true>, p);
   return i8 ? cudaLaunchKernelEx(&cfg, bounds_kernel<D, true, false>, p) : cudaLaunchKernelEx(&cfg, bounds_kernel<D, false, false>, p);
 }
@@ -658,7 +652,8 @@ cudaError_t launch_scores(const ScoreParams& p, int grid, cudaStream_t stream) {
   cfg.blockDim = dim3(kScoreThreads);
   cfg.dynamicSmemBytes = ScoreShape<D>::kSmem;
   cfg.stream = stream;
-  with_pdl(cfg, a);
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, 0);
   return cudaLaunchKernelEx(&cfg, scores_kernel<D>, p);
 }
 
@@ -670,7 +665,8 @@ cudaError_t launch_scores_stream(const ScoreParams& p, int grid, cudaStream_t st
   cfg.blockDim = dim3(kStreamThreads);
   cfg.dynamicSmemBytes = StreamShape<D>::kSmem;
   cfg.stream = stream;
-  with_pdl(cfg, a);
+  cfg.attrs = a;
+  cfg.numAttrs = launch_attributes(a, 0);
   return cudaLaunchKernelEx(&cfg, scores_stream_kernel<D>, p);
 }
 

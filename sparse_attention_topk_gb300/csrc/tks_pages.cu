@@ -22,6 +22,7 @@
 // an SM instead of four) 95.
 
 #include <algorithm>
+#include <iterator>
 
 #include "tks_attn.cuh"
 #include "tks_attn_host.h"
@@ -749,13 +750,18 @@ __global__ void __launch_bounds__(kThreads, 1) compact_bits_kernel(const __grid_
   peers_have_read<ONE>();
 }
 
-// By the entries of a lane, 1 << i, and by whether a single thread block makes the tables.
-constexpr int kBitKernels = 5;
+// By the entries of a lane, 1 << i, and by whether a single thread block makes the tables: it has kOneRows pieces at most, of
+// kForkPiece or kCompactPiece entries (one_block), one for each of its warps, and so never needs more entries a lane than these.
+constexpr int kBitKernels = 5, kForkPiece = 128, kCompactPiece = 64;
+static_assert(kOneRows <= kWarps, "a piece each warp");
 using PlanKernel = void (*)(const PlanParams);
-#define TKS_BY_LANES(kernel, one) {kernel<1, one>, kernel<2, one>, kernel<4, one>, kernel<8, one>, kernel<16, one>}
-constexpr PlanKernel kForkBits[2][kBitKernels] = {TKS_BY_LANES(fork_bits_kernel, false), TKS_BY_LANES(fork_bits_kernel, true)};
-constexpr PlanKernel kCompactBits[2][kBitKernels] = {TKS_BY_LANES(compact_bits_kernel, false), TKS_BY_LANES(compact_bits_kernel, true)};
-#undef TKS_BY_LANES
+constexpr PlanKernel kForkBits[kBitKernels] = {fork_bits_kernel<1, false>, fork_bits_kernel<2, false>, fork_bits_kernel<4, false>, fork_bits_kernel<8, false>,
+                                               fork_bits_kernel<16, false>};
+constexpr PlanKernel kForkOne[] = {fork_bits_kernel<1, true>, fork_bits_kernel<2, true>, fork_bits_kernel<4, true>};
+constexpr PlanKernel kCompactBits[kBitKernels] = {compact_bits_kernel<1, false>, compact_bits_kernel<2, false>, compact_bits_kernel<4, false>,
+                                                  compact_bits_kernel<8, false>, compact_bits_kernel<16, false>};
+constexpr PlanKernel kCompactOne[] = {compact_bits_kernel<1, true>, compact_bits_kernel<2, true>};
+static_assert(32 << (std::size(kForkOne) - 1) == kForkPiece && 32 << (std::size(kCompactOne) - 1) == kCompactPiece, "a kernel for every cut");
 // As many as give every warp one piece of the tables at most (64 rows of 1040: 9.7 us with 16 entries, 10.4 with 8, of which some
 // warps have two pieces).
 int cut(PlanParams& p, int rows, bool one) {
@@ -785,7 +791,6 @@ cudaError_t launch_plan(K kernel, const PlanParams& p, bool one, int smem, cudaS
 // ---------------------------------------------------------------------------
 struct CopyParams {
   unsigned char* base[4];  // keys, values, scales, bounds
-  int planes;              // (2 for keys and values without scales and bounds)
   long long page_b, token_b, head_b;
   int pages, tokens, heads, run;       // run: contiguous 16-byte pieces; of which a page has tokens * heads
   long long page_words[2];             // scales and bounds: words of 8 bytes of a page
@@ -914,7 +919,7 @@ int check_plan(const int32_t* page_table, int64_t table_stride, int32_t table_pa
 // more pages each than a few. Forks of 8 rows of 64 pages 3.9 us so and 5.1 otherwise, of 500 4.7 and 5.5, of 1000 6.1 and 6.1;
 // compactions of 8 rows of 64 pages in a pool of 1024 4.2 and 5.0, of 500 6.8 and 5.5, of 64 in 4096 6.9 and 5.7.
 bool one_block(bool fork, int32_t pages, int32_t rows, int32_t table_pages) {
-  const long long piece = fork ? 128 : 64;
+  const long long piece = fork ? kForkPiece : kCompactPiece;
   return pages <= (fork ? kOnePages : kOnePages / 8) && rows * std::max(1LL, (table_pages + piece - 1) / piece) <= kOneRows;
 }
 
@@ -949,8 +954,8 @@ static_assert(2 * kAllWarps <= 1024 && sizeof(Tally) == 16, "the scratch buffer'
 cudaError_t setup_pages() {
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < kBitKernels && e == cudaSuccess; ++i) {
-    e = allow(kForkBits[0][i], 4 * kBitPages / 8);
-    if (e == cudaSuccess) e = allow(kCompactBits[0][i], 5 * kBitPages / 8);
+    e = allow(kForkBits[i], 4 * kBitPages / 8);
+    if (e == cudaSuccess) e = allow(kCompactBits[i], 5 * kBitPages / 8);
   }
   return e;
 }
@@ -983,7 +988,7 @@ extern "C" int tks_cache_fork(const int32_t* page_table, int64_t table_stride, i
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
   const bool bits = pages <= kBitPages && children <= kHeldChildren;
-  const PlanKernel kernel = bits ? kForkBits[one][cut(p, children, one)] : fork_kernel;
+  const PlanKernel kernel = one ? kForkOne[cut(p, children, one)] : bits ? kForkBits[cut(p, children, one)] : fork_kernel;
   if (launch_plan(kernel, p, one, bits ? 4 * p.words * 4 : 0, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;
@@ -1010,7 +1015,7 @@ extern "C" int tks_cache_compact(const int32_t* page_table, int64_t table_stride
   p.status = place.status;
   std::lock_guard<std::mutex> lock(*place.order);
   const bool bits = pages <= kBitPages;
-  const PlanKernel kernel = bits ? kCompactBits[one][cut(p, sequences, one)] : compact_kernel;
+  const PlanKernel kernel = one ? kCompactOne[cut(p, sequences, one)] : bits ? kCompactBits[cut(p, sequences, one)] : compact_kernel;
   if (launch_plan(kernel, p, one, bits ? 5 * p.words * 4 : 0, (cudaStream_t)stream) != cudaSuccess) {
     cudaGetLastError();
     return TKS_E_CUDA;

@@ -44,11 +44,6 @@ __device__ __forceinline__ float final_score(const ScoreParams& p, float x, int 
   if (j >= seen) return -INFINITY;
   return !(x == x) || j < p.first || j >= seen - p.last ? INFINITY : x;
 }
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));

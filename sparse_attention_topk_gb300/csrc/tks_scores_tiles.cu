@@ -303,12 +303,11 @@ __device__ __forceinline__ void multiply(const ScoreParams& p, const Block& k, c
 // one half's columns. GROUP: columns of a token, a power of two; 32: or some thirty-twos. (Heads that are not a power of two
 // are filled up with the last one again, which changes no maximum: of 7 heads and 4 * 200 tokens of size 64 over up to 1250
 // blocks 17 us, 49 where columns were counted.) 32 columns are on their way while the 32 before them are joined. Most tiles hold
-// blocks that all their tokens see: what their scores go through is kept short (the whole way for all of them took 101 us for
-// 2048 tokens of 32 heads over 2048 blocks, and 69 so).
+// blocks that all their tokens see, and that are not picked anyway: what their scores go through is kept short (2048 tokens of
+// 32 heads over 2048 blocks 58 us, 131 by the whole way for all of them).
 template <int GROUP>
 __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k, Shared& s, uint32_t tmem) {
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31, quarter = warp & 3, half = warp >> 2;
-  const bool plain = p.first == 0 && p.last == 0 && !p.join;
   Items items;
   items.begin(p, s);
   Item it;
@@ -317,13 +316,13 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
   while (uniform((int)items.next(p, s, it))) {
     const int tokens = uniform(min(p.half_tokens, it.tokens - half * p.half_tokens)), first = it.t0 + half * p.half_tokens;
     const int chunks = tokens <= 0 ? 0 : uniform((tokens * p.group_room + 31) / 32), each = GROUP < 32 ? 1 : p.group_room / 32;
-    int least = p.n;  // blocks that all of these tokens see
+    int least = p.n;  // blocks that all of these tokens see, and that are not among the last ones of any
     __syncwarp();
     for (int t = lane; t < tokens; t += 32) {
       bool bad = false;
       const int seen = blocks_seen(p, it.b, first + t, bad);
       seen_s[t] = seen;
-      least = min(least, seen);
+      least = min(least, seen - p.last);
     }
     least = __reduce_min_sync(0xffffffffu, least);
     __syncwarp();
@@ -332,14 +331,14 @@ __device__ __forceinline__ void take_maxima(const ScoreParams& p, const Block& k
     auto page_of = [&](int j) -> int { return j < p.n ? __ldg(p.table + it.b * p.table_stride + (j >> p.of_page_shift)) : 0; };
     int next_page = page_of(it.j0 * kBlocks + 32 * quarter + lane);  // (looked up a tile ahead)
     for (int i = uniform(it.j0); i < j1; ++i, ++g) {
-      const int j = i * kBlocks + 32 * quarter + lane, page = next_page;
+      const int j0 = i * kBlocks + 32 * quarter, j = j0 + lane, page = next_page;
       if (i + 1 < j1) next_page = page_of(j + kBlocks);
       if (!k.wait(kSumFull + (g & 1), g >> 1 & 1)) return;
       tc_fence_after();
       const uint32_t from = tmem + ((uint32_t)(quarter * 32) << 16) + (g & 1) * kRows + half * p.half_rows;
       float* to = p.out + (((long long)it.b * p.tokens + first) * p.kv_heads + it.head) * p.n + j;
       const bool there = (unsigned)page < (unsigned)p.pages;
-      const bool simple = plain && i * kBlocks + 32 * quarter + 32 <= least && __all_sync(0xffffffffu, there);
+      const bool simple = !p.join && j0 >= p.first && j0 + 32 <= least && __all_sync(0xffffffffu, there);
       bool missing = false;
       auto put = [&](float x, int t) {
         const int seen = seen_s[t];

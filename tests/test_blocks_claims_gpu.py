@@ -66,3 +66,20 @@ def test_bounds_of_lengths_that_are_held_to_the_table():
     others = torch.ones(bounds.shape[0], dtype=torch.bool, device="cuda")
     others[table[0].long()] = False
     assert torch.equal(bounds[others], before[others])
+
+
+@pytest.mark.parametrize("first, last", [(0, 0), (1, 1), (32, 0), (33, 31), (0, 65), (40, 2 ** 31 - 1)])
+@pytest.mark.parametrize("lengths", ["equal", "causal", "none"])
+def test_scores_of_chunks_are_the_same_where_none_is_forced(lengths, first, last):
+    """(Whether scores take the short way is decided for 32 blocks at a time.)"""
+    g, n, tokens = gen(6), 300, 90
+    bounds = torch.randn(n, 1, 2, 2, 64, device="cuda", generator=g).sort(3).values.to(torch.bfloat16)
+    table = torch.randperm(n, device="cuda", generator=g).to(torch.int32)[None]
+    table[0, 270] = -1  # (reported where a token sees it)
+    q = torch.randn(1, tokens, 8, 64, device="cuda", generator=g).to(torch.bfloat16)
+    kv = {"equal": ints([[269 * 8] * tokens]), "causal": ints([[8 * 180 + t for t in range(tokens)]]), "none": ints([[0] * tokens])}[lengths]
+    want, seen = tks.block_scores(q, bounds, table, kv, 8)
+    got, again = tks.block_scores(q, bounds, table, kv, 8, first=first, last=last)
+    j = torch.arange(n, device="cuda")
+    forced = ((j < first) | (j >= seen.unsqueeze(-1).long() - last)) & (j < seen.unsqueeze(-1))
+    assert torch.equal(seen, again) and torch.equal(got, torch.where(forced, math.inf, want))

@@ -101,7 +101,11 @@ int tks_cache_bounds(const tks_cache *cache, const tks_bounds *bounds, const int
  * kv_heads is more than 16, waits inside the kernel are bounded, as those of the
  * attention calls are (TKS_E_TIMEOUT; scores are then undefined).  Sizes that cannot be
  * counted in 32 bits (batch * tokens * kv_heads, or batch * n / 8) return
- * TKS_E_TOO_LARGE.
+ * TKS_E_TOO_LARGE.  Work follows kv_len for up to 1024 sequences, or, where there
+ * are more than 16 rows (as above), tiles of tokens (of 256 / group, the group being
+ * q_heads / kv_heads filled up to a power of two; 2 from 128 on); beyond, all n
+ * blocks are read for every token, whatever it sees, so that n is better no larger
+ * than the longest sequence needs.
  */
 int tks_block_scores(const tks_bounds *bounds, const tks_queries *queries, const int32_t *kv_len,
                      int32_t first, int32_t last, float *scores, int32_t n, int32_t *row_len,

@@ -33,7 +33,7 @@
 // Lists of blocks (each head its own) are looked up by the chunk, not by the key (512
 // tokens of 64 heads on 4 over 32 blocks of 64 int8 keys: a fifth less time): these, 2048
 // lists of 2048 keys, 1.1 GB out of L2, 198 us; one token over 32 blocks of 8 heads 7.8 us; 64
-// ragged tokens over 64 blocks of 32 bfloat16 keys of 2 heads 28.9 us. A list's start and end
+// ragged tokens over 64 blocks of 32 bfloat16 keys of 2 heads 28.6 us (of int8 keys 19.5). A list's start and end
 // cost 3.5 us of a block, 64 of its keys 0.78.
 //
 // Layout.  A block is four warps; each takes every fourth chunk of the block's

@@ -17,13 +17,15 @@
 // Work is the axis of all (sequence, tile of tokens)s' heads' tiles of blocks that any of their
 // tokens sees, of which every thread block takes an equal run.
 //
-// What bounds it: shared memory. A product of 128 blocks, 256 rows and 16 elements takes
-// 128 cycles of the tensor cores and reads 12 KB of operands, 96 of the 128 bytes a
-// cycle; the ring's copies write 32 more, and the scores' stores go the same way.
+// What bounds it: while products run, the tensor cores (one of 128 blocks, 256 rows and 16
+// elements takes 128 cycles, and reads 96 of shared memory's 128 bytes a cycle; the ring's
+// copies write 32 more), but they run less than half of the time.
 // Measured: 2048 tokens of 32 heads on 8 over 131,072 positions in blocks of 64 (68
-// Gflop, 134 MB of scores) 58 us, 1.17 PFLOP/s, 64 from memory; without most of the
-// stores 50, without maxima and stores 48. (A pair of SMs on one product would halve the
-// reads of queries: not tried.)
+// Gflop, 134 MB of scores) 58 us, 1.17 PFLOP/s, 63 from memory. Of these, tensor cores are
+// busy 29 (27 tiles of blocks an SM); the start takes some 7, each of the 2.7 changes of query
+// tile an SM some 4, since the queries have one buffer, refilled only as the last products
+// before release it; without most of the stores it takes 50, without maxima and stores 48.
+// (A pair of SMs on one product would have room for two tiles of queries: not tried.)
 //
 // Every wait is bounded: a wait that runs out reports TKS_E_TIMEOUT and ends its
 // warp's role, which makes the waits on that warp run out; when all roles have

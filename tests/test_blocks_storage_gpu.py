@@ -55,3 +55,9 @@ def test_what_a_fork_returns_holds_nothing_else(pages, children):
 def test_what_a_compaction_returns_holds_nothing_else(pages):
     owns(*tks.cache_compact(ints([[5, 7, -1]]), ints([20]), pages, 16))
     assert tks.device_status() == tks.TKS_OK
+
+
+def test_a_pool_of_one_page_has_no_moves():
+    table, src, dst, count = tks.cache_compact(ints([[0, -1]]), ints([3]), 1, 4)
+    assert table.tolist() == [[0, -1]] and src.numel() == dst.numel() == 0 and count.tolist() == [0, 1]
+    assert tks.device_status() == tks.TKS_OK

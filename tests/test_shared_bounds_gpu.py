@@ -92,3 +92,13 @@ def test_pages_that_are_not_shared_are_as_before():
     tks.cache_bounds(cache.k, table, ints([100, 0]), bounds, scales=cache.scales)
     got = torch.cat([bounds[row[i].long()] for i in range(2)])
     assert torch.equal(got.float(), bounds_of(keys[:100], 32).float())
+
+
+@pytest.mark.parametrize("held", ["int8", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("sequences", [607, 608, 609])
+def test_about_as_many_sequences_as_take_all_heads_of_a_block_at_once(sequences, dim, held):
+    lens = [(53 * i) % 180 for i in range(sequences)]
+    cache, row, table, keys = pool(lens, 64, 5, dim, held)
+    check(cache, row, table, keys, lens, [0] * sequences, 64, 64)
+    check(cache, row, table, keys, lens, [max(0, n - 1) for n in lens], 64, 16)
